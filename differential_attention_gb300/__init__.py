@@ -178,6 +178,23 @@ _SIGNATURES = {
                                 + [ctypes.c_void_p, ctypes.c_float, ctypes.c_void_p,
                                    ctypes.c_float] + [ctypes.c_void_p] * 5 + [ctypes.c_int] * 7
                                 + [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "diffattn_paged_plan": (ctypes.c_int, [ctypes.c_void_p] * 11 + [ctypes.c_int] * 5
+                            + [ctypes.c_void_p]),
+    "diffattn_kv4_record_bytes": (ctypes.c_int, [ctypes.c_int] * 2),
+    "diffattn_kv4_append": (ctypes.c_int, [ctypes.c_void_p] * 2 + [ctypes.POINTER(ctypes.c_longlong)]
+                            + [ctypes.c_void_p] * 2 + [ctypes.c_int] * 8 + [ctypes.c_void_p]),
+    "diffattn_kv4_gather": (ctypes.c_int, [ctypes.c_void_p] * 6 + [ctypes.c_int] * 10
+                            + [ctypes.c_void_p]),
+    "diffattn_decode_kv4_workspace_size": (ctypes.c_int, [ctypes.c_int] * 4
+                                           + [ctypes.POINTER(ctypes.c_size_t)]),
+    "diffattn_decode_kv4": (ctypes.c_int, [ctypes.c_void_p] * 6 + [ctypes.c_float, ctypes.c_void_p,
+                                                                   ctypes.c_float]
+                            + [ctypes.c_int] * 10 + [ctypes.c_void_p, ctypes.c_size_t,
+                                                     ctypes.c_void_p]),
+    "diffattn_v2_decode_kv4_workspace_size": (ctypes.c_int, [ctypes.c_int] * 4
+                                              + [ctypes.POINTER(ctypes.c_size_t)]),
+    "diffattn_v2_decode_kv4": (ctypes.c_int, [ctypes.c_void_p] * 6 + [ctypes.c_int] * 10
+                               + [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
     "diffattn_gda_decode": (ctypes.c_int, [ctypes.c_void_p] * 6 + [ctypes.c_float, ctypes.c_void_p,
                                                                     ctypes.c_float]
                             + [ctypes.c_int] * 8 + [ctypes.c_void_p, ctypes.c_size_t,
@@ -1489,4 +1506,223 @@ def diffattn_v2_decode_fp8_paged(q8, k_pool8, v_pool, block_table, seqlens, lam_
         _ptr(out), float(q_descale), float(k_descale), B, Hq, Hkv, d, num_pages, page_size,
         max_pages, 0, _ptr(workspace), workspace.numel() * workspace.element_size(),
         _stream(stream)))
+    return out
+
+
+# ---- serving over a 4-bit cache ------------------------------------------------------------------
+
+def _same_device(first, *others):
+    """The operands of one call lie on one device, and that device is the current one while the
+    call runs (the library launches on the current device)."""
+    dev = first.device
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors are on {dev} and {t.device}")
+    return dev
+
+
+def _call(dev, fn, *args, stream=None):
+    """fn(*args, stream) with `dev` current; `stream` None is dev's current stream."""
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(stream)))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, _stream(stream)))
+
+
+def diffattn_paged_plan(seqlens, new_tokens, block_table, free_ring, ring_state, page_size: int,
+                        total_max: int, out=None, stream=None) -> dict:
+    """One serving step's page plan: seqlens, new_tokens [B] int32 (-1: the request has ended),
+    block_table [B, max_pages] and free_ring [num_pages] int32 (both written in place), ring_state
+    [2] int32 = {head, count}. Returns (and, given `out`, fills) a dict of int32 tensors: seqlens
+    [B], ring_state [2], cu_seqlens_q and cu_seqlens_k [B + 1], slot_map and positions [total_max].
+    out["seqlens"] and out["ring_state"] may be the inputs themselves."""
+    for name, t in (("seqlens", seqlens), ("new_tokens", new_tokens), ("block_table", block_table),
+                    ("free_ring", free_ring), ("ring_state", ring_state)):
+        _dev(name, t, torch.int32)
+    B = seqlens.numel()
+    if seqlens.dim() != 1 or new_tokens.shape != (B,) or block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("seqlens and new_tokens must be [B] and block_table [B, max_pages]")
+    if free_ring.dim() != 1 or ring_state.shape != (2,):
+        raise ValueError("free_ring must be [num_pages] and ring_state [2]")
+    dev = _same_device(seqlens, new_tokens, block_table, free_ring, ring_state)
+    total_max = int(total_max)
+    shapes = {"seqlens": B, "ring_state": 2, "cu_seqlens_q": B + 1, "cu_seqlens_k": B + 1,
+              "slot_map": total_max, "positions": total_max}
+    if out is None:
+        if total_max < 0:
+            raise ValueError("total_max must not be negative")
+        # one allocation; every piece begins on a 16-byte boundary, as the other calls want theirs
+        sizes = [(n + 3) // 4 * 4 for n in shapes.values()]
+        parts = torch.empty(sum(sizes), dtype=torch.int32, device=dev).split(sizes)
+        out = {name: part[:n] for (name, n), part in zip(shapes.items(), parts)}
+    else:
+        for name, n in shapes.items():
+            if _dev(name, out[name], torch.int32).shape != (n,):
+                raise ValueError(f"out[{name!r}] must be [{n}]")
+        _same_device(seqlens, *out.values())
+    _call(dev, lib().diffattn_paged_plan, _ptr(seqlens), _ptr(new_tokens), _ptr(out["seqlens"]),
+          _ptr(block_table), _ptr(free_ring), _ptr(ring_state), _ptr(out["ring_state"]),
+          _ptr(out["cu_seqlens_q"]), _ptr(out["cu_seqlens_k"]), _ptr(out["slot_map"]),
+          _ptr(out["positions"]), B, block_table.shape[1], free_ring.numel(), int(page_size),
+          total_max, stream=stream)
+    return out
+
+
+def diffattn_kv4_record_bytes(kw: int, vw: int) -> int:
+    """Bytes of one record (16 tokens of one head) of a 4-bit pool with K rows of kw and V rows of
+    vw channels: 4608 for 256 and 256 (V1), 2304 for 128 and 128 (V2), 0 for other widths."""
+    return lib().diffattn_kv4_record_bytes(int(kw), int(vw))
+
+
+def diffattn_kv4_pool(num_pages: int, page_size: int, H: int, kw: int, vw: int, device="cuda"):
+    """An empty 4-bit pool: zeros, uint8 [num_pages, H, page_size / 16, record]."""
+    rec = diffattn_kv4_record_bytes(kw, vw)
+    if rec == 0 or page_size % 16 != 0:
+        raise ValueError("need widths of 256 and 256 or 128 and 128, and page_size a multiple of 16")
+    return torch.zeros((num_pages, H, page_size // 16, rec), dtype=torch.uint8, device=device)
+
+
+def _kv4_pool(pool, H, kw, vw):
+    _dev("pool", pool, torch.uint8)
+    if pool.dim() != 4 or pool.shape[1] != H or pool.shape[3] != (kw + vw) * 9:
+        raise ValueError(f"pool must be [num_pages, {H}, page_size / 16, {(kw + vw) * 9}]")
+    return pool.shape[0], pool.shape[2] * 16
+
+
+def _kv4_table(block_table, B):
+    _dev("block_table", block_table, torch.int32)
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be [B, max_pages]")
+    return block_table.shape[1]
+
+
+def diffattn_kv4_append(k, v, slot_map, pool, k_exp: int = 0, v_exp: int = 0, stream=None) -> None:
+    """Rounds rows k [total, H, kw] and v [total, H, vw] (bf16, last dimension contiguous, otherwise
+    any strides that are multiples of 8 elements) to 4 bits and writes row i at slot slot_map[i]
+    (int32 [total]; -1: not at all) of every head of `pool`."""
+    for name, t in (("k", k), ("v", v)):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.bfloat16:
+            raise ValueError(f"{name} must be a bfloat16 CUDA tensor")
+        if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+            raise ValueError(f"{name} must be [total, H, width] with a contiguous last dimension")
+    total, H, kw = k.shape
+    vw = v.shape[2]
+    if v.shape[:2] != (total, H):
+        raise ValueError("k and v must have the same tokens and heads")
+    num_pages, page_size = _kv4_pool(pool, H, kw, vw)
+    if _dev("slot_map", slot_map, torch.int32).shape != (total,):
+        raise ValueError("slot_map must be [total]")
+    dev = _same_device(k, v, slot_map, pool)
+    # a dimension of one token or head is never stepped over, so its stride may be anything
+    st = [w if n == 1 else s for t, w in ((k, kw), (v, vw)) for n, s in ((total, t.stride(0)), (H, t.stride(1)))]
+    _call(dev, lib().diffattn_kv4_append, _ptr(k), _ptr(v), (ctypes.c_longlong * 4)(*st),
+          _ptr(slot_map), _ptr(pool), total, H, kw, vw, num_pages, page_size, int(k_exp), int(v_exp),
+          stream=stream)
+
+
+def diffattn_kv4_gather(pool, block_table, cu_seqlens, total: int, kw: int, vw: int, starts=None,
+                        k_exp: int = 0, v_exp: int = 0, out=None, stream=None):
+    """Cached rows as packed bf16: (k [total, H, kw], v [total, H, vw]), row cu_seqlens[b] + i being
+    token starts[b] + i (starts int32 [B]; None: 0) of sequence b. Without `out` = (k, v), rows
+    behind the last sequence are not initialised."""
+    _dev("cu_seqlens", cu_seqlens, torch.int32)
+    B = cu_seqlens.numel() - 1
+    if pool.dim() != 4:
+        raise ValueError("pool must be [num_pages, H, page_size / 16, record]")
+    H, total, kw, vw = pool.shape[1], int(total), int(kw), int(vw)
+    num_pages, page_size = _kv4_pool(pool, H, kw, vw)
+    max_pages = _kv4_table(block_table, B)
+    if starts is not None and _dev("starts", starts, torch.int32).shape != (B,):
+        raise ValueError("starts must be [B]")
+    if out is None:
+        k = torch.empty((max(0, total), H, kw), dtype=torch.bfloat16, device=pool.device)
+        v = torch.empty((max(0, total), H, vw), dtype=torch.bfloat16, device=pool.device)
+    else:
+        k, v = out
+        if _dev("out[0]", k, torch.bfloat16).shape != (total, H, kw) or \
+                _dev("out[1]", v, torch.bfloat16).shape != (total, H, vw):
+            raise ValueError("out must be ([total, H, kw], [total, H, vw])")
+    dev = _same_device(pool, block_table, cu_seqlens, starts, k, v)
+    _call(dev, lib().diffattn_kv4_gather, _ptr(pool), _ptr(block_table), _ptr(cu_seqlens),
+          _ptr(starts), _ptr(k), _ptr(v), total, B, H, kw, vw, num_pages, page_size, max_pages,
+          int(k_exp), int(v_exp), stream=stream)
+    return k, v
+
+
+def diffattn_decode_kv4_workspace_size(B: int, H: int, d: int = 128, dv: int = 256) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().diffattn_decode_kv4_workspace_size(B, H, d, dv, ctypes.byref(n)))
+    return n.value
+
+
+def diffattn_decode_kv4(q, pool, block_table, seqlens, lam, lambda_init: float = 0.0,
+                        norm_weight=None, eps: float = 1e-5, norm: bool = True, scale: bool = True,
+                        k_exp: int = 0, v_exp: int = 0, workspace=None, out=None, stream=None):
+    """V1 decode over a 4-bit pool [num_pages, H, page_size / 16, 4608]: q [B, H, 256], block_table
+    [B, max_pages] int32, seqlens [B] int32 (0: no keys, a row of zeros)."""
+    _dev("q", q, torch.bfloat16)
+    if q.dim() != 3:
+        raise ValueError("q must be [B, H, 2d]")
+    B, H, two_d = q.shape
+    num_pages, page_size = _kv4_pool(pool, H, two_d, two_d)
+    max_pages = _kv4_table(block_table, B)
+    if _dev("seqlens", seqlens, torch.int32).shape != (B,):
+        raise ValueError("seqlens must be [B]")
+    if _dev("lam", lam, torch.float32).shape != (H,):
+        raise ValueError("lam must be [H]")
+    if norm_weight is not None and _dev("norm_weight", norm_weight, torch.float32).shape != (two_d,):
+        raise ValueError("norm_weight must be [2d]")
+    if workspace is None:
+        workspace = torch.empty(diffattn_decode_kv4_workspace_size(B, H, two_d // 2, two_d),
+                                dtype=torch.uint8, device=q.device)
+    if out is None:
+        out = torch.empty_like(q)
+    elif _dev("out", out, torch.bfloat16).shape != q.shape:
+        raise ValueError("out must be [B, H, 2d]")
+    _dev("workspace", workspace)
+    dev = _same_device(q, pool, block_table, seqlens, lam, norm_weight, workspace, out)
+    flags = (DIFFATTN_NORM if norm else 0) | (DIFFATTN_SCALE if scale else 0)
+    _call(dev, lib().diffattn_decode_kv4, _ptr(q), _ptr(pool), _ptr(block_table), _ptr(seqlens),
+          _ptr(out), _ptr(lam), float(lambda_init), _ptr(norm_weight), float(eps), B, H, two_d // 2,
+          two_d, num_pages, page_size, max_pages, int(k_exp), int(v_exp), flags, _ptr(workspace),
+          workspace.numel() * workspace.element_size(), stream=stream)
+    return out
+
+
+def diffattn_v2_decode_kv4_workspace_size(B: int, Hq: int, Hkv: int, d: int = 128) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().diffattn_v2_decode_kv4_workspace_size(B, Hq, Hkv, d, ctypes.byref(n)))
+    return n.value
+
+
+def diffattn_v2_decode_kv4(q, pool, block_table, seqlens, lam_logit, k_exp: int = 0, v_exp: int = 0,
+                           workspace=None, out=None, stream=None):
+    """DIFF V2 decode over a 4-bit pool [num_pages, Hkv, page_size / 16, 2304]: q [B, Hq, 128],
+    block_table [B, max_pages] int32, seqlens [B] int32 (0: no keys, rows of zeros), lam_logit
+    [B, Hq/2] fp32. Returns [B, Hq/2, 128]."""
+    _dev("q", q, torch.bfloat16)
+    if q.dim() != 3 or pool.dim() != 4:
+        raise ValueError("q must be [B, Hq, d] and pool [num_pages, Hkv, page_size / 16, record]")
+    B, Hq, d = q.shape
+    Hkv = pool.shape[1]
+    num_pages, page_size = _kv4_pool(pool, Hkv, d, d)
+    max_pages = _kv4_table(block_table, B)
+    if _dev("seqlens", seqlens, torch.int32).shape != (B,):
+        raise ValueError("seqlens must be [B]")
+    if _dev("lam_logit", lam_logit, torch.float32).shape != (B, Hq // 2):
+        raise ValueError("lam_logit must be [B, Hq/2]")
+    if workspace is None:
+        workspace = torch.empty(diffattn_v2_decode_kv4_workspace_size(B, Hq, Hkv, d),
+                                dtype=torch.uint8, device=q.device)
+    if out is None:
+        out = torch.empty((B, Hq // 2, d), dtype=torch.bfloat16, device=q.device)
+    elif _dev("out", out, torch.bfloat16).shape != (B, Hq // 2, d):
+        raise ValueError("out must be [B, Hq/2, d]")
+    _dev("workspace", workspace)
+    dev = _same_device(q, pool, block_table, seqlens, lam_logit, workspace, out)
+    _call(dev, lib().diffattn_v2_decode_kv4, _ptr(q), _ptr(pool), _ptr(block_table), _ptr(seqlens),
+          _ptr(lam_logit), _ptr(out), B, Hq, Hkv, d, num_pages, page_size, max_pages, int(k_exp),
+          int(v_exp), 0, _ptr(workspace), workspace.numel() * workspace.element_size(),
+          stream=stream)
     return out

@@ -24,7 +24,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libdiffattn.so")
 BUILD_DEBUG = os.path.join(PKG, "_build_debug")
 LIB_DEBUG = os.path.join(PKG, "libdiffattn_debug.so")
-SOURCES = ["api.cu", "simt.cu", "decode.cu", "decode_v2_tc.cu", "backward.cu", "host_pipeline.cu", "tmap.cu", "prefill_tc.cu", "prefill_exact.cu", "prefill_v2.cu"]
+SOURCES = ["api.cu", "simt.cu", "decode.cu", "decode_v2_tc.cu", "decode_kv4.cu", "kv4_rows.cu", "paged_plan.cu", "backward.cu", "host_pipeline.cu", "tmap.cu", "prefill_tc.cu", "prefill_exact.cu", "prefill_v2.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -78,6 +78,11 @@ DIFFATTN_API int diffattn_device_status(void* stream) {
   if (e == cudaSuccess) e = da::status_backward(&z);
   int dd = 0;
   if (e == cudaSuccess) e = da::status_decode(&dd);
+  int kd = 0, kr = 0, pp = 0;
+  if (e == cudaSuccess) e = da::status_decode_kv4(&kd);
+  if (e == cudaSuccess) e = da::status_kv4_rows(&kr);
+  if (e == cudaSuccess) e = da::status_paged_plan(&pp);
+  dd |= kd | kr | pp;
   if (e != cudaSuccess) return cuda_fail(e, "reading the device status word");
   v |= w | x | y | z | dd;
   if (v & DEV_BOUNDS_BIT)
@@ -2112,3 +2117,230 @@ DIFFATTN_API int diffattn_gda_decode_paged(const void* q, const void* k_pool, co
   if (e != cudaSuccess) return cuda_fail(e, fn);
   return ok();
 }
+
+
+extern "C" {
+
+DIFFATTN_API int diffattn_paged_plan(const int* seqlens, const int* new_tokens, int* seqlens_out,
+                                     int* block_table, int* free_ring, const int* ring_state,
+                                     int* ring_state_out, int* cu_seqlens_q, int* cu_seqlens_k,
+                                     int* slot_map, int* positions, int B, int max_pages,
+                                     int num_pages, int page_size, int total_max, void* stream) {
+  const char* fn = "diffattn_paged_plan";
+  if (!seqlens || !new_tokens || !seqlens_out || !block_table || !free_ring || !ring_state ||
+      !ring_state_out || !cu_seqlens_q || !cu_seqlens_k || (!slot_map && total_max > 0))
+    return fail(DIFFATTN_ERR_ARG, "%s: null pointer", fn);
+  if (B < 1 || B > da::kPlanMaxRequests || max_pages < 1 || num_pages < 1 || page_size < 1 || total_max < 0)
+    return fail(DIFFATTN_ERR_SHAPE, "%s: need 1 <= B <= %d, max_pages, num_pages, page_size >= 1 and total_max >= 0",
+                fn, da::kPlanMaxRequests);
+  if (static_cast<long long>(max_pages) * page_size > (1LL << 30) ||
+      static_cast<long long>(num_pages) * page_size > 0x7fffffffLL || num_pages > (1 << 30))
+    return fail(DIFFATTN_ERR_SHAPE, "%s: need max_pages * page_size <= 2^30, num_pages * page_size < 2^31 and num_pages <= 2^30", fn);
+  for (const void* ptr : {static_cast<const void*>(seqlens), static_cast<const void*>(new_tokens),
+                          static_cast<const void*>(seqlens_out), static_cast<const void*>(block_table),
+                          static_cast<const void*>(free_ring), static_cast<const void*>(ring_state),
+                          static_cast<const void*>(ring_state_out), static_cast<const void*>(cu_seqlens_q),
+                          static_cast<const void*>(cu_seqlens_k), static_cast<const void*>(slot_map),
+                          static_cast<const void*>(positions)})
+    if (!aligned(ptr, 4)) return fail(DIFFATTN_ERR_ALIGN, "%s: int32 pointers must be 4-byte aligned", fn);
+  int rc = check_device();
+  if (rc) return rc;
+  da::PlanArgs a{seqlens, new_tokens, seqlens_out, block_table, free_ring, ring_state, ring_state_out,
+                 cu_seqlens_q, cu_seqlens_k, slot_map, positions, B, max_pages, num_pages, page_size,
+                 total_max};
+  cudaError_t e = da::launch_paged_plan(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, fn);
+  return ok();
+}
+
+DIFFATTN_API int diffattn_kv4_record_bytes(int kw, int vw) {
+  return kw == vw && (kw == 128 || kw == 256) ? (kw + vw) / 128 * 1152 : 0;
+}
+
+}  // extern "C"
+
+namespace {
+
+// the sizes that every call on a 4-bit pool shares
+int check_kv4(const char* fn, int H, int kw, int vw, int num_pages, int page_size, int k_exp, int v_exp) {
+  if (k_exp < -64 || k_exp > 64 || v_exp < -64 || v_exp > 64)
+    return fail(DIFFATTN_ERR_ARG, "%s: k_exp and v_exp must be in [-64, 64]", fn);
+  if (H < 1 || H > 65535) return fail(DIFFATTN_ERR_SHAPE, "%s: need 1 <= H <= 65535", fn);
+  if (diffattn_kv4_record_bytes(kw, vw) == 0)
+    return fail(DIFFATTN_ERR_SHAPE, "%s: need widths of 256 and 256 (V1) or 128 and 128 (V2), got %d and %d", fn, kw, vw);
+  if (num_pages < 1 || page_size < 16 || page_size % 16 != 0 ||
+      static_cast<long long>(num_pages) * page_size > 0x7fffffffLL)
+    return fail(DIFFATTN_ERR_SHAPE, "%s: need num_pages >= 1, page_size a multiple of 16 and num_pages * page_size < 2^31", fn);
+  return DIFFATTN_OK;
+}
+int check_kv4_tables(const char* fn, int B, int page_size, int max_pages) {
+  if (B < 1 || B > da::kPlanMaxRequests)
+    return fail(DIFFATTN_ERR_SHAPE, "%s: need 1 <= B <= %d", fn, da::kPlanMaxRequests);
+  if (max_pages < 1 || static_cast<long long>(max_pages) * page_size > (1LL << 30))
+    return fail(DIFFATTN_ERR_SHAPE, "%s: need max_pages >= 1 and max_pages * page_size <= 2^30", fn);
+  return DIFFATTN_OK;
+}
+
+int decode_kv4_impl(const char* fn, da::Kv4DecodeArgs& a, int cols, int width, int k_exp, int v_exp,
+                    size_t ws_bytes, void* stream) {
+  int rc = check_kv4(fn, a.H, width, width, a.num_pages, a.page_size, k_exp, v_exp);
+  if (!rc) rc = check_kv4_tables(fn, a.B, a.page_size, a.max_pages);
+  if (rc) return rc;
+  if (!aligned(a.q, 16) || !aligned(a.pool, 16) || !aligned(a.out, 16) || !aligned(a.block_table, 4) ||
+      !aligned(a.seqlens, 4) || !aligned(a.lambda, 4) || !aligned(a.lam_logit, 4) || !aligned(a.norm_w, 16))
+    return fail(DIFFATTN_ERR_ALIGN, "%s: tensors must be 16-byte aligned", fn);
+  const size_t need = da::kv4_decode_workspace_bytes(a.B, a.H, cols, width);
+  if (!a.ws || ws_bytes < need || !aligned(a.ws, 256))
+    return fail(DIFFATTN_ERR_WORKSPACE, "%s: need a 256-byte aligned workspace of %zu bytes", fn, need);
+  rc = check_device();
+  if (rc) return rc;
+  a.qk_scale = static_cast<float>(std::ldexp(1.4426950408889634 / std::sqrt(128.0), k_exp));
+  a.v_mul = std::ldexp(1.0f, v_exp);
+  cudaError_t e = da::launch_kv4_decode(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, fn);
+  return ok();
+}
+
+}  // namespace
+
+extern "C" {
+
+DIFFATTN_API int diffattn_kv4_append(const void* k, const void* v, const long long* strides,
+                                     const int* slot_map, void* pool, int total, int H, int kw,
+                                     int vw, int num_pages, int page_size, int k_exp, int v_exp,
+                                     void* stream) {
+  const char* fn = "diffattn_kv4_append";
+  if (!strides || !pool || (total > 0 && (!k || !v || !slot_map)))
+    return fail(DIFFATTN_ERR_ARG, "%s: null pointer", fn);
+  int rc = check_kv4(fn, H, kw, vw, num_pages, page_size, k_exp, v_exp);
+  if (rc) return rc;
+  if (total < 0 || static_cast<long long>(total) * H > (1LL << 30))
+    return fail(DIFFATTN_ERR_SHAPE, "%s: need total >= 0 and total * H <= 2^30", fn);
+  for (int i = 0; i < 4; ++i)
+    if (strides[i] < 1 || strides[i] % 8 != 0 || strides[i] > (1LL << 36))
+      return fail(DIFFATTN_ERR_ALIGN, "%s: stride %d (%lld) must be a positive multiple of 8 elements", fn, i, strides[i]);
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(pool, 16) || !aligned(slot_map, 4))
+    return fail(DIFFATTN_ERR_ALIGN, "%s: tensors must be 16-byte aligned", fn);
+  rc = check_device();
+  if (rc) return rc;
+  da::Kv4AppendArgs a{static_cast<const __nv_bfloat16*>(k), static_cast<const __nv_bfloat16*>(v),
+                      strides[0], strides[1], strides[2], strides[3], slot_map,
+                      static_cast<uint8_t*>(pool), total, H, kw / 128, vw / 128, num_pages, page_size,
+                      std::ldexp(1.0f, -k_exp), std::ldexp(1.0f, -v_exp)};
+  cudaError_t e = da::launch_kv4_append(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, fn);
+  return ok();
+}
+
+DIFFATTN_API int diffattn_kv4_gather(const void* pool, const int* block_table,
+                                     const int* cu_seqlens, const int* starts, void* k_out,
+                                     void* v_out, int total, int B, int H, int kw, int vw,
+                                     int num_pages, int page_size, int max_pages, int k_exp,
+                                     int v_exp, void* stream) {
+  const char* fn = "diffattn_kv4_gather";
+  if (!pool || !block_table || !cu_seqlens || (total > 0 && (!k_out || !v_out)))
+    return fail(DIFFATTN_ERR_ARG, "%s: null pointer", fn);
+  int rc = check_kv4(fn, H, kw, vw, num_pages, page_size, k_exp, v_exp);
+  if (!rc) rc = check_kv4_tables(fn, B, page_size, max_pages);
+  if (rc) return rc;
+  if (total < 0 || static_cast<long long>(total) * H > (1LL << 30))
+    return fail(DIFFATTN_ERR_SHAPE, "%s: need total >= 0 and total * H <= 2^30", fn);
+  if (!aligned(pool, 16) || !aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(block_table, 4) ||
+      !aligned(cu_seqlens, 4) || !aligned(starts, 4))
+    return fail(DIFFATTN_ERR_ALIGN, "%s: tensors must be 16-byte aligned", fn);
+  rc = check_device();
+  if (rc) return rc;
+  da::Kv4GatherArgs a{static_cast<const uint8_t*>(pool), block_table, cu_seqlens, starts,
+                      static_cast<__nv_bfloat16*>(k_out), static_cast<__nv_bfloat16*>(v_out), total, B,
+                      H, kw / 128, vw / 128, num_pages, page_size, max_pages, std::ldexp(1.0f, k_exp),
+                      std::ldexp(1.0f, v_exp)};
+  cudaError_t e = da::launch_kv4_gather(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, fn);
+  return ok();
+}
+
+DIFFATTN_API int diffattn_decode_kv4_workspace_size(int B, int H, int d, int dv, size_t* bytes) {
+  const char* fn = "diffattn_decode_kv4_workspace_size";
+  if (!bytes) return fail(DIFFATTN_ERR_ARG, "%s: null pointer", fn);
+  if (B < 1 || B > da::kPlanMaxRequests || H < 1 || H > 65535 || d != 128 || dv != 256)
+    return fail(DIFFATTN_ERR_SHAPE, "%s: need 1 <= B <= %d, 1 <= H <= 65535, d = 128, dv = 256", fn, da::kPlanMaxRequests);
+  *bytes = da::kv4_decode_workspace_bytes(B, H, 2, 256);
+  return ok();
+}
+
+DIFFATTN_API int diffattn_decode_kv4(const void* q, const void* pool, const int* block_table,
+                                     const int* seqlens, void* out, const float* lambda,
+                                     float lambda_init, const float* norm_weight, float eps, int B,
+                                     int H, int d, int dv, int num_pages, int page_size,
+                                     int max_pages, int k_exp, int v_exp, int flags,
+                                     void* workspace, size_t ws_bytes, void* stream) {
+  const char* fn = "diffattn_decode_kv4";
+  if (!q || !pool || !block_table || !seqlens || !out || !lambda)
+    return fail(DIFFATTN_ERR_ARG, "%s: null pointer", fn);
+  if (flags & ~(DIFFATTN_CAUSAL | DIFFATTN_NORM | DIFFATTN_SCALE))
+    return fail(DIFFATTN_ERR_ARG, "%s: unknown flag bits 0x%x", fn, flags);
+  if ((flags & DIFFATTN_NORM) && !(eps > 0.f))
+    return fail(DIFFATTN_ERR_ARG, "%s: eps must be > 0 with DIFFATTN_NORM", fn);
+  if (d != 128 || dv != 256)
+    return fail(DIFFATTN_ERR_SHAPE, "%s: need d = 128 and dv = 256 (got d=%d dv=%d)", fn, d, dv);
+  da::Kv4DecodeArgs a{};
+  a.q = q;
+  a.pool = static_cast<const uint8_t*>(pool);
+  a.block_table = block_table;
+  a.seqlens = seqlens;
+  a.out = out;
+  a.lambda = lambda;
+  a.norm_w = norm_weight;
+  a.eps = eps;
+  a.lambda_init = lambda_init;
+  a.flags = flags;
+  a.B = B;
+  a.H = H;
+  a.group = 0;
+  a.num_pages = num_pages;
+  a.page_size = page_size;
+  a.max_pages = max_pages;
+  a.ws = workspace;
+  return decode_kv4_impl(fn, a, 2, 256, k_exp, v_exp, ws_bytes, stream);
+}
+
+DIFFATTN_API int diffattn_v2_decode_kv4_workspace_size(int B, int Hq, int Hkv, int d,
+                                                       size_t* bytes) {
+  const char* fn = "diffattn_v2_decode_kv4_workspace_size";
+  if (!bytes) return fail(DIFFATTN_ERR_ARG, "%s: null pointer", fn);
+  if (B < 1 || B > da::kPlanMaxRequests || Hkv < 1 || Hkv > 65535 || Hq < 1 || d != 128 ||
+      !(Hq == 2LL * Hkv || Hq == 4LL * Hkv || Hq == 8LL * Hkv))
+    return fail(DIFFATTN_ERR_SHAPE, "%s: need 1 <= B <= %d, d = 128 and Hq / Hkv in {2, 4, 8}", fn, da::kPlanMaxRequests);
+  *bytes = da::kv4_decode_workspace_bytes(B, Hkv, Hq / Hkv, 128);
+  return ok();
+}
+
+DIFFATTN_API int diffattn_v2_decode_kv4(const void* q, const void* pool, const int* block_table,
+                                        const int* seqlens, const float* lam_logit, void* out,
+                                        int B, int Hq, int Hkv, int d, int num_pages, int page_size,
+                                        int max_pages, int k_exp, int v_exp, int flags,
+                                        void* workspace, size_t ws_bytes, void* stream) {
+  const char* fn = "diffattn_v2_decode_kv4";
+  if (!q || !pool || !block_table || !seqlens || !lam_logit || !out)
+    return fail(DIFFATTN_ERR_ARG, "%s: null pointer", fn);
+  if (flags & ~DIFFATTN_CAUSAL) return fail(DIFFATTN_ERR_ARG, "%s: unknown flag bits 0x%x", fn, flags);
+  if (Hkv < 1 || d != 128 || !(Hq == 2LL * Hkv || Hq == 4LL * Hkv || Hq == 8LL * Hkv))
+    return fail(DIFFATTN_ERR_SHAPE, "%s: need d = 128 and Hq / Hkv in {2, 4, 8} (got Hq=%d Hkv=%d d=%d)", fn, Hq, Hkv, d);
+  da::Kv4DecodeArgs a{};
+  a.q = q;
+  a.pool = static_cast<const uint8_t*>(pool);
+  a.block_table = block_table;
+  a.seqlens = seqlens;
+  a.out = out;
+  a.lam_logit = lam_logit;
+  a.B = B;
+  a.H = Hkv;
+  a.group = Hq / Hkv;
+  a.num_pages = num_pages;
+  a.page_size = page_size;
+  a.max_pages = max_pages;
+  a.ws = workspace;
+  return decode_kv4_impl(fn, a, a.group, 128, k_exp, v_exp, ws_bytes, stream);
+}
+
+}  // extern "C"

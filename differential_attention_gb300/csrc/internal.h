@@ -3,6 +3,7 @@
 #include <cstddef>
 #include <cstdint>
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 namespace da {
@@ -295,6 +296,70 @@ constexpr size_t kNoAllocScratchBytes = static_cast<size_t>(16) << 20;
 long long decode_noalloc_max_units();  // largest B * H whose partials fit (one split each)
 int decode_noalloc_splits(int B, int Lmax, int H, int* chunk_out);  // splits the no-alloc call runs
 cudaError_t launch_decode_noalloc(const DecodeArgs& a, cudaStream_t s);
+
+// The 4-bit cache (kv4_rows.cu, decode_kv4.cu). Pools: [num_pages, H, page_size / 16, record], a
+// record 16 tokens of one head: kp K planes and vp V planes of 128 channels (kv4.cuh).
+struct Kv4AppendArgs {
+  const __nv_bfloat16* k;  // [total, H, 128 kp], element strides of a token and a head
+  const __nv_bfloat16* v;
+  long long k_token, k_head, v_token, v_head;
+  const int* slot_map;
+  uint8_t* pool;
+  int total, H, kp, vp, num_pages, page_size;
+  float k_inv, v_inv;  // 2^-k_exp, 2^-v_exp
+};
+cudaError_t launch_kv4_append(const Kv4AppendArgs& a, cudaStream_t s);
+struct Kv4GatherArgs {
+  const uint8_t* pool;
+  const int* block_table;
+  const int* cu_seqlens;
+  const int* starts;  // or null: 0
+  __nv_bfloat16* k_out;
+  __nv_bfloat16* v_out;
+  int total, B, H, kp, vp, num_pages, page_size, max_pages;
+  float k_mul, v_mul;  // 2^k_exp, 2^v_exp
+};
+cudaError_t launch_kv4_gather(const Kv4GatherArgs& a, cudaStream_t s);
+cudaError_t status_kv4_rows(int* v);
+struct Kv4DecodeArgs {
+  const void* q;  // V1 [B, H, 256], V2 [B, H group, 128]
+  const uint8_t* pool;
+  const int* block_table;
+  const int* seqlens;
+  void* out;
+  const float* lambda;     // V1 [H]
+  const float* lam_logit;  // V2 [B, H group / 2]
+  const float* norm_w;
+  float eps, lambda_init;
+  int flags;
+  int B, H, group;  // KV heads; V2: query heads per KV head, V1: 0
+  int num_pages, page_size, max_pages;
+  float qk_scale;   // log2(e) / sqrt(128) 2^k_exp
+  float v_mul;      // 2^v_exp
+  void* ws;
+};
+size_t kv4_decode_workspace_bytes(int B, int H, int cols, int width);
+cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a, cudaStream_t s);
+cudaError_t status_decode_kv4(int* v);
+
+// A step's page plan (paged_plan.cu).
+constexpr int kPlanMaxRequests = 8192;
+struct PlanArgs {
+  const int* seqlens;
+  const int* new_tokens;
+  int* seqlens_out;
+  int* block_table;
+  int* free_ring;
+  const int* ring_state;
+  int* ring_state_out;
+  int* cu_seqlens_q;
+  int* cu_seqlens_k;
+  int* slot_map;
+  int* positions;  // or null
+  int B, max_pages, num_pages, page_size, total_max;
+};
+cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t s);
+cudaError_t status_paged_plan(int* v);
 
 // Two-pass tensor-core prefill (A1 - lambda A2 formed in fp32 before rounding).
 cudaError_t launch_prefill_exact(const Problem& p, cudaStream_t s, char* err, size_t err_len);

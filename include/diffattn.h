@@ -847,6 +847,138 @@ DIFFATTN_API int diffattn_gda_decode_paged(const void* q, const void* k_pool, co
                                            int page_size, int max_pages, int flags, int dtype,
                                            void* workspace, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------------------------
+ * Page plan of one serving step (the pages give no cache layout; this is the bookkeeping of the
+ * paged calls above): from the lengths of a batch's requests, on the device, the block tables,
+ * the slot of every new token, and the offsets that the packed calls take.
+ *   seqlens    : device int32 [B], tokens cached of each request before the step
+ *   new_tokens : device int32 [B]: n >= 0, the request gets n tokens in this step; -1, it has
+ *                ended (its pages go back to the ring, its length becomes 0)
+ *   seqlens_out : device int32 [B], the lengths after the step; may be `seqlens` itself
+ *   block_table : device int32 [B, max_pages], read and written in place: key j of request b lies in
+ *                page block_table[b][j / page_size]. Only the entries of pages that a request grows
+ *                into are written; those past a request's pages mean nothing
+ *   free_ring, ring_state : device int32 [num_pages] and [2] = {head, count}: the free pages are
+ *                free_ring[(head + i) % num_pages], i < count. Pages are taken from the front, in the
+ *                order of the requests; returned ones go behind the last (in the order of the
+ *                requests and of their tables), before any is taken. free_ring is written in place
+ *   ring_state_out : device int32 [2]; may be `ring_state` itself
+ *   cu_seqlens_q : device int32 [B + 1], new tokens before each request (0 .. their total)
+ *   cu_seqlens_k : device int32 [B + 1], the same sums over the lengths after the step of the
+ *                requests that have new tokens (0 for the others): with cu_seqlens_q what
+ *                diffattn_fwd_varlen_qk takes, and what diffattn_kv4_gather lays keys out by
+ *   slot_map   : device int32 [total_max]: page * page_size + offset of each new token, in the
+ *                order of cu_seqlens_q; -1 behind the last
+ *   positions  : device int32 [total_max] or NULL: each new token's position in its request; -1
+ *                behind the last
+ * A step that does not fit changes nothing: where a length, a new length or the ring's state is out
+ * of range, the new tokens are more than total_max, or the free and returned pages fewer than
+ * needed, then the tables and the ring stay, seqlens_out and ring_state_out repeat their inputs, the
+ * offsets are 0 and the slots -1, and diffattn_device_status() reports DIFFATTN_ERR_INDEX. A page
+ * id outside [0, num_pages) in the ring or a table is passed on as it is; its tokens get slot -1,
+ * and it is reported the same way.
+ * Supported: B <= 8192, num_pages * page_size < 2^31, max_pages * page_size <= 2^30. One launch.
+ * seqlens, new_tokens and the tables must not overlap other outputs than those named.
+ * Errors: ERR_ARG, ERR_SHAPE, ERR_ALIGN, ERR_UNSUPPORTED, ERR_CUDA. */
+DIFFATTN_API int diffattn_paged_plan(const int* seqlens, const int* new_tokens, int* seqlens_out,
+                                     int* block_table, int* free_ring, const int* ring_state,
+                                     int* ring_state_out, int* cu_seqlens_q, int* cu_seqlens_k,
+                                     int* slot_map, int* positions, int B, int max_pages,
+                                     int num_pages, int page_size, int total_max, void* stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Key/value cache in 4 bits. Every 16 channels of a K or V row share one e4m3 scale s and hold e2m1
+ * codes c (values 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives): channel = c * s * 2^e, e one
+ * exponent for all K and one for all V of the cache (k_exp, v_exp; in [-64, 64]). 4.5 bits a
+ * channel. Written from bf16 as
+ *   s = e4m3(min(amax 2^-e / 6, 448)), amax the block's largest magnitude;
+ *   c = e2m1(x 2^-e / s), ties to the even code, at most 6 (0 where s = 0),
+ * both of them the exact roundings (a power of two and 8 + 4 significant bits lose nothing in
+ * fp32). A block with an Inf or a NaN gets s = NaN and reads as NaN. Choose e so that the largest
+ * magnitude stays below 2688 * 2^e (larger ones are cut to it) and the blocks' largest above
+ * 2^-6 * 6 * 2^e (below, the scale itself loses bits): e = 0 does for rows of unit size.
+ *
+ * Pool: device uint8 [num_pages, H, page_size / 16, record], 16-byte aligned. A record holds 16
+ * consecutive tokens of one head in planes of 128 channels, first K's kw / 128 planes, then V's
+ * vw / 128: V1 kw = vw = 256 (K1, K2, V's halves; 4608 bytes), V2 kw = vw = 128 (2304 bytes). A
+ * plane is 1024 bytes of codes (the lower channel of a pair in the low nibble), then 128 scales:
+ *   K: channels 32t .. 32t+31 of token i at 512 (i/2 % 2) + 128 (i/4) + 64 (i % 2) + 16 t, scales of
+ *      channels 32t + 16u at 1024 + 32 (i/4) + 16 (i % 2) + 4 t + 2 (i/2 % 2) + u
+ *   V: channels 16g .. 16g+15 at 512 (i/2 % 2) + 64 g + 16 (i/4) + 8 (i % 2), scale at
+ *      1024 + 16 g + 4 (i/4) + i % 4
+ * (the order in which a warp's lanes take them for the attention's matrix products). Slot s is token
+ * s % page_size of page s / page_size; page_size is a multiple of 16.
+ * ------------------------------------------------------------------------------------------ */
+/* Bytes of one record; 0 for a pair of widths that is not supported. */
+DIFFATTN_API int diffattn_kv4_record_bytes(int kw, int vw);
+
+/* New rows into a 4-bit cache: row i of k and v goes to slot slot_map[i] of every head.
+ *   k : device bf16 [total, H, kw], v : device bf16 [total, H, vw]; the last dimension contiguous,
+ *       the others by strides: host int64 [4] = {k: token, head, v: token, head}, in elements,
+ *       positive multiples of 8 (views of one fused projection, for example)
+ *   slot_map : device int32 [total]; -1 skips a row; any other value outside [0, num_pages *
+ *       page_size) skips it and is reported by diffattn_device_status() as DIFFATTN_ERR_INDEX.
+ *       Slots that are not -1 must differ: of two rows with one slot, either's blocks may stay
+ *   pool : written at those slots alone. Rows of one call may share a record with rows that
+ *       another kernel reads or writes at the same time, at other slots
+ *   total : may be 0
+ * Errors: ERR_ARG, ERR_SHAPE, ERR_ALIGN, ERR_UNSUPPORTED, ERR_CUDA. */
+DIFFATTN_API int diffattn_kv4_append(const void* k, const void* v, const long long* strides,
+                                     const int* slot_map, void* pool, int total, int H, int kw,
+                                     int vw, int num_pages, int page_size, int k_exp, int v_exp,
+                                     void* stream);
+
+/* Rows of a 4-bit cache as packed bf16, for the packed prefills (a prompt's chunk over what is
+ * cached): row cu_seqlens[b] + i of k_out and v_out is token starts[b] + i of sequence b.
+ *   block_table : device int32 [B, max_pages];  cu_seqlens : device int32 [B + 1], non-decreasing
+ *       from 0, cu_seqlens[B] <= total (diffattn_paged_plan's cu_seqlens_k for whole sequences)
+ *   starts : device int32 [B] or NULL (0)
+ *   k_out : device bf16 [total, H, kw];  v_out : device bf16 [total, H, vw]. Rows behind the last
+ *       sequence are not written. A value is rounded to bf16 once (exact where |c s| needs no
+ *       more than its 6 bits: always, up to overflow and underflow of 2^e)
+ * A token outside its table is left unwritten, a used table entry outside [0, num_pages) reads
+ * page 0; both are reported by diffattn_device_status() as DIFFATTN_ERR_INDEX.
+ * Errors: ERR_ARG, ERR_SHAPE, ERR_ALIGN, ERR_UNSUPPORTED, ERR_CUDA. */
+DIFFATTN_API int diffattn_kv4_gather(const void* pool, const int* block_table,
+                                     const int* cu_seqlens, const int* starts, void* k_out,
+                                     void* v_out, int total, int B, int H, int kw, int vw,
+                                     int num_pages, int page_size, int max_pages, int k_exp,
+                                     int v_exp, void* stream);
+
+/* Decode over a 4-bit cache: diffattn_decode_paged (V1) and diffattn_v2_decode_paged (V2) with the
+ * keys and values in a pool as above. Scores, softmax statistics and sums in fp32; a cached value
+ * enters the products exactly (in fp16), the query with all its bits, a probability rounded to fp16.
+ *   q    : device bf16 [B, H, 2d] (V1) or [B, Hq, d] (V2)
+ *   pool : V1 kw = vw = 2d; V2 H = Hkv, kw = vw = d. k_exp, v_exp as written
+ *   block_table : device int32 [B, max_pages]; seqlens : device int32 [B], keys 0 .. seqlens[b] - 1
+ *          are attended; a value outside [0, max_pages * page_size] is clamped into it. A sequence of
+ *          no keys gives zeros (an empty place in the batch). Slots past a sequence's keys never
+ *          reach the result, whatever they hold
+ *   out, lambda, lambda_init, norm_weight, eps, flags; lam_logit : as for the calls named
+ *   workspace, ws_bytes : at least the *_workspace_size bytes, 256-byte aligned; contents need not be
+ *          initialised, and no call depends on what an earlier one left there. Not shared with a
+ *          call that can run at the same time.
+ * A used table entry outside [0, num_pages) reads page 0 and is reported by
+ * diffattn_device_status() as DIFFATTN_ERR_INDEX. A call's result does not depend on the order in
+ * which its blocks run: equal inputs give equal bits.
+ * Supported: d = 128 (V1: dv = 256), page_size a multiple of 16, B <= 8192; V2: Hq / Hkv in
+ * {2, 4, 8}.
+ * Errors: ERR_ARG, ERR_SHAPE, ERR_ALIGN, ERR_WORKSPACE, ERR_UNSUPPORTED, ERR_CUDA. */
+DIFFATTN_API int diffattn_decode_kv4_workspace_size(int B, int H, int d, int dv, size_t* bytes);
+DIFFATTN_API int diffattn_decode_kv4(const void* q, const void* pool, const int* block_table,
+                                     const int* seqlens, void* out, const float* lambda,
+                                     float lambda_init, const float* norm_weight, float eps, int B,
+                                     int H, int d, int dv, int num_pages, int page_size,
+                                     int max_pages, int k_exp, int v_exp, int flags,
+                                     void* workspace, size_t ws_bytes, void* stream);
+DIFFATTN_API int diffattn_v2_decode_kv4_workspace_size(int B, int Hq, int Hkv, int d,
+                                                       size_t* bytes);
+DIFFATTN_API int diffattn_v2_decode_kv4(const void* q, const void* pool, const int* block_table,
+                                        const int* seqlens, const float* lam_logit, void* out,
+                                        int B, int Hq, int Hkv, int d, int num_pages, int page_size,
+                                        int max_pages, int k_exp, int v_exp, int flags,
+                                        void* workspace, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
