@@ -13,6 +13,7 @@ Layouts (dense, row-major):
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -1510,24 +1511,44 @@ def diffattn_v2_decode_fp8_paged(q8, k_pool8, v_pool, block_table, seqlens, lam_
 
 
 # ---- serving over a 4-bit cache ------------------------------------------------------------------
+# A serving loop makes these calls for every token, and the smallest take the GPU a few microseconds:
+# each operand is checked once, in as few steps as Python allows, and pointers go to ctypes as ints.
 
-def _same_device(first, *others):
-    """The operands of one call lie on one device, and that device is the current one while the
-    call runs (the library launches on the current device)."""
-    dev = first.device
-    for t in others:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors are on {dev} and {t.device}")
-    return dev
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _call(dev, fn, *args, stream=None):
-    """fn(*args, stream) with `dev` current; `stream` None is dev's current stream."""
-    if dev.index is None or dev.index == torch.cuda.current_device():
-        _check(fn(*args, _stream(stream)))
+def _operand(name, t, dtype, index, shape=None) -> int:
+    """The address of a contiguous tensor of `dtype` (and `shape`) on CUDA device `index`."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_contiguous() or not t.is_cuda:
+        _dev(name, t, dtype)  # raises with the reason
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, and other operands on cuda:{index}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return t.data_ptr()
+
+
+def _index(name, t) -> int:
+    """The CUDA device that a call's first operand is on."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.get_device()
+
+
+def _call(index, fn, *args, stream=None):
+    """fn(*args, stream) with device `index` current; `stream` None is that device's current stream."""
+    if stream is None:
+        raw = _raw_stream(index)
     else:
-        with torch.cuda.device(dev):
-            _check(fn(*args, _stream(stream)))
+        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if index == torch._C._cuda_getDevice():
+        rc = fn(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, raw)
+    if rc != DIFFATTN_OK:
+        _check(rc)
 
 
 def diffattn_paged_plan(seqlens, new_tokens, block_table, free_ring, ring_state, page_size: int,
@@ -1537,35 +1558,27 @@ def diffattn_paged_plan(seqlens, new_tokens, block_table, free_ring, ring_state,
     [2] int32 = {head, count}. Returns (and, given `out`, fills) a dict of int32 tensors: seqlens
     [B], ring_state [2], cu_seqlens_q and cu_seqlens_k [B + 1], slot_map and positions [total_max].
     out["seqlens"] and out["ring_state"] may be the inputs themselves."""
-    for name, t in (("seqlens", seqlens), ("new_tokens", new_tokens), ("block_table", block_table),
-                    ("free_ring", free_ring), ("ring_state", ring_state)):
-        _dev(name, t, torch.int32)
+    i32, dev = torch.int32, _index("seqlens", seqlens)
     B = seqlens.numel()
-    if seqlens.dim() != 1 or new_tokens.shape != (B,) or block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError("seqlens and new_tokens must be [B] and block_table [B, max_pages]")
-    if free_ring.dim() != 1 or ring_state.shape != (2,):
-        raise ValueError("free_ring must be [num_pages] and ring_state [2]")
-    dev = _same_device(seqlens, new_tokens, block_table, free_ring, ring_state)
+    if block_table.dim() != 2 or free_ring.dim() != 1:
+        raise ValueError("block_table must be [B, max_pages] and free_ring [num_pages]")
+    max_pages, num_pages = block_table.shape[1], free_ring.shape[0]
     total_max = int(total_max)
-    shapes = {"seqlens": B, "ring_state": 2, "cu_seqlens_q": B + 1, "cu_seqlens_k": B + 1,
-              "slot_map": total_max, "positions": total_max}
+    sizes = [B, 2, B + 1, B + 1, total_max, total_max]
     if out is None:
         if total_max < 0:
             raise ValueError("total_max must not be negative")
-        # one allocation; every piece begins on a 16-byte boundary, as the other calls want theirs
-        sizes = [(n + 3) // 4 * 4 for n in shapes.values()]
-        parts = torch.empty(sum(sizes), dtype=torch.int32, device=dev).split(sizes)
-        out = {name: part[:n] for (name, n), part in zip(shapes.items(), parts)}
+        parts = torch.empty(sum(sizes), dtype=i32, device=seqlens.device).split(sizes)
+        out = dict(zip(("seqlens", "ring_state", "cu_seqlens_q", "cu_seqlens_k", "slot_map", "positions"), parts))
+        p = [t.data_ptr() for t in parts]
     else:
-        for name, n in shapes.items():
-            if _dev(name, out[name], torch.int32).shape != (n,):
-                raise ValueError(f"out[{name!r}] must be [{n}]")
-        _same_device(seqlens, *out.values())
-    _call(dev, lib().diffattn_paged_plan, _ptr(seqlens), _ptr(new_tokens), _ptr(out["seqlens"]),
-          _ptr(block_table), _ptr(free_ring), _ptr(ring_state), _ptr(out["ring_state"]),
-          _ptr(out["cu_seqlens_q"]), _ptr(out["cu_seqlens_k"]), _ptr(out["slot_map"]),
-          _ptr(out["positions"]), B, block_table.shape[1], free_ring.numel(), int(page_size),
-          total_max, stream=stream)
+        p = [_operand(f"out[{name!r}]", out[name], i32, dev, (n,)) for name, n in zip(
+            ("seqlens", "ring_state", "cu_seqlens_q", "cu_seqlens_k", "slot_map", "positions"), sizes)]
+    _call(dev, lib().diffattn_paged_plan, _operand("seqlens", seqlens, i32, dev, (B,)),
+          _operand("new_tokens", new_tokens, i32, dev, (B,)), p[0],
+          _operand("block_table", block_table, i32, dev, (B, max_pages)),
+          _operand("free_ring", free_ring, i32, dev), _operand("ring_state", ring_state, i32, dev, (2,)),
+          p[1], p[2], p[3], p[4], p[5], B, max_pages, num_pages, int(page_size), total_max, stream=stream)
     return out
 
 
@@ -1583,42 +1596,45 @@ def diffattn_kv4_pool(num_pages: int, page_size: int, H: int, kw: int, vw: int, 
     return torch.zeros((num_pages, H, page_size // 16, rec), dtype=torch.uint8, device=device)
 
 
-def _kv4_pool(pool, H, kw, vw):
-    _dev("pool", pool, torch.uint8)
-    if pool.dim() != 4 or pool.shape[1] != H or pool.shape[3] != (kw + vw) * 9:
-        raise ValueError(f"pool must be [num_pages, {H}, page_size / 16, {(kw + vw) * 9}]")
-    return pool.shape[0], pool.shape[2] * 16
+def _kv4_pool(pool, index, H, kw, vw):
+    """(address, num_pages, page_size) of a pool of H heads and rows of kw and vw channels."""
+    shape = pool.shape
+    if len(shape) != 4 or shape[1] != H or shape[3] != (kw + vw) * 9:
+        raise ValueError(f"pool must be [num_pages, {H}, page_size / 16, {(kw + vw) * 9}], got {list(shape)}")
+    return _operand("pool", pool, torch.uint8, index), shape[0], shape[2] * 16
 
 
-def _kv4_table(block_table, B):
-    _dev("block_table", block_table, torch.int32)
-    if block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError("block_table must be [B, max_pages]")
-    return block_table.shape[1]
+def _kv4_table(block_table, index, B):
+    """(address, max_pages) of a block table of B sequences."""
+    shape = block_table.shape
+    if len(shape) != 2 or shape[0] != B:
+        raise ValueError(f"block_table must be [{B}, max_pages], got {list(shape)}")
+    return _operand("block_table", block_table, torch.int32, index), shape[1]
 
 
 def diffattn_kv4_append(k, v, slot_map, pool, k_exp: int = 0, v_exp: int = 0, stream=None) -> None:
     """Rounds rows k [total, H, kw] and v [total, H, vw] (bf16, last dimension contiguous, otherwise
     any strides that are multiples of 8 elements) to 4 bits and writes row i at slot slot_map[i]
     (int32 [total]; -1: not at all) of every head of `pool`."""
-    for name, t in (("k", k), ("v", v)):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.bfloat16:
-            raise ValueError(f"{name} must be a bfloat16 CUDA tensor")
-        if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
-            raise ValueError(f"{name} must be [total, H, width] with a contiguous last dimension")
-    total, H, kw = k.shape
-    vw = v.shape[2]
-    if v.shape[:2] != (total, H):
-        raise ValueError("k and v must have the same tokens and heads")
-    num_pages, page_size = _kv4_pool(pool, H, kw, vw)
-    if _dev("slot_map", slot_map, torch.int32).shape != (total,):
-        raise ValueError("slot_map must be [total]")
-    dev = _same_device(k, v, slot_map, pool)
-    # a dimension of one token or head is never stepped over, so its stride may be anything
-    st = [w if n == 1 else s for t, w in ((k, kw), (v, vw)) for n, s in ((total, t.stride(0)), (H, t.stride(1)))]
-    _call(dev, lib().diffattn_kv4_append, _ptr(k), _ptr(v), (ctypes.c_longlong * 4)(*st),
-          _ptr(slot_map), _ptr(pool), total, H, kw, vw, num_pages, page_size, int(k_exp), int(v_exp),
-          stream=stream)
+    dev = _index("k", k)
+    _index("v", v)
+    if k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16 or k.dim() != 3 or v.dim() != 3:
+        raise ValueError("k and v must be bfloat16 [total, H, width]")
+    (total, H, kw), (kt, kh, kc) = k.shape, k.stride()
+    vw, (vt, vh, vc) = v.shape[2], v.stride()
+    if v.shape != (total, H, vw) or v.get_device() != dev:
+        raise ValueError("k and v must have the same tokens and heads, on the same device")
+    if (kc != 1 and kw > 1) or (vc != 1 and vw > 1):
+        raise ValueError("the last dimension of k and v must be contiguous")
+    # a dimension of one token or head is never stepped over: its stride may be anything
+    if total == 1:
+        kt, vt = kw, vw
+    if H == 1:
+        kh, vh = kw, vw
+    at, num_pages, page_size = _kv4_pool(pool, dev, H, kw, vw)
+    _call(dev, lib().diffattn_kv4_append, k.data_ptr(), v.data_ptr(), (ctypes.c_longlong * 4)(kt, kh, vt, vh),
+          _operand("slot_map", slot_map, torch.int32, dev, (total,)), at, total, H, kw, vw, num_pages,
+          page_size, int(k_exp), int(v_exp), stream=stream)
 
 
 def diffattn_kv4_gather(pool, block_table, cu_seqlens, total: int, kw: int, vw: int, starts=None,
@@ -1626,30 +1642,27 @@ def diffattn_kv4_gather(pool, block_table, cu_seqlens, total: int, kw: int, vw: 
     """Cached rows as packed bf16: (k [total, H, kw], v [total, H, vw]), row cu_seqlens[b] + i being
     token starts[b] + i (starts int32 [B]; None: 0) of sequence b. Without `out` = (k, v), rows
     behind the last sequence are not initialised."""
-    _dev("cu_seqlens", cu_seqlens, torch.int32)
+    dev = _index("pool", pool)
     B = cu_seqlens.numel() - 1
     if pool.dim() != 4:
         raise ValueError("pool must be [num_pages, H, page_size / 16, record]")
     H, total, kw, vw = pool.shape[1], int(total), int(kw), int(vw)
-    num_pages, page_size = _kv4_pool(pool, H, kw, vw)
-    max_pages = _kv4_table(block_table, B)
-    if starts is not None and _dev("starts", starts, torch.int32).shape != (B,):
-        raise ValueError("starts must be [B]")
+    at, num_pages, page_size = _kv4_pool(pool, dev, H, kw, vw)
+    table, max_pages = _kv4_table(block_table, dev, B)
     if out is None:
-        k = torch.empty((max(0, total), H, kw), dtype=torch.bfloat16, device=pool.device)
-        v = torch.empty((max(0, total), H, vw), dtype=torch.bfloat16, device=pool.device)
-    else:
-        k, v = out
-        if _dev("out[0]", k, torch.bfloat16).shape != (total, H, kw) or \
-                _dev("out[1]", v, torch.bfloat16).shape != (total, H, vw):
-            raise ValueError("out must be ([total, H, kw], [total, H, vw])")
-    dev = _same_device(pool, block_table, cu_seqlens, starts, k, v)
-    _call(dev, lib().diffattn_kv4_gather, _ptr(pool), _ptr(block_table), _ptr(cu_seqlens),
-          _ptr(starts), _ptr(k), _ptr(v), total, B, H, kw, vw, num_pages, page_size, max_pages,
-          int(k_exp), int(v_exp), stream=stream)
+        n = max(0, total)
+        out = (torch.empty((n, H, kw), dtype=torch.bfloat16, device=pool.device),
+               torch.empty((n, H, vw), dtype=torch.bfloat16, device=pool.device))
+    k, v = out
+    _call(dev, lib().diffattn_kv4_gather, at, table, _operand("cu_seqlens", cu_seqlens, torch.int32, dev, (B + 1,)),
+          None if starts is None else _operand("starts", starts, torch.int32, dev, (B,)),
+          _operand("out[0]", k, torch.bfloat16, dev, (max(0, total), H, kw)),
+          _operand("out[1]", v, torch.bfloat16, dev, (max(0, total), H, vw)), total, B, H, kw, vw, num_pages,
+          page_size, max_pages, int(k_exp), int(v_exp), stream=stream)
     return k, v
 
 
+@functools.lru_cache(maxsize=4096)
 def diffattn_decode_kv4_workspace_size(B: int, H: int, d: int = 128, dv: int = 256) -> int:
     n = ctypes.c_size_t(0)
     _check(lib().diffattn_decode_kv4_workspace_size(B, H, d, dv, ctypes.byref(n)))
@@ -1661,35 +1674,29 @@ def diffattn_decode_kv4(q, pool, block_table, seqlens, lam, lambda_init: float =
                         k_exp: int = 0, v_exp: int = 0, workspace=None, out=None, stream=None):
     """V1 decode over a 4-bit pool [num_pages, H, page_size / 16, 4608]: q [B, H, 256], block_table
     [B, max_pages] int32, seqlens [B] int32 (0: no keys, a row of zeros)."""
-    _dev("q", q, torch.bfloat16)
+    dev = _index("q", q)
     if q.dim() != 3:
         raise ValueError("q must be [B, H, 2d]")
     B, H, two_d = q.shape
-    num_pages, page_size = _kv4_pool(pool, H, two_d, two_d)
-    max_pages = _kv4_table(block_table, B)
-    if _dev("seqlens", seqlens, torch.int32).shape != (B,):
-        raise ValueError("seqlens must be [B]")
-    if _dev("lam", lam, torch.float32).shape != (H,):
-        raise ValueError("lam must be [H]")
-    if norm_weight is not None and _dev("norm_weight", norm_weight, torch.float32).shape != (two_d,):
-        raise ValueError("norm_weight must be [2d]")
+    at, num_pages, page_size = _kv4_pool(pool, dev, H, two_d, two_d)
+    table, max_pages = _kv4_table(block_table, dev, B)
     if workspace is None:
         workspace = torch.empty(diffattn_decode_kv4_workspace_size(B, H, two_d // 2, two_d),
                                 dtype=torch.uint8, device=q.device)
     if out is None:
         out = torch.empty_like(q)
-    elif _dev("out", out, torch.bfloat16).shape != q.shape:
-        raise ValueError("out must be [B, H, 2d]")
-    _dev("workspace", workspace)
-    dev = _same_device(q, pool, block_table, seqlens, lam, norm_weight, workspace, out)
     flags = (DIFFATTN_NORM if norm else 0) | (DIFFATTN_SCALE if scale else 0)
-    _call(dev, lib().diffattn_decode_kv4, _ptr(q), _ptr(pool), _ptr(block_table), _ptr(seqlens),
-          _ptr(out), _ptr(lam), float(lambda_init), _ptr(norm_weight), float(eps), B, H, two_d // 2,
-          two_d, num_pages, page_size, max_pages, int(k_exp), int(v_exp), flags, _ptr(workspace),
-          workspace.numel() * workspace.element_size(), stream=stream)
+    _call(dev, lib().diffattn_decode_kv4, _operand("q", q, torch.bfloat16, dev), at, table,
+          _operand("seqlens", seqlens, torch.int32, dev, (B,)), _operand("out", out, torch.bfloat16, dev, (B, H, two_d)),
+          _operand("lam", lam, torch.float32, dev, (H,)), lambda_init,
+          None if norm_weight is None else _operand("norm_weight", norm_weight, torch.float32, dev, (two_d,)),
+          eps, B, H, two_d // 2, two_d, num_pages, page_size, max_pages, int(k_exp), int(v_exp), flags,
+          _operand("workspace", workspace, workspace.dtype, dev), workspace.numel() * workspace.element_size(),
+          stream=stream)
     return out
 
 
+@functools.lru_cache(maxsize=4096)
 def diffattn_v2_decode_kv4_workspace_size(B: int, Hq: int, Hkv: int, d: int = 128) -> int:
     n = ctypes.c_size_t(0)
     _check(lib().diffattn_v2_decode_kv4_workspace_size(B, Hq, Hkv, d, ctypes.byref(n)))
@@ -1701,28 +1708,22 @@ def diffattn_v2_decode_kv4(q, pool, block_table, seqlens, lam_logit, k_exp: int 
     """DIFF V2 decode over a 4-bit pool [num_pages, Hkv, page_size / 16, 2304]: q [B, Hq, 128],
     block_table [B, max_pages] int32, seqlens [B] int32 (0: no keys, rows of zeros), lam_logit
     [B, Hq/2] fp32. Returns [B, Hq/2, 128]."""
-    _dev("q", q, torch.bfloat16)
+    dev = _index("q", q)
     if q.dim() != 3 or pool.dim() != 4:
         raise ValueError("q must be [B, Hq, d] and pool [num_pages, Hkv, page_size / 16, record]")
     B, Hq, d = q.shape
     Hkv = pool.shape[1]
-    num_pages, page_size = _kv4_pool(pool, Hkv, d, d)
-    max_pages = _kv4_table(block_table, B)
-    if _dev("seqlens", seqlens, torch.int32).shape != (B,):
-        raise ValueError("seqlens must be [B]")
-    if _dev("lam_logit", lam_logit, torch.float32).shape != (B, Hq // 2):
-        raise ValueError("lam_logit must be [B, Hq/2]")
+    at, num_pages, page_size = _kv4_pool(pool, dev, Hkv, d, d)
+    table, max_pages = _kv4_table(block_table, dev, B)
     if workspace is None:
         workspace = torch.empty(diffattn_v2_decode_kv4_workspace_size(B, Hq, Hkv, d),
                                 dtype=torch.uint8, device=q.device)
     if out is None:
         out = torch.empty((B, Hq // 2, d), dtype=torch.bfloat16, device=q.device)
-    elif _dev("out", out, torch.bfloat16).shape != (B, Hq // 2, d):
-        raise ValueError("out must be [B, Hq/2, d]")
-    _dev("workspace", workspace)
-    dev = _same_device(q, pool, block_table, seqlens, lam_logit, workspace, out)
-    _call(dev, lib().diffattn_v2_decode_kv4, _ptr(q), _ptr(pool), _ptr(block_table), _ptr(seqlens),
-          _ptr(lam_logit), _ptr(out), B, Hq, Hkv, d, num_pages, page_size, max_pages, int(k_exp),
-          int(v_exp), 0, _ptr(workspace), workspace.numel() * workspace.element_size(),
-          stream=stream)
+    _call(dev, lib().diffattn_v2_decode_kv4, _operand("q", q, torch.bfloat16, dev), at, table,
+          _operand("seqlens", seqlens, torch.int32, dev, (B,)),
+          _operand("lam_logit", lam_logit, torch.float32, dev, (B, Hq // 2)),
+          _operand("out", out, torch.bfloat16, dev, (B, Hq // 2, d)), B, Hq, Hkv, d, num_pages, page_size,
+          max_pages, int(k_exp), int(v_exp), 0, _operand("workspace", workspace, workspace.dtype, dev),
+          workspace.numel() * workspace.element_size(), stream=stream)
     return out

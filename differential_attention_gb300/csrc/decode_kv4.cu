@@ -1,11 +1,35 @@
 // decode_kv4.cu -- decode attention over the 4-bit cache: one query token per sequence.
 //
-// For one (sequence, KV head) the kernel keeps COLS running softmaxes (V1: the two maps of one
-// head; V2: the G query heads of the group) over the same keys and one output row of V's width for
-// each: o = sum_j 2^(s_j - m) v_j, l = sum_j 2^(s_j - m), rescaled where the maximum m grows.
-// Then V1: o1/l1 - lambda o2/l2, the norm and the scale; V2: o_2p/l_2p - sigmoid(lam) o_2p+1/l_2p+1.
-// This first form is the plain one: a block for each (sequence, KV head), 16 keys at a time unpacked
-// into shared memory as fp32, and CUDA-core products.
+// For one (sequence, KV head), a "row" here, there are up to 8 softmaxes over the same keys (V1: the two
+// maps of a head; V2: the G query heads of a group), each with an output of V's width:
+//   o = sum_j 2^(s_j - m) v_j,   l = sum_j 2^(s_j - m),   s_j = log2(e) / sqrt(d) q . k_j,
+// and then V1: o1/l1 - lambda o2/l2, the norm and the scale; V2: o_2p/l_2p - sigmoid(lam) o_2p+1/l_2p+1.
+//
+// What bounds it: the cache's bytes, 144 (V2) or 288 (V1) a key, read once. At 6.8 TB/s an SM gets
+// 23.5 bytes a cycle, a key of 256 channels every 6.1 cycles, so unpacking and both products have
+// to stay under that: some 24 instructions a key over all four schedulers.
+//
+// Products. Both run as m16n8k16 with the keys or V's channels on the 16 rows and the query heads
+// on the 8 columns, which is where G = 8 fits exactly:
+//   S^T [16 keys x 8] = K [16 keys x 128] Q^T,    O^T [channels x 8] += V^T [channels x 16 keys] P^T.
+// The operands come straight from registers: a record (16 tokens) holds its bytes in the order in
+// which the lanes need them, so one 16-byte shared-memory load gives a lane the codes of four
+// products, one cvt turns a byte into two fp16 values (exact: an e2m1 times an e4m3 has at most 6
+// significant bits), and one multiply puts the scale on. A tensor-memory product would want the
+// unpacked tile written to shared memory first, 512 bytes a key at 128 bytes a cycle: 4 of the 6.1
+// cycles for the writes alone. P^T's fragment is S^T's transposed, by movmatrix.
+//
+// Numerics. Q enters as fp16 after a power of two of its own for each head (its largest channel at
+// 2^14 .. 2^15: bf16's 8 bits fit, channels 2^-38 of the largest are lost, which fp32 sums lose as
+// well). P is rounded to fp16 at 2^10 times its value against the reference m, so that its absolute
+// error is 2^-35 of the largest probability; m follows the running maximum only where a score
+// passes it by 2^4, which leaves every P below 2^14. Sums and statistics are fp32.
+//
+// Work. The rows, one after the other, are cut into equal ranges, one for each resident block, whatever
+// the sequences' lengths; a row counts its tiles and a fixed cost. A block walks its range: a row that
+// lies in it whole is finished there; the pieces of one that does not go to the workspace, at most
+// two a block, and the second kernel merges them.
+#include <cfloat>
 #include <cmath>
 
 #include "internal.h"
@@ -15,134 +39,664 @@
 namespace da {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kWarps = 4;                        // consumer warps
+constexpr int kThreads = (kWarps + 1) * 32;      // and a producer
+constexpr int kSms = 152;
+constexpr int kMergeThreads = 1024;
+constexpr float kPScale = 10.f;                  // log2 of P's scale
+constexpr float kMoveRef = 14.f;                 // log2 P at which the reference moves
 
-template <int KP, int G>  // KP: planes of K (2: V1, 1: V2); G: query heads per KV head (V1: 1)
-__global__ void __launch_bounds__(KP * 128) kv4_decode_kernel(const Kv4DecodeArgs a) {
-  constexpr int W = KP * 128;             // row width of K and of V
-  constexpr int COLS = KP == 2 ? 2 : G;
-  __shared__ float sq[COLS][128];         // the queries, times log2(e) / sqrt(d) 2^k_exp
-  __shared__ float sk[16][W + 1], sv[16][W];
-  __shared__ float ss[COLS][16], sm[COLS], sl[COLS], sc[COLS];
-  __shared__ float red[W / 32];
-  const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
-  for (int i = tid; i < COLS * 128; i += W) {
-    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
-    sq[i >> 7][i & 127] = __bfloat162float(q[(static_cast<size_t>(b) * a.H + h) * COLS * 128 + i]) * a.qk_scale;
-  }
-  if (tid < COLS) sm[tid] = -INFINITY, sl[tid] = 0.f;
-  const long long cap = static_cast<long long>(a.max_pages) * a.page_size;
-  int len = a.seqlens[b];
-  len = len < 0 ? 0 : len > cap ? static_cast<int>(cap) : len;
-  float o[COLS];
+template <int KP>
+struct Cfg {
+  static constexpr int kRecs = KP == 1 ? 2 : 1;  // records of a tile for each consumer warp
+  static constexpr int kTileRecs = kWarps * kRecs;
+  static constexpr int kTileKeys = 16 * kTileRecs;
+  static constexpr int kCtas = 3;                // blocks of an SM
+  static constexpr int kGrid = kSms * kCtas;
+  static constexpr int kRowCost = KP == 1 ? 2 : 3;  // what a row costs besides its tiles, in tiles
+  static constexpr int kMinCost = KP == 1 ? 3 : 4;  // the smallest range
+  static constexpr int kRecord = 2 * KP * kKv4Plane;
+  static constexpr int kWidth = KP * 128;
+  static constexpr int kMaxCols = KP == 1 ? 8 : 2;
+  static constexpr int kQBytes = kMaxCols * 256;
+  static constexpr int kStage = kTileRecs * kRecord + kQBytes;
+  static constexpr int kStages = KP == 1 ? 2 : 3;
+  static constexpr int kPitch = kWidth + 4;      // floats of one column's row in the exchange
+  static constexpr int kSmem = kStages * kStage + kWarps * kMaxCols * kPitch * 4;
+};
+
+// where a block's range begins, for the merge
+struct Desc {
+  int b, h, tile, tiles;
+  long long total;
+  int n, pad;
+};
+
+struct Params {
+  Kv4DecodeArgs a;
+  int cols;
+  Desc* desc;
+  float* rec;  // [2 * grid][2 cols + cols * width]: m, l, o
+};
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                    uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(x));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+// place in the walk over rows (sequence-major, heads inner)
+struct Walk {
+  int b, h, tile, tiles, len;
+};
+__device__ __forceinline__ int clamp_len(const Kv4DecodeArgs& a, int b) {
+  const int cap = a.max_pages * a.page_size;
+  const int n = __ldg(a.seqlens + b);
+  return n < 0 ? 0 : n > cap ? cap : n;
+}
+template <int KP>
+__device__ __forceinline__ int tiles_of(int len) {
+  return (len + Cfg<KP>::kTileKeys - 1) / Cfg<KP>::kTileKeys;
+}
+// what a row takes of a range: its tiles, and kRowCost for its query, its join and its output
+template <int KP>
+__device__ __forceinline__ int cost_of(int len) {
+  return len == 0 ? 0 : tiles_of<KP>(len) + Cfg<KP>::kRowCost;
+}
+template <int KP>
+__device__ __forceinline__ void next_row(const Kv4DecodeArgs& a, Walk& w) {
+  w.tile = 0;
+  if (++w.h < a.H) return;
+  w.h = 0;
+  do {
+    if (++w.b >= a.B) return;  // the range ends here
+    w.len = clamp_len(a, w.b);
+  } while (w.len == 0);
+  w.tiles = tiles_of<KP>(w.len);
+}
+
+__device__ __forceinline__ long long range_start(long long total, int n, int i) { return total * i / n; }
+
+// the first product of a sum
+__device__ __forceinline__ void mma_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// S^T of one record: rows g (key 4 (g/2) + g%2) and g + 8 (that + 2), columns 2t and 2t + 1. `at`: the
+// K plane's codes for this lane.
+__device__ __forceinline__ void scores(float (&c)[4], uint32_t at, int lane, const uint32_t (&qf)[8][2]) {
+  const uint4 lo4 = lds128(at), hi4 = lds128(at + 512);
+  const uint32_t sc = lds32(at - lane * 12 + kKv4PlaneCodes);
+  const uint32_t slo = e4m3x2_to_half2(sc & 0xffffu), shi = e4m3x2_to_half2(sc >> 16);
+  const uint32_t wl[4] = {lo4.x, lo4.y, lo4.z, lo4.w}, wh[4] = {hi4.x, hi4.y, hi4.z, hi4.w};
 #pragma unroll
-  for (int c = 0; c < COLS; ++c) o[c] = 0.f;
+  for (int k = 0; k < 4; ++k) {
+    // the scale of channels 32t + 8k .. of row g, and of row g + 8, in both halves
+    const uint32_t sl = __byte_perm(slo, 0, k < 2 ? 0x1010 : 0x3232);
+    const uint32_t sh = __byte_perm(shi, 0, k < 2 ? 0x1010 : 0x3232);
+    uint32_t x[4], y[4];
+    e2m1x8_to_half2(wl[k], x);
+    e2m1x8_to_half2(wh[k], y);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = half2_mul(x[i], sl), y[i] = half2_mul(y[i], sh);
+    if (k == 0) mma_first(c, x[0], y[0], x[1], y[1], qf[0][0], qf[0][1]);
+    else mma(c, x[0], y[0], x[1], y[1], qf[2 * k][0], qf[2 * k][1]);
+    mma(c, x[2], y[2], x[3], y[3], qf[2 * k + 1][0], qf[2 * k + 1][1]);
+  }
+}
+
+// O^T += V^T P^T of one record and plane: rows g and g + 8 of product j are channels 16g + 2j and + 1.
+// `live`: how many of this lane's tokens 4t .. 4t + 3 count (4 or more: all).
+__device__ __forceinline__ void outputs(float (*o)[4], uint32_t at, int lane, int live, uint32_t b0, uint32_t b1) {
+  const uint4 va = lds128(at), vb = lds128(at + 512);
+  uint32_t sc = lds32(at - lane * 12 + kKv4PlaneCodes);
+  if (live < 4) sc = live <= 0 ? 0u : sc & (0xffffffffu >> (32 - 8 * live));  // rows past the end: scale 0
+  const uint32_t s01 = e4m3x2_to_half2(sc & 0xffffu), s23 = e4m3x2_to_half2(sc >> 16);
+  // pairs of tokens side by side: the low nibbles of two rows' bytes, then the high ones
+  const uint32_t r0[2] = {va.x, va.y}, r1[2] = {va.z, va.w}, r2[2] = {vb.x, vb.y}, r3[2] = {vb.z, vb.w};
+  constexpr uint32_t kLow = 0x0f0f0f0fu;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    uint32_t e01[4], d01[4], e23[4], d23[4];
+    e2m1x8_to_half2((r0[k] & kLow) | ((r1[k] << 4) & ~kLow), e01);
+    e2m1x8_to_half2(((r0[k] >> 4) & kLow) | (r1[k] & ~kLow), d01);
+    e2m1x8_to_half2((r2[k] & kLow) | ((r3[k] << 4) & ~kLow), e23);
+    e2m1x8_to_half2(((r2[k] >> 4) & kLow) | (r3[k] & ~kLow), d23);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      mma(o[4 * k + i], half2_mul(e01[i], s01), half2_mul(d01[i], s01), half2_mul(e23[i], s23),
+          half2_mul(d23[i], s23), b0, b1);
+  }
+}
+
+template <int KP>
+__global__ void __launch_bounds__(kThreads, Cfg<KP>::kCtas) kv4_split_kernel(const Params p) {
+  using C = Cfg<KP>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(8) uint64_t bars[2 * C::kStages];
+  __shared__ long long s_sum[kThreads / 32];
+  __shared__ long long s_pos;
+  __shared__ int s_b;
+  __shared__ int s_abort;
+  __shared__ float s_m[2][kWarps][8], s_l[2][kWarps][8];
+  __shared__ float s_red[kWarps];
+  const Kv4DecodeArgs& a = p.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t ring = smem_u32(smem), bar0 = smem_u32(bars);
+  auto full = [&](int s) { return bar0 + 8 * s; };
+  auto empty = [&](int s) { return bar0 + 8 * (C::kStages + s); };
+  float* s_o = reinterpret_cast<float*>(smem + C::kStages * C::kStage);
+
+  if (tid == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), kWarps);
+    }
+    fence_barrier_init();
+    s_abort = 0;
+  }
+
+  // The range: the batch's rows one behind the other, cut in n equal parts.
+  const int per = (a.B + kThreads - 1) / kThreads;
+  const int lo = min(a.B, tid * per), hi = min(a.B, lo + per);
+  long long mine = 0;
+  for (int b = lo; b < hi; ++b) mine += cost_of<KP>(clamp_len(a, b));
+  long long incl = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long o = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += o;
+  }
+  if (lane == 31) s_sum[warp] = incl;
   __syncthreads();
-  for (int k0 = 0; k0 < len; k0 += 16) {
-    const int pi = k0 / a.page_size, off = k0 - pi * a.page_size;
-    int page = a.block_table[static_cast<size_t>(b) * a.max_pages + pi];
-    if (page < 0 || page >= a.num_pages) {
-      if (tid == 0) flag_device_error(DEV_BAD_INDEX);
-      page = 0;
-    }
-    const uint8_t* rec = a.pool + ((static_cast<size_t>(page) * a.H + h) * (a.page_size >> 4) + (off >> 4)) *
-                                      static_cast<size_t>(2 * KP * kKv4Plane);
-    const int n = min(16, len - k0);
-    // 16 keys x 2 KP planes x 8 blocks of 16 channels
-    for (int i = tid; i < 16 * 2 * KP * 8; i += W) {
-      const int key = i / (2 * KP * 8), blk = i % (2 * KP * 8), plane = blk >> 3, b8 = blk & 7;
-      const bool is_k = plane < KP;
-      const uint8_t* p = rec + plane * kKv4Plane;
-      const int t = b8 >> 1, u = b8 & 1;
-      const uint2 c = *reinterpret_cast<const uint2*>(p + (is_k ? kv4_k_code(key, t) + u * 8 : kv4_v_code(key, b8)));
-      float s = e4m3_to_float(p[is_k ? kv4_k_scale(key, t) + u : kv4_v_scale(key, b8)]);
-      if (key >= n) s = 0.f;  // rows past the end may hold anything
-      float* dst = is_k ? &sk[key][blk * 16] : &sv[key][(blk - KP * 8) * 16];
-      uint32_t x[4], y[4];
-      e2m1x8_to_half2(c.x, x);
-      e2m1x8_to_half2(c.y, y);
+  long long before = incl - mine, total = 0;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x[j]));
-        const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&y[j]));
-        dst[2 * j] = f.x * s;
-        dst[2 * j + 1] = f.y * s;
-        dst[8 + 2 * j] = g.x * s;
-        dst[8 + 2 * j + 1] = g.y * s;
-      }
-    }
-    __syncthreads();
-    if (tid < COLS * 16) {
-      const int c = tid >> 4, key = tid & 15;
-      float s = 0.f;
-      for (int d = 0; d < 128; ++d) s = fmaf(sq[c][d], sk[key][(KP == 2 ? c * 128 : 0) + d], s);
-      ss[c][key] = key < n ? s : -INFINITY;
-    }
-    __syncthreads();
-    if (tid < COLS) {
-      float m = sm[tid];
-      for (int j = 0; j < n; ++j) m = ss[tid][j] > m ? ss[tid][j] : m;
-      const float ref = m == -INFINITY ? 0.f : m;
-      const float corr = exp2f(sm[tid] - ref);
-      float l = sl[tid] * corr;
-      for (int j = 0; j < 16; ++j) {
-        const float pj = exp2f(ss[tid][j] - ref);
-        ss[tid][j] = pj;
-        l += pj;
-      }
-      sm[tid] = m;
-      sl[tid] = l;
-      sc[tid] = corr;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int c = 0; c < COLS; ++c) {
-      float x = o[c] * sc[c];
-      for (int j = 0; j < 16; ++j) x = fmaf(ss[c][j], sv[j][tid], x);
-      o[c] = x;
-    }
-    __syncthreads();
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += s_sum[w];
+    total += s_sum[w];
   }
-  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
-  const bool none = len == 0;
+  total *= a.H;
+  const long long want = total / C::kMinCost;
+  const int n = static_cast<int>(want < 1 ? 1 : want > gridDim.x ? gridDim.x : want);
+  const int cta = blockIdx.x;
+  const bool active = cta < n && total > 0;
+  const long long t0 = active ? range_start(total, n, cta) : 0;
+  const long long t1 = active ? range_start(total, n, cta + 1) : 0;
+  if (active && before * a.H <= t0 && t0 < (before + mine) * a.H) {
+    long long at = before;
+    for (int b = lo; b < hi; ++b) {
+      const int cost = cost_of<KP>(clamp_len(a, b));
+      if (t0 < (at + cost) * a.H) {
+        s_b = b;
+        s_pos = t0 - at * a.H;
+        break;
+      }
+      at += cost;
+    }
+  }
+  __syncthreads();
+  // empty places in the batch get zeros
+  for (int b = cta; b < a.B; b += gridDim.x)
+    if (clamp_len(a, b) == 0) {
+      uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) +
+                                          static_cast<size_t>(b) * a.H * (p.cols / 2) * C::kWidth);
+      for (int i = tid; i < a.H * (p.cols / 2) * C::kWidth / 8; i += kThreads) o[i] = make_uint4(0, 0, 0, 0);
+    }
+  Walk w{};
+  int todo = 0;  // tiles of the range, and the costs of the rows that begin in it
+  if (active) {
+    w.b = s_b;
+    w.len = clamp_len(a, w.b);
+    w.tiles = tiles_of<KP>(w.len);
+    const int cost = w.tiles + C::kRowCost;
+    w.h = static_cast<int>(s_pos / cost);
+    const int pos = static_cast<int>(s_pos - static_cast<long long>(w.h) * cost) - C::kRowCost;
+    w.tile = max(pos, 0);
+    todo = static_cast<int>(t1 - t0) + min(pos, 0);
+  }
+  if (tid == 0) p.desc[cta] = Desc{w.b, w.h, w.tile, w.tiles, total, n, 0};
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (todo <= 0) return;
+
+  if (warp == kWarps) {
+    // Producer. Lane i looks up the page of record i of the next tiles of the row (32 records); the
+    // lanes of a tile's records then copy one each, and lane 0 the row's query with its first tile.
+    constexpr int kBatch = 32 / C::kTileRecs;
+    int stage = 0, issued = 0;
+    uint32_t phase = 0;
+    bool alive = true, first = true;
+    while (todo > 0 && alive) {
+      const int batch = min(min(kBatch, w.tiles - w.tile), todo);
+      const int r = w.tile * C::kTileRecs + lane, records = (w.len + 15) >> 4;
+      const bool mine_ok = lane < batch * C::kTileRecs && r < records;
+      const uint8_t* src = nullptr;
+      if (mine_ok) {
+        const int key = r * 16, pi = key / a.page_size, off = key - pi * a.page_size;
+        int page = __ldg(a.block_table + static_cast<size_t>(w.b) * a.max_pages + pi);
+        if (page < 0 || page >= a.num_pages) {
+          flag_device_error(DEV_BAD_INDEX);
+          page = 0;
+        }
+        src = a.pool + ((static_cast<size_t>(page) * a.H + w.h) * (a.page_size >> 4) + (off >> 4)) * C::kRecord;
+      }
+      for (int i = 0; i < batch; ++i) {
+        if (!__all_sync(0xffffffffu, mbar_wait(empty(stage), phase ^ 1, &s_abort))) {
+          alive = false;
+          break;
+        }
+        const uint32_t dst = ring + stage * C::kStage;
+        if (lane == 0) {
+          const int here = min(C::kTileRecs, records - (w.tile + i) * C::kTileRecs);
+          const uint32_t q_bytes = first ? p.cols * 256 : 0;
+          mbar_arrive_expect_tx(full(stage), here * C::kRecord + q_bytes);
+          if (first)
+            bulk_load(dst + C::kTileRecs * C::kRecord,
+                      static_cast<const uint8_t*>(a.q) + (static_cast<size_t>(w.b) * a.H + w.h) * (p.cols * 256), q_bytes,
+                      full(stage));
+        }
+        __syncwarp();
+        if (mine_ok && lane / C::kTileRecs == i)
+          bulk_load(dst + (lane % C::kTileRecs) * C::kRecord, src, C::kRecord, full(stage));
+        first = false;
+        ++issued;
+        if (++stage == C::kStages) stage = 0, phase ^= 1;
+      }
+      todo -= batch;
+      w.tile += batch;
+      if (w.tile == w.tiles) {
+        next_row<KP>(a, w);
+        todo -= C::kRowCost;
+        first = true;
+      }
+    }
+    if (!alive) {
+      // a wait ran out: the copies in flight still land in this block's memory
+      for (int back = 0; back < min(issued, C::kStages); ++back) {
+        if (--stage < 0) stage = C::kStages - 1, phase ^= 1;
+        mbar_wait_limit(full(stage), phase, nullptr, kWaitLimitNs);
+      }
+    }
+    return;
+  }
+
+  // Consumers.
+  const int g = lane >> 2, t = lane & 3;
+  const int cols = p.cols;
+  uint32_t qf[8][2];           // Q^T fragments: channels 32t + 4j .. + 3 of column g
+  float cs0 = 0.f, cs1 = 0.f;  // what a sum of columns 2t and 2t + 1 is to be multiplied with
+  float o[KP * 8][4];
+  float m0, m1, l0, l1;        // references (less kPScale) and sums of columns 2t, 2t + 1
+  int stage = 0, parity = 0;
+  uint32_t phase = 0;
+  bool alive = true;
+
+  auto load_q = [&](uint32_t at) {
+    uint32_t raw[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) raw[i] = 0;
+    if (g < cols) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 v = lds128(at + g * 256 + t * 64 + i * 16);
+        raw[4 * i] = v.x, raw[4 * i + 1] = v.y, raw[4 * i + 2] = v.z, raw[4 * i + 3] = v.w;
+      }
+    }
+    uint32_t top = 0;  // the largest magnitude's bits (ordered as the values are)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) top = max(top, max(raw[i] & 0x7fffu, (raw[i] >> 16) & 0x7fffu));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const int e = max(static_cast<int>(top >> 7) - 127, -100);
+    const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);     // 2^(14 - e)
+    // (never 0 or Inf, which a masked score's Inf or a score of 0 would turn into NaN)
+    const float down = fminf(fmaxf(ldexpf(a.qk_scale, e - 14), FLT_MIN), FLT_MAX);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t x = raw[2 * j + i];
+        qf[j][i] = pack_half2(__uint_as_float(x << 16) * up, __uint_as_float(x & 0xffff0000u) * up);
+      }
+    cs0 = __shfl_sync(0xffffffffu, down, 8 * t);
+    cs1 = __shfl_sync(0xffffffffu, down, 8 * t + 4);
+  };
+  auto wait = [&]() { alive = __all_sync(0xffffffffu, alive && mbar_wait(full(stage), phase, &s_abort)); };
+
+  while (todo > 0) {
+    const int seg = min(w.tiles - w.tile, todo);  // tiles of this row in the range
+    const bool starts = w.tile == 0, whole = starts && seg == w.tiles;
+    wait();
+    load_q(ring + stage * C::kStage + C::kTileRecs * C::kRecord);
+#pragma unroll
+    for (int j = 0; j < KP * 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+    m0 = m1 = -FLT_MAX;
+    l0 = l1 = 0.f;
+    for (int i = 0; i < seg; ++i) {
+      if (i > 0) wait();
+      // record w + 4 k of the tile is warp w's; `left`: keys from its first one on
+      const int left = w.len - ((w.tile + i) * C::kTileRecs + warp) * 16;
+      if (alive && left > 0) {
+        const uint32_t rec = ring + stage * C::kStage + warp * C::kRecord + lane * 16;
+        float y[C::kRecs][4];
+#pragma unroll
+        for (int r = 0; r < C::kRecs; ++r) {
+          const uint32_t at = rec + r * kWarps * C::kRecord;
+          if constexpr (KP == 1) {
+            scores(y[r], at, lane, qf);
+          } else {  // V1: column 0 from the first plane, column 1 from the second
+            float s1[4], s2[4];
+            scores(s1, at, lane, qf);
+            scores(s2, at + kKv4Plane, lane, qf);
+            y[r][0] = s1[0], y[r][1] = s2[1], y[r][2] = s1[2], y[r][3] = s2[3];
+          }
+        }
+        if (left < 16 * (1 + (C::kRecs - 1) * kWarps)) {  // the last tile: keys past the end
+#pragma unroll
+          for (int r = 0; r < C::kRecs; ++r) {
+            const int key = r * kWarps * 16 + (g >> 1) * 4 + (g & 1);
+            if (key >= left) y[r][0] = y[r][1] = -INFINITY;
+            if (key + 2 >= left) y[r][2] = y[r][3] = -INFINITY;
+          }
+        }
+        // exponents against the reference; it moves where one passes kMoveRef
+        float e[C::kRecs][4], top = -INFINITY;
+#pragma unroll
+        for (int r = 0; r < C::kRecs; ++r) {
+          e[r][0] = fmaf(y[r][0], cs0, -m0), e[r][1] = fmaf(y[r][1], cs1, -m1);
+          e[r][2] = fmaf(y[r][2], cs0, -m0), e[r][3] = fmaf(y[r][3], cs1, -m1);
+          top = fmaxf(top, fmaxf(fmaxf(e[r][0], e[r][1]), fmaxf(e[r][2], e[r][3])));
+        }
+        if (__any_sync(0xffffffffu, top > kMoveRef)) {
+          float n0 = -FLT_MAX, n1 = -FLT_MAX;
+#pragma unroll
+          for (int r = 0; r < C::kRecs; ++r) {
+            n0 = fmaxf(n0, fmaxf(y[r][0] * cs0, y[r][2] * cs0));
+            n1 = fmaxf(n1, fmaxf(y[r][1] * cs1, y[r][3] * cs1));
+          }
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) {
+            n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, d));
+            n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, d));
+          }
+          n0 = fmaxf(m0, n0 - kPScale), n1 = fmaxf(m1, n1 - kPScale);
+          const float f0 = ex2_approx(m0 - n0), f1 = ex2_approx(m1 - n1);
+          m0 = n0, m1 = n1;
+          l0 *= f0, l1 *= f1;
+#pragma unroll
+          for (int j = 0; j < KP * 8; ++j) o[j][0] *= f0, o[j][1] *= f1, o[j][2] *= f0, o[j][3] *= f1;
+#pragma unroll
+          for (int r = 0; r < C::kRecs; ++r) {
+            e[r][0] = fmaf(y[r][0], cs0, -m0), e[r][1] = fmaf(y[r][1], cs1, -m1);
+            e[r][2] = fmaf(y[r][2], cs0, -m0), e[r][3] = fmaf(y[r][3], cs1, -m1);
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < C::kRecs; ++r) {
+          const float p00 = ex2_approx(e[r][0]), p01 = ex2_approx(e[r][1]);
+          const float p10 = ex2_approx(e[r][2]), p11 = ex2_approx(e[r][3]);
+          l0 += p00 + p10;
+          l1 += p01 + p11;
+          // lane (g, t) now wants column g at keys 4t .. 4t + 3
+          const uint32_t b0 = transpose8x8(pack_half2(p00, p01)), b1 = transpose8x8(pack_half2(p10, p11));
+          const int live = left - r * kWarps * 16 - 4 * t;
+#pragma unroll
+          for (int pl = 0; pl < KP; ++pl)
+            outputs(o + pl * 8, rec + r * kWarps * C::kRecord + (KP + pl) * kKv4Plane, lane, live, b0, b1);
+        }
+      }
+      __syncwarp();
+      if (alive && lane == 0) mbar_arrive(empty(stage));
+      if (++stage == C::kStages) stage = 0, phase ^= 1;
+    }
+
+    // Join the warps' pieces.
+#pragma unroll
+    for (int d = 4; d < 32; d <<= 1) {
+      l0 += __shfl_xor_sync(0xffffffffu, l0, d);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, d);
+    }
+    if (g == 0) {
+      s_m[parity][warp][2 * t] = m0, s_m[parity][warp][2 * t + 1] = m1;
+      s_l[parity][warp][2 * t] = l0, s_l[parity][warp][2 * t + 1] = l1;
+    }
+    named_barrier_sync(1, kWarps * 32);
+    float top0 = m0, top1 = m1;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      top0 = fmaxf(top0, s_m[parity][i][2 * t]);
+      top1 = fmaxf(top1, s_m[parity][i][2 * t + 1]);
+    }
+    const float f0 = ex2_approx(m0 - top0), f1 = ex2_approx(m1 - top1);
+    if (2 * t < C::kMaxCols) {
+      float* mine0 = s_o + (warp * C::kMaxCols + 2 * t) * C::kPitch;
+      float* mine1 = mine0 + C::kPitch;
+#pragma unroll
+      for (int j = 0; j < KP * 8; ++j) {
+        const int ch = (j >> 3) * 128 + 16 * g + 2 * (j & 7);
+        *reinterpret_cast<float2*>(mine0 + ch) = make_float2(o[j][0] * f0, o[j][2] * f0);
+        *reinterpret_cast<float2*>(mine1 + ch) = make_float2(o[j][1] * f1, o[j][3] * f1);
+      }
+    }
+    named_barrier_sync(1, kWarps * 32);
+    // thread `tid` takes channel tid (V1: and tid + 128) of every column
+    float sum[C::kMaxCols][KP], l[C::kMaxCols], top[C::kMaxCols];
+#pragma unroll
+    for (int c = 0; c < C::kMaxCols; ++c) {
+      float mx = s_m[parity][0][c];
+#pragma unroll
+      for (int i = 1; i < kWarps; ++i) mx = fmaxf(mx, s_m[parity][i][c]);
+      top[c] = mx;
+      l[c] = 0.f;
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) l[c] += s_l[parity][i][c] * ex2_approx(s_m[parity][i][c] - mx);
+#pragma unroll
+      for (int k = 0; k < KP; ++k) {
+        sum[c][k] = 0.f;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) sum[c][k] += s_o[(i * C::kMaxCols + c) * C::kPitch + k * 128 + tid];
+      }
+    }
+    parity ^= 1;
+    const size_t row = static_cast<size_t>(w.b) * a.H + w.h;
+    if (!whole) {
+      float* rec = p.rec + static_cast<size_t>(2 * cta + (starts ? 1 : 0)) * (2 * cols + cols * C::kWidth);
+#pragma unroll
+      for (int c = 0; c < C::kMaxCols; ++c) {
+        if (c >= cols) break;
+        if (tid == 0) rec[c] = top[c], rec[cols + c] = l[c];
+#pragma unroll
+        for (int k = 0; k < KP; ++k) rec[2 * cols + c * C::kWidth + k * 128 + tid] = sum[c][k];
+      }
+    } else if constexpr (KP == 1) {
+#pragma unroll
+      for (int c = 0; c < C::kMaxCols; c += 2) {
+        if (c >= cols) break;
+        const size_t pair = row * (cols / 2) + c / 2;
+        const float sig = 1.f / (1.f + __expf(-__ldg(a.lam_logit + pair)));
+        const float y = (sum[c][0] / l[c] - sig * (sum[c + 1][0] / l[c + 1])) * a.v_mul;
+        static_cast<__nv_bfloat16*>(a.out)[pair * 128 + tid] = __float2bfloat16_rn(y);
+      }
+    } else {
+      const float lam = __ldg(a.lambda + w.h);
+      float y[KP];
+      float ss = 0.f;
+#pragma unroll
+      for (int k = 0; k < KP; ++k) {
+        y[k] = (sum[0][k] / l[0] - lam * (sum[1][k] / l[1])) * a.v_mul;
+        ss = fmaf(y[k], y[k], ss);
+      }
+      float f = 1.f;
+      if (a.flags & 2) {
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
+        if (lane == 0) s_red[warp] = ss;
+        named_barrier_sync(1, kWarps * 32);
+        ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) ss += s_red[i];
+        f = 1.f / sqrtf(ss / static_cast<float>(C::kWidth) + a.eps);
+      }
+      if (a.flags & 4) f *= 1.f - a.lambda_init;
+#pragma unroll
+      for (int k = 0; k < KP; ++k) {
+        const float wgt = (a.flags & 2) && a.norm_w ? __ldg(a.norm_w + k * 128 + tid) : 1.f;
+        static_cast<__nv_bfloat16*>(a.out)[row * C::kWidth + k * 128 + tid] = __float2bfloat16_rn(y[k] * f * wgt);
+      }
+    }
+    todo -= seg;
+    w.tile += seg;
+    if (w.tile == w.tiles) {
+      next_row<KP>(a, w);
+      todo -= C::kRowCost;
+    }
+  }
+}
+
+// Merge. Block i: the row that range i begins inside, unless an earlier range does as well. Its pieces
+// are that of range i - 1 (which began the row) and of ranges i, i + 1, .. up to the row's end, always
+// in this order; groups of threads take every n-th piece, and join.
+template <int KP>
+__global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const Params p) {
+  constexpr int W = KP * 128;
+  __shared__ float s_m[kMergeThreads / 64 * 2], s_l[kMergeThreads / 64 * 2];
+  __shared__ float4 s_o[kMergeThreads];
+  __shared__ float s_red[W / 32];
+  const Kv4DecodeArgs& a = p.a;
+  const int i = blockIdx.x + 1, tid = threadIdx.x;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Desc d = p.desc[i];
+  if (i >= d.n || d.total == 0 || d.tile == 0) return;
+  const long long first = range_start(d.total, d.n, i) - d.tile;  // where the row's tiles begin
+  if (range_start(d.total, d.n, i - 1) > first) return;
+  const int last = static_cast<int>(((first + d.tiles) * d.n - 1) / d.total);  // the last range that begins in the row
+  const int pieces = min(last, d.n - 1) - (i - 1) + 1;
+  const int cols = p.cols;
+  const int lanes = cols * (W / 4), groups = kMergeThreads / lanes;  // a float4 of all columns' outputs each
+  const size_t rec = 2 * cols + cols * W;
+  const int grp = tid / lanes, ln = tid % lanes, c = ln / (W / 4);
+  float m = -FLT_MAX, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int k = grp; k < pieces; k += groups) {
+    const float* r = p.rec + (k == 0 ? static_cast<size_t>(2 * (i - 1) + 1) : static_cast<size_t>(2 * (i - 1 + k))) * rec;
+    const float mk = r[c], lk = r[cols + c];
+    const float4 ok = *reinterpret_cast<const float4*>(r + 2 * cols + ln * 4);
+    const float top = fmaxf(m, mk), f = ex2_approx(m - top), fk = ex2_approx(mk - top);
+    m = top;
+    l = l * f + lk * fk;
+    o.x = o.x * f + ok.x * fk;
+    o.y = o.y * f + ok.y * fk;
+    o.z = o.z * f + ok.z * fk;
+    o.w = o.w * f + ok.w * fk;
+  }
+  s_o[tid] = o;
+  if (ln % (W / 4) == 0) s_m[grp * cols + c] = m, s_l[grp * cols + c] = l;
+  __syncthreads();
+  const size_t row = static_cast<size_t>(d.b) * a.H + d.h;
+  // an output channel: of a pair of columns, V1's only one
+  if (tid >= cols / 2 * W) return;
+  const int pair = tid / W, ch = tid % W;
+  float q[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int col = 2 * pair + e;
+    float top = s_m[col];
+    for (int k = 1; k < groups; ++k) top = fmaxf(top, s_m[k * cols + col]);
+    float sum = 0.f, ls = 0.f;
+    for (int k = 0; k < groups; ++k) {
+      const float f = ex2_approx(s_m[k * cols + col] - top);
+      ls = fmaf(s_l[k * cols + col], f, ls);
+      sum = fmaf(reinterpret_cast<const float*>(s_o + k * lanes)[col * W + ch], f, sum);
+    }
+    q[e] = sum / ls;
+  }
+  const float lam = KP == 2 ? __ldg(a.lambda + d.h)
+                            : 1.f / (1.f + __expf(-__ldg(a.lam_logit + row * (cols / 2) + pair)));
+  float y = (q[0] - lam * q[1]) * a.v_mul;
   if constexpr (KP == 2) {
-    float y = none ? 0.f : (o[0] / sl[0] - a.lambda[h] * (o[1] / sl[1])) * a.v_mul;
     if (a.flags & 2) {
-      float t = y * y;
-      for (int d = 16; d > 0; d >>= 1) t += __shfl_xor_sync(0xffffffffu, t, d);
-      if ((tid & 31) == 0) red[tid >> 5] = t;
-      __syncthreads();
-      float sum = 0.f;
-      for (int i = 0; i < W / 32; ++i) sum += red[i];
-      y *= (1.f / sqrtf(sum / static_cast<float>(W) + a.eps)) * (a.norm_w ? a.norm_w[tid] : 1.f);
+      float ss = y * y;
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, s);
+      if ((tid & 31) == 0) s_red[tid >> 5] = ss;
+      named_barrier_sync(1, W);
+      ss = 0.f;
+#pragma unroll
+      for (int k = 0; k < W / 32; ++k) ss += s_red[k];
+      y *= 1.f / sqrtf(ss / static_cast<float>(W) + a.eps) * (a.norm_w ? __ldg(a.norm_w + ch) : 1.f);
     }
     if (a.flags & 4) y *= 1.f - a.lambda_init;
-    out[(static_cast<size_t>(b) * a.H + h) * W + tid] = __float2bfloat16_rn(y);
-  } else {
-#pragma unroll
-    for (int c = 0; c < COLS; c += 2) {
-      const size_t pair = (static_cast<size_t>(b) * a.H + h) * (COLS / 2) + c / 2;
-      const float sig = 1.f / (1.f + expf(-a.lam_logit[pair]));
-      const float y = none ? 0.f : (o[c] / sl[c] - sig * (o[c + 1] / sl[c + 1])) * a.v_mul;
-      out[pair * W + tid] = __float2bfloat16_rn(y);
-    }
   }
+  static_cast<__nv_bfloat16*>(a.out)[(row * (cols / 2) + pair) * W + ch] = __float2bfloat16_rn(y);
+}
+
+template <int KP>
+cudaError_t launch(const Kv4DecodeArgs& a, cudaStream_t st) {
+  using C = Cfg<KP>;
+  Params p{};
+  p.a = a;
+  p.cols = KP == 2 ? 2 : a.group;
+  p.desc = static_cast<Desc*>(a.ws);
+  p.rec = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + C::kGrid * sizeof(Desc));
+  cudaError_t e = cudaFuncSetAttribute(kv4_split_kernel<KP>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  kv4_split_kernel<KP><<<C::kGrid, kThreads, C::kSmem, st>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // the merge's blocks are set up while the split's last ones end (they wait for its results)
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(C::kGrid - 1);
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.stream = st;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv4_merge_kernel<KP>, p);
 }
 
 }  // namespace
 
 size_t kv4_decode_workspace_bytes(int B, int H, int cols, int width) {
-  (void)B, (void)H, (void)cols, (void)width;
-  return 256;
+  (void)B, (void)H;
+  const size_t grid = width == 128 ? Cfg<1>::kGrid : Cfg<2>::kGrid;
+  return grid * sizeof(Desc) + 2 * grid * (2 * cols + static_cast<size_t>(cols) * width) * sizeof(float);
 }
 
 cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a, cudaStream_t st) {
-  const dim3 grid(a.H, a.B);
-  if (a.group == 0) kv4_decode_kernel<2, 1><<<grid, 256, 0, st>>>(a);
-  else if (a.group == 2) kv4_decode_kernel<1, 2><<<grid, 128, 0, st>>>(a);
-  else if (a.group == 4) kv4_decode_kernel<1, 4><<<grid, 128, 0, st>>>(a);
-  else kv4_decode_kernel<1, 8><<<grid, 128, 0, st>>>(a);
-  return cudaGetLastError();
+  return a.group == 0 ? launch<2>(a, st) : launch<1>(a, st);
 }
 
 cudaError_t status_decode_kv4(int* v) { return read_clear_status(v); }

@@ -147,11 +147,17 @@ def _weights(q, k):
     return ref.softmax_rows(s[None])[0]
 
 
+def _off(a, v, slack, floor):
+    """How far a @ v may be off where each weight errs by slack of itself and floor of the largest."""
+    return slack * (a @ np.abs(v)) + floor * a.max() * np.abs(v).sum(axis=0)
+
+
 def decode(q, pool, block_table, seqlens, lam, lam_init, norm_weight=None, eps=1e-5, norm=True,
-           apply_scale=True, k_exp=0, v_exp=0, slack=0.0):
+           apply_scale=True, k_exp=0, v_exp=0, slack=0.0, floor=0.0):
     """V1 decode over a pool: q [B, H, 256]. Returns (out, bound) [B, H, 256]: `bound` is how far an
-    output may be off where every product p * v of both maps carries a relative error of `slack`
-    (propagated through the norm), before the output's own rounding."""
+    output may be off where every product p * v of both maps carries a relative error of `slack` and
+    every p an absolute one of `floor` times the map's largest (propagated through the norm), before
+    the output's own rounding."""
     q = ref._f64(q)
     B, H, _ = q.shape
     out, bound = np.zeros((B, H, 256)), np.zeros((B, H, 256))
@@ -162,7 +168,7 @@ def decode(q, pool, block_table, seqlens, lam, lam_init, norm_weight=None, eps=1
         for h in range(H):
             a1, a2 = _weights(q[b, h, :128], k[:, h, :128]), _weights(q[b, h, 128:], k[:, h, 128:])
             o = a1 @ v[:, h] - lam[h] * (a2 @ v[:, h])
-            e = slack * (a1 @ np.abs(v[:, h]) + abs(lam[h]) * (a2 @ np.abs(v[:, h])))
+            e = _off(a1, v[:, h], slack, floor) + abs(lam[h]) * _off(a2, v[:, h], slack, floor)
             y = ref.head_epilogue(o[None], norm_weight, eps, lam_init, norm, apply_scale)[0]
             g = np.ones(256) if norm_weight is None or not norm else np.abs(ref._f64(norm_weight))
             g = g * (abs(1 - lam_init) if apply_scale else 1.0)
@@ -173,7 +179,7 @@ def decode(q, pool, block_table, seqlens, lam, lam_init, norm_weight=None, eps=1
     return out, bound
 
 
-def v2_decode(q, pool, block_table, seqlens, lam_logit, k_exp=0, v_exp=0, slack=0.0):
+def v2_decode(q, pool, block_table, seqlens, lam_logit, k_exp=0, v_exp=0, slack=0.0, floor=0.0):
     """V2 decode over a pool: q [B, Hq, 128]. Returns (out, bound) [B, Hq/2, 128] as above."""
     q = ref._f64(q)
     B, Hq, _ = q.shape
@@ -188,5 +194,6 @@ def v2_decode(q, pool, block_table, seqlens, lam_logit, k_exp=0, v_exp=0, slack=
             h = 2 * p // G
             a = [_weights(q[b, 2 * p + r], k[:, h]) for r in (0, 1)]
             out[b, p] = a[0] @ v[:, h] - sig[b, p] * (a[1] @ v[:, h])
-            bound[b, p] = slack * (a[0] @ np.abs(v[:, h]) + sig[b, p] * (a[1] @ np.abs(v[:, h])))
+            off = [_off(x, v[:, h], slack, floor) for x in a]
+            bound[b, p] = off[0] + sig[b, p] * off[1]
     return out, bound

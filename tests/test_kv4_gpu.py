@@ -12,10 +12,11 @@ sums are fp32. Each p_j carries
     sqrt(128) instead of 128 times as much as that of one for errors of either sign: 2^-11.4.
     ex2.approx adds 2^-22.
 Both errors move numerator and denominator alike, so twice their sum covers the quotient:
-SLACK = 2 (2^-10 + 2^-11) < 2^-8.4, on sum_j p_j |v_j| (reference `bound`). fp16 leaves a probability
-an absolute error of 2^-25 times its scale; the kernels scale p so that this stays below 2^-34 of
-the largest: 2^-14 of it even over 2^20 keys. The output's own rounding to bf16 is 2^-8 relative
-(half a step of eps = 2^-7 is 2^-8)."""
+SLACK = 2 (2^-10 + 2^-11) < 2^-8.4, on sum_j p_j |v_j| (reference `bound`). Below 2^-14 fp16 has an
+absolute error instead: half its smallest step 2^-24. The kernels hold p at 2^10 against a
+reference m that is never above the largest score, so the largest P is at least 2^10, and the
+error at most 2^-25 / 2^10 = FLOOR = 2^-35 of it, for each key. The output's own rounding to bf16 is
+2^-8 relative (half a step of eps = 2^-7 is 2^-8)."""
 import ctypes
 
 import numpy as np
@@ -31,7 +32,7 @@ from tests.test_kv4_cpu import random_step
 pytestmark = pytest.mark.gpu
 
 DEV = "cuda"
-SLACK = 2.0 ** -8.4
+SLACK, FLOOR = 2.0 ** -8.4, 2.0 ** -35
 BF16 = torch.finfo(torch.bfloat16).eps / 2
 
 
@@ -370,7 +371,7 @@ def test_v1_decode(lens, H, page_size):
     table, pool, q, lam, w = v1_case(rng, lens, H, page_size)
     got = da.diffattn_decode_kv4(q.to(DEV), torch.tensor(pool).to(DEV), dev32(table), dev32(lens), lam.to(DEV), 0.4,
                                  norm_weight=w.to(DEV))
-    within(got, *kv4.decode(q, pool, table, lens, lam.numpy(), 0.4, w, slack=SLACK))
+    within(got, *kv4.decode(q, pool, table, lens, lam.numpy(), 0.4, w, slack=SLACK, floor=FLOOR))
     for b, n in enumerate(lens):
         assert n or not got[b].any()
     da.diffattn_device_status()
@@ -382,7 +383,7 @@ def test_v1_decode_epilogues(norm, scale, weight):
     table, pool, q, lam, w = v1_case(rng, [77, 300], 2, 32)
     got = da.diffattn_decode_kv4(q.to(DEV), torch.tensor(pool).to(DEV), dev32(table), dev32([77, 300]), lam.to(DEV), 0.4,
                                  norm_weight=w.to(DEV) if weight else None, eps=1e-3, norm=norm, scale=scale)
-    within(got, *kv4.decode(q, pool, table, [77, 300], lam.numpy(), 0.4, w if weight else None, 1e-3, norm, scale, slack=SLACK))
+    within(got, *kv4.decode(q, pool, table, [77, 300], lam.numpy(), 0.4, w if weight else None, 1e-3, norm, scale, slack=SLACK, floor=FLOOR))
 
 
 @pytest.mark.parametrize("lens", LENS)
@@ -391,7 +392,7 @@ def test_v2_decode(lens, Hkv, G, page_size):
     rng = np.random.default_rng(sum(lens) * 5 + G)
     table, pool, q, lam = v2_case(rng, lens, Hkv, G, page_size)
     got = da.diffattn_v2_decode_kv4(q.to(DEV), torch.tensor(pool).to(DEV), dev32(table), dev32(lens), lam.to(DEV))
-    within(got, *kv4.v2_decode(q, pool, table, lens, lam.numpy(), slack=SLACK))
+    within(got, *kv4.v2_decode(q, pool, table, lens, lam.numpy(), slack=SLACK, floor=FLOOR))
     for b, n in enumerate(lens):
         assert n or not got[b].any()
     da.diffattn_device_status()
@@ -405,8 +406,8 @@ def both(rng, lens, page_size, std=1.0, heads=2, spare=2, width=None):
     dev = lambda x: x.to(DEV) if isinstance(x, torch.Tensor) else torch.tensor(x).to(DEV)  # noqa: E731
     v1 = lambda q, pool, table, lens, **k: da.diffattn_decode_kv4(dev(q), dev(pool), dev32(table), dev32(lens), D1, 0.4, norm_weight=W1, **k)  # noqa: E731
     v2 = lambda q, pool, table, lens, **k: da.diffattn_v2_decode_kv4(dev(q), dev(pool), dev32(table), dev32(lens), D2, **k)  # noqa: E731
-    r1 = lambda q, pool, table, lens, **k: kv4.decode(q, pool, table, lens, l1.numpy(), 0.4, w1, slack=SLACK, **k)  # noqa: E731
-    r2 = lambda q, pool, table, lens, **k: kv4.v2_decode(q, pool, table, lens, l2.numpy(), slack=SLACK, **k)  # noqa: E731
+    r1 = lambda q, pool, table, lens, **k: kv4.decode(q, pool, table, lens, l1.numpy(), 0.4, w1, slack=SLACK, floor=FLOOR, **k)  # noqa: E731
+    r2 = lambda q, pool, table, lens, **k: kv4.v2_decode(q, pool, table, lens, l2.numpy(), slack=SLACK, floor=FLOOR, **k)  # noqa: E731
     return [("v1", v1, r1, q1, p1, t1), ("v2", v2, r2, q2, p2, t2)]
 
 
@@ -602,8 +603,8 @@ def test_decode_captured_graphs_follow_their_inputs(name):
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         decode_pair(name, Q, P, T, S, L, out, ws, W)
-    want = (lambda q, t, s: kv4.decode(q, pool, t, s, lam.numpy(), 0.4, w, slack=SLACK) if name == "v1"
-            else kv4.v2_decode(q, pool, t, s, lam.numpy(), slack=SLACK))
+    want = (lambda q, t, s: kv4.decode(q, pool, t, s, lam.numpy(), 0.4, w, slack=SLACK, floor=FLOOR) if name == "v1"
+            else kv4.v2_decode(q, pool, t, s, lam.numpy(), slack=SLACK, floor=FLOOR))
     for step in range(3):
         q2 = torch.tensor(rng.normal(size=tuple(q.shape)), dtype=torch.float32).to(torch.bfloat16)
         s2 = [[200, 0, 1], [17, 64, 1], [1, 1, 0]][step]
@@ -663,7 +664,7 @@ def test_decode_pool_offsets_past_32_bits():
     lam = torch.full((H,), 0.3)
     got = da.diffattn_decode_kv4(q.to(DEV), pool, dev32([[pages - 1]]), dev32([140]), lam.to(DEV), 0.2)
     small = pool[-1:].cpu().numpy()
-    within(got, *kv4.decode(q, small, [[0]], [140], lam.numpy(), 0.2, slack=SLACK))
+    within(got, *kv4.decode(q, small, [[0]], [140], lam.numpy(), 0.2, slack=SLACK, floor=FLOOR))
 
 
 def test_v2_decode_agrees_with_the_bf16_decode_on_the_same_values():
