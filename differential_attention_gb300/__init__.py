@@ -15,6 +15,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import threading
 
 import torch
 
@@ -1520,13 +1521,15 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 
 def _operand(name, t, dtype, index, shape=None) -> int:
     """The address of a contiguous tensor of `dtype` (and `shape`) on CUDA device `index`."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_contiguous() or not t.is_cuda:
-        _dev(name, t, dtype)  # raises with the reason
+    try:
+        if t.dtype == dtype and t.get_device() == index and t.is_contiguous() and (shape is None or t.shape == shape):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _dev(name, t, dtype)  # raises with the reason, but for these two
     if t.get_device() != index:
         raise ValueError(f"{name} is on {t.device}, and other operands on cuda:{index}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
 def _index(name, t) -> int:
@@ -1538,10 +1541,7 @@ def _index(name, t) -> int:
 
 def _call(index, fn, *args, stream=None):
     """fn(*args, stream) with device `index` current; `stream` None is that device's current stream."""
-    if stream is None:
-        raw = _raw_stream(index)
-    else:
-        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    raw = _raw_stream(index) if stream is None else _stream(stream).value or 0
     if index == torch._C._cuda_getDevice():
         rc = fn(*args, raw)
     else:
@@ -1549,6 +1549,32 @@ def _call(index, fn, *args, stream=None):
             rc = fn(*args, raw)
     if rc != DIFFATTN_OK:
         _check(rc)
+
+
+_scratch = threading.local()
+
+
+def _workspace(index, n, stream):
+    """Scratch of n bytes for one call. Calls that one thread makes on one stream run one after the
+    other, so they share a buffer, which the thread keeps. A call that is being captured gets its
+    own (the graph may replay on any stream), and so does one on a stream that is not the current
+    one, to which the allocator is told to leave the buffer until the call is done."""
+    if stream is not None:
+        ws = torch.empty(n, dtype=torch.uint8, device=torch.device("cuda", index))
+        ws.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
+                         torch.cuda.ExternalStream(_stream(stream).value or 0, device=index))
+        return ws
+    if index != torch._C._cuda_getDevice() or torch._C._cuda_isCurrentStreamCapturing():
+        return torch.empty(n, dtype=torch.uint8, device=torch.device("cuda", index))
+    kept = _scratch.__dict__.setdefault("kept", {})
+    key = (index, _raw_stream(index))
+    ws = kept.get(key)
+    if ws is None or ws.shape[0] < n:
+        ws = kept[key] = torch.empty(n, dtype=torch.uint8, device=torch.device("cuda", index))
+    return ws
+
+
+_PLAN = ("seqlens", "ring_state", "cu_seqlens_q", "cu_seqlens_k", "slot_map", "positions")
 
 
 def diffattn_paged_plan(seqlens, new_tokens, block_table, free_ring, ring_state, page_size: int,
@@ -1568,12 +1594,12 @@ def diffattn_paged_plan(seqlens, new_tokens, block_table, free_ring, ring_state,
     if out is None:
         if total_max < 0:
             raise ValueError("total_max must not be negative")
-        parts = torch.empty(sum(sizes), dtype=i32, device=seqlens.device).split(sizes)
-        out = dict(zip(("seqlens", "ring_state", "cu_seqlens_q", "cu_seqlens_k", "slot_map", "positions"), parts))
-        p = [t.data_ptr() for t in parts]
+        buf = torch.empty(3 * B + 4 + 2 * total_max, dtype=i32, device=seqlens.device)
+        out = dict(zip(_PLAN, buf.split_with_sizes(sizes)))
+        p0 = buf.data_ptr()
+        p = (p0, p0 + 4 * B, p0 + 4 * B + 8, p0 + 8 * B + 12, p0 + 12 * B + 16, p0 + 12 * B + 16 + 4 * total_max)
     else:
-        p = [_operand(f"out[{name!r}]", out[name], i32, dev, (n,)) for name, n in zip(
-            ("seqlens", "ring_state", "cu_seqlens_q", "cu_seqlens_k", "slot_map", "positions"), sizes)]
+        p = [_operand(f"out[{name!r}]", out[name], i32, dev, (n,)) for name, n in zip(_PLAN, sizes)]
     _call(dev, lib().diffattn_paged_plan, _operand("seqlens", seqlens, i32, dev, (B,)),
           _operand("new_tokens", new_tokens, i32, dev, (B,)), p[0],
           _operand("block_table", block_table, i32, dev, (B, max_pages)),
@@ -1681,8 +1707,7 @@ def diffattn_decode_kv4(q, pool, block_table, seqlens, lam, lambda_init: float =
     at, num_pages, page_size = _kv4_pool(pool, dev, H, two_d, two_d)
     table, max_pages = _kv4_table(block_table, dev, B)
     if workspace is None:
-        workspace = torch.empty(diffattn_decode_kv4_workspace_size(B, H, two_d // 2, two_d),
-                                dtype=torch.uint8, device=q.device)
+        workspace = _workspace(dev, diffattn_decode_kv4_workspace_size(B, H, two_d // 2, two_d), stream)
     if out is None:
         out = torch.empty_like(q)
     flags = (DIFFATTN_NORM if norm else 0) | (DIFFATTN_SCALE if scale else 0)
@@ -1716,8 +1741,7 @@ def diffattn_v2_decode_kv4(q, pool, block_table, seqlens, lam_logit, k_exp: int 
     at, num_pages, page_size = _kv4_pool(pool, dev, Hkv, d, d)
     table, max_pages = _kv4_table(block_table, dev, B)
     if workspace is None:
-        workspace = torch.empty(diffattn_v2_decode_kv4_workspace_size(B, Hq, Hkv, d),
-                                dtype=torch.uint8, device=q.device)
+        workspace = _workspace(dev, diffattn_v2_decode_kv4_workspace_size(B, Hq, Hkv, d), stream)
     if out is None:
         out = torch.empty((B, Hq // 2, d), dtype=torch.bfloat16, device=q.device)
     _call(dev, lib().diffattn_v2_decode_kv4, _operand("q", q, torch.bfloat16, dev), at, table,

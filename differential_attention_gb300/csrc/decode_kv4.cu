@@ -39,8 +39,6 @@
 namespace da {
 namespace {
 
-constexpr int kWarps = 4;                        // consumer warps
-constexpr int kThreads = (kWarps + 1) * 32;      // and a producer
 constexpr int kSms = 152;
 constexpr int kMergeThreads = 1024;
 constexpr float kPScale = 10.f;                  // log2 of P's scale
@@ -48,6 +46,8 @@ constexpr float kMoveRef = 14.f;                 // log2 P at which the referenc
 
 template <int KP>
 struct Cfg {
+  static constexpr int kWarps = 4;               // consumer warps
+  static constexpr int kThreads = (kWarps + 1) * 32;  // and a producer
   static constexpr int kRecs = KP == 1 ? 2 : 1;  // records of a tile for each consumer warp
   static constexpr int kTileRecs = kWarps * kRecs;
   static constexpr int kTileKeys = 16 * kTileRecs;
@@ -60,9 +60,9 @@ struct Cfg {
   static constexpr int kMaxCols = KP == 1 ? 8 : 2;
   static constexpr int kQBytes = kMaxCols * 256;
   static constexpr int kStage = kTileRecs * kRecord + kQBytes;
-  static constexpr int kStages = KP == 1 ? 2 : 3;
+  static constexpr int kStages = 3;
   static constexpr int kPitch = kWidth + 4;      // floats of one column's row in the exchange
-  static constexpr int kSmem = kStages * kStage + kWarps * kMaxCols * kPitch * 4;
+  static constexpr int kSmem = kStages * kStage + kWarps / 2 * kMaxCols * kPitch * 4;
 };
 
 // where a block's range begins, for the merge
@@ -158,7 +158,8 @@ __device__ __forceinline__ void mma_first(float (&c)[4], uint32_t a0, uint32_t a
 __device__ __forceinline__ void scores(float (&c)[4], uint32_t at, int lane, const uint32_t (&qf)[8][2]) {
   const uint4 lo4 = lds128(at), hi4 = lds128(at + 512);
   const uint32_t sc = lds32(at - lane * 12 + kKv4PlaneCodes);
-  const uint32_t slo = e4m3x2_to_half2(sc & 0xffffu), shi = e4m3x2_to_half2(sc >> 16);
+  uint32_t slo, shi;
+  e4m3x4_to_half2(sc, slo, shi);
   const uint32_t wl[4] = {lo4.x, lo4.y, lo4.z, lo4.w}, wh[4] = {hi4.x, hi4.y, hi4.z, hi4.w};
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
@@ -177,12 +178,12 @@ __device__ __forceinline__ void scores(float (&c)[4], uint32_t at, int lane, con
 }
 
 // O^T += V^T P^T of one record and plane: rows g and g + 8 of product j are channels 16g + 2j and + 1.
-// `live`: how many of this lane's tokens 4t .. 4t + 3 count (4 or more: all).
-__device__ __forceinline__ void outputs(float (*o)[4], uint32_t at, int lane, int live, uint32_t b0, uint32_t b1) {
+// `keep`: a byte of ones for each of this lane's tokens 4t .. 4t + 3 that counts; the others' scale is 0.
+__device__ __forceinline__ void outputs(float (*o)[4], uint32_t at, int lane, uint32_t keep, uint32_t b0, uint32_t b1) {
   const uint4 va = lds128(at), vb = lds128(at + 512);
-  uint32_t sc = lds32(at - lane * 12 + kKv4PlaneCodes);
-  if (live < 4) sc = live <= 0 ? 0u : sc & (0xffffffffu >> (32 - 8 * live));  // rows past the end: scale 0
-  const uint32_t s01 = e4m3x2_to_half2(sc & 0xffffu), s23 = e4m3x2_to_half2(sc >> 16);
+  const uint32_t sc = lds32(at - lane * 12 + kKv4PlaneCodes);
+  uint32_t s01, s23;
+  e4m3x4_to_half2(sc & keep, s01, s23);
   // pairs of tokens side by side: the low nibbles of two rows' bytes, then the high ones
   const uint32_t r0[2] = {va.x, va.y}, r1[2] = {va.z, va.w}, r2[2] = {vb.x, vb.y}, r3[2] = {vb.z, vb.w};
   constexpr uint32_t kLow = 0x0f0f0f0fu;
@@ -201,8 +202,9 @@ __device__ __forceinline__ void outputs(float (*o)[4], uint32_t at, int lane, in
 }
 
 template <int KP>
-__global__ void __launch_bounds__(kThreads, Cfg<KP>::kCtas) kv4_split_kernel(const Params p) {
+__global__ void __launch_bounds__(Cfg<KP>::kThreads, Cfg<KP>::kCtas) kv4_split_kernel(const Params p) {
   using C = Cfg<KP>;
+  constexpr int kWarps = C::kWarps, kThreads = C::kThreads;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bars[2 * C::kStages];
   __shared__ long long s_sum[kThreads / 32];
@@ -421,9 +423,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<KP>::kCtas) kv4_split_kernel(con
             y[r][0] = s1[0], y[r][1] = s2[1], y[r][2] = s1[2], y[r][3] = s2[3];
           }
         }
+        uint32_t keep[C::kRecs];
+#pragma unroll
+        for (int r = 0; r < C::kRecs; ++r) keep[r] = 0xffffffffu;
         if (left < 16 * (1 + (C::kRecs - 1) * kWarps)) {  // the last tile: keys past the end
 #pragma unroll
           for (int r = 0; r < C::kRecs; ++r) {
+            const int live = left - r * kWarps * 16 - 4 * t;
+            keep[r] = live >= 4 ? 0xffffffffu : live <= 0 ? 0u : 0xffffffffu >> (32 - 8 * live);
             const int key = r * kWarps * 16 + (g >> 1) * 4 + (g & 1);
             if (key >= left) y[r][0] = y[r][1] = -INFINITY;
             if (key + 2 >= left) y[r][2] = y[r][3] = -INFINITY;
@@ -469,10 +476,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<KP>::kCtas) kv4_split_kernel(con
           l1 += p01 + p11;
           // lane (g, t) now wants column g at keys 4t .. 4t + 3
           const uint32_t b0 = transpose8x8(pack_half2(p00, p01)), b1 = transpose8x8(pack_half2(p10, p11));
-          const int live = left - r * kWarps * 16 - 4 * t;
 #pragma unroll
           for (int pl = 0; pl < KP; ++pl)
-            outputs(o + pl * 8, rec + r * kWarps * C::kRecord + (KP + pl) * kKv4Plane, lane, live, b0, b1);
+            outputs(o + pl * 8, rec + r * kWarps * C::kRecord + (KP + pl) * kKv4Plane, lane, keep[r], b0, b1);
         }
       }
       __syncwarp();
@@ -498,16 +504,25 @@ __global__ void __launch_bounds__(kThreads, Cfg<KP>::kCtas) kv4_split_kernel(con
       top1 = fmaxf(top1, s_m[parity][i][2 * t + 1]);
     }
     const float f0 = ex2_approx(m0 - top0), f1 = ex2_approx(m1 - top1);
-    if (2 * t < C::kMaxCols) {
-      float* mine0 = s_o + (warp * C::kMaxCols + 2 * t) * C::kPitch;
-      float* mine1 = mine0 + C::kPitch;
+    // the upper half of the warps hand their sums to the lower half
+    auto exchange = [&](auto&& step) {
+      if (2 * t < C::kMaxCols) {
+        float* at = s_o + (warp % (kWarps / 2) * C::kMaxCols + 2 * t) * C::kPitch;
 #pragma unroll
-      for (int j = 0; j < KP * 8; ++j) {
-        const int ch = (j >> 3) * 128 + 16 * g + 2 * (j & 7);
-        *reinterpret_cast<float2*>(mine0 + ch) = make_float2(o[j][0] * f0, o[j][2] * f0);
-        *reinterpret_cast<float2*>(mine1 + ch) = make_float2(o[j][1] * f1, o[j][3] * f1);
+        for (int j = 0; j < KP * 8; ++j) {
+          const int ch = (j >> 3) * 128 + 16 * g + 2 * (j & 7);
+          step(reinterpret_cast<float2*>(at + ch), o[j][0] * f0, o[j][2] * f0);
+          step(reinterpret_cast<float2*>(at + C::kPitch + ch), o[j][1] * f1, o[j][3] * f1);
+        }
       }
-    }
+    };
+    if (warp >= kWarps / 2) exchange([](float2* at, float x, float y) { *at = make_float2(x, y); });
+    named_barrier_sync(1, kWarps * 32);
+    if (warp < kWarps / 2)
+      exchange([](float2* at, float x, float y) {
+        const float2 v = *at;
+        *at = make_float2(v.x + x, v.y + y);
+      });
     named_barrier_sync(1, kWarps * 32);
     // thread `tid` takes channel tid (V1: and tid + 128) of every column
     float sum[C::kMaxCols][KP], l[C::kMaxCols], top[C::kMaxCols];
@@ -524,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<KP>::kCtas) kv4_split_kernel(con
       for (int k = 0; k < KP; ++k) {
         sum[c][k] = 0.f;
 #pragma unroll
-        for (int i = 0; i < kWarps; ++i) sum[c][k] += s_o[(i * C::kMaxCols + c) * C::kPitch + k * 128 + tid];
+        for (int i = 0; i < kWarps / 2; ++i) sum[c][k] += s_o[(i * C::kMaxCols + c) * C::kPitch + k * 128 + tid];
       }
     }
     parity ^= 1;
@@ -671,7 +686,7 @@ cudaError_t launch(const Kv4DecodeArgs& a, cudaStream_t st) {
   p.rec = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + C::kGrid * sizeof(Desc));
   cudaError_t e = cudaFuncSetAttribute(kv4_split_kernel<KP>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  kv4_split_kernel<KP><<<C::kGrid, kThreads, C::kSmem, st>>>(p);
+  kv4_split_kernel<KP><<<C::kGrid, C::kThreads, C::kSmem, st>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // the merge's blocks are set up while the split's last ones end (they wait for its results)

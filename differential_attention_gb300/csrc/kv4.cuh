@@ -48,6 +48,13 @@ __device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t two) {
   asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(d) : "r"(two));
   return d;
 }
+// Four e4m3 values (low byte first) as two half2, exactly.
+__device__ __forceinline__ void e4m3x4_to_half2(uint32_t four, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 h0, h1;\n\tmov.b32 {h0, h1}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, h0;\n\tcvt.rn.f16x2.e4m3x2 %1, h1;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(four));
+}
 __device__ __forceinline__ float e4m3_to_float(uint32_t byte) {
   const uint32_t h = e4m3x2_to_half2(byte);
   return __half2float(__ushort_as_half(static_cast<unsigned short>(h & 0xffffu)));

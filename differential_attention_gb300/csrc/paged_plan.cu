@@ -7,6 +7,11 @@
 // request whose range of the third holds a. The sums sit in shared memory and each token and page
 // finds its request by a binary search there, so that one long prompt costs no more than many
 // short ones.
+//
+// What bounds it is latency: a step moves a few hundred kilobytes at most. So it is one launch of one
+// cluster of up to 8 blocks. Every block forms all the sums (for 1024 requests one pass of its
+// threads), then the cluster meets once, and each block writes its share. The one meeting is what
+// lets the lengths and the ring's state be updated in place: all blocks have read them by then.
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -14,6 +19,7 @@ namespace da {
 namespace {
 
 constexpr int kPlanThreads = 1024;
+constexpr int kPlanCluster = 8;
 
 struct PlanParams {
   const int* seqlens;
@@ -59,6 +65,8 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanPara
   int* s_back = s_take + p.B + 1;      // [B + 1] pages returned before it
   __shared__ Four warp_sum[kPlanThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int all = static_cast<int>(gridDim.x) * kPlanThreads, gid = static_cast<int>(blockIdx.x) * kPlanThreads + tid;
+  const bool lead = blockIdx.x == 0;
   const int ps = p.page_size;
   const long long cap = static_cast<long long>(p.max_pages) * ps;
   const int head = p.state[0], count = p.state[1];
@@ -110,26 +118,27 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanPara
       s_q[i] = static_cast<int>(incl.q - v.q);
       s_take[i] = static_cast<int>(incl.take - v.take);
       s_back[i] = static_cast<int>(incl.back - v.back);
-      p.cu_k[i] = static_cast<int>(incl.k - v.k);
+      if (lead) p.cu_k[i] = static_cast<int>(incl.k - v.k);
     }
     carry = carry + warp_sum[kPlanThreads / 32 - 1];
     __syncthreads();
   }
   bad = bad || carry.q > p.total_max || carry.k > 0x7fffffffLL ||
         carry.take > count + carry.back || count + carry.back > p.num_pages;
+  bad = __syncthreads_or(bad);  // every block finds the same
   // every input that the outputs may overlay (lengths, ring state) has been read by now
-  bad = __syncthreads_or(bad);
+  if (gridDim.x > 1) cluster_sync_all();
   if (bad) {
     // the step does not fit: nothing is taken or returned, and no row has a slot
-    if (tid == 0) flag_device_error(DEV_BAD_INDEX);
-    for (int i = tid; i < p.B; i += kPlanThreads)
+    if (lead && tid == 0) flag_device_error(DEV_BAD_INDEX);
+    for (int i = gid; i < p.B; i += all)
       if (p.seqlens_out != p.seqlens) p.seqlens_out[i] = p.seqlens[i];
-    for (int i = tid; i <= p.B; i += kPlanThreads) p.cu_q[i] = p.cu_k[i] = 0;
-    for (int i = tid; i < p.total_max; i += kPlanThreads) {
+    for (int i = tid; lead && i <= p.B; i += kPlanThreads) p.cu_q[i] = p.cu_k[i] = 0;
+    for (int i = gid; i < p.total_max; i += all) {
       p.slots[i] = -1;
       if (p.positions) p.positions[i] = -1;
     }
-    if (tid == 0) {
+    if (lead && tid == 0) {
       p.state_out[0] = head;
       p.state_out[1] = count;
     }
@@ -141,6 +150,8 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanPara
     s_q[p.B] = total;
     s_take[p.B] = take;
     s_back[p.B] = back;
+  }
+  if (lead && tid == 0) {
     p.cu_k[p.B] = static_cast<int>(carry.k);
     p.state_out[0] = static_cast<int>((static_cast<long long>(head) + take) % p.num_pages);
     p.state_out[1] = count + back - take;
@@ -159,22 +170,22 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanPara
     return p.ring[at];
   };
   bool odd = false;
-  for (int f = tid; f < back; f += kPlanThreads) {
+  for (int f = gid; f < back; f += all) {
     const long long at = static_cast<long long>(head) + count + f;
     p.ring[at % p.num_pages] = returned(f);
   }
-  for (int a = tid; a < take; a += kPlanThreads) {
+  for (int a = gid; a < take; a += all) {
     const int b = owner(s_take, p.B, a);
     const int have = (s_len[b] + ps - 1) / ps;
     p.block_table[static_cast<size_t>(b) * p.max_pages + have + (a - s_take[b])] = taken(a);
   }
-  for (int i = tid; i < p.B; i += kPlanThreads) {
+  for (int i = gid; i < p.B; i += all) {
     const int n = s_q[i + 1] - s_q[i];
     const bool ended = s_back[i + 1] > s_back[i];
     p.seqlens_out[i] = ended ? 0 : s_len[i] + n;
   }
-  for (int i = tid; i <= p.B; i += kPlanThreads) p.cu_q[i] = s_q[i];
-  for (int i = tid; i < p.total_max; i += kPlanThreads) {
+  for (int i = gid; i <= p.B; i += all) p.cu_q[i] = s_q[i];
+  for (int i = gid; i < p.total_max; i += all) {
     int slot = -1, pos = -1;
     if (i < total) {
       const int b = owner(s_q, p.B, i);
@@ -202,8 +213,22 @@ cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (4 * kPlanMaxRequests + 3) * 4);
   if (e != cudaSuccess) return e;
-  paged_plan_kernel<<<1, kPlanThreads, smem, st>>>(p);
-  return cudaGetLastError();
+  // blocks for the slots and the requests, about two rounds of their threads each
+  const int work = a.total_max > a.B ? a.total_max : a.B;
+  int blocks = 1;
+  while (blocks < kPlanCluster && blocks * 2 * kPlanThreads < work) blocks *= 2;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = blocks;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(kPlanThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_plan_kernel, p);
 }
 
 cudaError_t status_paged_plan(int* v) { return read_clear_status(v); }
