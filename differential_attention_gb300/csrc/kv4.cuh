@@ -65,12 +65,23 @@ __device__ __forceinline__ uint32_t float_to_e4m3(float x) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(0.f), "f"(x));
   return d & 0xffu;
 }
-// lo, hi rounded to e2m1 (ties to the even code, at most 6) in the low and high nibble of a byte.
-__device__ __forceinline__ uint32_t float2_to_e2m1x2(float lo, float hi) {
+// Four half2 rounded to eight e2m1 codes (ties to the even code, at most 6), the first in the lowest
+// nibble.
+__device__ __forceinline__ uint32_t half2x4_to_e2m1x8(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  uint32_t w;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f16x2 b0, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f16x2 b1, %2;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f16x2 b2, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f16x2 b3, %4;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+      : "=r"(w)
+      : "r"(a), "r"(b), "r"(c), "r"(d));
+  return w;
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   uint32_t d;
-  asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\tcvt.u32.u8 %0, b;\n\t}"
-      : "=r"(d)
-      : "f"(hi), "f"(lo));
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
   return d;
 }
 __device__ __forceinline__ uint32_t half2_mul(uint32_t a, uint32_t b) {

@@ -18,42 +18,43 @@ struct Block {  // 16 channels as they are stored
 };
 
 // s = e4m3(amax / 6), c = e2m1(x / s) of 16 bf16 values.
-// x has 8 significant bits, s 4 and a border b of e2m1 (0.25, 0.75, .. 5) 3, so x / s is either b or at
-// least b / 512 >= 2^-11 from it. fma(|x|, 1/s, 6144) rounds |x| / s (but for the 2^-24 of 1/s) to a
-// multiple of 2^-11, as all borders are: a quotient on a border lands on it, any other stays on its
-// side. Three instructions instead of a division, and the decision of the exact quotient; the sign is
-// put back last, so that a code of 0 has it too.
+// x has 8 significant bits, s 4 and a border b of e2m1 (0.25, 0.75, .. 5) 3, so x / s is either b or
+// some 2^-8 b away from it. x times the rounded 1 / s, rounded once more to fp16's 11 bits, is then b
+// where the quotient is, and on its side of b where it is not: the decision of the exact quotient
+// without a division.
 __device__ __forceinline__ Block round_block(const uint4& w0, const uint4& w1, float exp_inv) {
   const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-  uint32_t top = 0;  // the largest magnitude's bits, ordered as the values are
+  uint32_t top2 = 0;  // the largest magnitudes' bits, ordered as the values are
 #pragma unroll
-  for (int j = 0; j < 8; ++j) top = max(top, max(w[j] & 0x7fffu, (w[j] >> 16) & 0x7fffu));
+  for (int j = 0; j < 8; ++j) top2 = __vmaxu2(top2, w[j] & 0x7fff7fffu);
+  const uint32_t top = max(top2 & 0xffffu, top2 >> 16);
   Block b{0, 0, 0x7fu};
   if (top >= 0x7f80u) return b;  // an Inf or NaN: the block reads as NaN
   b.scale = float_to_e4m3(__fdiv_rn(__uint_as_float(top << 16) * exp_inv, 6.f));
   if (b.scale == 0) return b;
   const float r = __frcp_rn(e4m3_to_float(b.scale)) * exp_inv;
+  uint32_t y[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const float2 x = bf16x2_to_float2(w[j] & 0x7fff7fffu);
-    const float y0 = __uint_as_float(__float_as_uint(fmaf(x.x, r, 6144.f) - 6144.f) | ((w[j] << 16) & 0x80000000u));
-    const float y1 = __uint_as_float(__float_as_uint(fmaf(x.y, r, 6144.f) - 6144.f) | (w[j] & 0x80000000u));
-    const uint32_t c = float2_to_e2m1x2(y0, y1) << (8 * (j & 3));
-    if (j < 4) b.lo |= c; else b.hi |= c;
+    const float2 x = bf16x2_to_float2(w[j]);
+    y[j] = pack_half2(x.x * r, x.y * r);
   }
+  b.lo = half2x4_to_e2m1x8(y[0], y[1], y[2], y[3]);
+  b.hi = half2x4_to_e2m1x8(y[4], y[5], y[6], y[7]);
   return b;
 }
 
-// A warp rounds 8 rows of one head and plane: a lane 32 channels of a row of K (two blocks, one
-// 16-byte piece of the record), or the same 16 channels of two rows of V, which are one piece too where
-// the rows' slots are the two of a pair. What bounds it: the bytes (2 read, 9/16 written a channel).
+// A warp rounds 8 rows of one head, plane after plane: a lane 32 channels of a row of K (two blocks, one
+// 16-byte piece of the record), then the same 16 channels of two rows of V, which are one piece too
+// where the rows' slots are the two of a pair. The next plane is loaded while one is rounded. What
+// bounds it: the bytes (2 read, 9/16 written a channel).
+template <int KP>
 __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const Kv4AppendArgs a) {
-  const int planes = a.kp + a.vp, lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31;
   const long long u = static_cast<long long>(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
-  const int plane = static_cast<int>(u % planes), h = static_cast<int>(u / planes % a.H);
-  const long long row0 = u / planes / a.H * 8;
+  const int h = static_cast<int>(u % a.H);
+  const long long row0 = u / a.H * 8;
   if (row0 >= a.total) return;
-  const bool is_k = plane < a.kp;
   auto slot_of = [&](long long row) {
     if (row >= a.total) return -1;
     const int s = __ldg(a.slot_map + row);
@@ -64,44 +65,60 @@ __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const Kv4Append
   auto place = [&](int slot) {
     const int page = slot / a.page_size, off = slot - page * a.page_size;
     return a.pool + ((static_cast<size_t>(page) * a.H + h) * (a.page_size >> 4) + (off >> 4)) *
-                        static_cast<size_t>(planes * kKv4Plane) + plane * kKv4Plane;
+                        static_cast<size_t>(2 * KP * kKv4Plane);
   };
-  if (is_k) {
-    const long long row = row0 + (lane >> 2);
-    const int t = lane & 3, slot = slot_of(row);
-    if (slot < 0) return;
-    const uint4* src = reinterpret_cast<const uint4*>(a.k + row * a.k_token + h * a.k_head + plane * 128 + t * 32);
-    const uint4 w0 = __ldg(src), w1 = __ldg(src + 1), w2 = __ldg(src + 2), w3 = __ldg(src + 3);
-    const Block x = round_block(w0, w1, a.k_inv), y = round_block(w2, w3, a.k_inv);
-    uint8_t* p = place(slot);
-    *reinterpret_cast<uint4*>(p + kv4_k_code(slot & 15, t)) = make_uint4(x.lo, x.hi, y.lo, y.hi);
-    *reinterpret_cast<uint16_t*>(p + kv4_k_scale(slot & 15, t)) = static_cast<uint16_t>(x.scale | (y.scale << 8));
-  } else {
-    const long long row = row0 + 2 * (lane >> 3);
-    const int g = lane & 7, s0 = slot_of(row), s1 = slot_of(row + 1);
-    const __nv_bfloat16* src = a.v + row * a.v_token + h * a.v_head + (plane - a.kp) * 128 + g * 16;
-    uint4 w[4];
-    if (s0 >= 0) w[0] = __ldg(reinterpret_cast<const uint4*>(src)), w[1] = __ldg(reinterpret_cast<const uint4*>(src) + 1);
-    src += a.v_token;
-    if (s1 >= 0) w[2] = __ldg(reinterpret_cast<const uint4*>(src)), w[3] = __ldg(reinterpret_cast<const uint4*>(src) + 1);
-    Block x{}, y{};
-    if (s0 >= 0) x = round_block(w[0], w[1], a.v_inv);
-    if (s1 >= 0) y = round_block(w[2], w[3], a.v_inv);
-    if (s0 >= 0 && s1 == s0 + 1 && (s0 & 1) == 0) {
-      uint8_t* p = place(s0);
+  const int t = lane & 3, g = lane & 7;
+  const long long krow = row0 + (lane >> 2), vrow = row0 + 2 * (lane >> 3);
+  const int ks = slot_of(krow), s0 = slot_of(vrow), s1 = slot_of(vrow + 1);
+  const uint4* ksrc = reinterpret_cast<const uint4*>(a.k + krow * a.k_token + h * a.k_head + t * 32);
+  const uint4* vsrc0 = reinterpret_cast<const uint4*>(a.v + vrow * a.v_token + h * a.v_head + g * 16);
+  const uint4* vsrc1 = reinterpret_cast<const uint4*>(a.v + (vrow + 1) * a.v_token + h * a.v_head + g * 16);
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  auto load = [&](int plane, uint4 (&w)[4]) {
+    if (plane < KP) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = ks >= 0 ? __ldg(ksrc + plane * 16 + i) : zero;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        w[i] = s0 >= 0 ? __ldg(vsrc0 + (plane - KP) * 16 + i) : zero;
+        w[2 + i] = s1 >= 0 ? __ldg(vsrc1 + (plane - KP) * 16 + i) : zero;
+      }
+    }
+  };
+  uint8_t* kdst = place(max(ks, 0));
+  uint8_t* vdst0 = place(max(s0, 0)) + KP * kKv4Plane;
+  uint8_t* vdst1 = place(max(s1, 0)) + KP * kKv4Plane;
+  const bool joined = s0 >= 0 && s1 == s0 + 1 && (s0 & 1) == 0;
+  uint4 w[2][4];
+  load(0, w[0]);
+#pragma unroll
+  for (int plane = 0; plane < 2 * KP; ++plane) {
+    if (plane + 1 < 2 * KP) load(plane + 1, w[(plane + 1) & 1]);
+    const uint4(&c)[4] = w[plane & 1];
+    const float inv = plane < KP ? a.k_inv : a.v_inv;
+    const Block x = round_block(c[0], c[1], inv), y = round_block(c[2], c[3], inv);
+    if (plane < KP) {
+      if (ks >= 0) {
+        uint8_t* p = kdst + plane * kKv4Plane;
+        *reinterpret_cast<uint4*>(p + kv4_k_code(ks & 15, t)) = make_uint4(x.lo, x.hi, y.lo, y.hi);
+        *reinterpret_cast<uint16_t*>(p + kv4_k_scale(ks & 15, t)) = static_cast<uint16_t>(x.scale | (y.scale << 8));
+      }
+    } else if (joined) {
+      uint8_t* p = vdst0 + (plane - KP) * kKv4Plane;
       *reinterpret_cast<uint4*>(p + kv4_v_code(s0 & 15, g)) = make_uint4(x.lo, x.hi, y.lo, y.hi);
       *reinterpret_cast<uint16_t*>(p + kv4_v_scale(s0 & 15, g)) = static_cast<uint16_t>(x.scale | (y.scale << 8));
-      return;
-    }
-    if (s0 >= 0) {
-      uint8_t* p = place(s0);
-      *reinterpret_cast<uint2*>(p + kv4_v_code(s0 & 15, g)) = make_uint2(x.lo, x.hi);
-      p[kv4_v_scale(s0 & 15, g)] = static_cast<uint8_t>(x.scale);
-    }
-    if (s1 >= 0) {
-      uint8_t* p = place(s1);
-      *reinterpret_cast<uint2*>(p + kv4_v_code(s1 & 15, g)) = make_uint2(y.lo, y.hi);
-      p[kv4_v_scale(s1 & 15, g)] = static_cast<uint8_t>(y.scale);
+    } else {
+      if (s0 >= 0) {
+        uint8_t* p = vdst0 + (plane - KP) * kKv4Plane;
+        *reinterpret_cast<uint2*>(p + kv4_v_code(s0 & 15, g)) = make_uint2(x.lo, x.hi);
+        p[kv4_v_scale(s0 & 15, g)] = static_cast<uint8_t>(x.scale);
+      }
+      if (s1 >= 0) {
+        uint8_t* p = vdst1 + (plane - KP) * kKv4Plane;
+        *reinterpret_cast<uint2*>(p + kv4_v_code(s1 & 15, g)) = make_uint2(y.lo, y.hi);
+        p[kv4_v_scale(s1 & 15, g)] = static_cast<uint8_t>(y.scale);
+      }
     }
   }
 }
@@ -112,17 +129,20 @@ __device__ __forceinline__ uint32_t half2_to_bf16x2(uint32_t h, float f) {
   return *reinterpret_cast<const uint32_t*>(&o);
 }
 
-// A warp reads one record of one head of one sequence, in the order in which it lies in memory, and
-// writes its rows: a lane 32 channels of two rows of K, and 16 channels of four rows of V. What bounds
-// it: the bytes (9/16 read, 2 written a channel).
+// A warp reads a record of one sequence for some of its heads, plane after plane with the next one's
+// loads under way, and writes its rows, two at a time: a lane 8 channels, so that each store of the warp
+// is whole rows of 128 channels (16 bytes a lane, side by side). What bounds it: the bytes (9/16 read,
+// 2 written a channel).
 //
 // Sequence b's records have the warps from cu[b] / 16 + 2 b on: n rows touch at most n / 16 + 2 records,
 // so that the ranges do not overlap, whatever the sequences' first tokens are.
-__global__ void __launch_bounds__(kRowThreads) kv4_gather_kernel(const Kv4GatherArgs a) {
+template <int KP>
+__global__ void __launch_bounds__(kRowThreads) kv4_gather_kernel(const Kv4GatherArgs a, int heads) {
   const int lane = threadIdx.x & 31;
   const long long i = static_cast<long long>(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
-  const int h = static_cast<int>(i % a.H);
-  const long long u = i / a.H;
+  const int groups = (a.H + heads - 1) / heads, h0 = static_cast<int>(i % groups) * heads;
+  const int n_steps = min(heads, a.H - h0) * 2 * KP;
+  const long long u = i / groups;
   if (u >= a.total / 16 + 2LL * a.B) return;
   // the last b whose first warp is not behind this one: 32 candidates at a time
   int lo = 0, n = a.B;
@@ -155,41 +175,52 @@ __global__ void __launch_bounds__(kRowThreads) kv4_gather_kernel(const Kv4Gather
     flag_device_error(DEV_BAD_INDEX);
     page = 0;
   }
-  const uint8_t* rec = a.pool + ((static_cast<size_t>(page) * a.H + h) * (a.page_size >> 4) + (off >> 4)) *
-                                    static_cast<size_t>((a.kp + a.vp) * kKv4Plane);
-  const int g = lane >> 2, t = lane & 3;
+  const size_t head_bytes = static_cast<size_t>(a.page_size >> 4) * (2 * KP * kKv4Plane);
+  const uint8_t* rec = a.pool + (static_cast<size_t>(page) * a.H + h0) * head_bytes + (off >> 4) * (2 * KP * kKv4Plane);
   const long long row0 = c0 + (tok - first);  // output row of the record's token 0 (it may not be wanted)
-  auto wanted = [&](int key) { return tok + key >= first && tok + key < end; };
-  for (int pl = 0; pl < a.kp + a.vp; ++pl) {
-    const uint8_t* p = rec + pl * kKv4Plane;
-    const uint4 x = __ldg(reinterpret_cast<const uint4*>(p) + lane), y = __ldg(reinterpret_cast<const uint4*>(p + 512) + lane);
-    uint32_t s01, s23;
-    e4m3x4_to_half2(__ldg(reinterpret_cast<const uint32_t*>(p + kKv4PlaneCodes) + lane), s01, s23);
-    const float2 s0 = __half22float2(*reinterpret_cast<const __half2*>(&s01));
-    const float2 s1 = __half22float2(*reinterpret_cast<const __half2*>(&s23));
-    // 8 codes, scale, 8 channels from `ch` of a token
-    auto put = [&](__nv_bfloat16* out, int w, int key, int ch, uint32_t codes, float s) {
-      if (!wanted(key)) return;
+  // lane: rows 2 i + hi, 8 channels from 8 c
+  const int c = lane & 15, hi = lane >> 4;
+  const int k_at = kv4_k_code(hi, c >> 2) + (c & 3) * 4, v_at = kv4_v_code(hi, c >> 1) + (c & 1) * 4;
+  const int k_sc = kv4_k_scale(hi, c >> 2), v_sc = kv4_v_scale(0, c >> 1);
+  const int k_sh = ((c >> 1) & 1) * 8, v_sh = hi * 8;
+  struct Plane {
+    uint32_t codes[8], scales[4];
+  };
+  auto load = [&](int step, Plane& x) {
+    const int pl = step % (2 * KP);
+    const bool is_k = pl < KP;
+    const uint8_t* p = rec + (step / (2 * KP)) * head_bytes + pl * kKv4Plane;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)  // tokens 2 i + hi: a quad of tokens is 128 (K) or 16 (V) bytes on, its second half 512
+      x.codes[i] = __ldg(reinterpret_cast<const uint32_t*>(p + (is_k ? k_at + (i >> 1) * 128 : v_at + (i >> 1) * 16) + (i & 1) * 512));
+#pragma unroll
+    for (int i = 0; i < 4; ++i)  // a quad's scales: K's two rows by two blocks, V's four rows
+      x.scales[i] = __ldg(reinterpret_cast<const uint32_t*>(p + (is_k ? k_sc + i * 32 : v_sc + i * 4)));
+  };
+  auto store = [&](int step, const Plane& x) {
+    const int pl = step % (2 * KP), h = h0 + step / (2 * KP);
+    const bool is_k = pl < KP;
+    const float mul = is_k ? a.k_mul : a.v_mul;
+    const int shift = is_k ? k_sh : v_sh;
+    __nv_bfloat16* out = (is_k ? a.k_out + pl * 128 : a.v_out + (pl - KP) * 128) + c * 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int key = 2 * i + hi;
+      if (tok + key < first || tok + key >= end) continue;
+      const float s = e4m3_to_float((x.scales[i >> 1] >> (shift + 16 * (i & 1))) & 0xffu) * mul;
       uint32_t v[4];
-      e2m1x8_to_half2(codes, v);
-      *reinterpret_cast<uint4*>(out + (static_cast<size_t>(row0 + key) * a.H + h) * w + ch) =
+      e2m1x8_to_half2(x.codes[i], v);
+      *reinterpret_cast<uint4*>(out + (static_cast<size_t>(row0 + key) * a.H + h) * (KP * 128)) =
           make_uint4(half2_to_bf16x2(v[0], s), half2_to_bf16x2(v[1], s), half2_to_bf16x2(v[2], s), half2_to_bf16x2(v[3], s));
-    };
-    if (pl < a.kp) {
-      const int key = (g >> 1) * 4 + (g & 1), ch = pl * 128 + 32 * t, w = a.kp * 128;
-      const float f[4] = {s0.x * a.k_mul, s0.y * a.k_mul, s1.x * a.k_mul, s1.y * a.k_mul};
-      put(a.k_out, w, key, ch, x.x, f[0]), put(a.k_out, w, key, ch + 8, x.y, f[0]);
-      put(a.k_out, w, key, ch + 16, x.z, f[1]), put(a.k_out, w, key, ch + 24, x.w, f[1]);
-      put(a.k_out, w, key + 2, ch, y.x, f[2]), put(a.k_out, w, key + 2, ch + 8, y.y, f[2]);
-      put(a.k_out, w, key + 2, ch + 16, y.z, f[3]), put(a.k_out, w, key + 2, ch + 24, y.w, f[3]);
-    } else {
-      const int key = 4 * t, ch = (pl - a.kp) * 128 + 16 * g, w = a.vp * 128;
-      const float f[4] = {s0.x * a.v_mul, s0.y * a.v_mul, s1.x * a.v_mul, s1.y * a.v_mul};
-      put(a.v_out, w, key, ch, x.x, f[0]), put(a.v_out, w, key, ch + 8, x.y, f[0]);
-      put(a.v_out, w, key + 1, ch, x.z, f[1]), put(a.v_out, w, key + 1, ch + 8, x.w, f[1]);
-      put(a.v_out, w, key + 2, ch, y.x, f[2]), put(a.v_out, w, key + 2, ch + 8, y.y, f[2]);
-      put(a.v_out, w, key + 3, ch, y.z, f[3]), put(a.v_out, w, key + 3, ch + 8, y.w, f[3]);
     }
+  };
+  Plane x, y;
+  load(0, x);
+  for (int step = 0; step < n_steps; step += 2) {  // n_steps is even
+    load(step + 1, y);
+    store(step, x);
+    if (step + 2 < n_steps) load(step + 2, x);
+    store(step + 1, y);
   }
 }
 
@@ -197,15 +228,24 @@ __global__ void __launch_bounds__(kRowThreads) kv4_gather_kernel(const Kv4Gather
 
 cudaError_t launch_kv4_append(const Kv4AppendArgs& a, cudaStream_t st) {
   if (a.total == 0) return cudaSuccess;
-  const long long warps = (static_cast<long long>(a.total) + 7) / 8 * a.H * (a.kp + a.vp);
-  kv4_append_kernel<<<static_cast<unsigned>((warps * 32 + kRowThreads - 1) / kRowThreads), kRowThreads, 0, st>>>(a);
+  const long long warps = (static_cast<long long>(a.total) + 7) / 8 * a.H;
+  const unsigned blocks = static_cast<unsigned>((warps * 32 + kRowThreads - 1) / kRowThreads);
+  if (a.kp == 1) kv4_append_kernel<1><<<blocks, kRowThreads, 0, st>>>(a);
+  else kv4_append_kernel<2><<<blocks, kRowThreads, 0, st>>>(a);
   return cudaGetLastError();
 }
 
 cudaError_t launch_kv4_gather(const Kv4GatherArgs& a, cudaStream_t st) {
   if (a.total == 0) return cudaSuccess;
-  const long long warps = (a.total / 16 + 2LL * a.B) * a.H;
-  kv4_gather_kernel<<<static_cast<unsigned>((warps * 32 + kRowThreads - 1) / kRowThreads), kRowThreads, 0, st>>>(a);
+  // Several heads a warp share one look-up of the sequence and the page, where that leaves warps
+  // enough to fill the machine (152 SMs, 24 each) twice.
+  const long long units = a.total / 16 + 2LL * a.B;
+  int heads = 4;
+  while (heads > 1 && units * ((a.H + heads - 1) / heads) < 2 * 152 * 24) heads >>= 1;
+  const long long warps = units * ((a.H + heads - 1) / heads);
+  const unsigned blocks = static_cast<unsigned>((warps * 32 + kRowThreads - 1) / kRowThreads);
+  if (a.kp == 1) kv4_gather_kernel<1><<<blocks, kRowThreads, 0, st>>>(a, heads);
+  else kv4_gather_kernel<2><<<blocks, kRowThreads, 0, st>>>(a, heads);
   return cudaGetLastError();
 }
 
