@@ -28,7 +28,12 @@
 // Work. The rows, one after the other, are cut into equal ranges, one for each resident block, whatever
 // the sequences' lengths; a row counts its tiles and a fixed cost. A block walks its range: a row that
 // lies in it whole is finished there; the pieces of one that does not go to the workspace, at most
-// two a block, and the second kernel merges them.
+// two a block, and the second kernel merges them, in the order of the ranges. Where the tables hold so
+// few keys that a block would get no more than kFewTiles tiles, a row is cut over the blocks of a
+// cluster instead, which join through each other's shared memory: one launch, no workspace. (Tried and dropped, V2
+// with lengths of 1 to 16K, 52 us as it is: two ranges a block, the second taken over by cluster launch
+// control, 58 us, as each range adds pieces; the last block of a row merging it, without a second
+// kernel, 60 us, as the blocks wait for their fence and their count.)
 #include <cfloat>
 #include <cmath>
 
@@ -40,7 +45,8 @@ namespace da {
 namespace {
 
 constexpr int kSms = 152;
-constexpr int kMergeThreads = 1024;
+constexpr int kMergeThreads = 512;
+constexpr int kFewTiles = 4;
 constexpr float kPScale = 10.f;                  // log2 of P's scale
 constexpr float kMoveRef = 14.f;                 // log2 P at which the reference moves
 
@@ -48,35 +54,27 @@ template <int KP>
 struct Cfg {
   static constexpr int kWarps = 4;               // consumer warps
   static constexpr int kThreads = (kWarps + 1) * 32;  // and a producer
-  static constexpr int kRecs = KP == 1 ? 2 : 1;  // records of a tile for each consumer warp
+  static constexpr int kRecs = 2;                // records of a tile for each of them
   static constexpr int kTileRecs = kWarps * kRecs;
   static constexpr int kTileKeys = 16 * kTileRecs;
-  static constexpr int kCtas = 3;                // blocks of an SM
+  static constexpr int kCtas = KP == 1 ? 3 : 2;  // blocks of an SM
   static constexpr int kGrid = kSms * kCtas;
-  static constexpr int kRowCost = KP == 1 ? 2 : 3;  // what a row costs besides its tiles, in tiles
-  static constexpr int kMinCost = KP == 1 ? 3 : 4;  // the smallest range
+  static constexpr int kRowCost = KP == 1 ? 2 : 1;  // what a row costs besides its tiles, in tiles
+  static constexpr int kMinCost = KP == 1 ? 3 : 2;  // the smallest range
   static constexpr int kRecord = 2 * KP * kKv4Plane;
   static constexpr int kWidth = KP * 128;
   static constexpr int kMaxCols = KP == 1 ? 8 : 2;
   static constexpr int kQBytes = kMaxCols * 256;
   static constexpr int kStage = kTileRecs * kRecord + kQBytes;
-  static constexpr int kStages = 3;
+  static constexpr int kStages = KP == 1 ? 3 : 2;
   static constexpr int kPitch = kWidth + 4;      // floats of one column's row in the exchange
   static constexpr int kSmem = kStages * kStage + kWarps / 2 * kMaxCols * kPitch * 4;
 };
 
-// where a block's range begins, for the merge
-struct Desc {
-  int b, h, tile, tiles;
-  long long total;
-  int n, pad;
-};
-
 struct Params {
   Kv4DecodeArgs a;
-  int cols;
-  Desc* desc;
-  float* rec;  // [2 * grid][2 cols + cols * width]: m, l, o
+  int cols, grid;  // grid: by rows, the blocks of a cluster
+  float* rec;  // [2 * grid][2 cols + cols * width]: m, l, o of a piece
 };
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
@@ -109,6 +107,8 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 // place in the walk over rows (sequence-major, heads inner)
 struct Walk {
   int b, h, tile, tiles, len;
+  int todo;         // tiles of the range, and the costs of the rows that begin in it, from here on
+  long long first;  // where the row's tiles begin among all costs
 };
 __device__ __forceinline__ int clamp_len(const Kv4DecodeArgs& a, int b) {
   const int cap = a.max_pages * a.page_size;
@@ -126,6 +126,8 @@ __device__ __forceinline__ int cost_of(int len) {
 }
 template <int KP>
 __device__ __forceinline__ void next_row(const Kv4DecodeArgs& a, Walk& w) {
+  w.first += w.tiles + Cfg<KP>::kRowCost;
+  w.todo -= Cfg<KP>::kRowCost;
   w.tile = 0;
   if (++w.h < a.H) return;
   w.h = 0;
@@ -136,7 +138,94 @@ __device__ __forceinline__ void next_row(const Kv4DecodeArgs& a, Walk& w) {
   w.tiles = tiles_of<KP>(w.len);
 }
 
-__device__ __forceinline__ long long range_start(long long total, int n, int i) { return total * i / n; }
+// x / y for 0 <= x, 0 < y; nearly always both have 32 bits
+__device__ __forceinline__ long long div(long long x, long long y) {
+  if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+  return x / y;
+}
+// 0 .. total cut in n parts whose lengths differ by at most one: the first `more` have len + 1
+struct Cut {
+  long long len;
+  int n, more;
+  __device__ __forceinline__ Cut(long long total, int parts) : len(div(total, parts)), n(parts), more(static_cast<int>(total - len * parts)) {}
+  __device__ __forceinline__ long long start(int i) const { return len * i + min(i, more); }
+  // the part that holds x < total (len > 0)
+  __device__ __forceinline__ int owner(long long x) const {
+    const long long head = (len + 1) * more;
+    return static_cast<int>(x < head ? div(x, len + 1) : more + div(x - head, len));
+  }
+};
+
+// The batch's rows one behind the other, cut in n equal parts. pre[i]: the costs (of one head) before
+// thread i's share of the sequences. A whole block of NT threads.
+template <int KP, int NT>
+struct Ranges {
+  long long pre[NT + 1];
+  long long sum[NT / 32];
+
+  __device__ __forceinline__ void fill(const Kv4DecodeArgs& a) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, per = (a.B + NT - 1) / NT;
+    const int lo = min(a.B, tid * per), hi = min(a.B, lo + per);
+    long long incl = 0;
+    for (int b = lo; b < hi; ++b) incl += cost_of<KP>(clamp_len(a, b));
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long o = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += o;
+    }
+    if (lane == 31) sum[warp] = incl;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) incl += sum[w];
+    pre[tid + 1] = incl;
+    if (tid == 0) pre[0] = 0;
+    __syncthreads();
+  }
+  __device__ __forceinline__ long long total(const Kv4DecodeArgs& a) const { return pre[NT] * a.H; }
+  static __device__ __forceinline__ int count(long long total, int grid) {
+    const long long want = total / Cfg<KP>::kMinCost;
+    return static_cast<int>(want < 1 ? 1 : want > grid ? grid : want);
+  }
+  // where range r of n begins (a whole warp)
+  __device__ __forceinline__ void locate(const Kv4DecodeArgs& a, const Cut& cut, int r, Walk& w) const {
+    const int lane = threadIdx.x & 31, per = (a.B + NT - 1) / NT;
+    const long long t0 = cut.start(r), t1 = cut.start(r + 1);
+    w = Walk{};
+    if (t1 <= t0) return;
+    int share = 0;
+    for (int i = 0; i < NT; i += 32)
+      if (const unsigned hit = __ballot_sync(0xffffffffu, pre[i + lane] * a.H <= t0 && t0 < pre[i + lane + 1] * a.H)) {
+        share = i + __ffs(hit) - 1;
+        break;
+      }
+    long long at = pre[share];
+    const int end = min(a.B, (share + 1) * per);
+    for (int b0 = share * per; b0 < end; b0 += 32) {
+      const int b = b0 + lane, len = b < end ? clamp_len(a, b) : 0, cost = cost_of<KP>(len);
+      int incl = cost;
+      if (per > 1) {
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int o = __shfl_up_sync(0xffffffffu, incl, d);
+          if (lane >= d) incl += o;
+        }
+      }
+      if (const unsigned hit = __ballot_sync(0xffffffffu, t0 < (at + incl) * a.H)) {
+        const int l = __ffs(hit) - 1;
+        at += __shfl_sync(0xffffffffu, incl - cost, l);
+        w.b = b0 + l;
+        w.len = __shfl_sync(0xffffffffu, len, l);
+        break;
+      }
+      at += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    w.tiles = tiles_of<KP>(w.len);
+    const int cost = w.tiles + Cfg<KP>::kRowCost;
+    w.h = static_cast<int>(div(t0 - at * a.H, cost));
+    w.first = at * a.H + static_cast<long long>(w.h) * cost + Cfg<KP>::kRowCost;
+    w.tile = static_cast<int>(max(t0 - w.first, 0LL));
+    w.todo = static_cast<int>(t1 - max(t0, w.first));
+  }
+};
 
 // the first product of a sum
 __device__ __forceinline__ void mma_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -195,15 +284,29 @@ __device__ __forceinline__ void outputs(float (*o)[4], uint32_t at, int lane, ui
   }
 }
 
-template <int KP>
-__global__ void __launch_bounds__(Cfg<KP>::kThreads, Cfg<KP>::kCtas) kv4_split_kernel(const Params p) {
+// V1's factor for a whole row of 256 channels: the norm's 1 / rms and the fixed scale. ss: the squares of
+// this thread's two channels. The first four warps.
+__device__ __forceinline__ float norm_scale(const Kv4DecodeArgs& a, float ss, float* s_red) {
+  float f = 1.f;
+  if (a.flags & 2) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
+    if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = ss;
+    named_barrier_sync(1, 128);
+    ss = (s_red[0] + s_red[1]) + (s_red[2] + s_red[3]);
+    f = 1.f / sqrtf(ss / 256.f + a.eps);
+  }
+  return (a.flags & 4) ? f * (1.f - a.lambda_init) : f;
+}
+
+// kByRow: one row for each cluster of p.grid blocks
+template <int KP, bool kByRow>
+__global__ void __launch_bounds__(Cfg<KP>::kThreads, Cfg<KP>::kCtas) kv4_decode_kernel(const Params p) {
   using C = Cfg<KP>;
   constexpr int kWarps = C::kWarps, kThreads = C::kThreads;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bars[2 * C::kStages];
-  __shared__ long long s_sum[kThreads / 32];
-  __shared__ long long s_pos;
-  __shared__ int s_b;
+  __shared__ Ranges<KP, kThreads> s_ranges;
   __shared__ int s_abort;
   __shared__ float s_m[2][kWarps][8], s_l[2][kWarps][8];
   __shared__ float s_red[kWarps];
@@ -213,6 +316,7 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, Cfg<KP>::kCtas) kv4_split_k
   auto full = [&](int s) { return bar0 + 8 * s; };
   auto empty = [&](int s) { return bar0 + 8 * (C::kStages + s); };
   float* s_o = reinterpret_cast<float*>(smem + C::kStages * C::kStage);
+  float* s_x = reinterpret_cast<float*>(smem);  // by rows: the block's piece, m, l, o
 
   if (tid == 0) {
     for (int s = 0; s < C::kStages; ++s) {
@@ -223,67 +327,27 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, Cfg<KP>::kCtas) kv4_split_k
     s_abort = 0;
   }
 
-  // The range: the batch's rows one behind the other, cut in n equal parts.
-  const int per = (a.B + kThreads - 1) / kThreads;
-  const int lo = min(a.B, tid * per), hi = min(a.B, lo + per);
-  long long mine = 0;
-  for (int b = lo; b < hi; ++b) mine += cost_of<KP>(clamp_len(a, b));
-  long long incl = mine;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const long long o = __shfl_up_sync(0xffffffffu, incl, d);
-    if (lane >= d) incl += o;
-  }
-  if (lane == 31) s_sum[warp] = incl;
-  __syncthreads();
-  long long before = incl - mine, total = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) before += s_sum[w];
-    total += s_sum[w];
-  }
-  total *= a.H;
-  const long long want = total / C::kMinCost;
-  const int n = static_cast<int>(want < 1 ? 1 : want > gridDim.x ? gridDim.x : want);
-  const int cta = blockIdx.x;
-  const bool active = cta < n && total > 0;
-  const long long t0 = active ? range_start(total, n, cta) : 0;
-  const long long t1 = active ? range_start(total, n, cta + 1) : 0;
-  if (active && before * a.H <= t0 && t0 < (before + mine) * a.H) {
-    long long at = before;
-    for (int b = lo; b < hi; ++b) {
-      const int cost = cost_of<KP>(clamp_len(a, b));
-      if (t0 < (at + cost) * a.H) {
-        s_b = b;
-        s_pos = t0 - at * a.H;
-        break;
-      }
-      at += cost;
-    }
-  }
-  __syncthreads();
-  // empty places in the batch get zeros
-  for (int b = cta; b < a.B; b += gridDim.x)
-    if (clamp_len(a, b) == 0) {
-      uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) +
-                                          static_cast<size_t>(b) * a.H * (p.cols / 2) * C::kWidth);
-      for (int i = tid; i < a.H * (p.cols / 2) * C::kWidth / 8; i += kThreads) o[i] = make_uint4(0, 0, 0, 0);
-    }
   Walk w{};
-  int todo = 0;  // tiles of the range, and the costs of the rows that begin in it
-  if (active) {
-    w.b = s_b;
+  int n = 0;
+  const int range = blockIdx.x;
+  if constexpr (kByRow) {
+    const int row = blockIdx.x / p.grid, rank = blockIdx.x - row * p.grid;
+    w.b = row / a.H;
+    w.h = row - w.b * a.H;
     w.len = clamp_len(a, w.b);
     w.tiles = tiles_of<KP>(w.len);
-    const int cost = w.tiles + C::kRowCost;
-    w.h = static_cast<int>(s_pos / cost);
-    const int pos = static_cast<int>(s_pos - static_cast<long long>(w.h) * cost) - C::kRowCost;
-    w.tile = max(pos, 0);
-    todo = static_cast<int>(t1 - t0) + min(pos, 0);
+    const int per = (w.tiles + p.grid - 1) / p.grid;
+    w.tile = min(rank * per, w.tiles);
+    w.todo = min(per, w.tiles - w.tile);
+    __syncthreads();
+  } else {
+    s_ranges.fill(a);
+    const long long total = s_ranges.total(a);
+    n = s_ranges.count(total, p.grid);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (range >= n) return;
+    s_ranges.locate(a, Cut(total, n), range, w);
   }
-  if (tid == 0) p.desc[cta] = Desc{w.b, w.h, w.tile, w.tiles, total, n, 0};
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (todo <= 0) return;
 
   if (warp == kWarps) {
     // Producer. Lane i looks up the page of record i of the next tiles of the row (32 records); the
@@ -291,9 +355,10 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, Cfg<KP>::kCtas) kv4_split_k
     constexpr int kBatch = 32 / C::kTileRecs;
     int stage = 0, issued = 0;
     uint32_t phase = 0;
-    bool alive = true, first = true;
-    while (todo > 0 && alive) {
-      const int batch = min(min(kBatch, w.tiles - w.tile), todo);
+    bool alive = true;
+    bool first = true;
+    while (w.todo > 0 && alive) {
+      const int batch = min(min(kBatch, w.tiles - w.tile), w.todo);
       const int r = w.tile * C::kTileRecs + lane, records = (w.len + 15) >> 4;
       const bool mine_ok = lane < batch * C::kTileRecs && r < records;
       const uint8_t* src = nullptr;
@@ -328,11 +393,10 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, Cfg<KP>::kCtas) kv4_split_k
         ++issued;
         if (++stage == C::kStages) stage = 0, phase ^= 1;
       }
-      todo -= batch;
+      w.todo -= batch;
       w.tile += batch;
-      if (w.tile == w.tiles) {
+      if (!kByRow && w.tile == w.tiles) {
         next_row<KP>(a, w);
-        todo -= C::kRowCost;
         first = true;
       }
     }
@@ -343,10 +407,11 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, Cfg<KP>::kCtas) kv4_split_k
         mbar_wait_limit(full(stage), phase, nullptr, kWaitLimitNs);
       }
     }
-    return;
+    if constexpr (!kByRow) return;
   }
 
   // Consumers.
+  if (warp < kWarps) {
   const int g = lane >> 2, t = lane & 3;
   const int cols = p.cols;
   uint32_t qf[8][2];           // Q^T fragments: channels 32t + 4j .. + 3 of column g
@@ -389,9 +454,18 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, Cfg<KP>::kCtas) kv4_split_k
   };
   auto wait = [&]() { alive = __all_sync(0xffffffffu, alive && mbar_wait(full(stage), phase, &s_abort)); };
 
-  while (todo > 0) {
-    const int seg = min(w.tiles - w.tile, todo);  // tiles of this row in the range
-    const bool starts = w.tile == 0, whole = starts && seg == w.tiles;
+  // empty places in the batch get zeros
+  for (int b = range; !kByRow && b < a.B; b += n)
+    if (clamp_len(a, b) == 0) {
+      const size_t size = static_cast<size_t>(a.H) * (cols / 2) * C::kWidth;
+      uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + b * size);
+      for (size_t i = tid; i < size / 8; i += kWarps * 32) out[i] = make_uint4(0, 0, 0, 0);
+    }
+  if (kByRow && w.todo <= 0)  // a piece of no keys
+    for (int i = tid; i < C::kMaxCols * (2 + C::kWidth); i += kWarps * 32) s_x[i] = i < C::kMaxCols ? -FLT_MAX : 0.f;
+  while (w.todo > 0) {
+    const int seg = min(w.tiles - w.tile, w.todo);  // tiles of this row in the range
+    const bool starts = w.tile == 0, whole = !kByRow && starts && seg == w.tiles;
     wait();
     load_q(ring + stage * C::kStage + C::kTileRecs * C::kRecord);
 #pragma unroll
@@ -538,8 +612,15 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, Cfg<KP>::kCtas) kv4_split_k
     }
     parity ^= 1;
     const size_t row = static_cast<size_t>(w.b) * a.H + w.h;
-    if (!whole) {
-      float* rec = p.rec + static_cast<size_t>(2 * cta + (starts ? 1 : 0)) * (2 * cols + cols * C::kWidth);
+    if constexpr (kByRow) {
+#pragma unroll
+      for (int c = 0; c < C::kMaxCols; ++c) {
+        if (tid == 0) s_x[c] = top[c], s_x[C::kMaxCols + c] = l[c];
+#pragma unroll
+        for (int k = 0; k < KP; ++k) s_x[2 * C::kMaxCols + c * C::kWidth + k * 128 + tid] = sum[c][k];
+      }
+    } else if (!whole) {
+      float* rec = p.rec + static_cast<size_t>(2 * range + (starts ? 1 : 0)) * (2 * cols + cols * C::kWidth);
 #pragma unroll
       for (int c = 0; c < C::kMaxCols; ++c) {
         if (c >= cols) break;
@@ -565,30 +646,61 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, Cfg<KP>::kCtas) kv4_split_k
         y[k] = (sum[0][k] / l[0] - lam * (sum[1][k] / l[1])) * a.v_mul;
         ss = fmaf(y[k], y[k], ss);
       }
-      float f = 1.f;
-      if (a.flags & 2) {
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
-        if (lane == 0) s_red[warp] = ss;
-        named_barrier_sync(1, kWarps * 32);
-        ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < kWarps; ++i) ss += s_red[i];
-        f = 1.f / sqrtf(ss / static_cast<float>(C::kWidth) + a.eps);
-      }
-      if (a.flags & 4) f *= 1.f - a.lambda_init;
+      const float f = norm_scale(a, ss, s_red);
 #pragma unroll
       for (int k = 0; k < KP; ++k) {
         const float wgt = (a.flags & 2) && a.norm_w ? __ldg(a.norm_w + k * 128 + tid) : 1.f;
         static_cast<__nv_bfloat16*>(a.out)[row * C::kWidth + k * 128 + tid] = __float2bfloat16_rn(y[k] * f * wgt);
       }
     }
-    todo -= seg;
+    w.todo -= seg;
     w.tile += seg;
-    if (w.tile == w.tiles) {
-      next_row<KP>(a, w);
-      todo -= C::kRowCost;
+    if (!kByRow && w.tile == w.tiles) next_row<KP>(a, w);
+  }
+  }  // consumers
+
+  if constexpr (kByRow) {
+    // Every block's piece lies in its ring, which nothing uses any more. The columns' pairs are dealt out
+    // over the blocks; thread `tid` takes channel tid (V1: and tid + 128).
+    cluster_sync_all();
+    const int parts = p.grid, rank = blockIdx.x % parts;
+    const size_t row = static_cast<size_t>(w.b) * a.H + w.h;
+    for (int pair = rank; pair < p.cols / 2 && tid < 128; pair += parts) {
+      float top[2] = {-FLT_MAX, -FLT_MAX}, l[2] = {0.f, 0.f}, sum[2][KP] = {};
+      const uint32_t x = smem_u32(s_x);
+      for (int i = 0; i < parts; ++i) {
+        const uint32_t from = mapa_shared(x, i);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) top[e] = fmaxf(top[e], ld_cluster_f32(from + 4 * (2 * pair + e)));
+      }
+      for (int i = 0; i < parts; ++i) {
+        const uint32_t from = mapa_shared(x, i);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int c = 2 * pair + e;
+          const float f = ex2_approx(ld_cluster_f32(from + 4 * c) - top[e]);
+          l[e] = fmaf(ld_cluster_f32(from + 4 * (C::kMaxCols + c)), f, l[e]);
+#pragma unroll
+          for (int k = 0; k < KP; ++k)
+            sum[e][k] = fmaf(ld_cluster_f32(from + 4 * (2 * C::kMaxCols + c * C::kWidth + k * 128 + tid)), f, sum[e][k]);
+        }
+      }
+      const float lam = KP == 2 ? __ldg(a.lambda + w.h)
+                                : 1.f / (1.f + __expf(-__ldg(a.lam_logit + row * (p.cols / 2) + pair)));
+      float y[KP], ss = 0.f, f = 1.f;
+#pragma unroll
+      for (int k = 0; k < KP; ++k) {
+        y[k] = w.len == 0 ? 0.f : (sum[0][k] / l[0] - lam * (sum[1][k] / l[1])) * a.v_mul;
+        ss = fmaf(y[k], y[k], ss);
+      }
+      if constexpr (KP == 2) f = norm_scale(a, ss, s_red);
+#pragma unroll
+      for (int k = 0; k < KP; ++k) {
+        const float wgt = KP == 2 && (a.flags & 2) && a.norm_w ? __ldg(a.norm_w + k * 128 + tid) : 1.f;
+        static_cast<__nv_bfloat16*>(a.out)[(row * (p.cols / 2) + pair) * C::kWidth + k * 128 + tid] = __float2bfloat16_rn(y[k] * f * wgt);
+      }
     }
+    cluster_sync_all();  // no block leaves while another reads its piece
   }
 }
 
@@ -603,17 +715,34 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const Params p
   __shared__ float s_red[W / 32];
   const Kv4DecodeArgs& a = p.a;
   const int i = blockIdx.x + 1, tid = threadIdx.x;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Desc d = p.desc[i];
-  if (i >= d.n || d.total == 0 || d.tile == 0) return;
-  const long long first = range_start(d.total, d.n, i) - d.tile;  // where the row's tiles begin
-  if (range_start(d.total, d.n, i - 1) > first) return;
-  const int last = static_cast<int>(((first + d.tiles) * d.n - 1) / d.total);  // the last range that begins in the row
-  const int pieces = min(last, d.n - 1) - (i - 1) + 1;
+  // (all but the pieces is known before the first kernel ends)
+  __shared__ Ranges<KP, kMergeThreads> s_ranges;
+  __shared__ Walk s_walk;
+  s_ranges.fill(a);
+  const long long total = s_ranges.total(a);
+  const int n = s_ranges.count(total, p.grid);
+  if (i >= n) return;
+  const Cut cut(total, n);
+  if (tid < 32) {
+    Walk w;
+    s_ranges.locate(a, cut, i, w);
+    if (tid == 0) s_walk = w;
+  }
+  __syncthreads();
+  const Walk d = s_walk;
+  if (d.tile == 0) return;
+  if (cut.start(i - 1) > d.first) return;
+  const int pieces = cut.owner(d.first + d.tiles - 1) - (i - 1) + 1;
   const int cols = p.cols;
   const int lanes = cols * (W / 4), groups = kMergeThreads / lanes;  // a float4 of all columns' outputs each
   const size_t rec = 2 * cols + cols * W;
   const int grp = tid / lanes, ln = tid % lanes, c = ln / (W / 4);
+  const size_t row = static_cast<size_t>(d.b) * a.H + d.h;
+  const int pair = tid / W, ch = tid % W;  // the output channel of the end
+  const bool mine = tid < cols / 2 * W;
+  const float lam = !mine ? 0.f : KP == 2 ? __ldg(a.lambda + d.h) : 1.f / (1.f + __expf(-__ldg(a.lam_logit + row * (cols / 2) + pair)));
+  const float wgt = KP == 2 && mine && (a.flags & 2) && a.norm_w ? __ldg(a.norm_w + ch) : 1.f;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   float m = -FLT_MAX, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
@@ -632,10 +761,8 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const Params p
   s_o[tid] = o;
   if (ln % (W / 4) == 0) s_m[grp * cols + c] = m, s_l[grp * cols + c] = l;
   __syncthreads();
-  const size_t row = static_cast<size_t>(d.b) * a.H + d.h;
   // an output channel: of a pair of columns, V1's only one
-  if (tid >= cols / 2 * W) return;
-  const int pair = tid / W, ch = tid % W;
+  if (!mine) return;
   float q[2];
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
@@ -650,8 +777,6 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const Params p
     }
     q[e] = sum / ls;
   }
-  const float lam = KP == 2 ? __ldg(a.lambda + d.h)
-                            : 1.f / (1.f + __expf(-__ldg(a.lam_logit + row * (cols / 2) + pair)));
   float y = (q[0] - lam * q[1]) * a.v_mul;
   if constexpr (KP == 2) {
     if (a.flags & 2) {
@@ -663,7 +788,7 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const Params p
       ss = 0.f;
 #pragma unroll
       for (int k = 0; k < W / 32; ++k) ss += s_red[k];
-      y *= 1.f / sqrtf(ss / static_cast<float>(W) + a.eps) * (a.norm_w ? __ldg(a.norm_w + ch) : 1.f);
+      y *= 1.f / sqrtf(ss / static_cast<float>(W) + a.eps) * wgt;
     }
     if (a.flags & 4) y *= 1.f - a.lambda_init;
   }
@@ -676,19 +801,45 @@ cudaError_t launch(const Kv4DecodeArgs& a, cudaStream_t st) {
   Params p{};
   p.a = a;
   p.cols = KP == 2 ? 2 : a.group;
-  p.desc = static_cast<Desc*>(a.ws);
-  p.rec = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + C::kGrid * sizeof(Desc));
-  cudaError_t e = cudaFuncSetAttribute(kv4_split_kernel<KP>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  p.rec = static_cast<float*>(a.ws);
+  static std::atomic<uint64_t> raised[2];
+  const long long tiles = (static_cast<long long>(a.max_pages) * a.page_size + C::kTileKeys - 1) / C::kTileKeys;
+  const long long rows = static_cast<long long>(a.B) * a.H;
+  // Few keys: a row over a cluster, of as many blocks as leave two tiles each and are resident at once.
+  // (Measured, GPU time of a call: 8 rows of 777 keys, V2, <ROWS_V2> us so and <RANGES_V2> by ranges; 48 rows
+  // of 1500 keys, V1, <ROWS_V1> and <RANGES_V1>; the host has one launch less as well.)
+  if (rows * tiles <= static_cast<long long>(kFewTiles) * C::kGrid && rows <= C::kGrid) {
+    p.grid = 1;
+    while (p.grid < 8 && p.grid * 2 < tiles && rows * p.grid * 2 <= C::kGrid) p.grid *= 2;
+    cudaError_t e = raise_smem(reinterpret_cast<const void*>(kv4_decode_kernel<KP, true>), C::kSmem, raised[1]);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = p.grid;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(rows * p.grid));
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = st;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kv4_decode_kernel<KP, true>, p);
+  }
+  cudaError_t e = raise_smem(reinterpret_cast<const void*>(kv4_decode_kernel<KP, false>), C::kSmem, raised[0]);
   if (e != cudaSuccess) return e;
-  kv4_split_kernel<KP><<<C::kGrid, C::kThreads, C::kSmem, st>>>(p);
+  // no more blocks than the tables' capacity can give ranges
+  const long long most = (tiles + C::kRowCost) * rows / C::kMinCost;
+  p.grid = static_cast<int>(most < 1 ? 1 : most > C::kGrid ? C::kGrid : most);
+  kv4_decode_kernel<KP, false><<<p.grid, C::kThreads, C::kSmem, st>>>(p);
   e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  // the merge's blocks are set up while the split's last ones end (they wait for its results)
+  if (e != cudaSuccess || p.grid == 1) return e;
+  // the merge's blocks find their rows while the last ranges end (they wait for the results)
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(C::kGrid - 1);
+  cfg.gridDim = dim3(p.grid - 1);
   cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = st;
   cfg.attrs = &at;
@@ -701,7 +852,7 @@ cudaError_t launch(const Kv4DecodeArgs& a, cudaStream_t st) {
 size_t kv4_decode_workspace_bytes(int B, int H, int cols, int width) {
   (void)B, (void)H;
   const size_t grid = width == 128 ? Cfg<1>::kGrid : Cfg<2>::kGrid;
-  return grid * sizeof(Desc) + 2 * grid * (2 * cols + static_cast<size_t>(cols) * width) * sizeof(float);
+  return 2 * grid * (2 * cols + static_cast<size_t>(cols) * width) * sizeof(float);
 }
 
 cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a, cudaStream_t st) {

@@ -1,5 +1,6 @@
 // internal.h -- declarations shared by the library's translation units (not part of the ABI).
 #pragma once
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda.h>
@@ -296,6 +297,18 @@ constexpr size_t kNoAllocScratchBytes = static_cast<size_t>(16) << 20;
 long long decode_noalloc_max_units();  // largest B * H whose partials fit (one split each)
 int decode_noalloc_splits(int B, int Lmax, int H, int* chunk_out);  // splits the no-alloc call runs
 cudaError_t launch_decode_noalloc(const DecodeArgs& a, cudaStream_t s);
+
+// Raises a kernel's dynamic shared memory limit, once for each device (`raised`: a bit each).
+inline cudaError_t raise_smem(const void* kernel, int bytes, std::atomic<uint64_t>& raised) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (raised.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) raised.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 // The 4-bit cache (kv4_rows.cu, decode_kv4.cu). Pools: [num_pages, H, page_size / 16, record], a
 // record 16 tokens of one head: kp K planes and vp V planes of 128 channels (kv4.cuh).

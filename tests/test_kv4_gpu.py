@@ -361,14 +361,25 @@ def v2_case(rng, lens, Hkv, G, page_size, std=1.0, spare=2, width=None):
     return table, pool, q, lam
 
 
+def widened(table, page_size, heads, wide):
+    """The table, or one of such a capacity that the decode cuts the batch into ranges for all blocks
+    (few keys at most: one row for each cluster)."""
+    if not wide:
+        return table
+    width = -(-5 * 456 * 128 // (page_size * heads * len(table))) + table.shape[1]
+    return np.concatenate([table, np.full((len(table), width - table.shape[1]), -1)], axis=1)
+
+
 LENS = [[1], [0], [2, 0, 15], [16, 17, 31, 32, 33], [63, 64, 65, 127, 128, 129, 0, 1], [1000, 3, 511], [4097]]
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("lens", LENS)
 @pytest.mark.parametrize("H,page_size", [(1, 16), (3, 48), (12, 64)])
-def test_v1_decode(lens, H, page_size):
+def test_v1_decode(lens, H, page_size, wide):
     rng = np.random.default_rng(sum(lens) * 7 + H)
     table, pool, q, lam, w = v1_case(rng, lens, H, page_size)
+    table = widened(table, page_size, H, wide)
     got = da.diffattn_decode_kv4(q.to(DEV), torch.tensor(pool).to(DEV), dev32(table), dev32(lens), lam.to(DEV), 0.4,
                                  norm_weight=w.to(DEV))
     within(got, *kv4.decode(q, pool, table, lens, lam.numpy(), 0.4, w, slack=SLACK, floor=FLOOR))
@@ -377,20 +388,24 @@ def test_v1_decode(lens, H, page_size):
     da.diffattn_device_status()
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("norm,scale,weight", [(False, False, False), (False, True, False), (True, False, True), (True, True, False)])
-def test_v1_decode_epilogues(norm, scale, weight):
+def test_v1_decode_epilogues(norm, scale, weight, wide):
     rng = np.random.default_rng(31)
     table, pool, q, lam, w = v1_case(rng, [77, 300], 2, 32)
+    table = widened(table, 32, 2, wide)
     got = da.diffattn_decode_kv4(q.to(DEV), torch.tensor(pool).to(DEV), dev32(table), dev32([77, 300]), lam.to(DEV), 0.4,
                                  norm_weight=w.to(DEV) if weight else None, eps=1e-3, norm=norm, scale=scale)
     within(got, *kv4.decode(q, pool, table, [77, 300], lam.numpy(), 0.4, w if weight else None, 1e-3, norm, scale, slack=SLACK, floor=FLOOR))
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("lens", LENS)
 @pytest.mark.parametrize("Hkv,G,page_size", [(1, 2, 16), (2, 4, 48), (3, 8, 64), (8, 8, 16)])
-def test_v2_decode(lens, Hkv, G, page_size):
+def test_v2_decode(lens, Hkv, G, page_size, wide):
     rng = np.random.default_rng(sum(lens) * 5 + G)
     table, pool, q, lam = v2_case(rng, lens, Hkv, G, page_size)
+    table = widened(table, page_size, Hkv, wide)
     got = da.diffattn_v2_decode_kv4(q.to(DEV), torch.tensor(pool).to(DEV), dev32(table), dev32(lens), lam.to(DEV))
     within(got, *kv4.v2_decode(q, pool, table, lens, lam.numpy(), slack=SLACK, floor=FLOOR))
     for b, n in enumerate(lens):
@@ -398,10 +413,16 @@ def test_v2_decode(lens, Hkv, G, page_size):
     da.diffattn_device_status()
 
 
-def both(rng, lens, page_size, std=1.0, heads=2, spare=2, width=None):
+@pytest.fixture(params=["by row", "by range"])
+def wide(request):
+    return request.param == "by range"
+
+
+def both(rng, lens, page_size, wide, std=1.0, heads=2, spare=2, width=None):
     """The two decodes as (name, call(pool, table, lens, q) -> out, reference(...), q, pool, table)."""
     t1, p1, q1, l1, w1 = v1_case(rng, lens, heads, page_size, std, spare, width)
     t2, p2, q2, l2 = v2_case(rng, lens, heads, 8, page_size, std, spare, width)
+    t1, t2 = widened(t1, page_size, heads, wide), widened(t2, page_size, heads, wide)
     D1, D2, W1 = l1.to(DEV), l2.to(DEV), w1.to(DEV)
     dev = lambda x: x.to(DEV) if isinstance(x, torch.Tensor) else torch.tensor(x).to(DEV)  # noqa: E731
     v1 = lambda q, pool, table, lens, **k: da.diffattn_decode_kv4(dev(q), dev(pool), dev32(table), dev32(lens), D1, 0.4, norm_weight=W1, **k)  # noqa: E731
@@ -411,31 +432,31 @@ def both(rng, lens, page_size, std=1.0, heads=2, spare=2, width=None):
     return [("v1", v1, r1, q1, p1, t1), ("v2", v2, r2, q2, p2, t2)]
 
 
-def test_decode_many_sequences():
+def test_decode_many_sequences(wide):
     """More (sequence, head) pairs than blocks at once, of every length up to 40."""
     lens = [i % 41 for i in range(700)]
-    for name, call, want, q, pool, table in both(np.random.default_rng(41), lens, 16, heads=2):
+    for name, call, want, q, pool, table in both(np.random.default_rng(41), lens, 16, wide, heads=2):
         within(call(q, pool, table, lens), *want(q, pool, table, lens))
 
 
-def test_decode_long_sequence_beside_short_ones():
+def test_decode_long_sequence_beside_short_ones(wide):
     lens = [3, 20011, 0, 130]
-    for name, call, want, q, pool, table in both(np.random.default_rng(43), lens, 64, heads=1):
+    for name, call, want, q, pool, table in both(np.random.default_rng(43), lens, 64, wide, heads=1):
         within(call(q, pool, table, lens), *want(q, pool, table, lens))
 
 
-def test_decode_exponents():
+def test_decode_exponents(wide):
     lens = [100, 37]
-    for name, call, want, q, pool, table in both(np.random.default_rng(47), lens, 16):
+    for name, call, want, q, pool, table in both(np.random.default_rng(47), lens, 16, wide):
         within(call(q, pool, table, lens, k_exp=1, v_exp=-7), *want(q, pool, table, lens, k_exp=1, v_exp=-7))
 
 
 @pytest.mark.parametrize("at", [0, 17, 900, 1499])
-def test_decode_one_key_far_above_the_rest(at):
+def test_decode_one_key_far_above_the_rest(at, wide):
     """A key whose score is 30 to 100 above the others takes all of the weight, wherever it stands
     (first, where it sets the reference of all others, or last, where all before it has to shrink)."""
     lens = [1500]
-    for name, call, want, q, pool, table in both(np.random.default_rng(53), lens, 16, heads=1):
+    for name, call, want, q, pool, table in both(np.random.default_rng(53), lens, 16, wide, heads=1):
         k, v = kv4.sequence_rows(pool, 2 if name == "v1" else 1, table, 0, 1500)
         row = np.sign(to64(q)[0, 0]) * 6.0
         kp = 2 if name == "v1" else 1
@@ -444,11 +465,11 @@ def test_decode_one_key_far_above_the_rest(at):
         within(call(q, pool, table, lens), *want(q, pool, table, lens))
 
 
-def test_decode_a_first_key_that_outweighs_each_but_not_all():
+def test_decode_a_first_key_that_outweighs_each_but_not_all(wide):
     """A first key some 13 above the rest in the exponent: each of the others has 2^-19 of its
     weight, and 9000 of them together still count."""
     lens = [9000]
-    for name, call, want, q, pool, table in both(np.random.default_rng(59), lens, 64, heads=1, std=0.02):
+    for name, call, want, q, pool, table in both(np.random.default_rng(59), lens, 64, wide, heads=1, std=0.02):
         kp = 2 if name == "v1" else 1
         q = torch.ones_like(q) * 0.5
         row = np.full(128 * kp, 2.25)  # 128 * 0.5 * 2.25 / sqrt(128) = 12.7
@@ -457,11 +478,11 @@ def test_decode_a_first_key_that_outweighs_each_but_not_all():
         within(call(q, pool, table, lens), *want(q, pool, table, lens))
 
 
-def test_decode_small_and_large_queries():
+def test_decode_small_and_large_queries(wide):
     """Queries far from unit size: tiny ones (uniform weights), and ones whose largest channel is
     2^40 times the others (which then count for nothing), with keys of matching exponents."""
     lens = [333]
-    for name, call, want, q, pool, table in both(np.random.default_rng(61), lens, 32):
+    for name, call, want, q, pool, table in both(np.random.default_rng(61), lens, 32, wide):
         tiny = (q.float() * 2.0 ** -60).to(torch.bfloat16)
         within(call(tiny, pool, table, lens), *want(tiny, pool, table, lens))
         big = (q.float() * 2.0 ** 60).to(torch.bfloat16)
@@ -473,11 +494,11 @@ def test_decode_small_and_large_queries():
         within(call(zero, pool, table, lens), *want(zero, pool, table, lens))
 
 
-def test_decode_slots_past_the_end_may_hold_anything():
+def test_decode_slots_past_the_end_may_hold_anything(wide):
     """NaN scales, any codes in the rest of the last record, of the last page, and in every page of
     no sequence; table entries past a sequence's pages are never used."""
     lens = [1, 30, 64, 75]
-    for name, call, want, q, pool, table in both(np.random.default_rng(67), lens, 32, width=9):
+    for name, call, want, q, pool, table in both(np.random.default_rng(67), lens, 32, wide, width=9):
         clean = call(q, pool, table, lens)
         within(clean, *want(q, pool, table, lens))
         kp, page_size = (2 if name == "v1" else 1), 32
@@ -500,9 +521,9 @@ def test_decode_slots_past_the_end_may_hold_anything():
         da.diffattn_device_status()
 
 
-def test_decode_nan_key_reaches_its_head_alone():
+def test_decode_nan_key_reaches_its_head_alone(wide):
     lens = [50, 50]
-    for name, call, want, q, pool, table in both(np.random.default_rng(71), lens, 16):
+    for name, call, want, q, pool, table in both(np.random.default_rng(71), lens, 16, wide):
         clean = call(q, pool, table, lens)
         kp = 2 if name == "v1" else 1
         for plane in (0, 2 * kp - 1):  # a K plane and a V plane
@@ -514,9 +535,9 @@ def test_decode_nan_key_reaches_its_head_alone():
             assert torch.equal(got[0], clean[0]) and torch.equal(got[1, :per], clean[1, :per])
 
 
-def test_decode_nan_and_inf_queries():
+def test_decode_nan_and_inf_queries(wide):
     lens = [40, 40]
-    for name, call, want, q, pool, table in both(np.random.default_rng(73), lens, 16):
+    for name, call, want, q, pool, table in both(np.random.default_rng(73), lens, 16, wide):
         clean = call(q, pool, table, lens)
         for x in (float("nan"), float("inf")):
             bad = q.clone()
@@ -526,17 +547,18 @@ def test_decode_nan_and_inf_queries():
             assert torch.equal(got[0], clean[0]) and torch.equal(got[1, -1], clean[1, -1])
 
 
-def test_decode_lengths_out_of_range_are_clamped():
+def test_decode_lengths_out_of_range_are_clamped(wide):
     lens = [64, 64, 5]
-    for name, call, want, q, pool, table in both(np.random.default_rng(79), lens, 32):
-        a = call(q, pool, table, [64, 0, 5])
+    for name, call, want, q, pool, table in both(np.random.default_rng(79), lens, 32, wide):
+        table = np.maximum(table, 0)  # every entry of the capacity may be used
+        a = call(q, pool, table, [table.shape[1] * 32, 0, 5])
         b = call(q, pool, table, [10 ** 9, -4, 5])
         assert torch.equal(a, b)
 
 
-def test_decode_bad_page_reads_page_0_and_is_reported():
+def test_decode_bad_page_reads_page_0_and_is_reported(wide):
     lens = [40, 20]
-    for name, call, want, q, pool, table in both(np.random.default_rng(83), lens, 16):
+    for name, call, want, q, pool, table in both(np.random.default_rng(83), lens, 16, wide):
         for bad in (-1, pool.shape[0], 2 ** 31 - 1):
             t, z = table.copy(), table.copy()
             t[0, 1], z[0, 1] = bad, 0
@@ -548,9 +570,9 @@ def test_decode_bad_page_reads_page_0_and_is_reported():
             da.diffattn_device_status()
 
 
-def test_decode_repeats_bit_for_bit_whatever_the_workspace_holds():
+def test_decode_repeats_bit_for_bit_whatever_the_workspace_holds(wide):
     lens = [5000, 1, 777, 0, 2048]
-    for name, call, want, q, pool, table in both(np.random.default_rng(89), lens, 64):
+    for name, call, want, q, pool, table in both(np.random.default_rng(89), lens, 64, wide):
         n = (da.diffattn_decode_kv4_workspace_size(5, 2) if name == "v1" else da.diffattn_v2_decode_kv4_workspace_size(5, 16, 2))
         first = call(q, pool, table, lens)
         for fill in (0x00, 0xFF, 0x7F):
@@ -560,9 +582,9 @@ def test_decode_repeats_bit_for_bit_whatever_the_workspace_holds():
             assert bool((ws[n:] == fill).all())
 
 
-def test_decode_on_another_stream_and_in_a_graph():
+def test_decode_on_another_stream_and_in_a_graph(wide):
     lens = [300, 41]
-    for name, call, want, q, pool, table in both(np.random.default_rng(97), lens, 16):
+    for name, call, want, q, pool, table in both(np.random.default_rng(97), lens, 16, wide):
         clean = call(q, pool, table, lens)
         Q, P, T, S = q.to(DEV), torch.tensor(pool).to(DEV), dev32(table), dev32(lens)
         fn = (lambda **k: call(Q, P, table, lens, **k))
@@ -585,7 +607,7 @@ def decode_pair(name, q, pool, table, lens, lam, out, ws, w=None):
 
 
 @pytest.mark.parametrize("name", ["v1", "v2"])
-def test_decode_captured_graphs_follow_their_inputs(name):
+def test_decode_captured_graphs_follow_their_inputs(name, wide):
     """A captured decode replays on new queries, lengths, tables and rows in the captured buffers."""
     rng = np.random.default_rng(101)
     lens = [200, 64, 1]
@@ -595,6 +617,7 @@ def test_decode_captured_graphs_follow_their_inputs(name):
     else:
         (table, pool, q, lam), w = v2_case(rng, lens, 2, 4, 16, width=20), None
         n, shape = da.diffattn_v2_decode_kv4_workspace_size(3, 8, 2), (3, 4, 128)
+    table = widened(table, 16, 2, wide)
     Q, P, T, S, L = q.to(DEV), torch.tensor(pool).to(DEV), dev32(table), dev32(lens), lam.to(DEV)
     W = w.to(DEV) if w is not None else None
     out, ws = torch.zeros(shape, dtype=torch.bfloat16, device=DEV), torch.empty(n, dtype=torch.uint8, device=DEV)
@@ -617,11 +640,11 @@ def test_decode_captured_graphs_follow_their_inputs(name):
         within(out, *want(q2, t2, s2))
 
 
-def test_two_decodes_at_once():
+def test_two_decodes_at_once(wide):
     """Two streams, a workspace each: neither disturbs the other."""
     rng = np.random.default_rng(103)
     lens = [3000, 1, 900]
-    cases = both(rng, lens, 32)
+    cases = both(rng, lens, 32, wide)
     want = [c[1](c[3], c[4], c[5], lens) for c in cases]
     P = [torch.tensor(c[4]).to(DEV) for c in cases]
     Q = [c[3].to(DEV) for c in cases]
@@ -637,9 +660,9 @@ def test_two_decodes_at_once():
         assert all(torch.equal(o, want[i]) for o in outs[i])
 
 
-def test_decode_guards():
+def test_decode_guards(wide):
     lens = [90, 33, 0]
-    for name, call, want, q, pool, table in both(np.random.default_rng(107), lens, 16):
+    for name, call, want, q, pool, table in both(np.random.default_rng(107), lens, 16, wide):
         clean = call(q, pool, table, lens)
         buf = torch.full((clean.numel() + 8192,), 7.0, dtype=torch.bfloat16, device=DEV)
         out = buf[4096:4096 + clean.numel()].view(clean.shape)
