@@ -2,6 +2,7 @@
 // error reporting and dispatch to the kernels. No arithmetic of the operator happens here.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -40,6 +41,9 @@ int check_device() {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  static std::atomic<uint64_t> known{0};  // devices found to be sm_103 (a bit each): asked once
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (known.load(std::memory_order_relaxed) & bit) return DIFFATTN_OK;
   int major = 0, minor = 0;
   e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
@@ -47,6 +51,7 @@ int check_device() {
   if (major != 10 || minor != 3)
     return fail(DIFFATTN_ERR_UNSUPPORTED, "device %d is sm_%d%d; this library is built for sm_103a",
                 dev, major, minor);
+  known.fetch_or(bit, std::memory_order_relaxed);
   return DIFFATTN_OK;
 }
 

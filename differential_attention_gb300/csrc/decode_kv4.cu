@@ -52,9 +52,10 @@ constexpr float kMoveRef = 14.f;                 // log2 P at which the referenc
 
 template <int KP>
 struct Cfg {
-  static constexpr int kWarps = 4;               // consumer warps
+  static constexpr int kWarps = 4;               // consumer warps (an even number, at least 4)
   static constexpr int kThreads = (kWarps + 1) * 32;  // and a producer
   static constexpr int kRecs = 2;                // records of a tile for each of them
+  static constexpr int kJoint = KP == 1 ? 2 : 2; // of these, taken together
   static constexpr int kTileRecs = kWarps * kRecs;
   static constexpr int kTileKeys = 16 * kTileRecs;
   static constexpr int kCtas = KP == 1 ? 3 : 2;  // blocks of an SM
@@ -143,17 +144,14 @@ __device__ __forceinline__ long long div(long long x, long long y) {
   if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
   return x / y;
 }
-// 0 .. total cut in n parts whose lengths differ by at most one: the first `more` have len + 1
+// 0 .. total cut in n equal parts
 struct Cut {
-  long long len;
-  int n, more;
-  __device__ __forceinline__ Cut(long long total, int parts) : len(div(total, parts)), n(parts), more(static_cast<int>(total - len * parts)) {}
-  __device__ __forceinline__ long long start(int i) const { return len * i + min(i, more); }
-  // the part that holds x < total (len > 0)
-  __device__ __forceinline__ int owner(long long x) const {
-    const long long head = (len + 1) * more;
-    return static_cast<int>(x < head ? div(x, len + 1) : more + div(x - head, len));
-  }
+  long long total;
+  int n;
+  __device__ __forceinline__ Cut(long long total_, int n_) : total(total_), n(n_) {}
+  __device__ __forceinline__ long long start(int i) const { return div(total * i, n); }
+  // the last part that begins at or before x < total: the largest i with total i / n < x + 1
+  __device__ __forceinline__ int owner(long long x) const { return static_cast<int>(div((x + 1) * n - 1, total)); }
 };
 
 // The batch's rows one behind the other, cut in n equal parts. pre[i]: the costs (of one head) before
@@ -292,7 +290,7 @@ __device__ __forceinline__ float norm_scale(const Kv4DecodeArgs& a, float ss, fl
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
     if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = ss;
-    named_barrier_sync(1, 128);
+    named_barrier_sync(2, 128);
     ss = (s_red[0] + s_red[1]) + (s_red[2] + s_red[3]);
     f = 1.f / sqrtf(ss / 256.f + a.eps);
   }
@@ -311,7 +309,7 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, Cfg<KP>::kCtas) kv4_decode_
   __shared__ float s_m[2][kWarps][8], s_l[2][kWarps][8];
   __shared__ float s_red[kWarps];
   const Kv4DecodeArgs& a = p.a;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const uint32_t ring = smem_u32(smem), bar0 = smem_u32(bars);
   auto full = [&](int s) { return bar0 + 8 * s; };
   auto empty = [&](int s) { return bar0 + 8 * (C::kStages + s); };
@@ -327,6 +325,8 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, Cfg<KP>::kCtas) kv4_decode_
     s_abort = 0;
   }
 
+  grid_wait();
+  grid_release();
   Walk w{};
   int n = 0;
   const int range = blockIdx.x;
@@ -344,7 +344,6 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, Cfg<KP>::kCtas) kv4_decode_
     s_ranges.fill(a);
     const long long total = s_ranges.total(a);
     n = s_ranges.count(total, p.grid);
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (range >= n) return;
     s_ranges.locate(a, Cut(total, n), range, w);
   }
@@ -352,25 +351,29 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, Cfg<KP>::kCtas) kv4_decode_
   if (warp == kWarps) {
     // Producer. Lane i looks up the page of record i of the next tiles of the row (32 records); the
     // lanes of a tile's records then copy one each, and lane 0 the row's query with its first tile.
+    // The next batch's pages are looked up before the copies of this one.
     constexpr int kBatch = 32 / C::kTileRecs;
     int stage = 0, issued = 0;
     uint32_t phase = 0;
-    bool alive = true;
-    bool first = true;
+    bool alive = true, first = true;
+    const int lane_rec = min(lane, kBatch * C::kTileRecs - 1);
+    auto look_up = [&](int tile) {  // the page of record tile * kTileRecs + lane, if the row has it
+      const int key = (tile * C::kTileRecs + lane_rec) * 16;
+      return key < w.len ? __ldg(a.block_table + static_cast<size_t>(w.b) * a.max_pages + key / a.page_size) : 0;
+    };
+    int page = w.todo > 0 ? look_up(w.tile) : 0;
     while (w.todo > 0 && alive) {
       const int batch = min(min(kBatch, w.tiles - w.tile), w.todo);
       const int r = w.tile * C::kTileRecs + lane, records = (w.len + 15) >> 4;
       const bool mine_ok = lane < batch * C::kTileRecs && r < records;
-      const uint8_t* src = nullptr;
-      if (mine_ok) {
-        const int key = r * 16, pi = key / a.page_size, off = key - pi * a.page_size;
-        int page = __ldg(a.block_table + static_cast<size_t>(w.b) * a.max_pages + pi);
-        if (page < 0 || page >= a.num_pages) {
-          flag_device_error(DEV_BAD_INDEX);
-          page = 0;
-        }
-        src = a.pool + ((static_cast<size_t>(page) * a.H + w.h) * (a.page_size >> 4) + (off >> 4)) * C::kRecord;
+      if (mine_ok && (page < 0 || page >= a.num_pages)) {
+        flag_device_error(DEV_BAD_INDEX);
+        page = 0;
       }
+      const int off = r * 16 % a.page_size;
+      const uint8_t* src =
+          a.pool + ((static_cast<size_t>(page) * a.H + w.h) * (a.page_size >> 4) + (off >> 4)) * C::kRecord;
+      if (w.tile + batch < w.tiles) page = look_up(w.tile + batch);
       for (int i = 0; i < batch; ++i) {
         if (!__all_sync(0xffffffffu, mbar_wait(empty(stage), phase ^ 1, &s_abort))) {
           alive = false;
@@ -398,6 +401,7 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, Cfg<KP>::kCtas) kv4_decode_
       if (!kByRow && w.tile == w.tiles) {
         next_row<KP>(a, w);
         first = true;
+        if (w.todo > 0) page = look_up(w.tile);
       }
     }
     if (!alive) {
@@ -452,7 +456,10 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, Cfg<KP>::kCtas) kv4_decode_
     cs0 = __shfl_sync(0xffffffffu, down, 8 * t);
     cs1 = __shfl_sync(0xffffffffu, down, 8 * t + 4);
   };
-  auto wait = [&]() { alive = __all_sync(0xffffffffu, alive && mbar_wait(full(stage), phase, &s_abort)); };
+  auto wait = [&]() {
+    if (__all_sync(0xffffffffu, mbar_try_wait(full(stage), phase))) return;
+    alive = __all_sync(0xffffffffu, alive && mbar_wait(full(stage), phase, &s_abort));
+  };
 
   // empty places in the batch get zeros
   for (int b = range; !kByRow && b < a.B; b += n)
@@ -475,12 +482,15 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, Cfg<KP>::kCtas) kv4_decode_
     for (int i = 0; i < seg; ++i) {
       if (i > 0) wait();
       // record w + 4 k of the tile is warp w's; `left`: keys from its first one on
-      const int left = w.len - ((w.tile + i) * C::kTileRecs + warp) * 16;
-      if (alive && left > 0) {
-        const uint32_t rec = ring + stage * C::kStage + warp * C::kRecord + lane * 16;
-        float y[C::kRecs][4];
+      constexpr int R = C::kJoint;
+#pragma unroll 1
+      for (int q0 = 0; q0 < C::kRecs; q0 += R) {
+        const int left = w.len - ((w.tile + i) * C::kTileRecs + q0 * kWarps + warp) * 16;
+        if (!alive || left <= 0) break;
+        const uint32_t rec = ring + stage * C::kStage + (q0 * kWarps + warp) * C::kRecord + lane * 16;
+        float y[R][4];
 #pragma unroll
-        for (int r = 0; r < C::kRecs; ++r) {
+        for (int r = 0; r < R; ++r) {
           const uint32_t at = rec + r * kWarps * C::kRecord;
           if constexpr (KP == 1) {
             scores(y[r], at, lane, qf);
@@ -491,12 +501,12 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, Cfg<KP>::kCtas) kv4_decode_
             y[r][0] = s1[0], y[r][1] = s2[1], y[r][2] = s1[2], y[r][3] = s2[3];
           }
         }
-        uint32_t keep[C::kRecs];
+        uint32_t keep[R];
 #pragma unroll
-        for (int r = 0; r < C::kRecs; ++r) keep[r] = 0xffffffffu;
-        if (left < 16 * (1 + (C::kRecs - 1) * kWarps)) {  // the last tile: keys past the end
+        for (int r = 0; r < R; ++r) keep[r] = 0xffffffffu;
+        if (left < 16 * (1 + (R - 1) * kWarps)) {  // the last tile: keys past the end
 #pragma unroll
-          for (int r = 0; r < C::kRecs; ++r) {
+          for (int r = 0; r < R; ++r) {
             const int live = left - r * kWarps * 16 - 4 * t;
             keep[r] = live >= 4 ? 0xffffffffu : live <= 0 ? 0u : 0xffffffffu >> (32 - 8 * live);
             const int key = r * kWarps * 16 + (g >> 1) * 4 + (g & 1);
@@ -505,9 +515,9 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, Cfg<KP>::kCtas) kv4_decode_
           }
         }
         // exponents against the reference; it moves where one passes kMoveRef
-        float e[C::kRecs][4], top = -INFINITY;
+        float e[R][4], top = -INFINITY;
 #pragma unroll
-        for (int r = 0; r < C::kRecs; ++r) {
+        for (int r = 0; r < R; ++r) {
           e[r][0] = fmaf(y[r][0], cs0, -m0), e[r][1] = fmaf(y[r][1], cs1, -m1);
           e[r][2] = fmaf(y[r][2], cs0, -m0), e[r][3] = fmaf(y[r][3], cs1, -m1);
           top = fmaxf(top, fmaxf(fmaxf(e[r][0], e[r][1]), fmaxf(e[r][2], e[r][3])));
@@ -515,7 +525,7 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, Cfg<KP>::kCtas) kv4_decode_
         if (__any_sync(0xffffffffu, top > kMoveRef)) {
           float n0 = -FLT_MAX, n1 = -FLT_MAX;
 #pragma unroll
-          for (int r = 0; r < C::kRecs; ++r) {
+          for (int r = 0; r < R; ++r) {
             n0 = fmaxf(n0, fmaxf(y[r][0] * cs0, y[r][2] * cs0));
             n1 = fmaxf(n1, fmaxf(y[r][1] * cs1, y[r][3] * cs1));
           }
@@ -531,13 +541,13 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, Cfg<KP>::kCtas) kv4_decode_
 #pragma unroll
           for (int j = 0; j < KP * 8; ++j) o[j][0] *= f0, o[j][1] *= f1, o[j][2] *= f0, o[j][3] *= f1;
 #pragma unroll
-          for (int r = 0; r < C::kRecs; ++r) {
+          for (int r = 0; r < R; ++r) {
             e[r][0] = fmaf(y[r][0], cs0, -m0), e[r][1] = fmaf(y[r][1], cs1, -m1);
             e[r][2] = fmaf(y[r][2], cs0, -m0), e[r][3] = fmaf(y[r][3], cs1, -m1);
           }
         }
 #pragma unroll
-        for (int r = 0; r < C::kRecs; ++r) {
+        for (int r = 0; r < R; ++r) {
           const float p00 = ex2_approx(e[r][0]), p01 = ex2_approx(e[r][1]);
           const float p10 = ex2_approx(e[r][2]), p11 = ex2_approx(e[r][3]);
           l0 += p00 + p10;
@@ -592,17 +602,20 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, Cfg<KP>::kCtas) kv4_decode_
         *at = make_float2(v.x + x, v.y + y);
       });
     named_barrier_sync(1, kWarps * 32);
-    // thread `tid` takes channel tid (V1: and tid + 128) of every column
+    // thread `tid` < 128 takes channel tid (V1: and tid + 128) of every column
+    const int last_parity = parity;
+    parity ^= 1;
+    if (tid < 128) {
     float sum[C::kMaxCols][KP], l[C::kMaxCols], top[C::kMaxCols];
 #pragma unroll
     for (int c = 0; c < C::kMaxCols; ++c) {
-      float mx = s_m[parity][0][c];
+      float mx = s_m[last_parity][0][c];
 #pragma unroll
-      for (int i = 1; i < kWarps; ++i) mx = fmaxf(mx, s_m[parity][i][c]);
+      for (int i = 1; i < kWarps; ++i) mx = fmaxf(mx, s_m[last_parity][i][c]);
       top[c] = mx;
       l[c] = 0.f;
 #pragma unroll
-      for (int i = 0; i < kWarps; ++i) l[c] += s_l[parity][i][c] * ex2_approx(s_m[parity][i][c] - mx);
+      for (int i = 0; i < kWarps; ++i) l[c] += s_l[last_parity][i][c] * ex2_approx(s_m[last_parity][i][c] - mx);
 #pragma unroll
       for (int k = 0; k < KP; ++k) {
         sum[c][k] = 0.f;
@@ -610,7 +623,6 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, Cfg<KP>::kCtas) kv4_decode_
         for (int i = 0; i < kWarps / 2; ++i) sum[c][k] += s_o[(i * C::kMaxCols + c) * C::kPitch + k * 128 + tid];
       }
     }
-    parity ^= 1;
     const size_t row = static_cast<size_t>(w.b) * a.H + w.h;
     if constexpr (kByRow) {
 #pragma unroll
@@ -652,6 +664,7 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, Cfg<KP>::kCtas) kv4_decode_
         const float wgt = (a.flags & 2) && a.norm_w ? __ldg(a.norm_w + k * 128 + tid) : 1.f;
         static_cast<__nv_bfloat16*>(a.out)[row * C::kWidth + k * 128 + tid] = __float2bfloat16_rn(y[k] * f * wgt);
       }
+    }
     }
     w.todo -= seg;
     w.tile += seg;
@@ -715,23 +728,26 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const Params p
   __shared__ float s_red[W / 32];
   const Kv4DecodeArgs& a = p.a;
   const int i = blockIdx.x + 1, tid = threadIdx.x;
-  // (all but the pieces is known before the first kernel ends)
+  // (All but the pieces is known before the first kernel ends: it released this one after its own wait, so
+  // the lengths are there.)
   __shared__ Ranges<KP, kMergeThreads> s_ranges;
   __shared__ Walk s_walk;
   s_ranges.fill(a);
   const long long total = s_ranges.total(a);
   const int n = s_ranges.count(total, p.grid);
-  if (i >= n) return;
   const Cut cut(total, n);
-  if (tid < 32) {
+  if (i < n && tid < 32) {
     Walk w;
     s_ranges.locate(a, cut, i, w);
     if (tid == 0) s_walk = w;
   }
   __syncthreads();
   const Walk d = s_walk;
-  if (d.tile == 0) return;
-  if (cut.start(i - 1) > d.first) return;
+  if (i >= n || d.tile == 0 || cut.start(i - 1) > d.first) {
+    grid_wait();
+    grid_release();
+    return;
+  }
   const int pieces = cut.owner(d.first + d.tiles - 1) - (i - 1) + 1;
   const int cols = p.cols;
   const int lanes = cols * (W / 4), groups = kMergeThreads / lanes;  // a float4 of all columns' outputs each
@@ -742,7 +758,8 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const Params p
   const bool mine = tid < cols / 2 * W;
   const float lam = !mine ? 0.f : KP == 2 ? __ldg(a.lambda + d.h) : 1.f / (1.f + __expf(-__ldg(a.lam_logit + row * (cols / 2) + pair)));
   const float wgt = KP == 2 && mine && (a.flags & 2) && a.norm_w ? __ldg(a.norm_w + ch) : 1.f;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  grid_wait();
+  grid_release();
   float m = -FLT_MAX, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
@@ -813,38 +830,16 @@ cudaError_t launch(const Kv4DecodeArgs& a, cudaStream_t st) {
     while (p.grid < 8 && p.grid * 2 < tiles && rows * p.grid * 2 <= C::kGrid) p.grid *= 2;
     cudaError_t e = raise_smem(reinterpret_cast<const void*>(kv4_decode_kernel<KP, true>), C::kSmem, raised[1]);
     if (e != cudaSuccess) return e;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = p.grid;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(rows * p.grid));
-    cfg.blockDim = dim3(C::kThreads);
-    cfg.dynamicSmemBytes = C::kSmem;
-    cfg.stream = st;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kv4_decode_kernel<KP, true>, p);
+    return launch_early(kv4_decode_kernel<KP, true>, static_cast<unsigned>(rows * p.grid), C::kThreads, C::kSmem, st, p.grid, p);
   }
   cudaError_t e = raise_smem(reinterpret_cast<const void*>(kv4_decode_kernel<KP, false>), C::kSmem, raised[0]);
   if (e != cudaSuccess) return e;
   // no more blocks than the tables' capacity can give ranges
   const long long most = (tiles + C::kRowCost) * rows / C::kMinCost;
   p.grid = static_cast<int>(most < 1 ? 1 : most > C::kGrid ? C::kGrid : most);
-  kv4_decode_kernel<KP, false><<<p.grid, C::kThreads, C::kSmem, st>>>(p);
-  e = cudaGetLastError();
+  e = launch_early(kv4_decode_kernel<KP, false>, p.grid, C::kThreads, C::kSmem, st, 1, p);
   if (e != cudaSuccess || p.grid == 1) return e;
-  // the merge's blocks find their rows while the last ranges end (they wait for the results)
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(p.grid - 1);
-  cfg.blockDim = dim3(kMergeThreads);
-  cfg.stream = st;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv4_merge_kernel<KP>, p);
+  return launch_early(kv4_merge_kernel<KP>, p.grid - 1, kMergeThreads, 0, st, 1, p);
 }
 
 }  // namespace

@@ -310,6 +310,26 @@ inline cudaError_t raise_smem(const void* kernel, int bytes, std::atomic<uint64_
   return e;
 }
 
+// Launches a kernel that calls grid_wait() first: it is set up while the one before it in the stream ends.
+template <typename P, typename... A>
+inline cudaError_t launch_early(void (*kernel)(P, A...), unsigned grid, int block, int smem, cudaStream_t st, int cluster,
+                                const P& p, A... more) {
+  cudaLaunchAttribute at[2] = {};
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p, more...);
+}
+
 // The 4-bit cache (kv4_rows.cu, decode_kv4.cu). Pools: [num_pages, H, page_size / 16, record], a
 // record 16 tokens of one head: kp K planes and vp V planes of 128 channels (kv4.cuh).
 struct Kv4AppendArgs {

@@ -50,6 +50,8 @@ __device__ __forceinline__ Block round_block(const uint4& w0, const uint4& w1, f
 // bounds it: the bytes (2 read, 9/16 written a channel).
 template <int KP>
 __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const Kv4AppendArgs a) {
+  grid_wait();
+  grid_release();
   const int lane = threadIdx.x & 31;
   const long long u = static_cast<long long>(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
   const int h = static_cast<int>(u % a.H);
@@ -138,6 +140,8 @@ __device__ __forceinline__ uint32_t half2_to_bf16x2(uint32_t h, float f) {
 // so that the ranges do not overlap, whatever the sequences' first tokens are.
 template <int KP>
 __global__ void __launch_bounds__(kRowThreads) kv4_gather_kernel(const Kv4GatherArgs a, int heads) {
+  grid_wait();
+  grid_release();
   const int lane = threadIdx.x & 31;
   const long long i = static_cast<long long>(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
   const int groups = (a.H + heads - 1) / heads, h0 = static_cast<int>(i % groups) * heads;
@@ -230,9 +234,7 @@ cudaError_t launch_kv4_append(const Kv4AppendArgs& a, cudaStream_t st) {
   if (a.total == 0) return cudaSuccess;
   const long long warps = (static_cast<long long>(a.total) + 7) / 8 * a.H;
   const unsigned blocks = static_cast<unsigned>((warps * 32 + kRowThreads - 1) / kRowThreads);
-  if (a.kp == 1) kv4_append_kernel<1><<<blocks, kRowThreads, 0, st>>>(a);
-  else kv4_append_kernel<2><<<blocks, kRowThreads, 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_early(a.kp == 1 ? kv4_append_kernel<1> : kv4_append_kernel<2>, blocks, kRowThreads, 0, st, 1, a);
 }
 
 cudaError_t launch_kv4_gather(const Kv4GatherArgs& a, cudaStream_t st) {
@@ -244,9 +246,7 @@ cudaError_t launch_kv4_gather(const Kv4GatherArgs& a, cudaStream_t st) {
   while (heads > 1 && units * ((a.H + heads - 1) / heads) < 2 * 152 * 24) heads >>= 1;
   const long long warps = units * ((a.H + heads - 1) / heads);
   const unsigned blocks = static_cast<unsigned>((warps * 32 + kRowThreads - 1) / kRowThreads);
-  if (a.kp == 1) kv4_gather_kernel<1><<<blocks, kRowThreads, 0, st>>>(a, heads);
-  else kv4_gather_kernel<2><<<blocks, kRowThreads, 0, st>>>(a, heads);
-  return cudaGetLastError();
+  return launch_early(a.kp == 1 ? kv4_gather_kernel<1> : kv4_gather_kernel<2>, blocks, kRowThreads, 0, st, 1, a, heads);
 }
 
 cudaError_t status_kv4_rows(int* v) { return read_clear_status(v); }

@@ -69,6 +69,8 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanPara
   const bool lead = blockIdx.x == 0;
   const int ps = p.page_size;
   const long long cap = static_cast<long long>(p.max_pages) * ps;
+  grid_wait();
+  grid_release();
   const int head = p.state[0], count = p.state[1];
   bool bad = head < 0 || head >= p.num_pages || count < 0 || count > p.num_pages;
 
@@ -217,18 +219,7 @@ cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t st) {
   const int work = a.total_max > a.B ? a.total_max : a.B;
   int blocks = 1;
   while (blocks < kPlanCluster && blocks * 2 * kPlanThreads < work) blocks *= 2;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = blocks;
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(blocks);
-  cfg.blockDim = dim3(kPlanThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_plan_kernel, p);
+  return launch_early(paged_plan_kernel, blocks, kPlanThreads, smem, st, blocks, p);
 }
 
 cudaError_t status_paged_plan(int* v) { return read_clear_status(v); }

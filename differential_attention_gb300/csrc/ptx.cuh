@@ -181,6 +181,15 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float a) {
 }
 
 // ---------------------------------------------------------------------------------------------
+// programmatic launches (a kernel set up while the one before it in the stream still runs)
+// ---------------------------------------------------------------------------------------------
+// Until the kernels before this one are done and their writes seen. Every block of a kernel that is
+// launched this way calls it, also one that has nothing to do: the kernel after it goes by that.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// From here on (in all blocks) the kernel after this one may be set up. After grid_wait().
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// ---------------------------------------------------------------------------------------------
 // TMA
 // ---------------------------------------------------------------------------------------------
 __device__ __forceinline__ void tma_load_4d(uint32_t smem_dst, const void* tmap, uint32_t bar,
