@@ -1539,31 +1539,34 @@ def _index(name, t) -> int:
     return t.get_device()
 
 
-def _call(index, fn, *args, stream=None):
-    """fn(*args, stream) with device `index` current; `stream` None is that device's current stream."""
-    raw = _raw_stream(index) if stream is None else _stream(stream).value or 0
+def _call(index, fn, *args):
+    """fn(*args, stream) on device `index` and its current stream."""
     if index == torch._C._cuda_getDevice():
-        rc = fn(*args, raw)
+        rc = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
-            rc = fn(*args, raw)
+            rc = fn(*args, _raw_stream(index))
     if rc != DIFFATTN_OK:
         _check(rc)
+
+
+def _current(stream, index):
+    """A context in which `stream` (a torch stream or a raw handle) is the current one: a call on
+    another stream also takes its output and its scratch from that stream's memory, where nothing
+    that still runs on the caller's stream can reuse them."""
+    if not isinstance(stream, torch.cuda.Stream):
+        raw = _stream(stream).value or 0
+        stream = torch.cuda.ExternalStream(raw, device=index) if raw else torch.cuda.default_stream(index)
+    return torch.cuda.stream(stream)
 
 
 _scratch = threading.local()
 
 
-def _workspace(index, n, stream):
+def _workspace(index, n):
     """Scratch of n bytes for one call. Calls that one thread makes on one stream run one after the
-    other, so they share a buffer, which the thread keeps. A call that is being captured gets its
-    own (the graph may replay on any stream), and so does one on a stream that is not the current
-    one, to which the allocator is told to leave the buffer until the call is done."""
-    if stream is not None:
-        ws = torch.empty(n, dtype=torch.uint8, device=torch.device("cuda", index))
-        ws.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
-                         torch.cuda.ExternalStream(_stream(stream).value or 0, device=index))
-        return ws
+    other, so they share a buffer, which the thread keeps; a call that is being captured gets its
+    own, as its graph may replay on any stream."""
     if index != torch._C._cuda_getDevice() or torch._C._cuda_isCurrentStreamCapturing():
         return torch.empty(n, dtype=torch.uint8, device=torch.device("cuda", index))
     kept = _scratch.__dict__.setdefault("kept", {})
@@ -1584,6 +1587,9 @@ def diffattn_paged_plan(seqlens, new_tokens, block_table, free_ring, ring_state,
     [2] int32 = {head, count}. Returns (and, given `out`, fills) a dict of int32 tensors: seqlens
     [B], ring_state [2], cu_seqlens_q and cu_seqlens_k [B + 1], slot_map and positions [total_max].
     out["seqlens"] and out["ring_state"] may be the inputs themselves."""
+    if stream is not None:
+        with _current(stream, _index("seqlens", seqlens)):
+            return diffattn_paged_plan(seqlens, new_tokens, block_table, free_ring, ring_state, page_size, total_max, out)
     i32, dev = torch.int32, _index("seqlens", seqlens)
     B = seqlens.numel()
     if block_table.dim() != 2 or free_ring.dim() != 1:
@@ -1604,7 +1610,7 @@ def diffattn_paged_plan(seqlens, new_tokens, block_table, free_ring, ring_state,
           _operand("new_tokens", new_tokens, i32, dev, (B,)), p[0],
           _operand("block_table", block_table, i32, dev, (B, max_pages)),
           _operand("free_ring", free_ring, i32, dev), _operand("ring_state", ring_state, i32, dev, (2,)),
-          p[1], p[2], p[3], p[4], p[5], B, max_pages, num_pages, int(page_size), total_max, stream=stream)
+          p[1], p[2], p[3], p[4], p[5], B, max_pages, num_pages, int(page_size), total_max)
     return out
 
 
@@ -1642,6 +1648,9 @@ def diffattn_kv4_append(k, v, slot_map, pool, k_exp: int = 0, v_exp: int = 0, st
     """Rounds rows k [total, H, kw] and v [total, H, vw] (bf16, last dimension contiguous, otherwise
     any strides that are multiples of 8 elements) to 4 bits and writes row i at slot slot_map[i]
     (int32 [total]; -1: not at all) of every head of `pool`."""
+    if stream is not None:
+        with _current(stream, _index("k", k)):
+            return diffattn_kv4_append(k, v, slot_map, pool, k_exp, v_exp)
     dev = _index("k", k)
     _index("v", v)
     if k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16 or k.dim() != 3 or v.dim() != 3:
@@ -1660,7 +1669,7 @@ def diffattn_kv4_append(k, v, slot_map, pool, k_exp: int = 0, v_exp: int = 0, st
     at, num_pages, page_size = _kv4_pool(pool, dev, H, kw, vw)
     _call(dev, lib().diffattn_kv4_append, k.data_ptr(), v.data_ptr(), (ctypes.c_longlong * 4)(kt, kh, vt, vh),
           _operand("slot_map", slot_map, torch.int32, dev, (total,)), at, total, H, kw, vw, num_pages,
-          page_size, int(k_exp), int(v_exp), stream=stream)
+          page_size, int(k_exp), int(v_exp))
 
 
 def diffattn_kv4_gather(pool, block_table, cu_seqlens, total: int, kw: int, vw: int, starts=None,
@@ -1668,6 +1677,9 @@ def diffattn_kv4_gather(pool, block_table, cu_seqlens, total: int, kw: int, vw: 
     """Cached rows as packed bf16: (k [total, H, kw], v [total, H, vw]), row cu_seqlens[b] + i being
     token starts[b] + i (starts int32 [B]; None: 0) of sequence b. Without `out` = (k, v), rows
     behind the last sequence are not initialised."""
+    if stream is not None:
+        with _current(stream, _index("pool", pool)):
+            return diffattn_kv4_gather(pool, block_table, cu_seqlens, total, kw, vw, starts, k_exp, v_exp, out)
     dev = _index("pool", pool)
     B = cu_seqlens.numel() - 1
     if pool.dim() != 4:
@@ -1684,7 +1696,7 @@ def diffattn_kv4_gather(pool, block_table, cu_seqlens, total: int, kw: int, vw: 
           None if starts is None else _operand("starts", starts, torch.int32, dev, (B,)),
           _operand("out[0]", k, torch.bfloat16, dev, (max(0, total), H, kw)),
           _operand("out[1]", v, torch.bfloat16, dev, (max(0, total), H, vw)), total, B, H, kw, vw, num_pages,
-          page_size, max_pages, int(k_exp), int(v_exp), stream=stream)
+          page_size, max_pages, int(k_exp), int(v_exp))
     return k, v
 
 
@@ -1700,6 +1712,10 @@ def diffattn_decode_kv4(q, pool, block_table, seqlens, lam, lambda_init: float =
                         k_exp: int = 0, v_exp: int = 0, workspace=None, out=None, stream=None):
     """V1 decode over a 4-bit pool [num_pages, H, page_size / 16, 4608]: q [B, H, 256], block_table
     [B, max_pages] int32, seqlens [B] int32 (0: no keys, a row of zeros)."""
+    if stream is not None:
+        with _current(stream, _index("q", q)):
+            return diffattn_decode_kv4(q, pool, block_table, seqlens, lam, lambda_init, norm_weight, eps, norm, scale,
+                                       k_exp, v_exp, workspace, out)
     dev = _index("q", q)
     if q.dim() != 3:
         raise ValueError("q must be [B, H, 2d]")
@@ -1707,7 +1723,7 @@ def diffattn_decode_kv4(q, pool, block_table, seqlens, lam, lambda_init: float =
     at, num_pages, page_size = _kv4_pool(pool, dev, H, two_d, two_d)
     table, max_pages = _kv4_table(block_table, dev, B)
     if workspace is None:
-        workspace = _workspace(dev, diffattn_decode_kv4_workspace_size(B, H, two_d // 2, two_d), stream)
+        workspace = _workspace(dev, diffattn_decode_kv4_workspace_size(B, H, two_d // 2, two_d))
     if out is None:
         out = torch.empty_like(q)
     flags = (DIFFATTN_NORM if norm else 0) | (DIFFATTN_SCALE if scale else 0)
@@ -1716,8 +1732,7 @@ def diffattn_decode_kv4(q, pool, block_table, seqlens, lam, lambda_init: float =
           _operand("lam", lam, torch.float32, dev, (H,)), lambda_init,
           None if norm_weight is None else _operand("norm_weight", norm_weight, torch.float32, dev, (two_d,)),
           eps, B, H, two_d // 2, two_d, num_pages, page_size, max_pages, int(k_exp), int(v_exp), flags,
-          _operand("workspace", workspace, workspace.dtype, dev), workspace.numel() * workspace.element_size(),
-          stream=stream)
+          _operand("workspace", workspace, workspace.dtype, dev), workspace.numel() * workspace.element_size())
     return out
 
 
@@ -1733,6 +1748,9 @@ def diffattn_v2_decode_kv4(q, pool, block_table, seqlens, lam_logit, k_exp: int 
     """DIFF V2 decode over a 4-bit pool [num_pages, Hkv, page_size / 16, 2304]: q [B, Hq, 128],
     block_table [B, max_pages] int32, seqlens [B] int32 (0: no keys, rows of zeros), lam_logit
     [B, Hq/2] fp32. Returns [B, Hq/2, 128]."""
+    if stream is not None:
+        with _current(stream, _index("q", q)):
+            return diffattn_v2_decode_kv4(q, pool, block_table, seqlens, lam_logit, k_exp, v_exp, workspace, out)
     dev = _index("q", q)
     if q.dim() != 3 or pool.dim() != 4:
         raise ValueError("q must be [B, Hq, d] and pool [num_pages, Hkv, page_size / 16, record]")
@@ -1741,7 +1759,7 @@ def diffattn_v2_decode_kv4(q, pool, block_table, seqlens, lam_logit, k_exp: int 
     at, num_pages, page_size = _kv4_pool(pool, dev, Hkv, d, d)
     table, max_pages = _kv4_table(block_table, dev, B)
     if workspace is None:
-        workspace = _workspace(dev, diffattn_v2_decode_kv4_workspace_size(B, Hq, Hkv, d), stream)
+        workspace = _workspace(dev, diffattn_v2_decode_kv4_workspace_size(B, Hq, Hkv, d))
     if out is None:
         out = q.new_empty((B, Hq // 2, d))
     _call(dev, lib().diffattn_v2_decode_kv4, _operand("q", q, torch.bfloat16, dev), at, table,
@@ -1749,5 +1767,5 @@ def diffattn_v2_decode_kv4(q, pool, block_table, seqlens, lam_logit, k_exp: int 
           _operand("lam_logit", lam_logit, torch.float32, dev, (B, Hq // 2)),
           _operand("out", out, torch.bfloat16, dev, (B, Hq // 2, d)), B, Hq, Hkv, d, num_pages, page_size,
           max_pages, int(k_exp), int(v_exp), 0, _operand("workspace", workspace, workspace.dtype, dev),
-          workspace.numel() * workspace.element_size(), stream=stream)
+          workspace.numel() * workspace.element_size())
     return out

@@ -28,9 +28,9 @@
 // Work. The rows, one after the other, are cut into equal ranges, one for each resident block, whatever
 // the sequences' lengths; a row counts its tiles and a fixed cost. A block walks its range: a row that
 // lies in it whole is finished there; the pieces of one that does not go to the workspace, at most
-// two a block, and the second kernel merges them, in the order of the ranges. Where the tables hold so
-// few keys that a block would get no more than kFewTiles tiles, a row is cut over the blocks of a
-// cluster instead, which join through each other's shared memory: one launch, no workspace. (Tried and dropped, V2
+// two a block, and the second kernel merges them, in the order of the ranges. Where the tables hold few
+// keys for each resident block, a row is cut over the blocks of a cluster instead, which join through
+// each other's shared memory: one launch, no workspace. (Tried and dropped, V2
 // with lengths of 1 to 16K, 52 us as it is: two ranges a block, the second taken over by cluster launch
 // control, 58 us, as each range adds pieces; the last block of a row merging it, without a second
 // kernel, 60 us, as the blocks wait for their fence and their count.)
@@ -359,7 +359,8 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, Cfg<KP>::kCtas) kv4_decode_
     const int lane_rec = min(lane, kBatch * C::kTileRecs - 1);
     auto look_up = [&](int tile) {  // the page of record tile * kTileRecs + lane, if the row has it
       const int key = (tile * C::kTileRecs + lane_rec) * 16;
-      return key < w.len ? __ldg(a.block_table + static_cast<size_t>(w.b) * a.max_pages + key / a.page_size) : 0;
+      if (key >= w.len || !dbg_index_ok(key / a.page_size, a.max_pages)) return 0;
+      return __ldg(a.block_table + static_cast<size_t>(w.b) * a.max_pages + key / a.page_size);
     };
     int page = w.todo > 0 ? look_up(w.tile) : 0;
     while (w.todo > 0 && alive) {
@@ -717,17 +718,18 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, Cfg<KP>::kCtas) kv4_decode_
   }
 }
 
-// Merge. Block i: the row that range i begins inside, unless an earlier range does as well. Its pieces
-// are that of range i - 1 (which began the row) and of ranges i, i + 1, .. up to the row's end, always
-// in this order; groups of threads take every n-th piece, and join.
-template <int KP>
+// Merge, of each row whose tiles lie in more than one range: its pieces are that of the range that begins it
+// and of the ranges that begin inside it, always in this order; groups of threads take every n-th piece,
+// and join. Few rows: a block for each pair of columns of each row. Else: block i for the row that range
+// i + 1 begins inside, if no earlier range does, with all its columns.
+template <int KP, bool kFewRows>
 __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const Params p) {
   constexpr int W = KP * 128;
   __shared__ float s_m[kMergeThreads / 64 * 2], s_l[kMergeThreads / 64 * 2];
   __shared__ float4 s_o[kMergeThreads];
   __shared__ float s_red[W / 32];
   const Kv4DecodeArgs& a = p.a;
-  const int i = blockIdx.x + 1, tid = threadIdx.x;
+  const int tid = threadIdx.x, cols = p.cols;
   // (All but the pieces is known before the first kernel ends: it released this one after its own wait, so
   // the lengths are there.)
   __shared__ Ranges<KP, kMergeThreads> s_ranges;
@@ -736,27 +738,38 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const Params p
   const long long total = s_ranges.total(a);
   const int n = s_ranges.count(total, p.grid);
   const Cut cut(total, n);
-  if (i < n && tid < 32) {
-    Walk w;
-    s_ranges.locate(a, cut, i, w);
+  const int c0 = kFewRows ? 2 * static_cast<int>(blockIdx.x % (cols / 2)) : 0, nc = kFewRows ? 2 : cols;  // the columns
+  if (tid < 32) {
+    Walk w{};
+    if constexpr (kFewRows) {  // B <= kMergeThreads: a share of one sequence a thread
+      const int row = blockIdx.x / (cols / 2);
+      w.b = row / a.H;
+      w.h = row - w.b * a.H;
+      w.len = clamp_len(a, w.b);
+      w.tiles = tiles_of<KP>(w.len);
+      w.first = s_ranges.pre[w.b] * a.H + static_cast<long long>(w.h) * cost_of<KP>(w.len) + Cfg<KP>::kRowCost;
+    } else if (static_cast<int>(blockIdx.x) + 1 < n) {
+      s_ranges.locate(a, cut, blockIdx.x + 1, w);
+      if (w.tile == 0 || cut.start(blockIdx.x) > w.first) w.tiles = 0;  // it begins no tile inside a row, or is not the first to
+    }
     if (tid == 0) s_walk = w;
   }
   __syncthreads();
   const Walk d = s_walk;
-  if (i >= n || d.tile == 0 || cut.start(i - 1) > d.first) {
+  const int i0 = d.tiles > 0 ? cut.owner(d.first) : 0;
+  const int pieces = d.tiles > 0 ? cut.owner(d.first + d.tiles - 1) - i0 + 1 : 0;
+  if (pieces < 2) {
     grid_wait();
     grid_release();
     return;
   }
-  const int pieces = cut.owner(d.first + d.tiles - 1) - (i - 1) + 1;
-  const int cols = p.cols;
-  const int lanes = cols * (W / 4), groups = kMergeThreads / lanes;  // a float4 of all columns' outputs each
+  const int lanes = nc * (W / 4), groups = kMergeThreads / lanes;  // a float4 of all its columns' outputs each
   const size_t rec = 2 * cols + cols * W;
   const int grp = tid / lanes, ln = tid % lanes, c = ln / (W / 4);
   const size_t row = static_cast<size_t>(d.b) * a.H + d.h;
   const int pair = tid / W, ch = tid % W;  // the output channel of the end
-  const bool mine = tid < cols / 2 * W;
-  const float lam = !mine ? 0.f : KP == 2 ? __ldg(a.lambda + d.h) : 1.f / (1.f + __expf(-__ldg(a.lam_logit + row * (cols / 2) + pair)));
+  const bool mine = tid < nc / 2 * W;
+  const float lam = !mine ? 0.f : KP == 2 ? __ldg(a.lambda + d.h) : 1.f / (1.f + __expf(-__ldg(a.lam_logit + row * (cols / 2) + c0 / 2 + pair)));
   const float wgt = KP == 2 && mine && (a.flags & 2) && a.norm_w ? __ldg(a.norm_w + ch) : 1.f;
   grid_wait();
   grid_release();
@@ -764,9 +777,9 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const Params p
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (int k = grp; k < pieces; k += groups) {
-    const float* r = p.rec + (k == 0 ? static_cast<size_t>(2 * (i - 1) + 1) : static_cast<size_t>(2 * (i - 1 + k))) * rec;
-    const float mk = r[c], lk = r[cols + c];
-    const float4 ok = *reinterpret_cast<const float4*>(r + 2 * cols + ln * 4);
+    const float* r = p.rec + static_cast<size_t>(2 * (i0 + k) + (k == 0 ? 1 : 0)) * rec;
+    const float mk = r[c0 + c], lk = r[cols + c0 + c];
+    const float4 ok = *reinterpret_cast<const float4*>(r + 2 * cols + c0 * W + ln * 4);
     const float top = fmaxf(m, mk), f = ex2_approx(m - top), fk = ex2_approx(mk - top);
     m = top;
     l = l * f + lk * fk;
@@ -776,7 +789,7 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const Params p
     o.w = o.w * f + ok.w * fk;
   }
   s_o[tid] = o;
-  if (ln % (W / 4) == 0) s_m[grp * cols + c] = m, s_l[grp * cols + c] = l;
+  if (ln % (W / 4) == 0) s_m[grp * nc + c] = m, s_l[grp * nc + c] = l;
   __syncthreads();
   // an output channel: of a pair of columns, V1's only one
   if (!mine) return;
@@ -785,11 +798,11 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const Params p
   for (int e = 0; e < 2; ++e) {
     const int col = 2 * pair + e;
     float top = s_m[col];
-    for (int k = 1; k < groups; ++k) top = fmaxf(top, s_m[k * cols + col]);
+    for (int k = 1; k < groups; ++k) top = fmaxf(top, s_m[k * nc + col]);
     float sum = 0.f, ls = 0.f;
     for (int k = 0; k < groups; ++k) {
-      const float f = ex2_approx(s_m[k * cols + col] - top);
-      ls = fmaf(s_l[k * cols + col], f, ls);
+      const float f = ex2_approx(s_m[k * nc + col] - top);
+      ls = fmaf(s_l[k * nc + col], f, ls);
       sum = fmaf(reinterpret_cast<const float*>(s_o + k * lanes)[col * W + ch], f, sum);
     }
     q[e] = sum / ls;
@@ -809,7 +822,7 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const Params p
     }
     if (a.flags & 4) y *= 1.f - a.lambda_init;
   }
-  static_cast<__nv_bfloat16*>(a.out)[(row * (cols / 2) + pair) * W + ch] = __float2bfloat16_rn(y);
+  static_cast<__nv_bfloat16*>(a.out)[(row * (cols / 2) + c0 / 2 + pair) * W + ch] = __float2bfloat16_rn(y);
 }
 
 template <int KP>
@@ -819,27 +832,33 @@ cudaError_t launch(const Kv4DecodeArgs& a, cudaStream_t st) {
   p.a = a;
   p.cols = KP == 2 ? 2 : a.group;
   p.rec = static_cast<float*>(a.ws);
-  static std::atomic<uint64_t> raised[2];
+  static std::atomic<uint64_t> raised[2] = {};
   const long long tiles = (static_cast<long long>(a.max_pages) * a.page_size + C::kTileKeys - 1) / C::kTileKeys;
   const long long rows = static_cast<long long>(a.B) * a.H;
-  // Few keys: a row over a cluster, of as many blocks as leave two tiles each and are resident at once.
-  // (Measured, GPU time of a call: 8 rows of 777 keys, V2, <ROWS_V2> us so and <RANGES_V2> by ranges; 48 rows
-  // of 1500 keys, V1, <ROWS_V1> and <RANGES_V1>; the host has one launch less as well.)
-  if (rows * tiles <= static_cast<long long>(kFewTiles) * C::kGrid && rows <= C::kGrid) {
-    p.grid = 1;
-    while (p.grid < 8 && p.grid * 2 < tiles && rows * p.grid * 2 <= C::kGrid) p.grid *= 2;
-    cudaError_t e = raise_smem(reinterpret_cast<const void*>(kv4_decode_kernel<KP, true>), C::kSmem, raised[1]);
-    if (e != cudaSuccess) return e;
-    return launch_early(kv4_decode_kernel<KP, true>, static_cast<unsigned>(rows * p.grid), C::kThreads, C::kSmem, st, p.grid, p);
+  // Few keys: a row over a cluster, of as many blocks as leave it two tiles each and are resident at once;
+  // where the rows' blocks then have at most kFewTiles more tiles than an equal share. (The second kernel
+  // and the ranges cost about that. GPU time of a call so and by ranges: 8 rows of 777 keys, V2, 5.8 and
+  // 8.7 us; 400 rows of 1000, 16.2 and 21.5; 48 rows of 1500, V1, 9.9 and 12.8; 96 rows of 3000, V1, where
+  // clusters of two leave a third of the machine idle, 23.6 and 20.9. The host has one launch less as well.
+  // Only up to 8 tiles a block, as the tables' capacity is not the sequences' length.)
+  int parts = 1;
+  while (parts < 8 && parts * 2 < tiles && rows * parts * 2 <= C::kGrid) parts *= 2;
+  if (rows <= C::kGrid && rows * tiles <= 8LL * C::kGrid &&
+      (tiles + parts - 1) / parts <= rows * tiles / C::kGrid + kFewTiles) {
+    p.grid = parts;
+    return launch_early_large(kv4_decode_kernel<KP, true>, static_cast<unsigned>(rows * p.grid), C::kThreads, C::kSmem,
+                              C::kSmem, st, p.grid, p, raised[1]);
   }
-  cudaError_t e = raise_smem(reinterpret_cast<const void*>(kv4_decode_kernel<KP, false>), C::kSmem, raised[0]);
-  if (e != cudaSuccess) return e;
   // no more blocks than the tables' capacity can give ranges
   const long long most = (tiles + C::kRowCost) * rows / C::kMinCost;
   p.grid = static_cast<int>(most < 1 ? 1 : most > C::kGrid ? C::kGrid : most);
-  e = launch_early(kv4_decode_kernel<KP, false>, p.grid, C::kThreads, C::kSmem, st, 1, p);
+  cudaError_t e = launch_early_large(kv4_decode_kernel<KP, false>, p.grid, C::kThreads, C::kSmem, C::kSmem, st, 1, p, raised[0]);
   if (e != cudaSuccess || p.grid == 1) return e;
-  return launch_early(kv4_merge_kernel<KP>, p.grid - 1, kMergeThreads, 0, st, 1, p);
+  // A block for each pair of columns of each row, where those are fewer: the rows are long then, and their
+  // many pieces are read by more threads (8 rows of 16K keys, V2: 13.1 us the whole call, 18.4 the other way).
+  if (rows * (p.cols / 2) < p.grid && a.B <= kMergeThreads)
+    return launch_early(kv4_merge_kernel<KP, true>, static_cast<unsigned>(rows * (p.cols / 2)), kMergeThreads, 0, st, 1, p);
+  return launch_early(kv4_merge_kernel<KP, false>, p.grid - 1, kMergeThreads, 0, st, 1, p);
 }
 
 }  // namespace

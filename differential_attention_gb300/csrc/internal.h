@@ -298,18 +298,6 @@ long long decode_noalloc_max_units();  // largest B * H whose partials fit (one 
 int decode_noalloc_splits(int B, int Lmax, int H, int* chunk_out);  // splits the no-alloc call runs
 cudaError_t launch_decode_noalloc(const DecodeArgs& a, cudaStream_t s);
 
-// Raises a kernel's dynamic shared memory limit, once for each device (`raised`: a bit each).
-inline cudaError_t raise_smem(const void* kernel, int bytes, std::atomic<uint64_t>& raised) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-  if (raised.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess) raised.fetch_or(bit, std::memory_order_relaxed);
-  return e;
-}
-
 // Launches a kernel that calls grid_wait() first: it is set up while the one before it in the stream ends.
 template <typename P, typename... A>
 inline cudaError_t launch_early(void (*kernel)(P, A...), unsigned grid, int block, int smem, cudaStream_t st, int cluster,
@@ -328,6 +316,27 @@ inline cudaError_t launch_early(void (*kernel)(P, A...), unsigned grid, int bloc
   cfg.attrs = at;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, p, more...);
+}
+
+// launch_early of a kernel with more than 48 KB of dynamic shared memory (at most `limit`). The limit is
+// raised on each device's first call (`raised`: a bit each), and again where a launch is refused, as
+// after a reset of the device.
+template <typename P>
+inline cudaError_t launch_early_large(void (*kernel)(P), unsigned grid, int block, int smem, int limit, cudaStream_t st,
+                                      int cluster, const P& p, std::atomic<uint64_t>& raised) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (raised.load(std::memory_order_relaxed) & bit) {
+    e = launch_early(kernel, grid, block, smem, st, cluster, p);
+    if (e != cudaErrorInvalidValue) return e;
+    cudaGetLastError();
+  }
+  e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, limit);
+  if (e != cudaSuccess) return e;
+  raised.fetch_or(bit, std::memory_order_relaxed);
+  return launch_early(kernel, grid, block, smem, st, cluster, p);
 }
 
 // The 4-bit cache (kv4_rows.cu, decode_kv4.cu). Pools: [num_pages, H, page_size / 16, record], a

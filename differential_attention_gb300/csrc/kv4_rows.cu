@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kRowThreads) kv4_gather_kernel(const Kv4Gather
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int key = 2 * i + hi;
-      if (tok + key < first || tok + key >= end) continue;
+      if (tok + key < first || tok + key >= end || !dbg_index_ok(row0 + key, a.total)) continue;
       const float s = e4m3_to_float((x.scales[i >> 1] >> (shift + 16 * (i & 1))) & 0xffu) * mul;
       uint32_t v[4];
       e2m1x8_to_half2(x.codes[i], v);

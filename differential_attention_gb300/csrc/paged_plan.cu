@@ -212,14 +212,12 @@ cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t st) {
                a.B, a.max_pages, a.num_pages, a.page_size, a.total_max};
   const int smem = (4 * a.B + 3) * static_cast<int>(sizeof(int));
   static_assert((4 * kPlanMaxRequests + 3) * 4 <= 200 * 1024, "shared memory");
-  static std::atomic<uint64_t> raised{0};
-  const cudaError_t e = raise_smem(reinterpret_cast<const void*>(paged_plan_kernel), (4 * kPlanMaxRequests + 3) * 4, raised);
-  if (e != cudaSuccess) return e;
   // blocks for the slots and the requests, about two rounds of their threads each
   const int work = a.total_max > a.B ? a.total_max : a.B;
   int blocks = 1;
   while (blocks < kPlanCluster && blocks * 2 * kPlanThreads < work) blocks *= 2;
-  return launch_early(paged_plan_kernel, blocks, kPlanThreads, smem, st, blocks, p);
+  static std::atomic<uint64_t> raised{0};
+  return launch_early_large(paged_plan_kernel, blocks, kPlanThreads, smem, (4 * kPlanMaxRequests + 3) * 4, st, blocks, p, raised);
 }
 
 cudaError_t status_paged_plan(int* v) { return read_clear_status(v); }

@@ -439,6 +439,14 @@ def test_decode_many_sequences(wide):
         within(call(q, pool, table, lens), *want(q, pool, table, lens))
 
 
+def test_decode_more_rows_than_blocks_of_mixed_lengths():
+    """480 (sequence, head) rows of up to 900 keys: ranges that hold several rows and rows that lie in
+    several ranges, merged by a block for each range."""
+    lens = [(i * 97) % 900 for i in range(60)]
+    for name, call, want, q, pool, table in both(np.random.default_rng(131), lens, 16, False, heads=8):
+        within(call(q, pool, table, lens), *want(q, pool, table, lens))
+
+
 def test_decode_long_sequence_beside_short_ones(wide):
     lens = [3, 20011, 0, 130]
     for name, call, want, q, pool, table in both(np.random.default_rng(43), lens, 64, wide, heads=1):
@@ -594,9 +602,10 @@ def test_decode_on_another_stream_and_in_a_graph(wide):
             got = call(Q, P, table, lens)
         torch.cuda.current_stream().wait_stream(other)
         assert torch.equal(got, clean)
-        got = fn(stream=other)
-        other.synchronize()
-        assert torch.equal(got, clean)
+        for stream in (other, other.cuda_stream):
+            got = fn(stream=stream)
+            other.synchronize()
+            assert torch.equal(got, clean)
 
 
 def decode_pair(name, q, pool, table, lens, lam, out, ws, w=None):
