@@ -1600,8 +1600,8 @@ def diffattn_paged_plan(seqlens, new_tokens, block_table, free_ring, ring_state,
     if out is None:
         if total_max < 0:
             raise ValueError("total_max must not be negative")
-        buf = seqlens.new_empty(3 * B + 4 + 2 * total_max, dtype=i32)
-        out = dict(zip(_PLAN, buf.split_with_sizes(sizes)))
+        buf = torch.empty(3 * B + 4 + 2 * total_max, dtype=i32, device=seqlens.device)
+        out = dict(zip(_PLAN, buf.unsafe_split_with_sizes(sizes)))  # (pieces, not views: the buffer itself is let go)
         p0 = buf.data_ptr()
         p = (p0, p0 + 4 * B, p0 + 4 * B + 8, p0 + 8 * B + 12, p0 + 12 * B + 16, p0 + 12 * B + 16 + 4 * total_max)
     else:
@@ -1761,7 +1761,7 @@ def diffattn_v2_decode_kv4(q, pool, block_table, seqlens, lam_logit, k_exp: int 
     if workspace is None:
         workspace = _workspace(dev, diffattn_v2_decode_kv4_workspace_size(B, Hq, Hkv, d))
     if out is None:
-        out = q.new_empty((B, Hq // 2, d))
+        out = torch.empty((B, Hq // 2, d), dtype=torch.bfloat16, device=q.device)
     _call(dev, lib().diffattn_v2_decode_kv4, _operand("q", q, torch.bfloat16, dev), at, table,
           _operand("seqlens", seqlens, torch.int32, dev, (B,)),
           _operand("lam_logit", lam_logit, torch.float32, dev, (B, Hq // 2)),

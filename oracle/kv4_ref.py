@@ -27,7 +27,7 @@ def nearest(x, grid):
 def quantize_blocks(x, exp: int = 0):
     """x [..., 16 n] to (codes 0..15 of the same shape, scale bytes [..., n])."""
     x = np.asarray(x, dtype=np.float64)
-    b = x.reshape(*x.shape[:-1], -1, 16) * 2.0 ** -exp
+    b = x.reshape(*x.shape[:-1], x.shape[-1] // 16, 16) * 2.0 ** -exp
     odd = ~np.all(np.isfinite(b), axis=-1)
     safe = np.where(odd[..., None], 0.0, b)
     s = nearest(np.max(np.abs(safe), axis=-1) / 6, E4M3)

@@ -776,3 +776,123 @@ def test_serving_steps(form):
             elif len(cached[b][0]) == 0:
                 assert not one[b].any()
     da.diffattn_device_status()
+
+
+@pytest.mark.parametrize("form", ["v1", "v2"])
+def test_captured_decode_step_replays(form):
+    """A whole decoding step (plan in place, append, decode) captured once and replayed: every replay
+    goes on from the lengths, tables and ring that the last one left; requests grow over page ends, and
+    an ended one's pages are taken again."""
+    rng = np.random.default_rng(137)
+    B, H, ps, num_pages, width = 3, 2, 16, 12, 8
+    kp = 2 if form == "v1" else 1
+    w, Hq = 128 * kp, H if form == "v1" else 4 * H
+    pool = da.diffattn_kv4_pool(num_pages, ps, H, w, w)
+    lens, new, state = dev32([14, 31, 0]), dev32([1, 1, 1]), dev32([0, num_pages])
+    table, ring = dev32(np.full((B, width), -1)), dev32(rng.permutation(num_pages))
+    lam = torch.tensor(rng.uniform(0.2, 0.8, H), dtype=torch.float32)
+    lg = torch.tensor(rng.normal(size=(B, Hq // 2)), dtype=torch.float32)
+    L, LG = lam.to(DEV), lg.to(DEV)
+    # the first rows, by a step of their own
+    first = [14, 31, 0]
+    out = da.diffattn_paged_plan(dev32([0, 0, 0]), dev32(first), table, ring, state, ps, 45)
+    rows = torch.tensor(rng.normal(size=(2, 45, H, w)), dtype=torch.float32).to(torch.bfloat16)
+    da.diffattn_kv4_append(rows[0].to(DEV), rows[1].to(DEV), out["slot_map"], pool)
+    state.copy_(out["ring_state"])
+    at, cached = 0, []
+    for n in first:
+        cached.append([kv4.values(*kv4.quantize_blocks(to64(r[at:at + n]))) for r in rows])
+        at += n
+    # the step, in place; rows of requests without a new token are padding
+    step = {"seqlens": lens, "ring_state": state}
+    for name, n in (("cu_seqlens_q", B + 1), ("cu_seqlens_k", B + 1), ("slot_map", B), ("positions", B)):
+        step[name] = torch.zeros(n, dtype=torch.int32, device=DEV)
+    k, v = (torch.zeros((B, H, w), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    q = torch.zeros((B, Hq, w), dtype=torch.bfloat16, device=DEV)
+
+    def run():
+        da.diffattn_paged_plan(lens, new, table, ring, state, ps, B, out=step)
+        da.diffattn_kv4_append(k, v, step["slot_map"], pool)
+        if form == "v1":
+            return da.diffattn_decode_kv4(q, pool, table, lens, L, 0.3)
+        return da.diffattn_v2_decode_kv4(q, pool, table, lens, LG)
+
+    keep = [t.clone() for t in (lens, state, table, ring, pool)]
+    run()  # (once outside, then everything as it was)
+    for t, was in zip((lens, state, table, ring, pool), keep):
+        t.copy_(was)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run()
+    for i in range(24):
+        n = [1, -1 if i == 9 else 1 if i < 9 or i > 12 else 0, 1 if i % 3 else 0]
+        rows = torch.tensor(rng.normal(size=(2, B, H, w)), dtype=torch.float32).to(torch.bfloat16)
+        qs = torch.tensor(rng.normal(size=(B, Hq, w)), dtype=torch.float32).to(torch.bfloat16)
+        order = [b for b in range(B) if n[b] > 0]
+        for x, r in ((k, rows[0]), (v, rows[1])):
+            x[:len(order)].copy_(r[order])
+        q.copy_(qs), new.copy_(dev32(n))
+        graph.replay()
+        torch.cuda.synchronize()
+        for b in range(B):
+            if n[b] < 0:
+                cached[b] = [x[:0] for x in cached[b]]
+            if n[b] > 0:
+                cached[b] = [np.concatenate([x, kv4.values(*kv4.quantize_blocks(to64(r[b:b + 1])))]) for x, r in zip(cached[b], rows)]
+        assert lens.tolist() == [len(c[0]) for c in cached]
+        for b in range(B):
+            N = len(cached[b][0])
+            if N == 0:
+                assert not got[b].any()
+                continue
+            kc, vc = (x[None] for x in cached[b])
+            if form == "v1":
+                want = ref.diffattn_decode(qs[b:b + 1], kc, vc, [N], lam.numpy(), 0.3)
+            else:
+                want = ref.diffattn_v2_decode(qs[b:b + 1], kc, vc, [N], lg[b:b + 1])
+            assert_bf16(got[b:b + 1], want)
+    da.diffattn_device_status()
+
+
+def test_rows_and_plan_on_another_stream():
+    """Plan, append and gather on a stream of their own, given by the caller."""
+    rng = np.random.default_rng(139)
+    other = torch.cuda.Stream()
+    s, n, table, ring, state, total = random_step(rng, 40, 16, 6, 3, 30)
+    want = kv4.paged_plan(s, n, table, ring, state, 16, total)
+    T, R = dev32(table), dev32(ring)
+    rows = random_rows(rng, (total, 2, 128)).to(DEV)
+    pool = torch.zeros((len(ring), 2, 1, 2304), dtype=torch.uint8, device=DEV)
+    S, N, St = dev32(s), dev32(n), dev32(state)
+    torch.cuda.synchronize()
+    p = da.diffattn_paged_plan(S, N, T, R, St, 16, total, stream=other)
+    da.diffattn_kv4_append(rows, rows, p["slot_map"], pool, stream=other)
+    new = torch.tensor(np.maximum(n, 0), dtype=torch.int32)
+    k, v = da.diffattn_kv4_gather(pool, T, p["cu_seqlens_q"], total, 128, 128, starts=S, stream=other.cuda_stream)
+    other.synchronize()
+    for name in ("slot_map", "seqlens", "cu_seqlens_q"):
+        assert np.array_equal(p[name].cpu().numpy(), want[name]), name
+    assert int(new.sum()) == total
+    x = kv4.values(*kv4.quantize_blocks(to64(rows)))
+    assert np.array_equal(to64(k), x) and np.array_equal(to64(v), x)
+    da.diffattn_device_status(other)
+
+
+def test_gather_and_append_of_many_sequences_and_heads():
+    """Sizes at which a warp of the read-out takes several heads, with odd head counts and ragged rows."""
+    rng = np.random.default_rng(149)
+    for H, lens, ps in ((13, [(i * 53) % 700 for i in range(40)], 32), (3, [5000, 1, 8191, 0, 77] * 4, 80)):
+        table, pages = random_table(rng, lens, ps)
+        total = sum(lens)
+        cu = np.concatenate([[0], np.cumsum(lens)])
+        k, v = (torch.randn((total, H, 128), device=DEV).to(torch.bfloat16) for _ in range(2))
+        pos = np.concatenate([np.arange(n) for n in lens])
+        seq = np.repeat(np.arange(len(lens)), lens)
+        slots = table[seq, pos // ps] * ps + pos % ps
+        pool = torch.zeros((pages, H, ps // 16, 2304), dtype=torch.uint8, device=DEV)
+        da.diffattn_kv4_append(k, v, dev32(slots), pool)
+        got = da.diffattn_kv4_gather(pool, dev32(table), dev32(cu), total, 128, 128)
+        for x, g in zip((k, v), got):
+            assert np.array_equal(to64(g), kv4.values(*kv4.quantize_blocks(to64(x))))
+    da.diffattn_device_status()
