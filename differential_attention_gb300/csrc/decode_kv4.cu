@@ -113,7 +113,7 @@ struct Walk {
 };
 __device__ __forceinline__ int clamp_len(const Kv4DecodeArgs& a, int b) {
   const int cap = a.max_pages * a.page_size;
-  const int n = __ldg(a.seqlens + b);
+  const int n = *(a.seqlens + b);
   return n < 0 ? 0 : n > cap ? cap : n;
 }
 template <int KP>
@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, Cfg<KP>::kCtas) kv4_decode_
     auto look_up = [&](int tile) {  // the page of record tile * kTileRecs + lane, if the row has it
       const int key = (tile * C::kTileRecs + lane_rec) * 16;
       if (key >= w.len || !dbg_index_ok(key / a.page_size, a.max_pages)) return 0;
-      return __ldg(a.block_table + static_cast<size_t>(w.b) * a.max_pages + key / a.page_size);
+      return *(a.block_table + static_cast<size_t>(w.b) * a.max_pages + key / a.page_size);
     };
     int page = w.todo > 0 ? look_up(w.tile) : 0;
     while (w.todo > 0 && alive) {
@@ -646,12 +646,12 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, Cfg<KP>::kCtas) kv4_decode_
       for (int c = 0; c < C::kMaxCols; c += 2) {
         if (c >= cols) break;
         const size_t pair = row * (cols / 2) + c / 2;
-        const float sig = 1.f / (1.f + __expf(-__ldg(a.lam_logit + pair)));
+        const float sig = 1.f / (1.f + __expf(-*(a.lam_logit + pair)));
         const float y = (sum[c][0] / l[c] - sig * (sum[c + 1][0] / l[c + 1])) * a.v_mul;
         static_cast<__nv_bfloat16*>(a.out)[pair * 128 + tid] = __float2bfloat16_rn(y);
       }
     } else {
-      const float lam = __ldg(a.lambda + w.h);
+      const float lam = *(a.lambda + w.h);
       float y[KP];
       float ss = 0.f;
 #pragma unroll
@@ -662,7 +662,7 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, Cfg<KP>::kCtas) kv4_decode_
       const float f = norm_scale(a, ss, s_red);
 #pragma unroll
       for (int k = 0; k < KP; ++k) {
-        const float wgt = (a.flags & 2) && a.norm_w ? __ldg(a.norm_w + k * 128 + tid) : 1.f;
+        const float wgt = (a.flags & 2) && a.norm_w ? *(a.norm_w + k * 128 + tid) : 1.f;
         static_cast<__nv_bfloat16*>(a.out)[row * C::kWidth + k * 128 + tid] = __float2bfloat16_rn(y[k] * f * wgt);
       }
     }
@@ -699,8 +699,8 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, Cfg<KP>::kCtas) kv4_decode_
             sum[e][k] = fmaf(ld_cluster_f32(from + 4 * (2 * C::kMaxCols + c * C::kWidth + k * 128 + tid)), f, sum[e][k]);
         }
       }
-      const float lam = KP == 2 ? __ldg(a.lambda + w.h)
-                                : 1.f / (1.f + __expf(-__ldg(a.lam_logit + row * (p.cols / 2) + pair)));
+      const float lam = KP == 2 ? *(a.lambda + w.h)
+                                : 1.f / (1.f + __expf(-*(a.lam_logit + row * (p.cols / 2) + pair)));
       float y[KP], ss = 0.f, f = 1.f;
 #pragma unroll
       for (int k = 0; k < KP; ++k) {
@@ -710,7 +710,7 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, Cfg<KP>::kCtas) kv4_decode_
       if constexpr (KP == 2) f = norm_scale(a, ss, s_red);
 #pragma unroll
       for (int k = 0; k < KP; ++k) {
-        const float wgt = KP == 2 && (a.flags & 2) && a.norm_w ? __ldg(a.norm_w + k * 128 + tid) : 1.f;
+        const float wgt = KP == 2 && (a.flags & 2) && a.norm_w ? *(a.norm_w + k * 128 + tid) : 1.f;
         static_cast<__nv_bfloat16*>(a.out)[(row * (p.cols / 2) + pair) * C::kWidth + k * 128 + tid] = __float2bfloat16_rn(y[k] * f * wgt);
       }
     }
@@ -769,8 +769,8 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const Params p
   const size_t row = static_cast<size_t>(d.b) * a.H + d.h;
   const int pair = tid / W, ch = tid % W;  // the output channel of the end
   const bool mine = tid < nc / 2 * W;
-  const float lam = !mine ? 0.f : KP == 2 ? __ldg(a.lambda + d.h) : 1.f / (1.f + __expf(-__ldg(a.lam_logit + row * (cols / 2) + c0 / 2 + pair)));
-  const float wgt = KP == 2 && mine && (a.flags & 2) && a.norm_w ? __ldg(a.norm_w + ch) : 1.f;
+  const float lam = !mine ? 0.f : KP == 2 ? *(a.lambda + d.h) : 1.f / (1.f + __expf(-*(a.lam_logit + row * (cols / 2) + c0 / 2 + pair)));
+  const float wgt = KP == 2 && mine && (a.flags & 2) && a.norm_w ? *(a.norm_w + ch) : 1.f;
   grid_wait();
   grid_release();
   float m = -FLT_MAX, l = 0.f;

@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const Kv4Append
   if (row0 >= a.total) return;
   auto slot_of = [&](long long row) {
     if (row >= a.total) return -1;
-    const int s = __ldg(a.slot_map + row);
+    const int s = *(a.slot_map + row);
     if (s >= 0 && s < a.num_pages * a.page_size) return s;
     if (s != -1) flag_device_error(DEV_BAD_INDEX);
     return -1;
@@ -79,12 +79,12 @@ __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const Kv4Append
   auto load = [&](int plane, uint4 (&w)[4]) {
     if (plane < KP) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = ks >= 0 ? __ldg(ksrc + plane * 16 + i) : zero;
+      for (int i = 0; i < 4; ++i) w[i] = ks >= 0 ? *(ksrc + plane * 16 + i) : zero;
     } else {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        w[i] = s0 >= 0 ? __ldg(vsrc0 + (plane - KP) * 16 + i) : zero;
-        w[2 + i] = s1 >= 0 ? __ldg(vsrc1 + (plane - KP) * 16 + i) : zero;
+        w[i] = s0 >= 0 ? *(vsrc0 + (plane - KP) * 16 + i) : zero;
+        w[2 + i] = s1 >= 0 ? *(vsrc1 + (plane - KP) * 16 + i) : zero;
       }
     }
   };
@@ -152,18 +152,18 @@ __global__ void __launch_bounds__(kRowThreads) kv4_gather_kernel(const Kv4Gather
   int lo = 0, n = a.B;
   while (n > 1) {
     const int step = (n + 31) >> 5, b = lo + lane * step;
-    const bool at = lane * step < n && __ldg(a.cu_seqlens + b) / 16 + 2LL * b <= u;
+    const bool at = lane * step < n && *(a.cu_seqlens + b) / 16 + 2LL * b <= u;
     const unsigned hit = __ballot_sync(0xffffffffu, at);
     const int last = hit ? 31 - __clz(hit) : 0;
     lo += last * step;
     n = min(step, n - last * step);
   }
-  const int c0 = __ldg(a.cu_seqlens + lo), c1 = __ldg(a.cu_seqlens + lo + 1);
+  const int c0 = *(a.cu_seqlens + lo), c1 = *(a.cu_seqlens + lo + 1);
   if (c0 < 0 || c1 > a.total || c0 >= c1) {
     if (c0 < 0 || c1 > a.total || c0 > c1) flag_device_error(DEV_BAD_INDEX);
     return;
   }
-  const long long first = a.starts ? __ldg(a.starts + lo) : 0, end = first + (c1 - c0);
+  const long long first = a.starts ? *(a.starts + lo) : 0, end = first + (c1 - c0);
   // token of this record's first row (its record counted from the sequence's first one, towards
   // minus infinity where the first token is negative)
   const long long tok = (((first - (first & 15)) >> 4) + (u - c0 / 16 - 2LL * lo)) * 16;
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kRowThreads) kv4_gather_kernel(const Kv4Gather
     return;
   }
   const int pi = static_cast<int>(tok / a.page_size), off = static_cast<int>(tok - static_cast<long long>(pi) * a.page_size);
-  int page = __ldg(a.block_table + static_cast<size_t>(lo) * a.max_pages + pi);
+  int page = *(a.block_table + static_cast<size_t>(lo) * a.max_pages + pi);
   if (page < 0 || page >= a.num_pages) {
     flag_device_error(DEV_BAD_INDEX);
     page = 0;
@@ -196,10 +196,10 @@ __global__ void __launch_bounds__(kRowThreads) kv4_gather_kernel(const Kv4Gather
     const uint8_t* p = rec + (step / (2 * KP)) * head_bytes + pl * kKv4Plane;
 #pragma unroll
     for (int i = 0; i < 8; ++i)  // tokens 2 i + hi: a quad of tokens is 128 (K) or 16 (V) bytes on, its second half 512
-      x.codes[i] = __ldg(reinterpret_cast<const uint32_t*>(p + (is_k ? k_at + (i >> 1) * 128 : v_at + (i >> 1) * 16) + (i & 1) * 512));
+      x.codes[i] = *reinterpret_cast<const uint32_t*>(p + (is_k ? k_at + (i >> 1) * 128 : v_at + (i >> 1) * 16) + (i & 1) * 512);
 #pragma unroll
     for (int i = 0; i < 4; ++i)  // a quad's scales: K's two rows by two blocks, V's four rows
-      x.scales[i] = __ldg(reinterpret_cast<const uint32_t*>(p + (is_k ? k_sc + i * 32 : v_sc + i * 4)));
+      x.scales[i] = *reinterpret_cast<const uint32_t*>(p + (is_k ? k_sc + i * 32 : v_sc + i * 4));
   };
   auto store = [&](int step, const Plane& x) {
     const int pl = step % (2 * KP), h = h0 + step / (2 * KP);

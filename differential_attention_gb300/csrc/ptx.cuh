@@ -183,7 +183,8 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float a) {
 // ---------------------------------------------------------------------------------------------
 // programmatic launches (a kernel set up while the one before it in the stream still runs)
 // ---------------------------------------------------------------------------------------------
-// Until the kernels before this one are done and their writes seen. Every block of a kernel that is
+// Until the kernels before this one are done and their writes seen (by plain loads: what they wrote was not
+// constant while this kernel ran, so nothing of it is read through __ldg). Every block of a kernel that is
 // launched this way calls it, also one that has nothing to do: the kernel after it goes by that.
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // From here on (in all blocks) the kernel after this one may be set up. After grid_wait().
