@@ -30,12 +30,20 @@
 // lies in it whole is finished there; the pieces of one that does not go to the workspace, at most
 // two a block, and the second kernel merges them, in the order of the ranges. Where the tables hold few
 // keys for each resident block, a row is cut over the blocks of a cluster instead, which join through
-// each other's shared memory: one launch, no workspace. (Tried and dropped, V2
-// with lengths of 1 to 16K, 52 us as it is: two ranges a block, the second taken over by cluster launch
-// control, 58 us, as each range adds pieces; the last block of a row merging it, without a second
-// kernel, 60 us, as the blocks wait for their fence and their count.)
+// each other's shared memory: one launch, no workspace. (Tried and dropped, V2 with lengths of 1 to 16K, 52
+// us at the time: two ranges a block, the second taken over by cluster launch control, 58 us, as each
+// range adds pieces; the last block of a row merging it, without a second kernel, 60 us, as the blocks
+// wait for their fence and their count; shares by a block's age on its SM, whose schedulers serve the
+// older first, 52 us, and 400 instead of 388 for 64 x 32768 keys.)
+//
+// Where it stands: 64 x 32768 keys, 8 KV heads, G = 8 (2.42 GB): 361 us, 6.70 TB/s of the 6.78 that a copy
+// reaches; with all pages in L2 the same work takes 360, so that the unpacking (116 of 250 instructions a
+// record go to the ALU pipe, most of them the 64 conversions) is as near its limit as the memory. 96
+// sequences of 1 to 16K keys, G = 4 (235 MB): 51 us, of which the loads alone take 39, the products 7 and
+// the second kernel 4. V1, 24 x 32768 keys, 12 heads (2.72 GB): 405 us, 6.71 TB/s.
 #include <cfloat>
 #include <cmath>
+#include <type_traits>
 
 #include "internal.h"
 #include "kv4.cuh"
@@ -52,15 +60,18 @@ constexpr float kMoveRef = 14.f;                 // log2 P at which the referenc
 
 template <int KP>
 struct Cfg {
+  // Measured, V2, 64 x 32768 keys, 367 us so: 4 blocks an SM at 96 registers 375; 1 record a warp and 4
+  // blocks 415; 4 records and 2 blocks 384; 6 warps and 2 blocks 446 (they lie unevenly on the four
+  // schedulers); 8 warps and 2 blocks 421, 12 and 1 523 (more of them wait for each tile). V1, 24 x 32768
+  // keys x 12, 405 us so: 1 record a warp and 3 blocks 412.
   static constexpr int kWarps = 4;               // consumer warps (an even number, at least 4)
   static constexpr int kThreads = (kWarps + 1) * 32;  // and a producer
   static constexpr int kRecs = 2;                // records of a tile for each of them
-  static constexpr int kJoint = KP == 1 ? 2 : 2; // of these, taken together
   static constexpr int kTileRecs = kWarps * kRecs;
   static constexpr int kTileKeys = 16 * kTileRecs;
   static constexpr int kCtas = KP == 1 ? 3 : 2;  // blocks of an SM
   static constexpr int kGrid = kSms * kCtas;
-  static constexpr int kRowCost = KP == 1 ? 2 : 1;  // what a row costs besides its tiles, in tiles
+  static constexpr int kRowCost = 2;             // what a row costs besides its tiles, in tiles
   static constexpr int kMinCost = KP == 1 ? 3 : 2;  // the smallest range
   static constexpr int kRecord = 2 * KP * kKv4Plane;
   static constexpr int kWidth = KP * 128;
@@ -236,7 +247,7 @@ __device__ __forceinline__ void mma_first(float (&c)[4], uint32_t a0, uint32_t a
 
 // S^T of one record: rows g (key 4 (g/2) + g%2) and g + 8 (that + 2), columns 2t and 2t + 1. `at`: the
 // K plane's codes for this lane.
-__device__ __forceinline__ void scores(float (&c)[4], uint32_t at, int lane, const uint32_t (&qf)[8][2]) {
+__device__ __forceinline__ void scores(float (&c)[4], uint32_t at, int lane, const uint4 (&qf)[4]) {
   const uint4 lo4 = lds128(at), hi4 = lds128(at + 512);
   const uint32_t sc = lds32(at - lane * 12 + kKv4PlaneCodes);
   uint32_t slo, shi;
@@ -252,9 +263,9 @@ __device__ __forceinline__ void scores(float (&c)[4], uint32_t at, int lane, con
     e2m1x8_to_half2(wh[k], y);
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i] = half2_mul(x[i], sl), y[i] = half2_mul(y[i], sh);
-    if (k == 0) mma_first(c, x[0], y[0], x[1], y[1], qf[0][0], qf[0][1]);
-    else mma(c, x[0], y[0], x[1], y[1], qf[2 * k][0], qf[2 * k][1]);
-    mma(c, x[2], y[2], x[3], y[3], qf[2 * k + 1][0], qf[2 * k + 1][1]);
+    if (k == 0) mma_first(c, x[0], y[0], x[1], y[1], qf[k].x, qf[k].y);
+    else mma(c, x[0], y[0], x[1], y[1], qf[k].x, qf[k].y);
+    mma(c, x[2], y[2], x[3], y[3], qf[k].z, qf[k].w);
   }
 }
 
@@ -417,261 +428,274 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, Cfg<KP>::kCtas) kv4_decode_
 
   // Consumers.
   if (warp < kWarps) {
-  const int g = lane >> 2, t = lane & 3;
-  const int cols = p.cols;
-  uint32_t qf[8][2];           // Q^T fragments: channels 32t + 4j .. + 3 of column g
-  float cs0 = 0.f, cs1 = 0.f;  // what a sum of columns 2t and 2t + 1 is to be multiplied with
-  float o[KP * 8][4];
-  float m0, m1, l0, l1;        // references (less kPScale) and sums of columns 2t, 2t + 1
-  int stage = 0, parity = 0;
-  uint32_t phase = 0;
-  bool alive = true;
+    const int g = lane >> 2, t = lane & 3;
+    const int cols = p.cols;
+    uint4 qf[4];                 // Q^T fragments: channels 32t + 8k .. + 7 of column g
+    float cs0 = 0.f, cs1 = 0.f;  // what a sum of columns 2t and 2t + 1 is to be multiplied with
+    float o[KP * 8][4];
+    float m0, m1, l0, l1;        // references (less kPScale) and sums of columns 2t, 2t + 1
+    int stage = 0, parity = 0;
+    uint32_t phase = 0;
+    bool alive = true;
 
-  auto load_q = [&](uint32_t at) {
-    uint32_t raw[16];
+    auto load_q = [&](uint32_t at) {
+      uint32_t raw[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) raw[i] = 0;
-    if (g < cols) {
+      for (int i = 0; i < 16; ++i) raw[i] = 0;
+      if (g < cols) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint4 v = lds128(at + g * 256 + t * 64 + i * 16);
-        raw[4 * i] = v.x, raw[4 * i + 1] = v.y, raw[4 * i + 2] = v.z, raw[4 * i + 3] = v.w;
-      }
-    }
-    uint32_t top = 0;  // the largest magnitude's bits (ordered as the values are)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) top = max(top, max(raw[i] & 0x7fffu, (raw[i] >> 16) & 0x7fffu));
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    const int e = max(static_cast<int>(top >> 7) - 127, -100);
-    const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);     // 2^(14 - e)
-    // (never 0 or Inf, which a masked score's Inf or a score of 0 would turn into NaN)
-    const float down = fminf(fmaxf(ldexpf(a.qk_scale, e - 14), FLT_MIN), FLT_MAX);
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint32_t x = raw[2 * j + i];
-        qf[j][i] = pack_half2(__uint_as_float(x << 16) * up, __uint_as_float(x & 0xffff0000u) * up);
-      }
-    cs0 = __shfl_sync(0xffffffffu, down, 8 * t);
-    cs1 = __shfl_sync(0xffffffffu, down, 8 * t + 4);
-  };
-  auto wait = [&]() {
-    if (__all_sync(0xffffffffu, mbar_try_wait(full(stage), phase))) return;
-    alive = __all_sync(0xffffffffu, alive && mbar_wait(full(stage), phase, &s_abort));
-  };
-
-  // empty places in the batch get zeros
-  for (int b = range; !kByRow && b < a.B; b += n)
-    if (clamp_len(a, b) == 0) {
-      const size_t size = static_cast<size_t>(a.H) * (cols / 2) * C::kWidth;
-      uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + b * size);
-      for (size_t i = tid; i < size / 8; i += kWarps * 32) out[i] = make_uint4(0, 0, 0, 0);
-    }
-  if (kByRow && w.todo <= 0)  // a piece of no keys
-    for (int i = tid; i < C::kMaxCols * (2 + C::kWidth); i += kWarps * 32) s_x[i] = i < C::kMaxCols ? -FLT_MAX : 0.f;
-  while (w.todo > 0) {
-    const int seg = min(w.tiles - w.tile, w.todo);  // tiles of this row in the range
-    const bool starts = w.tile == 0, whole = !kByRow && starts && seg == w.tiles;
-    wait();
-    load_q(ring + stage * C::kStage + C::kTileRecs * C::kRecord);
-#pragma unroll
-    for (int j = 0; j < KP * 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-    m0 = m1 = -FLT_MAX;
-    l0 = l1 = 0.f;
-    for (int i = 0; i < seg; ++i) {
-      if (i > 0) wait();
-      // record w + 4 k of the tile is warp w's; `left`: keys from its first one on
-      constexpr int R = C::kJoint;
-#pragma unroll 1
-      for (int q0 = 0; q0 < C::kRecs; q0 += R) {
-        const int left = w.len - ((w.tile + i) * C::kTileRecs + q0 * kWarps + warp) * 16;
-        if (!alive || left <= 0) break;
-        const uint32_t rec = ring + stage * C::kStage + (q0 * kWarps + warp) * C::kRecord + lane * 16;
-        float y[R][4];
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const uint32_t at = rec + r * kWarps * C::kRecord;
-          if constexpr (KP == 1) {
-            scores(y[r], at, lane, qf);
-          } else {  // V1: column 0 from the first plane, column 1 from the second
-            float s1[4], s2[4];
-            scores(s1, at, lane, qf);
-            scores(s2, at + kKv4Plane, lane, qf);
-            y[r][0] = s1[0], y[r][1] = s2[1], y[r][2] = s1[2], y[r][3] = s2[3];
-          }
+        for (int i = 0; i < 4; ++i) {
+          const uint4 v = lds128(at + g * 256 + t * 64 + i * 16);
+          raw[4 * i] = v.x, raw[4 * i + 1] = v.y, raw[4 * i + 2] = v.z, raw[4 * i + 3] = v.w;
         }
-        uint32_t keep[R];
+      }
+      uint32_t top = 0;  // the largest magnitude's bits (ordered as the values are)
 #pragma unroll
-        for (int r = 0; r < R; ++r) keep[r] = 0xffffffffu;
-        if (left < 16 * (1 + (R - 1) * kWarps)) {  // the last tile: keys past the end
+      for (int i = 0; i < 16; ++i) top = max(top, max(raw[i] & 0x7fffu, (raw[i] >> 16) & 0x7fffu));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const int e = max(static_cast<int>(top >> 7) - 127, -100);
+      const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);     // 2^(14 - e)
+      // (never 0 or Inf, which a masked score's Inf or a score of 0 would turn into NaN)
+      const float down = fminf(fmaxf(ldexpf(a.qk_scale, e - 14), FLT_MIN), FLT_MAX);
+      auto two = [&](uint32_t x) { return pack_half2(__uint_as_float(x << 16) * up, __uint_as_float(x & 0xffff0000u) * up); };
+#pragma unroll
+      for (int k = 0; k < 4; ++k) qf[k] = make_uint4(two(raw[4 * k]), two(raw[4 * k + 1]), two(raw[4 * k + 2]), two(raw[4 * k + 3]));
+      cs0 = __shfl_sync(0xffffffffu, down, 8 * t);
+      cs1 = __shfl_sync(0xffffffffu, down, 8 * t + 4);
+    };
+    auto wait = [&]() {
+      if (__all_sync(0xffffffffu, mbar_try_wait(full(stage), phase))) return;
+      alive = __all_sync(0xffffffffu, alive && mbar_wait(full(stage), phase, &s_abort));
+    };
+
+    // empty places in the batch get zeros
+    for (int b = range; !kByRow && b < a.B; b += n)
+      if (clamp_len(a, b) == 0) {
+        const size_t size = static_cast<size_t>(a.H) * (cols / 2) * C::kWidth;
+        uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + b * size);
+        for (size_t i = tid; i < size / 8; i += kWarps * 32) out[i] = make_uint4(0, 0, 0, 0);
+      }
+    if (kByRow && w.todo <= 0)  // a piece of no keys
+      for (int i = tid; i < C::kMaxCols * (2 + C::kWidth); i += kWarps * 32) s_x[i] = i < C::kMaxCols ? -FLT_MAX : 0.f;
+    while (w.todo > 0) {
+      const int seg = min(w.tiles - w.tile, w.todo);  // tiles of this row in the range
+      const bool starts = w.tile == 0, whole = !kByRow && starts && seg == w.tiles;
+      wait();
+      load_q(ring + stage * C::kStage + C::kTileRecs * C::kRecord);
+#pragma unroll
+      for (int j = 0; j < KP * 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+      m0 = m1 = -FLT_MAX;
+      l0 = l1 = 0.f;
+      // One tile; `last`: it may be the row's last one, and short.
+      auto take = [&](int i, auto last) {
+        // record w + 4 k of the tile is warp w's; `left`: keys from its first one on
+        constexpr int R = C::kRecs;
+        // record w + 4 r of the tile is warp w's; `left`: keys from its first one on
+        const int left = last ? w.len - ((w.tile + i) * C::kTileRecs + warp) * 16 : 0;
+        if (alive && !(last && left <= 0)) {
+          const uint32_t rec = ring + stage * C::kStage + warp * C::kRecord + lane * 16;
+          float y[R][4];
 #pragma unroll
           for (int r = 0; r < R; ++r) {
-            const int live = left - r * kWarps * 16 - 4 * t;
-            keep[r] = live >= 4 ? 0xffffffffu : live <= 0 ? 0u : 0xffffffffu >> (32 - 8 * live);
-            const int key = r * kWarps * 16 + (g >> 1) * 4 + (g & 1);
-            if (key >= left) y[r][0] = y[r][1] = -INFINITY;
-            if (key + 2 >= left) y[r][2] = y[r][3] = -INFINITY;
+            const uint32_t at = rec + r * kWarps * C::kRecord;
+            if constexpr (KP == 1) {
+              scores(y[r], at, lane, qf);
+            } else {  // V1: column 0 from the first plane, column 1 from the second
+              float s1[4], s2[4];
+              scores(s1, at, lane, qf);
+              scores(s2, at + kKv4Plane, lane, qf);
+              y[r][0] = s1[0], y[r][1] = s2[1], y[r][2] = s1[2], y[r][3] = s2[3];
+            }
           }
-        }
-        // exponents against the reference; it moves where one passes kMoveRef
-        float e[R][4], top = -INFINITY;
+          uint32_t keep[R];
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          e[r][0] = fmaf(y[r][0], cs0, -m0), e[r][1] = fmaf(y[r][1], cs1, -m1);
-          e[r][2] = fmaf(y[r][2], cs0, -m0), e[r][3] = fmaf(y[r][3], cs1, -m1);
-          top = fmaxf(top, fmaxf(fmaxf(e[r][0], e[r][1]), fmaxf(e[r][2], e[r][3])));
-        }
-        if (__any_sync(0xffffffffu, top > kMoveRef)) {
-          float n0 = -FLT_MAX, n1 = -FLT_MAX;
+          for (int r = 0; r < R; ++r) keep[r] = 0xffffffffu;
+          if (last && left < 16 * (1 + (R - 1) * kWarps)) {  // keys past the end
 #pragma unroll
-          for (int r = 0; r < R; ++r) {
-            n0 = fmaxf(n0, fmaxf(y[r][0] * cs0, y[r][2] * cs0));
-            n1 = fmaxf(n1, fmaxf(y[r][1] * cs1, y[r][3] * cs1));
+            for (int r = 0; r < R; ++r) {
+              const int live = left - r * kWarps * 16 - 4 * t;
+              keep[r] = live >= 4 ? 0xffffffffu : live <= 0 ? 0u : 0xffffffffu >> (32 - 8 * live);
+              const int key = r * kWarps * 16 + (g >> 1) * 4 + (g & 1);
+              if (key >= left) y[r][0] = y[r][1] = -INFINITY;
+              if (key + 2 >= left) y[r][2] = y[r][3] = -INFINITY;
+            }
           }
-#pragma unroll
-          for (int d = 4; d < 32; d <<= 1) {
-            n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, d));
-            n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, d));
-          }
-          n0 = fmaxf(m0, n0 - kPScale), n1 = fmaxf(m1, n1 - kPScale);
-          const float f0 = ex2_approx(m0 - n0), f1 = ex2_approx(m1 - n1);
-          m0 = n0, m1 = n1;
-          l0 *= f0, l1 *= f1;
-#pragma unroll
-          for (int j = 0; j < KP * 8; ++j) o[j][0] *= f0, o[j][1] *= f1, o[j][2] *= f0, o[j][3] *= f1;
+          // exponents against the reference; it moves where one passes kMoveRef
+          float e[R][4], top = -INFINITY;
 #pragma unroll
           for (int r = 0; r < R; ++r) {
             e[r][0] = fmaf(y[r][0], cs0, -m0), e[r][1] = fmaf(y[r][1], cs1, -m1);
             e[r][2] = fmaf(y[r][2], cs0, -m0), e[r][3] = fmaf(y[r][3], cs1, -m1);
+            top = fmaxf(top, fmaxf(fmaxf(e[r][0], e[r][1]), fmaxf(e[r][2], e[r][3])));
+          }
+          if (__any_sync(0xffffffffu, top > kMoveRef)) {
+            float n0 = -FLT_MAX, n1 = -FLT_MAX;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+              n0 = fmaxf(n0, fmaxf(y[r][0] * cs0, y[r][2] * cs0));
+              n1 = fmaxf(n1, fmaxf(y[r][1] * cs1, y[r][3] * cs1));
+            }
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) {
+              n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, d));
+              n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, d));
+            }
+            n0 = fmaxf(m0, n0 - kPScale), n1 = fmaxf(m1, n1 - kPScale);
+            const float f0 = ex2_approx(m0 - n0), f1 = ex2_approx(m1 - n1);
+            m0 = n0, m1 = n1;
+            l0 *= f0, l1 *= f1;
+#pragma unroll
+            for (int j = 0; j < KP * 8; ++j) o[j][0] *= f0, o[j][1] *= f1, o[j][2] *= f0, o[j][3] *= f1;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+              e[r][0] = fmaf(y[r][0], cs0, -m0), e[r][1] = fmaf(y[r][1], cs1, -m1);
+              e[r][2] = fmaf(y[r][2], cs0, -m0), e[r][3] = fmaf(y[r][3], cs1, -m1);
+            }
+          }
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            const float p00 = ex2_approx(e[r][0]), p01 = ex2_approx(e[r][1]);
+            const float p10 = ex2_approx(e[r][2]), p11 = ex2_approx(e[r][3]);
+            l0 += p00 + p10;
+            l1 += p01 + p11;
+            // lane (g, t) now wants column g at keys 4t .. 4t + 3
+            const uint32_t b0 = transpose8x8(pack_half2(p00, p01)), b1 = transpose8x8(pack_half2(p10, p11));
+#pragma unroll
+            for (int pl = 0; pl < KP; ++pl)
+              outputs(o + pl * 8, rec + r * kWarps * C::kRecord + (KP + pl) * kKv4Plane, lane, keep[r], b0, b1);
           }
         }
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const float p00 = ex2_approx(e[r][0]), p01 = ex2_approx(e[r][1]);
-          const float p10 = ex2_approx(e[r][2]), p11 = ex2_approx(e[r][3]);
-          l0 += p00 + p10;
-          l1 += p01 + p11;
-          // lane (g, t) now wants column g at keys 4t .. 4t + 3
-          const uint32_t b0 = transpose8x8(pack_half2(p00, p01)), b1 = transpose8x8(pack_half2(p10, p11));
-#pragma unroll
-          for (int pl = 0; pl < KP; ++pl)
-            outputs(o + pl * 8, rec + r * kWarps * C::kRecord + (KP + pl) * kKv4Plane, lane, keep[r], b0, b1);
+        __syncwarp();
+        if (alive && lane == 0) mbar_arrive(empty(stage));
+        if (++stage == C::kStages) stage = 0, phase ^= 1;
+      };
+      if constexpr (KP == 1) {
+        // V2: whole tiles without the tests (367 -> 361 us for 64 x 32768 keys). V1's code is twice as long,
+        // and a second copy of it costs more than the tests do (24 x 32768 x 12: 401 and 403 us).
+        const int whole_tiles = min(seg, w.len / C::kTileKeys - w.tile);
+        for (int i = 0; i < whole_tiles; ++i) {
+          if (i > 0) wait();
+          take(i, std::false_type{});
+        }
+        if (whole_tiles < seg) {
+          if (seg > 1) wait();
+          take(seg - 1, std::true_type{});
+        }
+      } else {
+        for (int i = 0; i < seg; ++i) {
+          if (i > 0) wait();
+          take(i, std::true_type{});
         }
       }
-      __syncwarp();
-      if (alive && lane == 0) mbar_arrive(empty(stage));
-      if (++stage == C::kStages) stage = 0, phase ^= 1;
-    }
 
-    // Join the warps' pieces.
+      // Join the warps' pieces.
 #pragma unroll
-    for (int d = 4; d < 32; d <<= 1) {
-      l0 += __shfl_xor_sync(0xffffffffu, l0, d);
-      l1 += __shfl_xor_sync(0xffffffffu, l1, d);
-    }
-    if (g == 0) {
-      s_m[parity][warp][2 * t] = m0, s_m[parity][warp][2 * t + 1] = m1;
-      s_l[parity][warp][2 * t] = l0, s_l[parity][warp][2 * t + 1] = l1;
-    }
-    named_barrier_sync(1, kWarps * 32);
-    float top0 = m0, top1 = m1;
+      for (int d = 4; d < 32; d <<= 1) {
+        l0 += __shfl_xor_sync(0xffffffffu, l0, d);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, d);
+      }
+      if (g == 0) {
+        s_m[parity][warp][2 * t] = m0, s_m[parity][warp][2 * t + 1] = m1;
+        s_l[parity][warp][2 * t] = l0, s_l[parity][warp][2 * t + 1] = l1;
+      }
+      named_barrier_sync(1, kWarps * 32);
+      float top0 = m0, top1 = m1;
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-      top0 = fmaxf(top0, s_m[parity][i][2 * t]);
-      top1 = fmaxf(top1, s_m[parity][i][2 * t + 1]);
-    }
-    const float f0 = ex2_approx(m0 - top0), f1 = ex2_approx(m1 - top1);
-    // the upper half of the warps hand their sums to the lower half
-    auto exchange = [&](auto&& step) {
-      if (2 * t < C::kMaxCols) {
-        float* at = s_o + (warp % (kWarps / 2) * C::kMaxCols + 2 * t) * C::kPitch;
+      for (int i = 0; i < kWarps; ++i) {
+        top0 = fmaxf(top0, s_m[parity][i][2 * t]);
+        top1 = fmaxf(top1, s_m[parity][i][2 * t + 1]);
+      }
+      const float f0 = ex2_approx(m0 - top0), f1 = ex2_approx(m1 - top1);
+      // the upper half of the warps hand their sums to the lower half
+      auto exchange = [&](auto&& step) {
+        if (2 * t < C::kMaxCols) {
+          float* at = s_o + (warp % (kWarps / 2) * C::kMaxCols + 2 * t) * C::kPitch;
 #pragma unroll
-        for (int j = 0; j < KP * 8; ++j) {
-          const int ch = (j >> 3) * 128 + 16 * g + 2 * (j & 7);
-          step(reinterpret_cast<float2*>(at + ch), o[j][0] * f0, o[j][2] * f0);
-          step(reinterpret_cast<float2*>(at + C::kPitch + ch), o[j][1] * f1, o[j][3] * f1);
+          for (int j = 0; j < KP * 8; ++j) {
+            const int ch = (j >> 3) * 128 + 16 * g + 2 * (j & 7);
+            step(reinterpret_cast<float2*>(at + ch), o[j][0] * f0, o[j][2] * f0);
+            step(reinterpret_cast<float2*>(at + C::kPitch + ch), o[j][1] * f1, o[j][3] * f1);
+          }
+        }
+      };
+      if (warp >= kWarps / 2) exchange([](float2* at, float x, float y) { *at = make_float2(x, y); });
+      named_barrier_sync(1, kWarps * 32);
+      if (warp < kWarps / 2)
+        exchange([](float2* at, float x, float y) {
+          const float2 v = *at;
+          *at = make_float2(v.x + x, v.y + y);
+        });
+      named_barrier_sync(1, kWarps * 32);
+      // thread `tid` < 128 takes channel tid (V1: and tid + 128) of every column
+      const int last_parity = parity;
+      parity ^= 1;
+      if (tid < 128) {
+      float sum[C::kMaxCols][KP], l[C::kMaxCols], top[C::kMaxCols];
+#pragma unroll
+      for (int c = 0; c < C::kMaxCols; ++c) {
+        float mx = s_m[last_parity][0][c];
+#pragma unroll
+        for (int i = 1; i < kWarps; ++i) mx = fmaxf(mx, s_m[last_parity][i][c]);
+        top[c] = mx;
+        l[c] = 0.f;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) l[c] += s_l[last_parity][i][c] * ex2_approx(s_m[last_parity][i][c] - mx);
+#pragma unroll
+        for (int k = 0; k < KP; ++k) {
+          sum[c][k] = 0.f;
+#pragma unroll
+          for (int i = 0; i < kWarps / 2; ++i) sum[c][k] += s_o[(i * C::kMaxCols + c) * C::kPitch + k * 128 + tid];
         }
       }
-    };
-    if (warp >= kWarps / 2) exchange([](float2* at, float x, float y) { *at = make_float2(x, y); });
-    named_barrier_sync(1, kWarps * 32);
-    if (warp < kWarps / 2)
-      exchange([](float2* at, float x, float y) {
-        const float2 v = *at;
-        *at = make_float2(v.x + x, v.y + y);
-      });
-    named_barrier_sync(1, kWarps * 32);
-    // thread `tid` < 128 takes channel tid (V1: and tid + 128) of every column
-    const int last_parity = parity;
-    parity ^= 1;
-    if (tid < 128) {
-    float sum[C::kMaxCols][KP], l[C::kMaxCols], top[C::kMaxCols];
+      const size_t row = static_cast<size_t>(w.b) * a.H + w.h;
+      if constexpr (kByRow) {
 #pragma unroll
-    for (int c = 0; c < C::kMaxCols; ++c) {
-      float mx = s_m[last_parity][0][c];
+        for (int c = 0; c < C::kMaxCols; ++c) {
+          if (tid == 0) s_x[c] = top[c], s_x[C::kMaxCols + c] = l[c];
 #pragma unroll
-      for (int i = 1; i < kWarps; ++i) mx = fmaxf(mx, s_m[last_parity][i][c]);
-      top[c] = mx;
-      l[c] = 0.f;
+          for (int k = 0; k < KP; ++k) s_x[2 * C::kMaxCols + c * C::kWidth + k * 128 + tid] = sum[c][k];
+        }
+      } else if (!whole) {
+        float* rec = p.rec + static_cast<size_t>(2 * range + (starts ? 1 : 0)) * (2 * cols + cols * C::kWidth);
 #pragma unroll
-      for (int i = 0; i < kWarps; ++i) l[c] += s_l[last_parity][i][c] * ex2_approx(s_m[last_parity][i][c] - mx);
+        for (int c = 0; c < C::kMaxCols; ++c) {
+          if (c >= cols) break;
+          if (tid == 0) rec[c] = top[c], rec[cols + c] = l[c];
 #pragma unroll
-      for (int k = 0; k < KP; ++k) {
-        sum[c][k] = 0.f;
+          for (int k = 0; k < KP; ++k) rec[2 * cols + c * C::kWidth + k * 128 + tid] = sum[c][k];
+        }
+      } else if constexpr (KP == 1) {
 #pragma unroll
-        for (int i = 0; i < kWarps / 2; ++i) sum[c][k] += s_o[(i * C::kMaxCols + c) * C::kPitch + k * 128 + tid];
+        for (int c = 0; c < C::kMaxCols; c += 2) {
+          if (c >= cols) break;
+          const size_t pair = row * (cols / 2) + c / 2;
+          const float sig = 1.f / (1.f + __expf(-*(a.lam_logit + pair)));
+          const float y = (sum[c][0] / l[c] - sig * (sum[c + 1][0] / l[c + 1])) * a.v_mul;
+          static_cast<__nv_bfloat16*>(a.out)[pair * 128 + tid] = __float2bfloat16_rn(y);
+        }
+      } else {
+        const float lam = *(a.lambda + w.h);
+        float y[KP];
+        float ss = 0.f;
+#pragma unroll
+        for (int k = 0; k < KP; ++k) {
+          y[k] = (sum[0][k] / l[0] - lam * (sum[1][k] / l[1])) * a.v_mul;
+          ss = fmaf(y[k], y[k], ss);
+        }
+        const float f = norm_scale(a, ss, s_red);
+#pragma unroll
+        for (int k = 0; k < KP; ++k) {
+          const float wgt = (a.flags & 2) && a.norm_w ? *(a.norm_w + k * 128 + tid) : 1.f;
+          static_cast<__nv_bfloat16*>(a.out)[row * C::kWidth + k * 128 + tid] = __float2bfloat16_rn(y[k] * f * wgt);
+        }
       }
+      }
+      w.todo -= seg;
+      w.tile += seg;
+      if (!kByRow && w.tile == w.tiles) next_row<KP>(a, w);
     }
-    const size_t row = static_cast<size_t>(w.b) * a.H + w.h;
-    if constexpr (kByRow) {
-#pragma unroll
-      for (int c = 0; c < C::kMaxCols; ++c) {
-        if (tid == 0) s_x[c] = top[c], s_x[C::kMaxCols + c] = l[c];
-#pragma unroll
-        for (int k = 0; k < KP; ++k) s_x[2 * C::kMaxCols + c * C::kWidth + k * 128 + tid] = sum[c][k];
-      }
-    } else if (!whole) {
-      float* rec = p.rec + static_cast<size_t>(2 * range + (starts ? 1 : 0)) * (2 * cols + cols * C::kWidth);
-#pragma unroll
-      for (int c = 0; c < C::kMaxCols; ++c) {
-        if (c >= cols) break;
-        if (tid == 0) rec[c] = top[c], rec[cols + c] = l[c];
-#pragma unroll
-        for (int k = 0; k < KP; ++k) rec[2 * cols + c * C::kWidth + k * 128 + tid] = sum[c][k];
-      }
-    } else if constexpr (KP == 1) {
-#pragma unroll
-      for (int c = 0; c < C::kMaxCols; c += 2) {
-        if (c >= cols) break;
-        const size_t pair = row * (cols / 2) + c / 2;
-        const float sig = 1.f / (1.f + __expf(-*(a.lam_logit + pair)));
-        const float y = (sum[c][0] / l[c] - sig * (sum[c + 1][0] / l[c + 1])) * a.v_mul;
-        static_cast<__nv_bfloat16*>(a.out)[pair * 128 + tid] = __float2bfloat16_rn(y);
-      }
-    } else {
-      const float lam = *(a.lambda + w.h);
-      float y[KP];
-      float ss = 0.f;
-#pragma unroll
-      for (int k = 0; k < KP; ++k) {
-        y[k] = (sum[0][k] / l[0] - lam * (sum[1][k] / l[1])) * a.v_mul;
-        ss = fmaf(y[k], y[k], ss);
-      }
-      const float f = norm_scale(a, ss, s_red);
-#pragma unroll
-      for (int k = 0; k < KP; ++k) {
-        const float wgt = (a.flags & 2) && a.norm_w ? *(a.norm_w + k * 128 + tid) : 1.f;
-        static_cast<__nv_bfloat16*>(a.out)[row * C::kWidth + k * 128 + tid] = __float2bfloat16_rn(y[k] * f * wgt);
-      }
-    }
-    }
-    w.todo -= seg;
-    w.tile += seg;
-    if (!kByRow && w.tile == w.tiles) next_row<KP>(a, w);
   }
-  }  // consumers
 
   if constexpr (kByRow) {
     // Every block's piece lies in its ring, which nothing uses any more. The columns' pairs are dealt out
@@ -836,11 +860,12 @@ cudaError_t launch(const Kv4DecodeArgs& a, cudaStream_t st) {
   const long long tiles = (static_cast<long long>(a.max_pages) * a.page_size + C::kTileKeys - 1) / C::kTileKeys;
   const long long rows = static_cast<long long>(a.B) * a.H;
   // Few keys: a row over a cluster, of as many blocks as leave it two tiles each and are resident at once;
-  // where the rows' blocks then have at most kFewTiles more tiles than an equal share. (The second kernel
-  // and the ranges cost about that. GPU time of a call so and by ranges: 8 rows of 777 keys, V2, 5.8 and
-  // 8.7 us; 400 rows of 1000, 16.2 and 21.5; 48 rows of 1500, V1, 9.9 and 12.8; 96 rows of 3000, V1, where
-  // clusters of two leave a third of the machine idle, 23.6 and 20.9. The host has one launch less as well.
-  // Only up to 8 tiles a block, as the tables' capacity is not the sequences' length.)
+  // where the rows' blocks then have at most kFewTiles more tiles than an equal share: the second kernel
+  // and the ranges cost about that. (GPU time of a call so and by ranges: 8 rows of 777 keys, V2, 5.9 and
+  // 9.1 us; 400 rows of 1000, 16.0 and 21.8; 48 rows of 1500, V1, 10.1 and 12.2; 240 of 800, 15.2 and 18.6;
+  // 96 of 3000, V1, where clusters of two would leave a third of the machine idle, 23.6 and 20.3. The host
+  // has one launch less as well. Only up to 8 tiles a block: the tables' capacity, which is all the host
+  // knows, is not the sequences' length.)
   int parts = 1;
   while (parts < 8 && parts * 2 < tiles && rows * parts * 2 <= C::kGrid) parts *= 2;
   if (rows <= C::kGrid && rows * tiles <= 8LL * C::kGrid &&
