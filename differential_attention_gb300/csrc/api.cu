@@ -2135,8 +2135,9 @@ DIFFATTN_API int diffattn_paged_plan(const int* seqlens, const int* new_tokens, 
   if (!seqlens || !new_tokens || !seqlens_out || !block_table || !free_ring || !ring_state ||
       !ring_state_out || !cu_seqlens_q || !cu_seqlens_k || (!slot_map && total_max > 0))
     return fail(DIFFATTN_ERR_ARG, "%s: null pointer", fn);
-  if (B < 1 || B > da::kPlanMaxRequests || max_pages < 1 || num_pages < 1 || page_size < 1 || total_max < 0)
-    return fail(DIFFATTN_ERR_SHAPE, "%s: need 1 <= B <= %d, max_pages, num_pages, page_size >= 1 and total_max >= 0",
+  if (B < 1 || B > da::kPlanMaxRequests || max_pages < 1 || num_pages < 1 || page_size < 1 || total_max < 0 ||
+      total_max > (1 << 30))
+    return fail(DIFFATTN_ERR_SHAPE, "%s: need 1 <= B <= %d, max_pages, num_pages, page_size >= 1 and 0 <= total_max <= 2^30",
                 fn, da::kPlanMaxRequests);
   if (static_cast<long long>(max_pages) * page_size > (1LL << 30) ||
       static_cast<long long>(num_pages) * page_size > 0x7fffffffLL || num_pages > (1 << 30))
@@ -2191,10 +2192,13 @@ int decode_kv4_impl(const char* fn, da::Kv4DecodeArgs& a, int cols, int width, i
   int rc = check_kv4(fn, a.H, width, width, a.num_pages, a.page_size, k_exp, v_exp);
   if (!rc) rc = check_kv4_tables(fn, a.B, a.page_size, a.max_pages);
   if (rc) return rc;
+  // (a block's share of the tiles is counted in 32 bits)
+  if (static_cast<long long>(a.B) * a.H > (1LL << 46) / (static_cast<long long>(a.max_pages) * a.page_size))
+    return fail(DIFFATTN_ERR_SHAPE, "%s: need B * heads of the cache * max_pages * page_size <= 2^46", fn);
   if (!aligned(a.q, 16) || !aligned(a.pool, 16) || !aligned(a.out, 16) || !aligned(a.block_table, 4) ||
       !aligned(a.seqlens, 4) || !aligned(a.lambda, 4) || !aligned(a.lam_logit, 4) || !aligned(a.norm_w, 16))
     return fail(DIFFATTN_ERR_ALIGN, "%s: tensors must be 16-byte aligned", fn);
-  const size_t need = da::kv4_decode_workspace_bytes(a.B, a.H, cols, width);
+  const size_t need = da::kv4_decode_workspace_bytes(cols, width);
   if (!a.ws || ws_bytes < need || !aligned(a.ws, 256))
     return fail(DIFFATTN_ERR_WORKSPACE, "%s: need a 256-byte aligned workspace of %zu bytes", fn, need);
   rc = check_device();
@@ -2269,7 +2273,7 @@ DIFFATTN_API int diffattn_decode_kv4_workspace_size(int B, int H, int d, int dv,
   if (!bytes) return fail(DIFFATTN_ERR_ARG, "%s: null pointer", fn);
   if (B < 1 || B > da::kPlanMaxRequests || H < 1 || H > 65535 || d != 128 || dv != 256)
     return fail(DIFFATTN_ERR_SHAPE, "%s: need 1 <= B <= %d, 1 <= H <= 65535, d = 128, dv = 256", fn, da::kPlanMaxRequests);
-  *bytes = da::kv4_decode_workspace_bytes(B, H, 2, 256);
+  *bytes = da::kv4_decode_workspace_bytes(2, 256);
   return ok();
 }
 
@@ -2316,7 +2320,7 @@ DIFFATTN_API int diffattn_v2_decode_kv4_workspace_size(int B, int Hq, int Hkv, i
   if (B < 1 || B > da::kPlanMaxRequests || Hkv < 1 || Hkv > 65535 || Hq < 1 || d != 128 ||
       !(Hq == 2LL * Hkv || Hq == 4LL * Hkv || Hq == 8LL * Hkv))
     return fail(DIFFATTN_ERR_SHAPE, "%s: need 1 <= B <= %d, d = 128 and Hq / Hkv in {2, 4, 8}", fn, da::kPlanMaxRequests);
-  *bytes = da::kv4_decode_workspace_bytes(B, Hkv, Hq / Hkv, 128);
+  *bytes = da::kv4_decode_workspace_bytes(Hq / Hkv, 128);
   return ok();
 }
 

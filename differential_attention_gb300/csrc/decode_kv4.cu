@@ -45,6 +45,7 @@
 #include <cmath>
 #include <type_traits>
 
+#include "early.cuh"
 #include "internal.h"
 #include "kv4.cuh"
 #include "ptx.cuh"
@@ -105,6 +106,11 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
   return v;
 }
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float a;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(a) : "r"(addr) : "memory");
+  return a;
+}
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                     uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -122,9 +128,12 @@ struct Walk {
   int todo;         // tiles of the range, and the costs of the rows that begin in it, from here on
   long long first;  // where the row's tiles begin among all costs
 };
+// kEarly: before grid_wait(), in a kernel that knows of the write by the release of the one before it; from
+// L2, so that no line an SM kept from an earlier kernel is read.
+template <bool kEarly = false>
 __device__ __forceinline__ int clamp_len(const Kv4DecodeArgs& a, int b) {
   const int cap = a.max_pages * a.page_size;
-  const int n = *(a.seqlens + b);
+  const int n = kEarly ? __ldcg(a.seqlens + b) : *(a.seqlens + b);
   return n < 0 ? 0 : n > cap ? cap : n;
 }
 template <int KP>
@@ -167,7 +176,7 @@ struct Cut {
 
 // The batch's rows one behind the other, cut in n equal parts. pre[i]: the costs (of one head) before
 // thread i's share of the sequences. A whole block of NT threads.
-template <int KP, int NT>
+template <int KP, int NT, bool kEarly>
 struct Ranges {
   long long pre[NT + 1];
   long long sum[NT / 32];
@@ -176,7 +185,7 @@ struct Ranges {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, per = (a.B + NT - 1) / NT;
     const int lo = min(a.B, tid * per), hi = min(a.B, lo + per);
     long long incl = 0;
-    for (int b = lo; b < hi; ++b) incl += cost_of<KP>(clamp_len(a, b));
+    for (int b = lo; b < hi; ++b) incl += cost_of<KP>(clamp_len<kEarly>(a, b));
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const long long o = __shfl_up_sync(0xffffffffu, incl, d);
@@ -209,7 +218,7 @@ struct Ranges {
     long long at = pre[share];
     const int end = min(a.B, (share + 1) * per);
     for (int b0 = share * per; b0 < end; b0 += 32) {
-      const int b = b0 + lane, len = b < end ? clamp_len(a, b) : 0, cost = cost_of<KP>(len);
+      const int b = b0 + lane, len = b < end ? clamp_len<kEarly>(a, b) : 0, cost = cost_of<KP>(len);
       int incl = cost;
       if (per > 1) {
 #pragma unroll
@@ -315,7 +324,7 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, Cfg<KP>::kCtas) kv4_decode_
   constexpr int kWarps = C::kWarps, kThreads = C::kThreads;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bars[2 * C::kStages];
-  __shared__ Ranges<KP, kThreads> s_ranges;
+  __shared__ Ranges<KP, kThreads, false> s_ranges;
   __shared__ int s_abort;
   __shared__ float s_m[2][kWarps][8], s_l[2][kWarps][8];
   __shared__ float s_red[kWarps];
@@ -489,9 +498,8 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, Cfg<KP>::kCtas) kv4_decode_
       l0 = l1 = 0.f;
       // One tile; `last`: it may be the row's last one, and short.
       auto take = [&](int i, auto last) {
-        // record w + 4 k of the tile is warp w's; `left`: keys from its first one on
         constexpr int R = C::kRecs;
-        // record w + 4 r of the tile is warp w's; `left`: keys from its first one on
+        // record w + kWarps r of the tile is warp w's; `left`: keys from its first one on
         const int left = last ? w.len - ((w.tile + i) * C::kTileRecs + warp) * 16 : 0;
         if (alive && !(last && left <= 0)) {
           const uint32_t rec = ring + stage * C::kStage + warp * C::kRecord + lane * 16;
@@ -631,65 +639,65 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, Cfg<KP>::kCtas) kv4_decode_
       const int last_parity = parity;
       parity ^= 1;
       if (tid < 128) {
-      float sum[C::kMaxCols][KP], l[C::kMaxCols], top[C::kMaxCols];
-#pragma unroll
-      for (int c = 0; c < C::kMaxCols; ++c) {
-        float mx = s_m[last_parity][0][c];
-#pragma unroll
-        for (int i = 1; i < kWarps; ++i) mx = fmaxf(mx, s_m[last_parity][i][c]);
-        top[c] = mx;
-        l[c] = 0.f;
-#pragma unroll
-        for (int i = 0; i < kWarps; ++i) l[c] += s_l[last_parity][i][c] * ex2_approx(s_m[last_parity][i][c] - mx);
-#pragma unroll
-        for (int k = 0; k < KP; ++k) {
-          sum[c][k] = 0.f;
-#pragma unroll
-          for (int i = 0; i < kWarps / 2; ++i) sum[c][k] += s_o[(i * C::kMaxCols + c) * C::kPitch + k * 128 + tid];
-        }
-      }
-      const size_t row = static_cast<size_t>(w.b) * a.H + w.h;
-      if constexpr (kByRow) {
+        float sum[C::kMaxCols][KP], l[C::kMaxCols], top[C::kMaxCols];
 #pragma unroll
         for (int c = 0; c < C::kMaxCols; ++c) {
-          if (tid == 0) s_x[c] = top[c], s_x[C::kMaxCols + c] = l[c];
+          float mx = s_m[last_parity][0][c];
 #pragma unroll
-          for (int k = 0; k < KP; ++k) s_x[2 * C::kMaxCols + c * C::kWidth + k * 128 + tid] = sum[c][k];
+          for (int i = 1; i < kWarps; ++i) mx = fmaxf(mx, s_m[last_parity][i][c]);
+          top[c] = mx;
+          l[c] = 0.f;
+#pragma unroll
+          for (int i = 0; i < kWarps; ++i) l[c] += s_l[last_parity][i][c] * ex2_approx(s_m[last_parity][i][c] - mx);
+#pragma unroll
+          for (int k = 0; k < KP; ++k) {
+            sum[c][k] = 0.f;
+#pragma unroll
+            for (int i = 0; i < kWarps / 2; ++i) sum[c][k] += s_o[(i * C::kMaxCols + c) * C::kPitch + k * 128 + tid];
+          }
         }
-      } else if (!whole) {
-        float* rec = p.rec + static_cast<size_t>(2 * range + (starts ? 1 : 0)) * (2 * cols + cols * C::kWidth);
+        const size_t row = static_cast<size_t>(w.b) * a.H + w.h;
+        if constexpr (kByRow) {
 #pragma unroll
-        for (int c = 0; c < C::kMaxCols; ++c) {
-          if (c >= cols) break;
-          if (tid == 0) rec[c] = top[c], rec[cols + c] = l[c];
+          for (int c = 0; c < C::kMaxCols; ++c) {
+            if (tid == 0) s_x[c] = top[c], s_x[C::kMaxCols + c] = l[c];
 #pragma unroll
-          for (int k = 0; k < KP; ++k) rec[2 * cols + c * C::kWidth + k * 128 + tid] = sum[c][k];
+            for (int k = 0; k < KP; ++k) s_x[2 * C::kMaxCols + c * C::kWidth + k * 128 + tid] = sum[c][k];
+          }
+        } else if (!whole) {
+          float* rec = p.rec + static_cast<size_t>(2 * range + (starts ? 1 : 0)) * (2 * cols + cols * C::kWidth);
+#pragma unroll
+          for (int c = 0; c < C::kMaxCols; ++c) {
+            if (c >= cols) break;
+            if (tid == 0) rec[c] = top[c], rec[cols + c] = l[c];
+#pragma unroll
+            for (int k = 0; k < KP; ++k) rec[2 * cols + c * C::kWidth + k * 128 + tid] = sum[c][k];
+          }
+        } else if constexpr (KP == 1) {
+#pragma unroll
+          for (int c = 0; c < C::kMaxCols; c += 2) {
+            if (c >= cols) break;
+            const size_t pair = row * (cols / 2) + c / 2;
+            const float sig = 1.f / (1.f + __expf(-*(a.lam_logit + pair)));
+            const float y = (sum[c][0] / l[c] - sig * (sum[c + 1][0] / l[c + 1])) * a.v_mul;
+            static_cast<__nv_bfloat16*>(a.out)[pair * 128 + tid] = __float2bfloat16_rn(y);
+          }
+        } else {
+          const float lam = *(a.lambda + w.h);
+          float y[KP];
+          float ss = 0.f;
+#pragma unroll
+          for (int k = 0; k < KP; ++k) {
+            y[k] = (sum[0][k] / l[0] - lam * (sum[1][k] / l[1])) * a.v_mul;
+            ss = fmaf(y[k], y[k], ss);
+          }
+          const float f = norm_scale(a, ss, s_red);
+#pragma unroll
+          for (int k = 0; k < KP; ++k) {
+            const float wgt = (a.flags & 2) && a.norm_w ? *(a.norm_w + k * 128 + tid) : 1.f;
+            static_cast<__nv_bfloat16*>(a.out)[row * C::kWidth + k * 128 + tid] = __float2bfloat16_rn(y[k] * f * wgt);
+          }
         }
-      } else if constexpr (KP == 1) {
-#pragma unroll
-        for (int c = 0; c < C::kMaxCols; c += 2) {
-          if (c >= cols) break;
-          const size_t pair = row * (cols / 2) + c / 2;
-          const float sig = 1.f / (1.f + __expf(-*(a.lam_logit + pair)));
-          const float y = (sum[c][0] / l[c] - sig * (sum[c + 1][0] / l[c + 1])) * a.v_mul;
-          static_cast<__nv_bfloat16*>(a.out)[pair * 128 + tid] = __float2bfloat16_rn(y);
-        }
-      } else {
-        const float lam = *(a.lambda + w.h);
-        float y[KP];
-        float ss = 0.f;
-#pragma unroll
-        for (int k = 0; k < KP; ++k) {
-          y[k] = (sum[0][k] / l[0] - lam * (sum[1][k] / l[1])) * a.v_mul;
-          ss = fmaf(y[k], y[k], ss);
-        }
-        const float f = norm_scale(a, ss, s_red);
-#pragma unroll
-        for (int k = 0; k < KP; ++k) {
-          const float wgt = (a.flags & 2) && a.norm_w ? *(a.norm_w + k * 128 + tid) : 1.f;
-          static_cast<__nv_bfloat16*>(a.out)[row * C::kWidth + k * 128 + tid] = __float2bfloat16_rn(y[k] * f * wgt);
-        }
-      }
       }
       w.todo -= seg;
       w.tile += seg;
@@ -754,9 +762,9 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const Params p
   __shared__ float s_red[W / 32];
   const Kv4DecodeArgs& a = p.a;
   const int tid = threadIdx.x, cols = p.cols;
-  // (All but the pieces is known before the first kernel ends: it released this one after its own wait, so
-  // the lengths are there.)
-  __shared__ Ranges<KP, kMergeThreads> s_ranges;
+  // All but the pieces is known before the first kernel ends: it released this one after its own wait, so
+  // the lengths, the lambdas and the weights are there.
+  __shared__ Ranges<KP, kMergeThreads, true> s_ranges;
   __shared__ Walk s_walk;
   s_ranges.fill(a);
   const long long total = s_ranges.total(a);
@@ -769,12 +777,13 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const Params p
       const int row = blockIdx.x / (cols / 2);
       w.b = row / a.H;
       w.h = row - w.b * a.H;
-      w.len = clamp_len(a, w.b);
+      w.len = clamp_len<true>(a, w.b);
       w.tiles = tiles_of<KP>(w.len);
       w.first = s_ranges.pre[w.b] * a.H + static_cast<long long>(w.h) * cost_of<KP>(w.len) + Cfg<KP>::kRowCost;
     } else if (static_cast<int>(blockIdx.x) + 1 < n) {
       s_ranges.locate(a, cut, blockIdx.x + 1, w);
-      if (w.tile == 0 || cut.start(blockIdx.x) > w.first) w.tiles = 0;  // it begins no tile inside a row, or is not the first to
+      // no row is this block's: range i + 1 begins with one, or is not the first to begin inside its row
+      if (w.tile == 0 || cut.start(blockIdx.x) > w.first) w.tiles = 0;
     }
     if (tid == 0) s_walk = w;
   }
@@ -793,8 +802,10 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const Params p
   const size_t row = static_cast<size_t>(d.b) * a.H + d.h;
   const int pair = tid / W, ch = tid % W;  // the output channel of the end
   const bool mine = tid < nc / 2 * W;
-  const float lam = !mine ? 0.f : KP == 2 ? *(a.lambda + d.h) : 1.f / (1.f + __expf(-*(a.lam_logit + row * (cols / 2) + c0 / 2 + pair)));
-  const float wgt = KP == 2 && mine && (a.flags & 2) && a.norm_w ? *(a.norm_w + ch) : 1.f;
+  const float lam = !mine     ? 0.f
+                    : KP == 2 ? __ldcg(a.lambda + d.h)
+                              : 1.f / (1.f + __expf(-__ldcg(a.lam_logit + row * (cols / 2) + c0 / 2 + pair)));
+  const float wgt = KP == 2 && mine && (a.flags & 2) && a.norm_w ? __ldcg(a.norm_w + ch) : 1.f;
   grid_wait();
   grid_release();
   float m = -FLT_MAX, l = 0.f;
@@ -888,8 +899,7 @@ cudaError_t launch(const Kv4DecodeArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-size_t kv4_decode_workspace_bytes(int B, int H, int cols, int width) {
-  (void)B, (void)H;
+size_t kv4_decode_workspace_bytes(int cols, int width) {
   const size_t grid = width == 128 ? Cfg<1>::kGrid : Cfg<2>::kGrid;
   return 2 * grid * (2 * cols + static_cast<size_t>(cols) * width) * sizeof(float);
 }

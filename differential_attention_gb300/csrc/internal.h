@@ -1,6 +1,5 @@
 // internal.h -- declarations shared by the library's translation units (not part of the ABI).
 #pragma once
-#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda.h>
@@ -298,47 +297,6 @@ long long decode_noalloc_max_units();  // largest B * H whose partials fit (one 
 int decode_noalloc_splits(int B, int Lmax, int H, int* chunk_out);  // splits the no-alloc call runs
 cudaError_t launch_decode_noalloc(const DecodeArgs& a, cudaStream_t s);
 
-// Launches a kernel that calls grid_wait() first: it is set up while the one before it in the stream ends.
-template <typename P, typename... A>
-inline cudaError_t launch_early(void (*kernel)(P, A...), unsigned grid, int block, int smem, cudaStream_t st, int cluster,
-                                const P& p, A... more) {
-  cudaLaunchAttribute at[2] = {};
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = cluster;
-  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cfg.attrs = at;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p, more...);
-}
-
-// launch_early of a kernel with more than 48 KB of dynamic shared memory (at most `limit`). The limit is
-// raised on each device's first call (`raised`: a bit each), and again where a launch is refused, as
-// after a reset of the device.
-template <typename P>
-inline cudaError_t launch_early_large(void (*kernel)(P), unsigned grid, int block, int smem, int limit, cudaStream_t st,
-                                      int cluster, const P& p, std::atomic<uint64_t>& raised) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-  if (raised.load(std::memory_order_relaxed) & bit) {
-    e = launch_early(kernel, grid, block, smem, st, cluster, p);
-    if (e != cudaErrorInvalidValue) return e;
-    cudaGetLastError();
-  }
-  e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, limit);
-  if (e != cudaSuccess) return e;
-  raised.fetch_or(bit, std::memory_order_relaxed);
-  return launch_early(kernel, grid, block, smem, st, cluster, p);
-}
-
 // The 4-bit cache (kv4_rows.cu, decode_kv4.cu). Pools: [num_pages, H, page_size / 16, record], a
 // record 16 tokens of one head: kp K planes and vp V planes of 128 channels (kv4.cuh).
 struct Kv4AppendArgs {
@@ -380,7 +338,7 @@ struct Kv4DecodeArgs {
   float v_mul;      // 2^v_exp
   void* ws;
 };
-size_t kv4_decode_workspace_bytes(int B, int H, int cols, int width);
+size_t kv4_decode_workspace_bytes(int cols, int width);
 cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a, cudaStream_t s);
 cudaError_t status_decode_kv4(int* v);
 

@@ -1,5 +1,6 @@
 // kv4_rows.cu -- rows into and out of the 4-bit cache: diffattn_kv4_append rounds new K and V rows
 // and writes them at their slots, diffattn_kv4_gather reads cached rows back as packed bf16.
+#include "early.cuh"
 #include "internal.h"
 #include "kv4.cuh"
 #include "ptx.cuh"
@@ -47,7 +48,9 @@ __device__ __forceinline__ Block round_block(const uint4& w0, const uint4& w1, f
 // A warp rounds 8 rows of one head, plane after plane: a lane 32 channels of a row of K (two blocks, one
 // 16-byte piece of the record), then the same 16 channels of two rows of V, which are one piece too
 // where the rows' slots are the two of a pair. The next plane is loaded while one is rounded. What
-// bounds it: the bytes (2 read, 9/16 written a channel).
+// bounds it: the bytes (2 read, 9/16 written a channel): 16K rows of 12 V1 heads, 258 MB, take 43.9 us,
+// 5.9 TB/s of a copy's 6.78, with 55 % of the ALU pipe and 63 % of the issue slots in use. (The
+// first form, with a division for each value, took about 100.)
 template <int KP>
 __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const Kv4AppendArgs a) {
   grid_wait();
@@ -131,22 +134,23 @@ __device__ __forceinline__ uint32_t half2_to_bf16x2(uint32_t h, float f) {
   return *reinterpret_cast<const uint32_t*>(&o);
 }
 
-// A warp reads a record of one sequence for some of its heads, plane after plane with the next one's
-// loads under way, and writes its rows, two at a time: a lane 8 channels, so that each store of the warp
-// is whole rows of 128 channels (16 bytes a lane, side by side). What bounds it: the bytes (9/16 read,
-// 2 written a channel).
+// A warp reads a record of one sequence and head, plane after plane with the next one's loads under way,
+// and writes its rows, two at a time: a lane 8 channels, so that each store of the warp is whole rows of
+// 128 channels (16 bytes a lane, side by side). What bounds it: the bytes (9/16 read, 2 written a channel,
+// so four fifths of them writes): 6 x 8160 tokens of 8 V2 heads, 257 MB, take 41.4 us, 6.2 TB/s of a
+// copy's 6.78, 4 x 4080 of 12 V1 heads 42.5. (Two or four heads a warp, which share one look-up of the
+// sequence and the page: 42.3 and 42.3 us, 43.8 and 43.7. Streaming stores: no difference.)
 //
 // Sequence b's records have the warps from cu[b] / 16 + 2 b on: n rows touch at most n / 16 + 2 records,
 // so that the ranges do not overlap, whatever the sequences' first tokens are.
 template <int KP>
-__global__ void __launch_bounds__(kRowThreads) kv4_gather_kernel(const Kv4GatherArgs a, int heads) {
+__global__ void __launch_bounds__(kRowThreads) kv4_gather_kernel(const Kv4GatherArgs a) {
   grid_wait();
   grid_release();
   const int lane = threadIdx.x & 31;
   const long long i = static_cast<long long>(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
-  const int groups = (a.H + heads - 1) / heads, h0 = static_cast<int>(i % groups) * heads;
-  const int n_steps = min(heads, a.H - h0) * 2 * KP;
-  const long long u = i / groups;
+  const int h = static_cast<int>(i % a.H);
+  const long long u = i / a.H;
   if (u >= a.total / 16 + 2LL * a.B) return;
   // the last b whose first warp is not behind this one: 32 candidates at a time
   int lo = 0, n = a.B;
@@ -179,8 +183,8 @@ __global__ void __launch_bounds__(kRowThreads) kv4_gather_kernel(const Kv4Gather
     flag_device_error(DEV_BAD_INDEX);
     page = 0;
   }
-  const size_t head_bytes = static_cast<size_t>(a.page_size >> 4) * (2 * KP * kKv4Plane);
-  const uint8_t* rec = a.pool + (static_cast<size_t>(page) * a.H + h0) * head_bytes + (off >> 4) * (2 * KP * kKv4Plane);
+  const uint8_t* rec = a.pool + ((static_cast<size_t>(page) * a.H + h) * (a.page_size >> 4) + (off >> 4)) *
+                                    static_cast<size_t>(2 * KP * kKv4Plane);
   const long long row0 = c0 + (tok - first);  // output row of the record's token 0 (it may not be wanted)
   // lane: rows 2 i + hi, 8 channels from 8 c
   const int c = lane & 15, hi = lane >> 4;
@@ -190,10 +194,9 @@ __global__ void __launch_bounds__(kRowThreads) kv4_gather_kernel(const Kv4Gather
   struct Plane {
     uint32_t codes[8], scales[4];
   };
-  auto load = [&](int step, Plane& x) {
-    const int pl = step % (2 * KP);
+  auto load = [&](int pl, Plane& x) {
     const bool is_k = pl < KP;
-    const uint8_t* p = rec + (step / (2 * KP)) * head_bytes + pl * kKv4Plane;
+    const uint8_t* p = rec + pl * kKv4Plane;
 #pragma unroll
     for (int i = 0; i < 8; ++i)  // tokens 2 i + hi: a quad of tokens is 128 (K) or 16 (V) bytes on, its second half 512
       x.codes[i] = *reinterpret_cast<const uint32_t*>(p + (is_k ? k_at + (i >> 1) * 128 : v_at + (i >> 1) * 16) + (i & 1) * 512);
@@ -201,8 +204,7 @@ __global__ void __launch_bounds__(kRowThreads) kv4_gather_kernel(const Kv4Gather
     for (int i = 0; i < 4; ++i)  // a quad's scales: K's two rows by two blocks, V's four rows
       x.scales[i] = *reinterpret_cast<const uint32_t*>(p + (is_k ? k_sc + i * 32 : v_sc + i * 4));
   };
-  auto store = [&](int step, const Plane& x) {
-    const int pl = step % (2 * KP), h = h0 + step / (2 * KP);
+  auto store = [&](int pl, const Plane& x) {
     const bool is_k = pl < KP;
     const float mul = is_k ? a.k_mul : a.v_mul;
     const int shift = is_k ? k_sh : v_sh;
@@ -218,13 +220,12 @@ __global__ void __launch_bounds__(kRowThreads) kv4_gather_kernel(const Kv4Gather
           make_uint4(half2_to_bf16x2(v[0], s), half2_to_bf16x2(v[1], s), half2_to_bf16x2(v[2], s), half2_to_bf16x2(v[3], s));
     }
   };
-  Plane x, y;
-  load(0, x);
-  for (int step = 0; step < n_steps; step += 2) {  // n_steps is even
-    load(step + 1, y);
-    store(step, x);
-    if (step + 2 < n_steps) load(step + 2, x);
-    store(step + 1, y);
+  Plane x[2];
+  load(0, x[0]);
+#pragma unroll
+  for (int pl = 0; pl < 2 * KP; ++pl) {
+    if (pl + 1 < 2 * KP) load(pl + 1, x[(pl + 1) & 1]);
+    store(pl, x[pl & 1]);
   }
 }
 
@@ -239,14 +240,9 @@ cudaError_t launch_kv4_append(const Kv4AppendArgs& a, cudaStream_t st) {
 
 cudaError_t launch_kv4_gather(const Kv4GatherArgs& a, cudaStream_t st) {
   if (a.total == 0) return cudaSuccess;
-  // Several heads a warp share one look-up of the sequence and the page, where that leaves warps
-  // enough to fill the machine (152 SMs, 24 each) twice.
-  const long long units = a.total / 16 + 2LL * a.B;
-  int heads = 4;
-  while (heads > 1 && units * ((a.H + heads - 1) / heads) < 2 * 152 * 24) heads >>= 1;
-  const long long warps = units * ((a.H + heads - 1) / heads);
+  const long long warps = (a.total / 16 + 2LL * a.B) * a.H;
   const unsigned blocks = static_cast<unsigned>((warps * 32 + kRowThreads - 1) / kRowThreads);
-  return launch_early(a.kp == 1 ? kv4_gather_kernel<1> : kv4_gather_kernel<2>, blocks, kRowThreads, 0, st, 1, a, heads);
+  return launch_early(a.kp == 1 ? kv4_gather_kernel<1> : kv4_gather_kernel<2>, blocks, kRowThreads, 0, st, 1, a);
 }
 
 cudaError_t status_kv4_rows(int* v) { return read_clear_status(v); }

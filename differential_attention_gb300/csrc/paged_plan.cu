@@ -11,7 +11,9 @@
 // What bounds it is latency: a step moves a few hundred kilobytes at most. So it is one launch of one
 // cluster of up to 8 blocks. Every block forms all the sums (for 1024 requests one pass of its
 // threads), then the cluster meets once, and each block writes its share. The one meeting is what
-// lets the lengths and the ring's state be updated in place: all blocks have read them by then.
+// lets the lengths and the ring's state be updated in place: all blocks have read them by then. 256
+// requests of one new token take 5.1 us, 48 with 33K new tokens 8.5 (GPU time of a call).
+#include "early.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -212,7 +214,9 @@ cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t st) {
                a.B, a.max_pages, a.num_pages, a.page_size, a.total_max};
   const int smem = (4 * a.B + 3) * static_cast<int>(sizeof(int));
   static_assert((4 * kPlanMaxRequests + 3) * 4 <= 200 * 1024, "shared memory");
-  // blocks for the slots and the requests, about two rounds of their threads each
+  // Blocks for the slots and the requests, about two rounds of their threads each. (GPU time of 1, 2, 4 and
+  // 8 blocks for 33K new tokens: 31.3, 18.3, 11.7, 8.5 us; for 256 requests of one token one block takes
+  // 5.1 and 8 take 5.5.)
   const int work = a.total_max > a.B ? a.total_max : a.B;
   int blocks = 1;
   while (blocks < kPlanCluster && blocks * 2 * kPlanThreads < work) blocks *= 2;

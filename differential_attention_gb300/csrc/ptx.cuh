@@ -171,24 +171,9 @@ __device__ __forceinline__ void st_cluster_v4(uint32_t addr, float a, float b, f
                "f"(c), "f"(d)
                : "memory");
 }
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float a;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(a) : "r"(addr) : "memory");
-  return a;
-}
 __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float a) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(a) : "memory");
 }
-
-// ---------------------------------------------------------------------------------------------
-// programmatic launches (a kernel set up while the one before it in the stream still runs)
-// ---------------------------------------------------------------------------------------------
-// Until the kernels before this one are done and their writes seen (by plain loads: what they wrote was not
-// constant while this kernel ran, so nothing of it is read through __ldg). Every block of a kernel that is
-// launched this way calls it, also one that has nothing to do: the kernel after it goes by that.
-__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-// From here on (in all blocks) the kernel after this one may be set up. After grid_wait().
-__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // ---------------------------------------------------------------------------------------------
 // TMA

@@ -877,7 +877,8 @@ DIFFATTN_API int diffattn_gda_decode_paged(const void* q, const void* k_pool, co
  * offsets are 0 and the slots -1, and diffattn_device_status() reports DIFFATTN_ERR_INDEX. A page
  * id outside [0, num_pages) in the ring or a table is passed on as it is; its tokens get slot -1,
  * and it is reported the same way.
- * Supported: B <= 8192, num_pages * page_size < 2^31, max_pages * page_size <= 2^30. One launch.
+ * Supported: B <= 8192, total_max <= 2^30, num_pages * page_size < 2^31, max_pages * page_size <=
+ * 2^30. One launch.
  * seqlens, new_tokens and the tables must not overlap other outputs than those named.
  * Errors: ERR_ARG, ERR_SHAPE, ERR_ALIGN, ERR_UNSUPPORTED, ERR_CUDA. */
 DIFFATTN_API int diffattn_paged_plan(const int* seqlens, const int* new_tokens, int* seqlens_out,
@@ -961,8 +962,8 @@ DIFFATTN_API int diffattn_kv4_gather(const void* pool, const int* block_table,
  * A used table entry outside [0, num_pages) reads page 0 and is reported by
  * diffattn_device_status() as DIFFATTN_ERR_INDEX. A call's result does not depend on the order in
  * which its blocks run: equal inputs give equal bits.
- * Supported: d = 128 (V1: dv = 256), page_size a multiple of 16, B <= 8192; V2: Hq / Hkv in
- * {2, 4, 8}.
+ * Supported: d = 128 (V1: dv = 256), page_size a multiple of 16, B <= 8192, B * H (V2: Hkv) *
+ * max_pages * page_size <= 2^46; V2: Hq / Hkv in {2, 4, 8}.
  * Errors: ERR_ARG, ERR_SHAPE, ERR_ALIGN, ERR_WORKSPACE, ERR_UNSUPPORTED, ERR_CUDA. */
 DIFFATTN_API int diffattn_decode_kv4_workspace_size(int B, int H, int d, int dv, size_t* bytes);
 DIFFATTN_API int diffattn_decode_kv4(const void* q, const void* pool, const int* block_table,

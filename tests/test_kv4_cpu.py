@@ -137,7 +137,7 @@ def test_plan_refusals(L):
         assert plan([(i, ODD4)]) == ALIGN, i
     assert plan(B=0) == SHAPE and plan(B=8193) == SHAPE
     assert plan(max_pages=0) == SHAPE and plan(num_pages=0) == SHAPE and plan(page_size=0) == SHAPE
-    assert plan(total_max=-1) == SHAPE
+    assert plan(total_max=-1) == SHAPE and plan(total_max=(1 << 30) + 1) == SHAPE
     assert plan(max_pages=1 << 20, page_size=2048) == SHAPE
     assert plan(num_pages=1 << 20, page_size=2048) == SHAPE
 
@@ -196,6 +196,7 @@ def test_decode_refusals(L):
     assert dec(flags=8) == ARG and dec(eps=0.0) == ARG and dec(ke=65) == ARG
     assert dec(d=64, dv=128) == SHAPE and dec(dv=128) == SHAPE and dec(B=0) == SHAPE and dec(B=8193) == SHAPE
     assert dec(H=0) == SHAPE and dec(page_size=20) == SHAPE and dec(max_pages=0) == SHAPE
+    assert dec(B=8192, H=9, max_pages=1 << 26) == SHAPE
     assert dec([(0, ODD16)]) == ALIGN and dec([(1, ODD16)]) == ALIGN and dec([(4, ODD16)]) == ALIGN
     assert dec([(2, ODD4)]) == ALIGN and dec([(3, ODD4)]) == ALIGN and dec([(5, ODD4)]) == ALIGN
     assert dec(ws=None) == WORKSPACE and dec(ws_bytes=need - 1) == WORKSPACE
@@ -222,6 +223,7 @@ def test_v2_decode_refusals(L):
     assert dec(flags=8) == ARG and dec(flags=2) == ARG and dec(ve=-70) == ARG
     assert dec(Hq=24) == SHAPE and dec(Hkv=0) == SHAPE and dec(d=64) == SHAPE and dec(B=0) == SHAPE
     assert dec(page_size=8) == SHAPE and dec(num_pages=0) == SHAPE and dec(max_pages=1 << 27) == SHAPE
+    assert dec(B=8192, Hq=36, Hkv=9, max_pages=1 << 26) == SHAPE
     assert dec([(0, ODD16)]) == ALIGN and dec([(5, ODD16)]) == ALIGN
     assert dec(ws_bytes=need - 1) == WORKSPACE
 
