@@ -1600,7 +1600,7 @@ def diffattn_paged_plan(seqlens, new_tokens, block_table, free_ring, ring_state,
     if out is None:
         if total_max < 0:
             raise ValueError("total_max must not be negative")
-        buf = torch.empty(3 * B + 4 + 2 * total_max, dtype=i32, device=seqlens.device)
+        buf = seqlens.new_empty(3 * B + 4 + 2 * total_max)  # (int32: `seqlens` is checked below)
         out = dict(zip(_PLAN, buf.unsafe_split_with_sizes(sizes)))  # (pieces, not views: the buffer itself is let go)
         p0 = buf.data_ptr()
         p = (p0, p0 + 4 * B, p0 + 4 * B + 8, p0 + 8 * B + 12, p0 + 12 * B + 16, p0 + 12 * B + 16 + 4 * total_max)
@@ -1689,8 +1689,7 @@ def diffattn_kv4_gather(pool, block_table, cu_seqlens, total: int, kw: int, vw: 
     table, max_pages = _kv4_table(block_table, dev, B)
     if out is None:
         n = max(0, total)
-        out = (torch.empty((n, H, kw), dtype=torch.bfloat16, device=pool.device),
-               torch.empty((n, H, vw), dtype=torch.bfloat16, device=pool.device))
+        out = (pool.new_empty(n, H, kw, dtype=torch.bfloat16), pool.new_empty(n, H, vw, dtype=torch.bfloat16))
     k, v = out
     _call(dev, lib().diffattn_kv4_gather, at, table, _operand("cu_seqlens", cu_seqlens, torch.int32, dev, (B + 1,)),
           None if starts is None else _operand("starts", starts, torch.int32, dev, (B,)),
@@ -1761,7 +1760,7 @@ def diffattn_v2_decode_kv4(q, pool, block_table, seqlens, lam_logit, k_exp: int 
     if workspace is None:
         workspace = _workspace(dev, diffattn_v2_decode_kv4_workspace_size(B, Hq, Hkv, d))
     if out is None:
-        out = torch.empty((B, Hq // 2, d), dtype=torch.bfloat16, device=q.device)
+        out = q.new_empty(B, Hq // 2, d)  # (bf16: `q` is checked below)
     _call(dev, lib().diffattn_v2_decode_kv4, _operand("q", q, torch.bfloat16, dev), at, table,
           _operand("seqlens", seqlens, torch.int32, dev, (B,)),
           _operand("lam_logit", lam_logit, torch.float32, dev, (B, Hq // 2)),

@@ -54,7 +54,6 @@ namespace da {
 namespace {
 
 constexpr int kSms = 152;
-constexpr int kMergeThreads = 512;
 constexpr int kFewTiles = 4;
 constexpr float kPScale = 10.f;                  // log2 of P's scale
 constexpr float kMoveRef = 14.f;                 // log2 P at which the reference moves
@@ -82,6 +81,10 @@ struct Cfg {
   static constexpr int kStages = KP == 1 ? 3 : 2;
   static constexpr int kPitch = kWidth + 4;      // floats of one column's row in the exchange
   static constexpr int kSmem = kStages * kStage + kWarps / 2 * kMaxCols * kPitch * 4;
+  // Threads of the second kernel, with few rows and else. Small blocks find room beside the first kernel's
+  // last ones, large ones have more pieces under way (V2, 96 sequences of 1 to 16K keys: 48.8 us with 256,
+  // 50.0 with 512; V1, 48 of 1 to 9001: 41.6 and 41.2).
+  static constexpr int kMergeFew = 512, kMerge = KP == 1 ? 256 : 512;
 };
 
 struct Params {
@@ -326,7 +329,7 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, Cfg<KP>::kCtas) kv4_decode_
   __shared__ __align__(8) uint64_t bars[2 * C::kStages];
   __shared__ Ranges<KP, kThreads, false> s_ranges;
   __shared__ int s_abort;
-  __shared__ float s_m[2][kWarps][8], s_l[2][kWarps][8];
+  __shared__ float s_m[kWarps][8], s_l[kWarps][8];
   __shared__ float s_red[kWarps];
   const Kv4DecodeArgs& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -443,7 +446,7 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, Cfg<KP>::kCtas) kv4_decode_
     float cs0 = 0.f, cs1 = 0.f;  // what a sum of columns 2t and 2t + 1 is to be multiplied with
     float o[KP * 8][4];
     float m0, m1, l0, l1;        // references (less kPScale) and sums of columns 2t, 2t + 1
-    int stage = 0, parity = 0;
+    int stage = 0;
     uint32_t phase = 0;
     bool alive = true;
 
@@ -597,24 +600,47 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, Cfg<KP>::kCtas) kv4_decode_
         }
       }
 
-      // Join the warps' pieces.
+      // Join the warps' pieces. (What the row's end needs of global memory is loaded first.)
+      const size_t row = static_cast<size_t>(w.b) * a.H + w.h;
+      const bool out_thread = tid < 128;
+      float lam[C::kMaxCols / 2], wgt[KP];
+#pragma unroll
+      for (int c = 0; c < C::kMaxCols / 2; ++c)
+        lam[c] = !whole || 2 * c >= cols ? 0.f : KP == 2 ? *(a.lambda + w.h) : *(a.lam_logit + row * (cols / 2) + c);
+#pragma unroll
+      for (int k = 0; k < KP; ++k)
+        wgt[k] = KP == 2 && whole && out_thread && (a.flags & 2) && a.norm_w ? *(a.norm_w + k * 128 + tid) : 1.f;
 #pragma unroll
       for (int d = 4; d < 32; d <<= 1) {
         l0 += __shfl_xor_sync(0xffffffffu, l0, d);
         l1 += __shfl_xor_sync(0xffffffffu, l1, d);
       }
       if (g == 0) {
-        s_m[parity][warp][2 * t] = m0, s_m[parity][warp][2 * t + 1] = m1;
-        s_l[parity][warp][2 * t] = l0, s_l[parity][warp][2 * t + 1] = l1;
+        s_m[warp][2 * t] = m0, s_m[warp][2 * t + 1] = m1;
+        s_l[warp][2 * t] = l0, s_l[warp][2 * t + 1] = l1;
       }
       named_barrier_sync(1, kWarps * 32);
       float top0 = m0, top1 = m1;
 #pragma unroll
       for (int i = 0; i < kWarps; ++i) {
-        top0 = fmaxf(top0, s_m[parity][i][2 * t]);
-        top1 = fmaxf(top1, s_m[parity][i][2 * t + 1]);
+        top0 = fmaxf(top0, s_m[i][2 * t]);
+        top1 = fmaxf(top1, s_m[i][2 * t + 1]);
       }
-      const float f0 = ex2_approx(m0 - top0), f1 = ex2_approx(m1 - top1);
+      l0 = l1 = 0.f;
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) {
+        l0 = fmaf(s_l[i][2 * t], ex2_approx(s_m[i][2 * t] - top0), l0);
+        l1 = fmaf(s_l[i][2 * t + 1], ex2_approx(s_m[i][2 * t + 1] - top1), l1);
+      }
+      float* rec = kByRow ? s_x : p.rec + static_cast<size_t>(2 * range + (starts ? 1 : 0)) * (2 * cols + cols * C::kWidth);
+      const int rec_cols = kByRow ? C::kMaxCols : cols;
+      float f0 = ex2_approx(m0 - top0), f1 = ex2_approx(m1 - top1);
+      if (whole) {
+        f0 *= 1.f / l0, f1 *= 1.f / l1;
+      } else if (warp == 0 && g == 0 && 2 * t < rec_cols) {  // a piece: m, l of each column, and o below
+        rec[2 * t] = top0, rec[2 * t + 1] = top1;
+        rec[rec_cols + 2 * t] = l0, rec[rec_cols + 2 * t + 1] = l1;
+      }
       // the upper half of the warps hand their sums to the lower half
       auto exchange = [&](auto&& step) {
         if (2 * t < C::kMaxCols) {
@@ -636,67 +662,42 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, Cfg<KP>::kCtas) kv4_decode_
         });
       named_barrier_sync(1, kWarps * 32);
       // thread `tid` < 128 takes channel tid (V1: and tid + 128) of every column
-      const int last_parity = parity;
-      parity ^= 1;
-      if (tid < 128) {
-        float sum[C::kMaxCols][KP], l[C::kMaxCols], top[C::kMaxCols];
+      if (out_thread) {
+        float sum[C::kMaxCols][KP];
 #pragma unroll
-        for (int c = 0; c < C::kMaxCols; ++c) {
-          float mx = s_m[last_parity][0][c];
-#pragma unroll
-          for (int i = 1; i < kWarps; ++i) mx = fmaxf(mx, s_m[last_parity][i][c]);
-          top[c] = mx;
-          l[c] = 0.f;
-#pragma unroll
-          for (int i = 0; i < kWarps; ++i) l[c] += s_l[last_parity][i][c] * ex2_approx(s_m[last_parity][i][c] - mx);
+        for (int c = 0; c < C::kMaxCols; ++c)
 #pragma unroll
           for (int k = 0; k < KP; ++k) {
             sum[c][k] = 0.f;
 #pragma unroll
             for (int i = 0; i < kWarps / 2; ++i) sum[c][k] += s_o[(i * C::kMaxCols + c) * C::kPitch + k * 128 + tid];
           }
-        }
-        const size_t row = static_cast<size_t>(w.b) * a.H + w.h;
-        if constexpr (kByRow) {
+        if (!whole) {
 #pragma unroll
           for (int c = 0; c < C::kMaxCols; ++c) {
-            if (tid == 0) s_x[c] = top[c], s_x[C::kMaxCols + c] = l[c];
+            if (c >= rec_cols) break;
 #pragma unroll
-            for (int k = 0; k < KP; ++k) s_x[2 * C::kMaxCols + c * C::kWidth + k * 128 + tid] = sum[c][k];
-          }
-        } else if (!whole) {
-          float* rec = p.rec + static_cast<size_t>(2 * range + (starts ? 1 : 0)) * (2 * cols + cols * C::kWidth);
-#pragma unroll
-          for (int c = 0; c < C::kMaxCols; ++c) {
-            if (c >= cols) break;
-            if (tid == 0) rec[c] = top[c], rec[cols + c] = l[c];
-#pragma unroll
-            for (int k = 0; k < KP; ++k) rec[2 * cols + c * C::kWidth + k * 128 + tid] = sum[c][k];
+            for (int k = 0; k < KP; ++k) rec[2 * rec_cols + c * C::kWidth + k * 128 + tid] = sum[c][k];
           }
         } else if constexpr (KP == 1) {
 #pragma unroll
           for (int c = 0; c < C::kMaxCols; c += 2) {
             if (c >= cols) break;
-            const size_t pair = row * (cols / 2) + c / 2;
-            const float sig = 1.f / (1.f + __expf(-*(a.lam_logit + pair)));
-            const float y = (sum[c][0] / l[c] - sig * (sum[c + 1][0] / l[c + 1])) * a.v_mul;
-            static_cast<__nv_bfloat16*>(a.out)[pair * 128 + tid] = __float2bfloat16_rn(y);
+            const float sig = 1.f / (1.f + __expf(-lam[c / 2]));
+            const float y = (sum[c][0] - sig * sum[c + 1][0]) * a.v_mul;
+            static_cast<__nv_bfloat16*>(a.out)[(row * (cols / 2) + c / 2) * 128 + tid] = __float2bfloat16_rn(y);
           }
         } else {
-          const float lam = *(a.lambda + w.h);
-          float y[KP];
-          float ss = 0.f;
+          float y[KP], ss = 0.f;
 #pragma unroll
           for (int k = 0; k < KP; ++k) {
-            y[k] = (sum[0][k] / l[0] - lam * (sum[1][k] / l[1])) * a.v_mul;
+            y[k] = (sum[0][k] - lam[0] * sum[1][k]) * a.v_mul;
             ss = fmaf(y[k], y[k], ss);
           }
           const float f = norm_scale(a, ss, s_red);
 #pragma unroll
-          for (int k = 0; k < KP; ++k) {
-            const float wgt = (a.flags & 2) && a.norm_w ? *(a.norm_w + k * 128 + tid) : 1.f;
-            static_cast<__nv_bfloat16*>(a.out)[row * C::kWidth + k * 128 + tid] = __float2bfloat16_rn(y[k] * f * wgt);
-          }
+          for (int k = 0; k < KP; ++k)
+            static_cast<__nv_bfloat16*>(a.out)[row * C::kWidth + k * 128 + tid] = __float2bfloat16_rn(y[k] * f * wgt[k]);
         }
       }
       w.todo -= seg;
@@ -708,9 +709,11 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, Cfg<KP>::kCtas) kv4_decode_
   if constexpr (kByRow) {
     // Every block's piece lies in its ring, which nothing uses any more. The columns' pairs are dealt out
     // over the blocks; thread `tid` takes channel tid (V1: and tid + 128).
-    cluster_sync_all();
     const int parts = p.grid, rank = blockIdx.x % parts;
     const size_t row = static_cast<size_t>(w.b) * a.H + w.h;
+    auto lambda_of = [&](int pair) { return KP == 2 ? *(a.lambda + w.h) : *(a.lam_logit + row * (p.cols / 2) + pair); };
+    float raw = KP == 1 && rank < p.cols / 2 ? lambda_of(rank) : 0.f;  // (V2: on its way over the barrier)
+    cluster_sync_all();
     for (int pair = rank; pair < p.cols / 2 && tid < 128; pair += parts) {
       float top[2] = {-FLT_MAX, -FLT_MAX}, l[2] = {0.f, 0.f}, sum[2][KP] = {};
       const uint32_t x = smem_u32(s_x);
@@ -731,8 +734,8 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, Cfg<KP>::kCtas) kv4_decode_
             sum[e][k] = fmaf(ld_cluster_f32(from + 4 * (2 * C::kMaxCols + c * C::kWidth + k * 128 + tid)), f, sum[e][k]);
         }
       }
-      const float lam = KP == 2 ? *(a.lambda + w.h)
-                                : 1.f / (1.f + __expf(-*(a.lam_logit + row * (p.cols / 2) + pair)));
+      if (KP == 2 || pair != rank) raw = lambda_of(pair);
+      const float lam = KP == 2 ? raw : 1.f / (1.f + __expf(-raw));
       float y[KP], ss = 0.f, f = 1.f;
 #pragma unroll
       for (int k = 0; k < KP; ++k) {
@@ -755,16 +758,16 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, Cfg<KP>::kCtas) kv4_decode_
 // and join. Few rows: a block for each pair of columns of each row. Else: block i for the row that range
 // i + 1 begins inside, if no earlier range does, with all its columns.
 template <int KP, bool kFewRows>
-__global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const Params p) {
-  constexpr int W = KP * 128;
-  __shared__ float s_m[kMergeThreads / 64 * 2], s_l[kMergeThreads / 64 * 2];
-  __shared__ float4 s_o[kMergeThreads];
+__global__ void __launch_bounds__(kFewRows ? Cfg<KP>::kMergeFew : Cfg<KP>::kMerge) kv4_merge_kernel(const Params p) {
+  constexpr int W = KP * 128, NT = kFewRows ? Cfg<KP>::kMergeFew : Cfg<KP>::kMerge;
+  __shared__ float s_m[NT / (W / 4)], s_l[NT / (W / 4)];  // a column of a group each
+  __shared__ float4 s_o[NT];
   __shared__ float s_red[W / 32];
   const Kv4DecodeArgs& a = p.a;
   const int tid = threadIdx.x, cols = p.cols;
   // All but the pieces is known before the first kernel ends: it released this one after its own wait, so
   // the lengths, the lambdas and the weights are there.
-  __shared__ Ranges<KP, kMergeThreads, true> s_ranges;
+  __shared__ Ranges<KP, NT, true> s_ranges;
   __shared__ Walk s_walk;
   s_ranges.fill(a);
   const long long total = s_ranges.total(a);
@@ -773,7 +776,7 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const Params p
   const int c0 = kFewRows ? 2 * static_cast<int>(blockIdx.x % (cols / 2)) : 0, nc = kFewRows ? 2 : cols;  // the columns
   if (tid < 32) {
     Walk w{};
-    if constexpr (kFewRows) {  // B <= kMergeThreads: a share of one sequence a thread
+    if constexpr (kFewRows) {  // B <= NT: a share of one sequence a thread
       const int row = blockIdx.x / (cols / 2);
       w.b = row / a.H;
       w.h = row - w.b * a.H;
@@ -796,16 +799,21 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const Params p
     grid_release();
     return;
   }
-  const int lanes = nc * (W / 4), groups = kMergeThreads / lanes;  // a float4 of all its columns' outputs each
+  const int lanes = nc * (W / 4), groups = NT / lanes;  // a float4 of all its columns' outputs each
   const size_t rec = 2 * cols + cols * W;
   const int grp = tid / lanes, ln = tid % lanes, c = ln / (W / 4);
   const size_t row = static_cast<size_t>(d.b) * a.H + d.h;
-  const int pair = tid / W, ch = tid % W;  // the output channel of the end
-  const bool mine = tid < nc / 2 * W;
-  const float lam = !mine     ? 0.f
-                    : KP == 2 ? __ldcg(a.lambda + d.h)
-                              : 1.f / (1.f + __expf(-__ldcg(a.lam_logit + row * (cols / 2) + c0 / 2 + pair)));
-  const float wgt = KP == 2 && mine && (a.flags & 2) && a.norm_w ? __ldcg(a.norm_w + ch) : 1.f;
+  // the output channels of the end: `tid` and every NT-th on (V1: the row's 256)
+  constexpr int kOuts = KP == 2 ? 1 : 512 / NT;
+  float lam[kOuts];
+#pragma unroll
+  for (int i = 0; i < kOuts; ++i) {
+    const int pair = (tid + i * NT) / W;
+    lam[i] = 2 * pair >= nc ? 0.f
+             : KP == 2      ? __ldcg(a.lambda + d.h)
+                            : 1.f / (1.f + __expf(-__ldcg(a.lam_logit + row * (cols / 2) + c0 / 2 + pair)));
+  }
+  const float wgt = KP == 2 && tid < W && (a.flags & 2) && a.norm_w ? __ldcg(a.norm_w + tid) : 1.f;
   grid_wait();
   grid_release();
   float m = -FLT_MAX, l = 0.f;
@@ -826,38 +834,41 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const Params p
   s_o[tid] = o;
   if (ln % (W / 4) == 0) s_m[grp * nc + c] = m, s_l[grp * nc + c] = l;
   __syncthreads();
-  // an output channel: of a pair of columns, V1's only one
-  if (!mine) return;
-  float q[2];
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int col = 2 * pair + e;
-    float top = s_m[col];
-    for (int k = 1; k < groups; ++k) top = fmaxf(top, s_m[k * nc + col]);
-    float sum = 0.f, ls = 0.f;
-    for (int k = 0; k < groups; ++k) {
-      const float f = ex2_approx(s_m[k * nc + col] - top);
-      ls = fmaf(s_l[k * nc + col], f, ls);
-      sum = fmaf(reinterpret_cast<const float*>(s_o + k * lanes)[col * W + ch], f, sum);
+  for (int i = 0; i < kOuts; ++i) {
+    const int pair = (tid + i * NT) / W, ch = (tid + i * NT) % W;
+    if (2 * pair >= nc) return;
+    float q[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int col = 2 * pair + e;
+      float top = s_m[col];
+      for (int k = 1; k < groups; ++k) top = fmaxf(top, s_m[k * nc + col]);
+      float sum = 0.f, ls = 0.f;
+      for (int k = 0; k < groups; ++k) {
+        const float f = ex2_approx(s_m[k * nc + col] - top);
+        ls = fmaf(s_l[k * nc + col], f, ls);
+        sum = fmaf(reinterpret_cast<const float*>(s_o + k * lanes)[col * W + ch], f, sum);
+      }
+      q[e] = sum / ls;
     }
-    q[e] = sum / ls;
-  }
-  float y = (q[0] - lam * q[1]) * a.v_mul;
-  if constexpr (KP == 2) {
-    if (a.flags & 2) {
-      float ss = y * y;
+    float y = (q[0] - lam[i] * q[1]) * a.v_mul;
+    if constexpr (KP == 2) {
+      if (a.flags & 2) {
+        float ss = y * y;
 #pragma unroll
-      for (int s = 16; s > 0; s >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, s);
-      if ((tid & 31) == 0) s_red[tid >> 5] = ss;
-      named_barrier_sync(1, W);
-      ss = 0.f;
+        for (int x = 16; x > 0; x >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, x);
+        if ((tid & 31) == 0) s_red[tid >> 5] = ss;
+        named_barrier_sync(1, W);
+        ss = 0.f;
 #pragma unroll
-      for (int k = 0; k < W / 32; ++k) ss += s_red[k];
-      y *= 1.f / sqrtf(ss / static_cast<float>(W) + a.eps) * wgt;
+        for (int k = 0; k < W / 32; ++k) ss += s_red[k];
+        y *= 1.f / sqrtf(ss / static_cast<float>(W) + a.eps) * wgt;
+      }
+      if (a.flags & 4) y *= 1.f - a.lambda_init;
     }
-    if (a.flags & 4) y *= 1.f - a.lambda_init;
+    static_cast<__nv_bfloat16*>(a.out)[(row * (cols / 2) + c0 / 2 + pair) * W + ch] = __float2bfloat16_rn(y);
   }
-  static_cast<__nv_bfloat16*>(a.out)[(row * (cols / 2) + c0 / 2 + pair) * W + ch] = __float2bfloat16_rn(y);
 }
 
 template <int KP>
@@ -892,9 +903,9 @@ cudaError_t launch(const Kv4DecodeArgs& a, cudaStream_t st) {
   if (e != cudaSuccess || p.grid == 1) return e;
   // A block for each pair of columns of each row, where those are fewer: the rows are long then, and their
   // many pieces are read by more threads (8 rows of 16K keys, V2: 13.1 us the whole call, 18.4 the other way).
-  if (rows * (p.cols / 2) < p.grid && a.B <= kMergeThreads)
-    return launch_early(kv4_merge_kernel<KP, true>, static_cast<unsigned>(rows * (p.cols / 2)), kMergeThreads, 0, st, 1, p);
-  return launch_early(kv4_merge_kernel<KP, false>, p.grid - 1, kMergeThreads, 0, st, 1, p);
+  if (rows * (p.cols / 2) < p.grid && a.B <= C::kMergeFew)
+    return launch_early(kv4_merge_kernel<KP, true>, static_cast<unsigned>(rows * (p.cols / 2)), C::kMergeFew, 0, st, 1, p);
+  return launch_early(kv4_merge_kernel<KP, false>, p.grid - 1, C::kMerge, 0, st, 1, p);
 }
 
 }  // namespace
