@@ -1513,49 +1513,54 @@ def diffattn_v2_decode_fp8_paged(q8, k_pool8, v_pool, block_table, seqlens, lam_
 
 # ---- serving over a 4-bit cache ------------------------------------------------------------------
 # A serving loop makes these calls for every token, and the smallest take the GPU a few microseconds:
-# each operand is checked once, in as few steps as Python allows, and pointers go to ctypes as ints.
+# the operands are checked in one expression, the reason is looked for where it fails, and pointers go
+# to ctypes as ints.
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_get_device, _capturing = torch._C._cuda_getDevice, torch._C._cuda_isCurrentStreamCapturing
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
 
-def _operand(name, t, dtype, index, shape=None) -> int:
-    """The address of a contiguous tensor of `dtype` (and `shape`) on CUDA device `index`."""
-    try:
-        if t.dtype == dtype and t.get_device() == index and t.is_contiguous() and (shape is None or t.shape == shape):
-            return t.data_ptr()
-    except AttributeError:
-        pass
-    _dev(name, t, dtype)  # raises with the reason, but for these two
-    if t.get_device() != index:
-        raise ValueError(f"{name} is on {t.device}, and other operands on cuda:{index}")
-    raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+def _refuse(index, *operands):
+    """Raises for the first of the operands (name, tensor, dtype, shape) that is not a contiguous tensor
+    of its dtype and shape on CUDA device `index`."""
+    for name, t, dtype, shape in operands:
+        _dev(name, t, dtype)
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+        if t.get_device() != index:
+            raise ValueError(f"{name} is on {t.device}, and other operands on cuda:{index}")
 
 
-def _index(name, t) -> int:
-    """The CUDA device that a call's first operand is on."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return t.get_device()
+def _operand(name, t, dtype, index, shape) -> int:
+    """The address of a contiguous tensor of `dtype` and `shape` on CUDA device `index`."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.is_contiguous()
+            and t.shape == shape):
+        _refuse(index, (name, t, dtype, shape))
+    return t.data_ptr()
 
 
 def _call(index, fn, *args):
     """fn(*args, stream) on device `index` and its current stream."""
-    if index == torch._C._cuda_getDevice():
+    if index == _get_device():
         rc = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
             rc = fn(*args, _raw_stream(index))
-    if rc != DIFFATTN_OK:
+    if rc:
         _check(rc)
 
 
-def _current(stream, index):
-    """A context in which `stream` (a torch stream or a raw handle) is the current one: a call on
-    another stream also takes its output and its scratch from that stream's memory, where nothing
-    that still runs on the caller's stream can reuse them."""
+def _current(stream, t):
+    """A context in which `stream` (a torch stream or a raw handle) is the current one, on the device of
+    the operand t: a call on another stream also takes its output and its scratch from that stream's
+    memory, where nothing that still runs on the caller's stream can reuse them."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError("operands must be CUDA tensors")
     if not isinstance(stream, torch.cuda.Stream):
         raw = _stream(stream).value or 0
+        index = t.get_device()
         stream = torch.cuda.ExternalStream(raw, device=index) if raw else torch.cuda.default_stream(index)
     return torch.cuda.stream(stream)
 
@@ -1564,17 +1569,27 @@ _scratch = threading.local()
 
 
 def _workspace(index, n):
-    """Scratch of n bytes for one call. Calls that one thread makes on one stream run one after the
-    other, so they share a buffer, which the thread keeps; a call that is being captured gets its
-    own, as its graph may replay on any stream."""
-    if index != torch._C._cuda_getDevice() or torch._C._cuda_isCurrentStreamCapturing():
-        return torch.empty(n, dtype=torch.uint8, device=torch.device("cuda", index))
+    """(tensor, its address, its bytes): scratch of at least n bytes for one call. Calls that one thread makes
+    on one stream run one after the other, so they share a buffer, which the thread keeps; a call that is
+    being captured gets its own, as its graph may replay on any stream."""
+    if index != _get_device() or _capturing():
+        ws = torch.empty(n, dtype=_U8, device=torch.device("cuda", index))
+        return ws, ws.data_ptr(), n
     kept = _scratch.__dict__.setdefault("kept", {})
     key = (index, _raw_stream(index))
     ws = kept.get(key)
-    if ws is None or ws.shape[0] < n:
-        ws = kept[key] = torch.empty(n, dtype=torch.uint8, device=torch.device("cuda", index))
+    if ws is None or ws[2] < n:
+        t = torch.empty(n, dtype=_U8, device=torch.device("cuda", index))
+        ws = kept[key] = (t, t.data_ptr(), n)
     return ws
+
+
+def _given(workspace, index):
+    """The same of a caller's workspace."""
+    _dev("workspace", workspace)
+    if workspace.get_device() != index:
+        raise ValueError(f"workspace is on {workspace.device}, and other operands on cuda:{index}")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 _PLAN = ("seqlens", "ring_state", "cu_seqlens_q", "cu_seqlens_k", "slot_map", "positions")
@@ -1588,29 +1603,36 @@ def diffattn_paged_plan(seqlens, new_tokens, block_table, free_ring, ring_state,
     [B], ring_state [2], cu_seqlens_q and cu_seqlens_k [B + 1], slot_map and positions [total_max].
     out["seqlens"] and out["ring_state"] may be the inputs themselves."""
     if stream is not None:
-        with _current(stream, _index("seqlens", seqlens)):
+        with _current(stream, seqlens):
             return diffattn_paged_plan(seqlens, new_tokens, block_table, free_ring, ring_state, page_size, total_max, out)
-    i32, dev = torch.int32, _index("seqlens", seqlens)
-    B = seqlens.numel()
-    if block_table.dim() != 2 or free_ring.dim() != 1:
-        raise ValueError("block_table must be [B, max_pages] and free_ring [num_pages]")
-    max_pages, num_pages = block_table.shape[1], free_ring.shape[0]
-    total_max = int(total_max)
+    try:
+        dev, total_max = seqlens.get_device(), int(total_max)
+        (B,), (rows, max_pages), (num_pages,) = seqlens.shape, block_table.shape, free_ring.shape
+        fit = (dev == new_tokens.get_device() == block_table.get_device() == free_ring.get_device() == ring_state.get_device()
+               and rows == B and new_tokens.shape == (B,) and ring_state.shape == (2,)
+               and seqlens.dtype is new_tokens.dtype is block_table.dtype is free_ring.dtype is ring_state.dtype is _I32
+               and seqlens.is_contiguous() and new_tokens.is_contiguous() and block_table.is_contiguous()
+               and free_ring.is_contiguous() and ring_state.is_contiguous() and dev >= 0)
+    except (AttributeError, ValueError):
+        raise ValueError("need tensors seqlens, new_tokens [B], block_table [B, max_pages], free_ring [num_pages] "
+                         "and ring_state [2]") from None
+    if not fit:
+        _refuse(dev, ("seqlens", seqlens, _I32, (B,)), ("new_tokens", new_tokens, _I32, (B,)),
+                ("block_table", block_table, _I32, (B, max_pages)), ("free_ring", free_ring, _I32, (num_pages,)),
+                ("ring_state", ring_state, _I32, (2,)))
     sizes = [B, 2, B + 1, B + 1, total_max, total_max]
     if out is None:
         if total_max < 0:
             raise ValueError("total_max must not be negative")
-        buf = seqlens.new_empty(3 * B + 4 + 2 * total_max)  # (int32: `seqlens` is checked below)
+        buf = seqlens.new_empty(3 * B + 4 + 2 * total_max)
         out = dict(zip(_PLAN, buf.unsafe_split_with_sizes(sizes)))  # (pieces, not views: the buffer itself is let go)
         p0 = buf.data_ptr()
         p = (p0, p0 + 4 * B, p0 + 4 * B + 8, p0 + 8 * B + 12, p0 + 12 * B + 16, p0 + 12 * B + 16 + 4 * total_max)
     else:
-        p = [_operand(f"out[{name!r}]", out[name], i32, dev, (n,)) for name, n in zip(_PLAN, sizes)]
-    _call(dev, lib().diffattn_paged_plan, _operand("seqlens", seqlens, i32, dev, (B,)),
-          _operand("new_tokens", new_tokens, i32, dev, (B,)), p[0],
-          _operand("block_table", block_table, i32, dev, (B, max_pages)),
-          _operand("free_ring", free_ring, i32, dev), _operand("ring_state", ring_state, i32, dev, (2,)),
-          p[1], p[2], p[3], p[4], p[5], B, max_pages, num_pages, int(page_size), total_max)
+        p = [_operand(f"out[{name!r}]", out[name], _I32, dev, (n,)) for name, n in zip(_PLAN, sizes)]
+    _call(dev, lib().diffattn_paged_plan, seqlens.data_ptr(), new_tokens.data_ptr(), p[0], block_table.data_ptr(),
+          free_ring.data_ptr(), ring_state.data_ptr(), p[1], p[2], p[3], p[4], p[5], B, max_pages, num_pages,
+          int(page_size), total_max)
     return out
 
 
@@ -1628,48 +1650,37 @@ def diffattn_kv4_pool(num_pages: int, page_size: int, H: int, kw: int, vw: int, 
     return torch.zeros((num_pages, H, page_size // 16, rec), dtype=torch.uint8, device=device)
 
 
-def _kv4_pool(pool, index, H, kw, vw):
-    """(address, num_pages, page_size) of a pool of H heads and rows of kw and vw channels."""
-    shape = pool.shape
-    if len(shape) != 4 or shape[1] != H or shape[3] != (kw + vw) * 9:
-        raise ValueError(f"pool must be [num_pages, {H}, page_size / 16, {(kw + vw) * 9}], got {list(shape)}")
-    return _operand("pool", pool, torch.uint8, index), shape[0], shape[2] * 16
-
-
-def _kv4_table(block_table, index, B):
-    """(address, max_pages) of a block table of B sequences."""
-    shape = block_table.shape
-    if len(shape) != 2 or shape[0] != B:
-        raise ValueError(f"block_table must be [{B}, max_pages], got {list(shape)}")
-    return _operand("block_table", block_table, torch.int32, index), shape[1]
-
-
 def diffattn_kv4_append(k, v, slot_map, pool, k_exp: int = 0, v_exp: int = 0, stream=None) -> None:
     """Rounds rows k [total, H, kw] and v [total, H, vw] (bf16, last dimension contiguous, otherwise
     any strides that are multiples of 8 elements) to 4 bits and writes row i at slot slot_map[i]
     (int32 [total]; -1: not at all) of every head of `pool`."""
     if stream is not None:
-        with _current(stream, _index("k", k)):
+        with _current(stream, k):
             return diffattn_kv4_append(k, v, slot_map, pool, k_exp, v_exp)
-    dev = _index("k", k)
-    _index("v", v)
-    if k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16 or k.dim() != 3 or v.dim() != 3:
-        raise ValueError("k and v must be bfloat16 [total, H, width]")
-    (total, H, kw), (kt, kh, kc) = k.shape, k.stride()
-    vw, (vt, vh, vc) = v.shape[2], v.stride()
-    if v.shape != (total, H, vw) or v.get_device() != dev:
-        raise ValueError("k and v must have the same tokens and heads, on the same device")
+    try:
+        dev = k.get_device()
+        (total, H, kw), (rows, heads, vw), (num_pages, pool_heads, recs, rec) = k.shape, v.shape, pool.shape
+        (kt, kh, kc), (vt, vh, vc) = k.stride(), v.stride()
+        fit = (dev == v.get_device() == pool.get_device() == slot_map.get_device()
+               and rows == total and heads == H == pool_heads and rec == (kw + vw) * 9 and slot_map.shape == (total,)
+               and k.dtype is v.dtype is _BF16 and pool.dtype is _U8 and slot_map.dtype is _I32
+               and pool.is_contiguous() and slot_map.is_contiguous() and dev >= 0)
+    except (AttributeError, ValueError):
+        raise ValueError("need tensors k [total, H, kw], v [total, H, vw], slot_map [total] and "
+                         "pool [num_pages, H, page_size / 16, record]") from None
     if (kc != 1 and kw > 1) or (vc != 1 and vw > 1):
         raise ValueError("the last dimension of k and v must be contiguous")
+    if not fit:
+        if k.dtype is not _BF16 or v.dtype is not _BF16 or v.get_device() != dev or dev < 0 or (rows, heads) != (total, H):
+            raise ValueError("k and v must be bfloat16, of the same tokens and heads, on one CUDA device")
+        _refuse(dev, ("slot_map", slot_map, _I32, (total,)), ("pool", pool, _U8, (num_pages, H, recs, (kw + vw) * 9)))
     # a dimension of one token or head is never stepped over: its stride may be anything
     if total == 1:
         kt, vt = kw, vw
     if H == 1:
         kh, vh = kw, vw
-    at, num_pages, page_size = _kv4_pool(pool, dev, H, kw, vw)
     _call(dev, lib().diffattn_kv4_append, k.data_ptr(), v.data_ptr(), (ctypes.c_longlong * 4)(kt, kh, vt, vh),
-          _operand("slot_map", slot_map, torch.int32, dev, (total,)), at, total, H, kw, vw, num_pages,
-          page_size, int(k_exp), int(v_exp))
+          slot_map.data_ptr(), pool.data_ptr(), total, H, kw, vw, num_pages, recs * 16, int(k_exp), int(v_exp))
 
 
 def diffattn_kv4_gather(pool, block_table, cu_seqlens, total: int, kw: int, vw: int, starts=None,
@@ -1678,24 +1689,30 @@ def diffattn_kv4_gather(pool, block_table, cu_seqlens, total: int, kw: int, vw: 
     token starts[b] + i (starts int32 [B]; None: 0) of sequence b. Without `out` = (k, v), rows
     behind the last sequence are not initialised."""
     if stream is not None:
-        with _current(stream, _index("pool", pool)):
+        with _current(stream, pool):
             return diffattn_kv4_gather(pool, block_table, cu_seqlens, total, kw, vw, starts, k_exp, v_exp, out)
-    dev = _index("pool", pool)
-    B = cu_seqlens.numel() - 1
-    if pool.dim() != 4:
-        raise ValueError("pool must be [num_pages, H, page_size / 16, record]")
-    H, total, kw, vw = pool.shape[1], int(total), int(kw), int(vw)
-    at, num_pages, page_size = _kv4_pool(pool, dev, H, kw, vw)
-    table, max_pages = _kv4_table(block_table, dev, B)
+    try:
+        dev, total, kw, vw = pool.get_device(), int(total), int(kw), int(vw)
+        (num_pages, H, recs, rec), (B, max_pages), (ends,) = pool.shape, block_table.shape, cu_seqlens.shape
+        fit = (dev == block_table.get_device() == cu_seqlens.get_device() and ends == B + 1
+               and rec == (kw + vw) * 9 and pool.dtype is _U8 and block_table.dtype is cu_seqlens.dtype is _I32
+               and pool.is_contiguous() and block_table.is_contiguous() and cu_seqlens.is_contiguous() and dev >= 0)
+    except (AttributeError, ValueError):
+        raise ValueError("need tensors pool [num_pages, H, page_size / 16, record], block_table [B, max_pages] and "
+                         "cu_seqlens [B + 1]") from None
+    if not fit:
+        _refuse(dev, ("pool", pool, _U8, (num_pages, H, recs, (kw + vw) * 9)), ("block_table", block_table, _I32, (B, max_pages)),
+                ("cu_seqlens", cu_seqlens, _I32, (B + 1,)))
+    first = None if starts is None else _operand("starts", starts, _I32, dev, (B,))
+    n = max(0, total)
     if out is None:
-        n = max(0, total)
-        out = (pool.new_empty(n, H, kw, dtype=torch.bfloat16), pool.new_empty(n, H, vw, dtype=torch.bfloat16))
-    k, v = out
-    _call(dev, lib().diffattn_kv4_gather, at, table, _operand("cu_seqlens", cu_seqlens, torch.int32, dev, (B + 1,)),
-          None if starts is None else _operand("starts", starts, torch.int32, dev, (B,)),
-          _operand("out[0]", k, torch.bfloat16, dev, (max(0, total), H, kw)),
-          _operand("out[1]", v, torch.bfloat16, dev, (max(0, total), H, vw)), total, B, H, kw, vw, num_pages,
-          page_size, max_pages, int(k_exp), int(v_exp))
+        k, v = pool.new_empty(n, H, kw, dtype=_BF16), pool.new_empty(n, H, vw, dtype=_BF16)
+        k_at, v_at = k.data_ptr(), v.data_ptr()
+    else:
+        k, v = out
+        k_at, v_at = _operand("out[0]", k, _BF16, dev, (n, H, kw)), _operand("out[1]", v, _BF16, dev, (n, H, vw))
+    _call(dev, lib().diffattn_kv4_gather, pool.data_ptr(), block_table.data_ptr(), cu_seqlens.data_ptr(), first,
+          k_at, v_at, total, B, H, kw, vw, num_pages, recs * 16, max_pages, int(k_exp), int(v_exp))
     return k, v
 
 
@@ -1712,26 +1729,36 @@ def diffattn_decode_kv4(q, pool, block_table, seqlens, lam, lambda_init: float =
     """V1 decode over a 4-bit pool [num_pages, H, page_size / 16, 4608]: q [B, H, 256], block_table
     [B, max_pages] int32, seqlens [B] int32 (0: no keys, a row of zeros)."""
     if stream is not None:
-        with _current(stream, _index("q", q)):
+        with _current(stream, q):
             return diffattn_decode_kv4(q, pool, block_table, seqlens, lam, lambda_init, norm_weight, eps, norm, scale,
                                        k_exp, v_exp, workspace, out)
-    dev = _index("q", q)
-    if q.dim() != 3:
-        raise ValueError("q must be [B, H, 2d]")
-    B, H, two_d = q.shape
-    at, num_pages, page_size = _kv4_pool(pool, dev, H, two_d, two_d)
-    table, max_pages = _kv4_table(block_table, dev, B)
+    try:
+        dev = q.get_device()
+        (B, H, two_d), (num_pages, heads, recs, rec), (rows, max_pages) = q.shape, pool.shape, block_table.shape
+        fit = (dev == pool.get_device() == block_table.get_device() == seqlens.get_device() == lam.get_device()
+               and heads == H and rec == two_d * 18 and rows == B and seqlens.shape == (B,) and lam.shape == (H,)
+               and q.dtype is _BF16 and pool.dtype is _U8 and block_table.dtype is seqlens.dtype is _I32 and lam.dtype is _F32
+               and q.is_contiguous() and pool.is_contiguous() and block_table.is_contiguous() and seqlens.is_contiguous()
+               and lam.is_contiguous() and dev >= 0)
+    except (AttributeError, ValueError):
+        raise ValueError("need tensors q [B, H, 2d], pool [num_pages, H, page_size / 16, record], "
+                         "block_table [B, max_pages], seqlens [B] and lam [H]") from None
+    if not fit:
+        _refuse(dev, ("q", q, _BF16, (B, H, two_d)), ("pool", pool, _U8, (num_pages, H, recs, two_d * 18)),
+                ("block_table", block_table, _I32, (B, max_pages)), ("seqlens", seqlens, _I32, (B,)), ("lam", lam, _F32, (H,)))
+    weight = None if norm_weight is None else _operand("norm_weight", norm_weight, _F32, dev, (two_d,))
     if workspace is None:
-        workspace = _workspace(dev, diffattn_decode_kv4_workspace_size(B, H, two_d // 2, two_d))
+        _, ws, ws_bytes = _workspace(dev, diffattn_decode_kv4_workspace_size(B, H, two_d // 2, two_d))
+    else:
+        _, ws, ws_bytes = _given(workspace, dev)
     if out is None:
         out = torch.empty_like(q)
-    flags = (DIFFATTN_NORM if norm else 0) | (DIFFATTN_SCALE if scale else 0)
-    _call(dev, lib().diffattn_decode_kv4, _operand("q", q, torch.bfloat16, dev), at, table,
-          _operand("seqlens", seqlens, torch.int32, dev, (B,)), _operand("out", out, torch.bfloat16, dev, (B, H, two_d)),
-          _operand("lam", lam, torch.float32, dev, (H,)), lambda_init,
-          None if norm_weight is None else _operand("norm_weight", norm_weight, torch.float32, dev, (two_d,)),
-          eps, B, H, two_d // 2, two_d, num_pages, page_size, max_pages, int(k_exp), int(v_exp), flags,
-          _operand("workspace", workspace, workspace.dtype, dev), workspace.numel() * workspace.element_size())
+        out_at = out.data_ptr()
+    else:
+        out_at = _operand("out", out, _BF16, dev, (B, H, two_d))
+    _call(dev, lib().diffattn_decode_kv4, q.data_ptr(), pool.data_ptr(), block_table.data_ptr(), seqlens.data_ptr(),
+          out_at, lam.data_ptr(), lambda_init, weight, eps, B, H, two_d // 2, two_d, num_pages, recs * 16, max_pages,
+          int(k_exp), int(v_exp), (DIFFATTN_NORM if norm else 0) | (DIFFATTN_SCALE if scale else 0), ws, ws_bytes)
     return out
 
 
@@ -1748,23 +1775,33 @@ def diffattn_v2_decode_kv4(q, pool, block_table, seqlens, lam_logit, k_exp: int 
     block_table [B, max_pages] int32, seqlens [B] int32 (0: no keys, rows of zeros), lam_logit
     [B, Hq/2] fp32. Returns [B, Hq/2, 128]."""
     if stream is not None:
-        with _current(stream, _index("q", q)):
+        with _current(stream, q):
             return diffattn_v2_decode_kv4(q, pool, block_table, seqlens, lam_logit, k_exp, v_exp, workspace, out)
-    dev = _index("q", q)
-    if q.dim() != 3 or pool.dim() != 4:
-        raise ValueError("q must be [B, Hq, d] and pool [num_pages, Hkv, page_size / 16, record]")
-    B, Hq, d = q.shape
-    Hkv = pool.shape[1]
-    at, num_pages, page_size = _kv4_pool(pool, dev, Hkv, d, d)
-    table, max_pages = _kv4_table(block_table, dev, B)
+    try:
+        dev = q.get_device()
+        (B, Hq, d), (num_pages, Hkv, recs, rec), (rows, max_pages) = q.shape, pool.shape, block_table.shape
+        fit = (dev == pool.get_device() == block_table.get_device() == seqlens.get_device() == lam_logit.get_device()
+               and rec == d * 18 and rows == B and seqlens.shape == (B,) and lam_logit.shape == (B, Hq // 2)
+               and q.dtype is _BF16 and pool.dtype is _U8 and block_table.dtype is seqlens.dtype is _I32
+               and lam_logit.dtype is _F32 and q.is_contiguous() and pool.is_contiguous() and block_table.is_contiguous()
+               and seqlens.is_contiguous() and lam_logit.is_contiguous() and dev >= 0)
+    except (AttributeError, ValueError):
+        raise ValueError("need tensors q [B, Hq, d], pool [num_pages, Hkv, page_size / 16, record], "
+                         "block_table [B, max_pages], seqlens [B] and lam_logit [B, Hq / 2]") from None
+    if not fit:
+        _refuse(dev, ("q", q, _BF16, (B, Hq, d)), ("pool", pool, _U8, (num_pages, Hkv, recs, d * 18)),
+                ("block_table", block_table, _I32, (B, max_pages)), ("seqlens", seqlens, _I32, (B,)),
+                ("lam_logit", lam_logit, _F32, (B, Hq // 2)))
     if workspace is None:
-        workspace = _workspace(dev, diffattn_v2_decode_kv4_workspace_size(B, Hq, Hkv, d))
+        _, ws, ws_bytes = _workspace(dev, diffattn_v2_decode_kv4_workspace_size(B, Hq, Hkv, d))
+    else:
+        _, ws, ws_bytes = _given(workspace, dev)
     if out is None:
-        out = q.new_empty(B, Hq // 2, d)  # (bf16: `q` is checked below)
-    _call(dev, lib().diffattn_v2_decode_kv4, _operand("q", q, torch.bfloat16, dev), at, table,
-          _operand("seqlens", seqlens, torch.int32, dev, (B,)),
-          _operand("lam_logit", lam_logit, torch.float32, dev, (B, Hq // 2)),
-          _operand("out", out, torch.bfloat16, dev, (B, Hq // 2, d)), B, Hq, Hkv, d, num_pages, page_size,
-          max_pages, int(k_exp), int(v_exp), 0, _operand("workspace", workspace, workspace.dtype, dev),
-          workspace.numel() * workspace.element_size())
+        out = q.new_empty(B, Hq // 2, d)
+        out_at = out.data_ptr()
+    else:
+        out_at = _operand("out", out, _BF16, dev, (B, Hq // 2, d))
+    _call(dev, lib().diffattn_v2_decode_kv4, q.data_ptr(), pool.data_ptr(), block_table.data_ptr(), seqlens.data_ptr(),
+          lam_logit.data_ptr(), out_at, B, Hq, Hkv, d, num_pages, recs * 16, max_pages, int(k_exp), int(v_exp), 0, ws,
+          ws_bytes)
     return out

@@ -896,3 +896,41 @@ def test_gather_and_append_of_many_sequences_and_heads():
         for x, g in zip((k, v), got):
             assert np.array_equal(to64(g), kv4.values(*kv4.quantize_blocks(to64(x))))
     da.diffattn_device_status()
+
+
+def test_binding_names_the_operand_that_does_not_fit():
+    """Of a fitting call, each operand in turn with another type, a size too many, strides of its own or
+    on the host: a ValueError that names it, or the shapes that go together."""
+    z = lambda shape, dtype=torch.int32: torch.zeros(shape, dtype=dtype, device=DEV)  # noqa: E731
+    bf16, f32, u8 = torch.bfloat16, torch.float32, torch.uint8
+    calls = {
+        "plan": (lambda **o: da.diffattn_paged_plan(**o, page_size=16, total_max=4),
+                 dict(seqlens=z(3), new_tokens=z(3), block_table=z((3, 5)), free_ring=z(9), ring_state=z(2))),
+        "append": (da.diffattn_kv4_append,
+                   dict(k=z((4, 2, 128), bf16), v=z((4, 2, 128), bf16), slot_map=z(4), pool=z((9, 2, 1, 2304), u8))),
+        "gather": (lambda **o: da.diffattn_kv4_gather(**o, total=4, kw=128, vw=128),
+                   dict(pool=z((9, 2, 1, 2304), u8), block_table=z((3, 5)), cu_seqlens=z(4), starts=z(3))),
+        "v1": (da.diffattn_decode_kv4,
+               dict(q=z((3, 2, 256), bf16), pool=z((9, 2, 1, 4608), u8), block_table=z((3, 5)), seqlens=z(3), lam=z(2, f32),
+                    norm_weight=z(256, f32), out=z((3, 2, 256), bf16))),
+        "v2": (da.diffattn_v2_decode_kv4,
+               dict(q=z((3, 4, 128), bf16), pool=z((9, 2, 1, 2304), u8), block_table=z((3, 5)), seqlens=z(3),
+                    lam_logit=z((3, 2), f32), out=z((3, 2, 128), bf16))),
+    }
+    for name, (call, good) in calls.items():
+        call(**good)
+        for key, t in good.items():
+            longer = torch.cat([t, t[:1]])
+            spread = torch.stack([t, t], -1)[..., 0]
+            for bad in (t.double(), longer, spread, t.cpu(), None):
+                if bad is None and key in ("starts", "norm_weight", "out"):
+                    continue
+                if bad is longer and (name, key) in (("plan", "free_ring"), ("append", "pool"), ("gather", "pool"), ("v1", "pool"), ("v2", "pool")):
+                    continue  # one more page
+                if bad is spread and (name, key) in (("append", "k"), ("append", "v")):
+                    with pytest.raises(ValueError, match="contiguous"):
+                        call(**{**good, key: bad})
+                    continue
+                with pytest.raises(ValueError):
+                    call(**{**good, key: bad})
+    da.diffattn_device_status()
