@@ -1624,7 +1624,7 @@ def diffattn_paged_plan(seqlens, new_tokens, block_table, free_ring, ring_state,
     if out is None:
         if total_max < 0:
             raise ValueError("total_max must not be negative")
-        buf = seqlens.new_empty(3 * B + 4 + 2 * total_max)
+        buf = torch.empty(3 * B + 4 + 2 * total_max, dtype=_I32, device=seqlens.device)
         out = dict(zip(_PLAN, buf.unsafe_split_with_sizes(sizes)))  # (pieces, not views: the buffer itself is let go)
         p0 = buf.data_ptr()
         p = (p0, p0 + 4 * B, p0 + 4 * B + 8, p0 + 8 * B + 12, p0 + 12 * B + 16, p0 + 12 * B + 16 + 4 * total_max)
@@ -1706,7 +1706,8 @@ def diffattn_kv4_gather(pool, block_table, cu_seqlens, total: int, kw: int, vw: 
     first = None if starts is None else _operand("starts", starts, _I32, dev, (B,))
     n = max(0, total)
     if out is None:
-        k, v = pool.new_empty(n, H, kw, dtype=_BF16), pool.new_empty(n, H, vw, dtype=_BF16)
+        k = torch.empty((n, H, kw), dtype=_BF16, device=pool.device)
+        v = torch.empty((n, H, vw), dtype=_BF16, device=pool.device)
         k_at, v_at = k.data_ptr(), v.data_ptr()
     else:
         k, v = out
@@ -1797,7 +1798,7 @@ def diffattn_v2_decode_kv4(q, pool, block_table, seqlens, lam_logit, k_exp: int 
     else:
         _, ws, ws_bytes = _given(workspace, dev)
     if out is None:
-        out = q.new_empty(B, Hq // 2, d)
+        out = torch.empty((B, Hq // 2, d), dtype=_BF16, device=q.device)
         out_at = out.data_ptr()
     else:
         out_at = _operand("out", out, _BF16, dev, (B, Hq // 2, d))
