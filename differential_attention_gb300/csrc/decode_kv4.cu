@@ -36,11 +36,15 @@
 // wait for their fence and their count; shares by a block's age on its SM, whose schedulers serve the
 // older first, 52 us, and 400 instead of 388 for 64 x 32768 keys.)
 //
-// Where it stands: 64 x 32768 keys, 8 KV heads, G = 8 (2.42 GB): 361 us, 6.70 TB/s of the 6.78 that a copy
-// reaches; with all pages in L2 the same work takes 360, so that the unpacking (116 of 250 instructions a
+// Where it stands: 64 x 32768 keys, 8 KV heads, G = 8 (2.42 GB): 360 us, 6.71 TB/s, where a copy reaches
+// 6.78; with all pages in L2 the same work takes as long, so that the unpacking (116 of 250 instructions a
 // record go to the ALU pipe, most of them the 64 conversions) is as near its limit as the memory. 96
-// sequences of 1 to 16K keys, G = 4 (235 MB): 51 us, of which the loads alone take 39, the products 7 and
-// the second kernel 4. V1, 24 x 32768 keys, 12 heads (2.72 GB): 405 us, 6.71 TB/s.
+// sequences of 1 to 16K keys, G = 4 (235 MB): 49 us, of which the loads alone take 39 and the second kernel
+// 3. V1, 24 x 32768 keys, 12 heads (2.72 GB): 405 us, 6.71 TB/s. While all blocks run, tiles arrive at 7.1
+// TB/s; what is lost is the end, as the SMs, and the blocks of one SM, get unequal shares of it (the first
+// are done after 85 % of the time). Ranges that the blocks take late, by a counter, even that out (the last
+// tile of the 32768 keys arrives after 345 instead of 355 us), but their pieces cost as much: the call took
+// 365 to 368.
 #include <cfloat>
 #include <cmath>
 #include <type_traits>
@@ -83,8 +87,9 @@ struct Cfg {
   static constexpr int kSmem = kStages * kStage + kWarps / 2 * kMaxCols * kPitch * 4;
   // Threads of the second kernel, with few rows and else. Small blocks find room beside the first kernel's
   // last ones, large ones have more pieces under way (V2, 96 sequences of 1 to 16K keys: 48.8 us with 256,
-  // 50.0 with 512; V1, 48 of 1 to 9001: 41.6 and 41.2).
-  static constexpr int kMergeFew = 512, kMerge = KP == 1 ? 256 : 512;
+  // 50.0 with 512; V1, 48 of 1 to 9001: 41.6 and 41.2. Few rows: a V1 row of 65000 keys 19.8 with 1024, 29.1
+  // with 512; a V2 row of 200000 20.5 and 27.9).
+  static constexpr int kMergeFew = 1024, kMerge = KP == 1 ? 256 : 512;
 };
 
 struct Params {
@@ -804,7 +809,7 @@ __global__ void __launch_bounds__(kFewRows ? Cfg<KP>::kMergeFew : Cfg<KP>::kMerg
   const int grp = tid / lanes, ln = tid % lanes, c = ln / (W / 4);
   const size_t row = static_cast<size_t>(d.b) * a.H + d.h;
   // the output channels of the end: `tid` and every NT-th on (V1: the row's 256)
-  constexpr int kOuts = KP == 2 ? 1 : 512 / NT;
+  constexpr int kOuts = KP == 2 || kFewRows ? 1 : 512 / NT;
   float lam[kOuts];
 #pragma unroll
   for (int i = 0; i < kOuts; ++i) {
@@ -883,9 +888,9 @@ cudaError_t launch(const Kv4DecodeArgs& a, cudaStream_t st) {
   const long long rows = static_cast<long long>(a.B) * a.H;
   // Few keys: a row over a cluster, of as many blocks as leave it two tiles each and are resident at once;
   // where the rows' blocks then have at most kFewTiles more tiles than an equal share: the second kernel
-  // and the ranges cost about that. (GPU time of a call so and by ranges: 8 rows of 777 keys, V2, 5.9 and
-  // 9.1 us; 400 rows of 1000, 16.0 and 21.8; 48 rows of 1500, V1, 10.1 and 12.2; 240 of 800, 15.2 and 18.6;
-  // 96 of 3000, V1, where clusters of two would leave a third of the machine idle, 23.6 and 20.3. The host
+  // and the ranges cost about that. (GPU time of a call so and by ranges: 8 rows of 777 keys, V2, 5.6 and
+  // 8.7 us; 400 rows of 1000, 15.6 and 19.2; 48 rows of 1500, V1, 10.1 and 12.9; 240 of 800, 15.3 and 18.7;
+  // 96 of 3000, V1, where clusters of two would leave a third of the machine idle, 23.6 and 21.2. The host
   // has one launch less as well. Only up to 8 tiles a block: the tables' capacity, which is all the host
   // knows, is not the sequences' length.)
   int parts = 1;
@@ -902,7 +907,7 @@ cudaError_t launch(const Kv4DecodeArgs& a, cudaStream_t st) {
   cudaError_t e = launch_early_large(kv4_decode_kernel<KP, false>, p.grid, C::kThreads, C::kSmem, C::kSmem, st, 1, p, raised[0]);
   if (e != cudaSuccess || p.grid == 1) return e;
   // A block for each pair of columns of each row, where those are fewer: the rows are long then, and their
-  // many pieces are read by more threads (8 rows of 16K keys, V2: 13.1 us the whole call, 18.4 the other way).
+  // many pieces are read by more threads (8 rows of 16K keys, V2: 12.9 us the whole call, 18.4 the other way).
   if (rows * (p.cols / 2) < p.grid && a.B <= C::kMergeFew)
     return launch_early(kv4_merge_kernel<KP, true>, static_cast<unsigned>(rows * (p.cols / 2)), C::kMergeFew, 0, st, 1, p);
   return launch_early(kv4_merge_kernel<KP, false>, p.grid - 1, C::kMerge, 0, st, 1, p);
