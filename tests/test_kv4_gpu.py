@@ -934,3 +934,38 @@ def test_binding_names_the_operand_that_does_not_fit():
                 with pytest.raises(ValueError):
                     call(**{**good, key: bad})
     da.diffattn_device_status()
+
+
+def unwritten(name, B, H):
+    """A workspace of NaN."""
+    n = (da.diffattn_decode_kv4_workspace_size(B, H) if name == "v1" else da.diffattn_v2_decode_kv4_workspace_size(B, 8 * H, H))
+    return torch.full((n,), 255, dtype=torch.uint8, device=DEV)
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_decode_random_batches(seed):
+    """Batches of few long, many short and mixed sequences, cut into ranges: every piece that is read was
+    written in the same call."""
+    rng = np.random.default_rng(500 + seed)
+    B, top, heads = int(rng.choice([1, 2, 5, 40, 300, 600])), int(rng.choice([3, 40, 300, 3000])), int(rng.integers(1, 4))
+    top = min(top, 120000 // (B * heads))
+    lens = [int(n) if rng.random() < 0.9 else 0 for n in np.exp(rng.uniform(0, np.log(top + 1), B))]
+    lens[int(rng.integers(B))] = top
+    for name, call, want, q, pool, table in both(rng, lens, 16, True, heads=heads):
+        within(call(q, pool, table, lens, workspace=unwritten(name, B, heads)), *want(q, pool, table, lens))
+    da.diffattn_device_status()
+
+
+def test_decode_of_the_largest_batch():
+    """8192 sequences, most of a few keys and some of none, a few of 700 at the ends and in the middle."""
+    lens = [700 if i in (0, 4000, 4001, 8191) else i % 7 for i in range(8192)]
+    for name, call, want, q, pool, table in both(np.random.default_rng(8), lens, 16, False, heads=1):
+        within(call(q, pool, table, lens, workspace=unwritten(name, 8192, 1)), *want(q, pool, table, lens))
+    da.diffattn_device_status()
+
+
+def test_decode_one_row_in_as_many_pieces_as_there_are_blocks():
+    """One (sequence, head) over every block, and two of them."""
+    for lens in ([70000], [61000, 52001]):
+        for name, call, want, q, pool, table in both(np.random.default_rng(9), lens, 64, True, heads=1):
+            within(call(q, pool, table, lens, workspace=unwritten(name, len(lens), 1)), *want(q, pool, table, lens))
