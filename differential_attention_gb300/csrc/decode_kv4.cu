@@ -37,7 +37,7 @@
 // older first, 52 us, and 400 instead of 388 for 64 x 32768 keys.)
 //
 // Where it stands: 64 x 32768 keys, 8 KV heads, G = 8 (2.42 GB): 360 us, 6.71 TB/s, where a copy reaches
-// 6.78; with all pages in L2 the same work takes as long, so that the unpacking (116 of 250 instructions a
+// 6.78; with all pages in L2 the same work takes as long, so that the unpacking (116 of 245 instructions a
 // record go to the ALU pipe, most of them the 64 conversions) is as near its limit as the memory. 96
 // sequences of 1 to 16K keys, G = 4 (235 MB): 49 us, of which the loads alone take 39 and the second kernel
 // 3. V1, 24 x 32768 keys, 12 heads (2.72 GB): 405 us, 6.71 TB/s. While all blocks run, tiles arrive at 7.1

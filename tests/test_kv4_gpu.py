@@ -969,3 +969,43 @@ def test_decode_one_row_in_as_many_pieces_as_there_are_blocks():
     for lens in ([70000], [61000, 52001]):
         for name, call, want, q, pool, table in both(np.random.default_rng(9), lens, 64, True, heads=1):
             within(call(q, pool, table, lens, workspace=unwritten(name, len(lens), 1)), *want(q, pool, table, lens))
+
+
+def test_captured_behind_two_streams_that_join(wide):
+    """A graph in which rows are appended on one stream while another copies the lengths and forms the
+    lambdas: decodes behind the join, replayed with other inputs."""
+    lens = [900, 33, 0, 417]
+    for name, call, want, q, pool, table in both(np.random.default_rng(71), lens, 32, wide):
+        H, w = pool.shape[1], pool.shape[3] // 18
+        Q, P, T, given, seq = q.to(DEV), torch.tensor(pool).to(DEV), dev32(table), dev32(lens), dev32([0] * 4)
+        rows = torch.zeros((1, H, w), dtype=torch.bfloat16, device=DEV)
+        slot = dev32([int(table[3][0]) * 32])
+        raw = torch.full((H,) if name == "v1" else (4, 4 * H), 0.25, device=DEV)
+
+        def step(side):
+            main = torch.cuda.current_stream()
+            side.wait_stream(main)
+            with torch.cuda.stream(side):
+                lam = raw * 2.0
+                seq.copy_(given)
+            da.diffattn_kv4_append(rows, rows, slot, P)
+            main.wait_stream(side)
+            if name == "v1":
+                return da.diffattn_decode_kv4(Q, P, T, seq, lam, 0.4)
+            return da.diffattn_v2_decode_kv4(Q, P, T, seq, lam)
+
+        side = torch.cuda.Stream()
+        step(side)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = step(side)
+        for n, scale in (([5, 33, 0, 400], 0.1), ([900, 0, 0, 417], 0.4)):  # (none past its pages)
+            given.copy_(dev32(n))
+            raw.fill_(scale)
+            rows.normal_()
+            for _ in range(3):
+                g.replay()
+            got = out.clone()
+            assert torch.equal(got, step(torch.cuda.Stream()))
+    da.diffattn_device_status()
