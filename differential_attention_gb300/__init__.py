@@ -1541,17 +1541,6 @@ def _operand(name, t, dtype, index, shape) -> int:
     return t.data_ptr()
 
 
-def _call(index, fn, *args):
-    """fn(*args, stream) on device `index` and its current stream."""
-    if index == _get_device():
-        rc = fn(*args, _raw_stream(index))
-    else:
-        with torch.cuda.device(index):
-            rc = fn(*args, _raw_stream(index))
-    if rc:
-        _check(rc)
-
-
 def _current(stream, t):
     """A context in which `stream` (a torch stream or a raw handle) is the current one, on the device of
     the operand t: a call on another stream also takes its output and its scratch from that stream's
@@ -1566,21 +1555,25 @@ def _current(stream, t):
 
 
 _scratch = threading.local()
+_Strides = ctypes.c_longlong * 4
 
 
-def _workspace(index, n):
-    """(tensor, its address, its bytes): scratch of at least n bytes for one call. Calls that one thread makes
-    on one stream run one after the other, so they share a buffer, which the thread keeps; a call that is
-    being captured gets its own, as its graph may replay on any stream."""
-    if index != _get_device() or _capturing():
-        ws = torch.empty(n, dtype=_U8, device=torch.device("cuda", index))
-        return ws, ws.data_ptr(), n
-    kept = _scratch.__dict__.setdefault("kept", {})
-    key = (index, _raw_stream(index))
-    ws = kept.get(key)
+def _workspace(index, raw, n):
+    """(tensor, its address, its bytes): scratch of at least n bytes for one call on the current device's
+    stream `raw`. Calls that one thread makes on one stream run one after the other, so they share a
+    buffer, which the thread keeps; a call that is being captured gets its own, as its graph may replay
+    on any stream."""
+    if _capturing():
+        t = torch.empty(n, dtype=_U8, device=torch.device("cuda", index))
+        return t, t.data_ptr(), n
+    try:
+        kept = _scratch.kept
+    except AttributeError:
+        kept = _scratch.kept = {}
+    ws = kept.get((index, raw))
     if ws is None or ws[2] < n:
         t = torch.empty(n, dtype=_U8, device=torch.device("cuda", index))
-        ws = kept[key] = (t, t.data_ptr(), n)
+        ws = kept[index, raw] = (t, t.data_ptr(), n)
     return ws
 
 
@@ -1620,6 +1613,9 @@ def diffattn_paged_plan(seqlens, new_tokens, block_table, free_ring, ring_state,
         _refuse(dev, ("seqlens", seqlens, _I32, (B,)), ("new_tokens", new_tokens, _I32, (B,)),
                 ("block_table", block_table, _I32, (B, max_pages)), ("free_ring", free_ring, _I32, (num_pages,)),
                 ("ring_state", ring_state, _I32, (2,)))
+    if dev != _get_device():
+        with torch.cuda.device(dev):
+            return diffattn_paged_plan(seqlens, new_tokens, block_table, free_ring, ring_state, page_size, total_max, out)
     sizes = [B, 2, B + 1, B + 1, total_max, total_max]
     if out is None:
         if total_max < 0:
@@ -1630,9 +1626,11 @@ def diffattn_paged_plan(seqlens, new_tokens, block_table, free_ring, ring_state,
         p = (p0, p0 + 4 * B, p0 + 4 * B + 8, p0 + 8 * B + 12, p0 + 12 * B + 16, p0 + 12 * B + 16 + 4 * total_max)
     else:
         p = [_operand(f"out[{name!r}]", out[name], _I32, dev, (n,)) for name, n in zip(_PLAN, sizes)]
-    _call(dev, lib().diffattn_paged_plan, seqlens.data_ptr(), new_tokens.data_ptr(), p[0], block_table.data_ptr(),
-          free_ring.data_ptr(), ring_state.data_ptr(), p[1], p[2], p[3], p[4], p[5], B, max_pages, num_pages,
-          int(page_size), total_max)
+    rc = lib().diffattn_paged_plan(seqlens.data_ptr(), new_tokens.data_ptr(), p[0], block_table.data_ptr(),
+                                   free_ring.data_ptr(), ring_state.data_ptr(), p[1], p[2], p[3], p[4], p[5], B, max_pages,
+                                   num_pages, int(page_size), total_max, _raw_stream(dev))
+    if rc:
+        _check(rc)
     return out
 
 
@@ -1674,13 +1672,18 @@ def diffattn_kv4_append(k, v, slot_map, pool, k_exp: int = 0, v_exp: int = 0, st
         if k.dtype is not _BF16 or v.dtype is not _BF16 or v.get_device() != dev or dev < 0 or (rows, heads) != (total, H):
             raise ValueError("k and v must be bfloat16, of the same tokens and heads, on one CUDA device")
         _refuse(dev, ("slot_map", slot_map, _I32, (total,)), ("pool", pool, _U8, (num_pages, H, recs, (kw + vw) * 9)))
+    if dev != _get_device():
+        with torch.cuda.device(dev):
+            return diffattn_kv4_append(k, v, slot_map, pool, k_exp, v_exp)
     # a dimension of one token or head is never stepped over: its stride may be anything
     if total == 1:
         kt, vt = kw, vw
     if H == 1:
         kh, vh = kw, vw
-    _call(dev, lib().diffattn_kv4_append, k.data_ptr(), v.data_ptr(), (ctypes.c_longlong * 4)(kt, kh, vt, vh),
-          slot_map.data_ptr(), pool.data_ptr(), total, H, kw, vw, num_pages, recs * 16, int(k_exp), int(v_exp))
+    rc = lib().diffattn_kv4_append(k.data_ptr(), v.data_ptr(), _Strides(kt, kh, vt, vh), slot_map.data_ptr(), pool.data_ptr(),
+                                   total, H, kw, vw, num_pages, recs * 16, int(k_exp), int(v_exp), _raw_stream(dev))
+    if rc:
+        _check(rc)
 
 
 def diffattn_kv4_gather(pool, block_table, cu_seqlens, total: int, kw: int, vw: int, starts=None,
@@ -1703,6 +1706,9 @@ def diffattn_kv4_gather(pool, block_table, cu_seqlens, total: int, kw: int, vw: 
     if not fit:
         _refuse(dev, ("pool", pool, _U8, (num_pages, H, recs, (kw + vw) * 9)), ("block_table", block_table, _I32, (B, max_pages)),
                 ("cu_seqlens", cu_seqlens, _I32, (B + 1,)))
+    if dev != _get_device():
+        with torch.cuda.device(dev):
+            return diffattn_kv4_gather(pool, block_table, cu_seqlens, total, kw, vw, starts, k_exp, v_exp, out)
     first = None if starts is None else _operand("starts", starts, _I32, dev, (B,))
     n = max(0, total)
     if out is None:
@@ -1712,8 +1718,10 @@ def diffattn_kv4_gather(pool, block_table, cu_seqlens, total: int, kw: int, vw: 
     else:
         k, v = out
         k_at, v_at = _operand("out[0]", k, _BF16, dev, (n, H, kw)), _operand("out[1]", v, _BF16, dev, (n, H, vw))
-    _call(dev, lib().diffattn_kv4_gather, pool.data_ptr(), block_table.data_ptr(), cu_seqlens.data_ptr(), first,
-          k_at, v_at, total, B, H, kw, vw, num_pages, recs * 16, max_pages, int(k_exp), int(v_exp))
+    rc = lib().diffattn_kv4_gather(pool.data_ptr(), block_table.data_ptr(), cu_seqlens.data_ptr(), first, k_at, v_at, total, B, H,
+                                   kw, vw, num_pages, recs * 16, max_pages, int(k_exp), int(v_exp), _raw_stream(dev))
+    if rc:
+        _check(rc)
     return k, v
 
 
@@ -1747,9 +1755,14 @@ def diffattn_decode_kv4(q, pool, block_table, seqlens, lam, lambda_init: float =
     if not fit:
         _refuse(dev, ("q", q, _BF16, (B, H, two_d)), ("pool", pool, _U8, (num_pages, H, recs, two_d * 18)),
                 ("block_table", block_table, _I32, (B, max_pages)), ("seqlens", seqlens, _I32, (B,)), ("lam", lam, _F32, (H,)))
+    if dev != _get_device():
+        with torch.cuda.device(dev):
+            return diffattn_decode_kv4(q, pool, block_table, seqlens, lam, lambda_init, norm_weight, eps, norm, scale,
+                                       k_exp, v_exp, workspace, out)
+    raw = _raw_stream(dev)
     weight = None if norm_weight is None else _operand("norm_weight", norm_weight, _F32, dev, (two_d,))
     if workspace is None:
-        _, ws, ws_bytes = _workspace(dev, diffattn_decode_kv4_workspace_size(B, H, two_d // 2, two_d))
+        _, ws, ws_bytes = _workspace(dev, raw, diffattn_decode_kv4_workspace_size(B, H, two_d // 2, two_d))
     else:
         _, ws, ws_bytes = _given(workspace, dev)
     if out is None:
@@ -1757,9 +1770,12 @@ def diffattn_decode_kv4(q, pool, block_table, seqlens, lam, lambda_init: float =
         out_at = out.data_ptr()
     else:
         out_at = _operand("out", out, _BF16, dev, (B, H, two_d))
-    _call(dev, lib().diffattn_decode_kv4, q.data_ptr(), pool.data_ptr(), block_table.data_ptr(), seqlens.data_ptr(),
-          out_at, lam.data_ptr(), lambda_init, weight, eps, B, H, two_d // 2, two_d, num_pages, recs * 16, max_pages,
-          int(k_exp), int(v_exp), (DIFFATTN_NORM if norm else 0) | (DIFFATTN_SCALE if scale else 0), ws, ws_bytes)
+    rc = lib().diffattn_decode_kv4(q.data_ptr(), pool.data_ptr(), block_table.data_ptr(), seqlens.data_ptr(), out_at,
+                                   lam.data_ptr(), lambda_init, weight, eps, B, H, two_d // 2, two_d, num_pages, recs * 16,
+                                   max_pages, int(k_exp), int(v_exp),
+                                   (DIFFATTN_NORM if norm else 0) | (DIFFATTN_SCALE if scale else 0), ws, ws_bytes, raw)
+    if rc:
+        _check(rc)
     return out
 
 
@@ -1793,8 +1809,12 @@ def diffattn_v2_decode_kv4(q, pool, block_table, seqlens, lam_logit, k_exp: int 
         _refuse(dev, ("q", q, _BF16, (B, Hq, d)), ("pool", pool, _U8, (num_pages, Hkv, recs, d * 18)),
                 ("block_table", block_table, _I32, (B, max_pages)), ("seqlens", seqlens, _I32, (B,)),
                 ("lam_logit", lam_logit, _F32, (B, Hq // 2)))
+    if dev != _get_device():
+        with torch.cuda.device(dev):
+            return diffattn_v2_decode_kv4(q, pool, block_table, seqlens, lam_logit, k_exp, v_exp, workspace, out)
+    raw = _raw_stream(dev)
     if workspace is None:
-        _, ws, ws_bytes = _workspace(dev, diffattn_v2_decode_kv4_workspace_size(B, Hq, Hkv, d))
+        _, ws, ws_bytes = _workspace(dev, raw, diffattn_v2_decode_kv4_workspace_size(B, Hq, Hkv, d))
     else:
         _, ws, ws_bytes = _given(workspace, dev)
     if out is None:
@@ -1802,7 +1822,9 @@ def diffattn_v2_decode_kv4(q, pool, block_table, seqlens, lam_logit, k_exp: int 
         out_at = out.data_ptr()
     else:
         out_at = _operand("out", out, _BF16, dev, (B, Hq // 2, d))
-    _call(dev, lib().diffattn_v2_decode_kv4, q.data_ptr(), pool.data_ptr(), block_table.data_ptr(), seqlens.data_ptr(),
-          lam_logit.data_ptr(), out_at, B, Hq, Hkv, d, num_pages, recs * 16, max_pages, int(k_exp), int(v_exp), 0, ws,
-          ws_bytes)
+    rc = lib().diffattn_v2_decode_kv4(q.data_ptr(), pool.data_ptr(), block_table.data_ptr(), seqlens.data_ptr(),
+                                      lam_logit.data_ptr(), out_at, B, Hq, Hkv, d, num_pages, recs * 16, max_pages,
+                                      int(k_exp), int(v_exp), 0, ws, ws_bytes, raw)
+    if rc:
+        _check(rc)
     return out

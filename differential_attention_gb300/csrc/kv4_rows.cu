@@ -8,7 +8,9 @@
 namespace da {
 namespace {
 
-constexpr int kRowThreads = 256;
+// (Append of 16K rows of 12 V1 heads and their read-out: 87.3 us with 256 and 256 threads, 86.0 so; the
+// read-out alone is 0.3 slower with 64.)
+constexpr int kAppendThreads = 64, kGatherThreads = 256;
 
 __device__ __forceinline__ float2 bf16x2_to_float2(uint32_t w) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
@@ -52,11 +54,11 @@ __device__ __forceinline__ Block round_block(const uint4& w0, const uint4& w1, f
 // 5.9 TB/s of a copy's 6.78, with 55 % of the ALU pipe and 63 % of the issue slots in use. (The
 // first form, with a division for each value, took about 100.)
 template <int KP>
-__global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const Kv4AppendArgs a) {
+__global__ void __launch_bounds__(kAppendThreads) kv4_append_kernel(const Kv4AppendArgs a) {
   grid_wait();
   grid_release();
   const int lane = threadIdx.x & 31;
-  const long long u = static_cast<long long>(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
+  const long long u = static_cast<long long>(blockIdx.x) * (kAppendThreads / 32) + (threadIdx.x >> 5);
   const int h = static_cast<int>(u % a.H);
   const long long row0 = u / a.H * 8;
   if (row0 >= a.total) return;
@@ -144,11 +146,11 @@ __device__ __forceinline__ uint32_t half2_to_bf16x2(uint32_t h, float f) {
 // Sequence b's records have the warps from cu[b] / 16 + 2 b on: n rows touch at most n / 16 + 2 records,
 // so that the ranges do not overlap, whatever the sequences' first tokens are.
 template <int KP>
-__global__ void __launch_bounds__(kRowThreads) kv4_gather_kernel(const Kv4GatherArgs a) {
+__global__ void __launch_bounds__(kGatherThreads) kv4_gather_kernel(const Kv4GatherArgs a) {
   grid_wait();
   grid_release();
   const int lane = threadIdx.x & 31;
-  const long long i = static_cast<long long>(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
+  const long long i = static_cast<long long>(blockIdx.x) * (kGatherThreads / 32) + (threadIdx.x >> 5);
   const int h = static_cast<int>(i % a.H);
   const long long u = i / a.H;
   if (u >= a.total / 16 + 2LL * a.B) return;
@@ -234,15 +236,15 @@ __global__ void __launch_bounds__(kRowThreads) kv4_gather_kernel(const Kv4Gather
 cudaError_t launch_kv4_append(const Kv4AppendArgs& a, cudaStream_t st) {
   if (a.total == 0) return cudaSuccess;
   const long long warps = (static_cast<long long>(a.total) + 7) / 8 * a.H;
-  const unsigned blocks = static_cast<unsigned>((warps * 32 + kRowThreads - 1) / kRowThreads);
-  return launch_early(a.kp == 1 ? kv4_append_kernel<1> : kv4_append_kernel<2>, blocks, kRowThreads, 0, st, 1, a);
+  const unsigned blocks = static_cast<unsigned>((warps * 32 + kAppendThreads - 1) / kAppendThreads);
+  return launch_early(a.kp == 1 ? kv4_append_kernel<1> : kv4_append_kernel<2>, blocks, kAppendThreads, 0, st, 1, a);
 }
 
 cudaError_t launch_kv4_gather(const Kv4GatherArgs& a, cudaStream_t st) {
   if (a.total == 0) return cudaSuccess;
   const long long warps = (a.total / 16 + 2LL * a.B) * a.H;
-  const unsigned blocks = static_cast<unsigned>((warps * 32 + kRowThreads - 1) / kRowThreads);
-  return launch_early(a.kp == 1 ? kv4_gather_kernel<1> : kv4_gather_kernel<2>, blocks, kRowThreads, 0, st, 1, a);
+  const unsigned blocks = static_cast<unsigned>((warps * 32 + kGatherThreads - 1) / kGatherThreads);
+  return launch_early(a.kp == 1 ? kv4_gather_kernel<1> : kv4_gather_kernel<2>, blocks, kGatherThreads, 0, st, 1, a);
 }
 
 cudaError_t status_kv4_rows(int* v) { return read_clear_status(v); }
