@@ -2,7 +2,9 @@
 // error reporting and dispatch to the kernels. No arithmetic of the operator happens here.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
+#include <cfloat>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -2204,7 +2206,16 @@ int decode_kv4_impl(const char* fn, da::Kv4DecodeArgs& a, int cols, int width, i
   rc = check_device();
   if (rc) return rc;
   a.qk_scale = static_cast<float>(std::ldexp(1.4426950408889634 / std::sqrt(128.0), k_exp));
-  a.v_mul = std::ldexp(1.0f, v_exp);
+  // y 2^v_exp / sqrt(mean(y^2) 2^(2 v_exp) + eps) is the same with 2^c in place of 2^v_exp and eps
+  // 2^(2 (c - v_exp)) in place of eps. Where a norm follows, c stays where the squares of what a pool can
+  // give (values up to 2688, lambda up to 2^15) are finite in fp32 and small ones are not lost.
+  int v_pow = v_exp;
+  if (a.flags & DIFFATTN_NORM) {
+    v_pow = std::max(-32, std::min(32, v_exp));
+    if (v_pow != v_exp)
+      a.eps = static_cast<float>(std::min<double>(std::max<double>(std::ldexp(static_cast<double>(a.eps), 2 * (v_pow - v_exp)), FLT_MIN), FLT_MAX));
+  }
+  a.v_mul = std::ldexp(1.0f, v_pow);
   cudaError_t e = da::launch_kv4_decode(a, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, fn);
   return ok();

@@ -335,7 +335,7 @@ struct Kv4DecodeArgs {
   int B, H, group;  // KV heads; V2: query heads per KV head, V1: 0
   int num_pages, page_size, max_pages;
   float qk_scale;   // log2(e) / sqrt(128) 2^k_exp
-  float v_mul;      // 2^v_exp
+  float v_mul;      // 2^v_exp; where a norm follows, a power of two that it gives the same result with (and eps with it)
   void* ws;
 };
 size_t kv4_decode_workspace_bytes(int cols, int width);

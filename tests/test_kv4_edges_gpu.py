@@ -1,0 +1,40 @@
+"""The 4-bit cache's calls at the far ends of what their header allows: exponents, weights that are not
+finite, streams of other libraries, joins of every piece. Bounds as in test_kv4_gpu.py."""
+import numpy as np
+import pytest
+import torch
+
+import differential_attention_gb300 as da
+from oracle import kv4_ref as kv4
+from tests.test_kv4_gpu import DEV, FLOOR, SLACK, dev32, v1_case, widened, within
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    da.build()
+    da.lib()
+    yield
+    da.diffattn_device_status()
+
+
+# how a V1 row's end is reached: (lens, heads, by ranges)
+ROW_ENDS = {"cluster": ([100, 37], 2, False), "whole": ([100] * 350, 2, True), "pieces of few rows": ([3000, 900], 2, True),
+            "pieces of many rows": ([900] * 80, 4, True)}
+
+
+@pytest.mark.parametrize("end", list(ROW_ENDS))
+@pytest.mark.parametrize("norm", [True, False])
+@pytest.mark.parametrize("v_exp,eps", [(64, 1e-5), (48, 1e-5), (-64, 1e-5), (-64, 1e-30), (33, 1e-12)])
+def test_v1_decode_norm_at_far_exponents(v_exp, eps, norm, end):
+    """The norm's sum of squares stays in fp32's range whatever power of two the values carry."""
+    lens, H, wide = ROW_ENDS[end]
+    table, pool, q, lam, w = v1_case(np.random.default_rng(211), lens, H, 16)
+    table = widened(table, 16, H, wide)
+    got = da.diffattn_decode_kv4(q.to(DEV), torch.tensor(pool).to(DEV), dev32(table), dev32(lens), lam.to(DEV), 0.4,
+                                 norm_weight=w.to(DEV), eps=eps, norm=norm, v_exp=v_exp)
+    within(got, *kv4.decode(q, pool, table, lens, lam.numpy(), 0.4, w, eps, norm, v_exp=v_exp, slack=SLACK, floor=FLOOR))
+    da.diffattn_device_status()
