@@ -744,14 +744,15 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, Cfg<KP>::kCtas) kv4_decode_
       float y[KP], ss = 0.f, f = 1.f;
 #pragma unroll
       for (int k = 0; k < KP; ++k) {
-        y[k] = w.len == 0 ? 0.f : (sum[0][k] / l[0] - lam * (sum[1][k] / l[1])) * a.v_mul;
+        y[k] = (sum[0][k] / l[0] - lam * (sum[1][k] / l[1])) * a.v_mul;
         ss = fmaf(y[k], y[k], ss);
       }
       if constexpr (KP == 2) f = norm_scale(a, ss, s_red);
 #pragma unroll
       for (int k = 0; k < KP; ++k) {
         const float wgt = KP == 2 && (a.flags & 2) && a.norm_w ? *(a.norm_w + k * 128 + tid) : 1.f;
-        static_cast<__nv_bfloat16*>(a.out)[(row * (p.cols / 2) + pair) * C::kWidth + k * 128 + tid] = __float2bfloat16_rn(y[k] * f * wgt);
+        const float o = w.len == 0 ? 0.f : y[k] * f * wgt;  // (zeros, whatever the weight and the scale hold)
+        static_cast<__nv_bfloat16*>(a.out)[(row * (p.cols / 2) + pair) * C::kWidth + k * 128 + tid] = __float2bfloat16_rn(o);
       }
     }
     cluster_sync_all();  // no block leaves while another reads its piece

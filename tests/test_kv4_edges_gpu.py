@@ -38,3 +38,18 @@ def test_v1_decode_norm_at_far_exponents(v_exp, eps, norm, end):
                                  norm_weight=w.to(DEV), eps=eps, norm=norm, v_exp=v_exp)
     within(got, *kv4.decode(q, pool, table, lens, lam.numpy(), 0.4, w, eps, norm, v_exp=v_exp, slack=SLACK, floor=FLOOR))
     da.diffattn_device_status()
+
+
+@pytest.mark.parametrize("wide", [False, True])
+def test_v1_decode_of_no_keys_gives_zeros_whatever_the_norm_holds(wide):
+    """An empty place in the batch is zeros also where the norm's weight is not finite or the scale is."""
+    lens = [0, 70, 0]
+    table, pool, q, lam, w = v1_case(np.random.default_rng(223), lens, 2, 16)
+    table = widened(table, 16, 2, wide)
+    w[3], w[200] = float("nan"), float("inf")
+    for lambda_init in (0.4, float("nan")):
+        got = da.diffattn_decode_kv4(q.to(DEV), torch.tensor(pool).to(DEV), dev32(table), dev32(lens), lam.to(DEV), lambda_init,
+                                     norm_weight=w.to(DEV))
+        assert not got[0].any() and not got[2].any()
+        assert torch.isnan(got[1, :, 3]).all()
+    da.diffattn_device_status()
