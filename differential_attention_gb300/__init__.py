@@ -12,6 +12,7 @@ Layouts (dense, row-major):
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -1562,7 +1563,7 @@ def _workspace(index, raw, n):
     """(tensor, its address, its bytes): scratch of at least n bytes for one call on the current device's
     stream `raw`. Calls that one thread makes on one stream run one after the other, so they share a
     buffer, which the thread keeps; a call that is being captured gets its own, as its graph may replay
-    on any stream."""
+    on any stream. None on a stream that torch did not make: see _lent."""
     if _capturing():
         t = torch.empty(n, dtype=_U8, device=torch.device("cuda", index))
         return t, t.data_ptr(), n
@@ -1572,9 +1573,33 @@ def _workspace(index, raw, n):
         kept = _scratch.kept = {}
     ws = kept.get((index, raw))
     if ws is None or ws[2] < n:
+        if raw and torch.cuda.current_stream(index).stream_id == raw:  # (torch's own streams are numbered)
+            return None
         t = torch.empty(n, dtype=_U8, device=torch.device("cuda", index))
         ws = kept[index, raw] = (t, t.data_ptr(), n)
     return ws
+
+
+_lent_buffers, _lent_lock = {}, threading.Lock()
+
+
+@contextlib.contextmanager
+def _lent(index):
+    """Scratch for one decode on a current stream that torch did not make. Such a stream may be destroyed,
+    and its handle come back, while its work still runs, so that nothing is kept by the handle: each
+    device has one buffer, large enough for any decode, which goes from call to call by an event.
+    (Decodes of several such streams so run one after the other, unless they are given workspaces.)"""
+    with _lent_lock:
+        if index not in _lent_buffers:
+            n = max(diffattn_decode_kv4_workspace_size(1, 1), diffattn_v2_decode_kv4_workspace_size(1, 8, 1))
+            _lent_buffers[index] = torch.empty(n, dtype=_U8, device=torch.device("cuda", index)), torch.cuda.Event()
+        buffer, done = _lent_buffers[index]
+        stream = torch.cuda.current_stream(index)
+        done.wait(stream)
+        try:
+            yield buffer
+        finally:
+            done.record(stream)
 
 
 def _given(workspace, index):
@@ -1762,7 +1787,12 @@ def diffattn_decode_kv4(q, pool, block_table, seqlens, lam, lambda_init: float =
     raw = _raw_stream(dev)
     weight = None if norm_weight is None else _operand("norm_weight", norm_weight, _F32, dev, (two_d,))
     if workspace is None:
-        _, ws, ws_bytes = _workspace(dev, raw, diffattn_decode_kv4_workspace_size(B, H, two_d // 2, two_d))
+        kept = _workspace(dev, raw, diffattn_decode_kv4_workspace_size(B, H, two_d // 2, two_d))
+        if kept is None:
+            with _lent(dev) as workspace:
+                return diffattn_decode_kv4(q, pool, block_table, seqlens, lam, lambda_init, norm_weight, eps, norm, scale,
+                                           k_exp, v_exp, workspace, out)
+        _, ws, ws_bytes = kept
     else:
         _, ws, ws_bytes = _given(workspace, dev)
     if out is None:
@@ -1814,7 +1844,11 @@ def diffattn_v2_decode_kv4(q, pool, block_table, seqlens, lam_logit, k_exp: int 
             return diffattn_v2_decode_kv4(q, pool, block_table, seqlens, lam_logit, k_exp, v_exp, workspace, out)
     raw = _raw_stream(dev)
     if workspace is None:
-        _, ws, ws_bytes = _workspace(dev, raw, diffattn_v2_decode_kv4_workspace_size(B, Hq, Hkv, d))
+        kept = _workspace(dev, raw, diffattn_v2_decode_kv4_workspace_size(B, Hq, Hkv, d))
+        if kept is None:
+            with _lent(dev) as workspace:
+                return diffattn_v2_decode_kv4(q, pool, block_table, seqlens, lam_logit, k_exp, v_exp, workspace, out)
+        _, ws, ws_bytes = kept
     else:
         _, ws, ws_bytes = _given(workspace, dev)
     if out is None:

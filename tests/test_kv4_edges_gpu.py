@@ -1,5 +1,7 @@
 """The 4-bit cache's calls at the far ends of what their header allows: exponents, weights that are not
 finite, streams of other libraries, joins of every piece. Bounds as in test_kv4_gpu.py."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -52,4 +54,63 @@ def test_v1_decode_of_no_keys_gives_zeros_whatever_the_norm_holds(wide):
                                      norm_weight=w.to(DEV))
         assert not got[0].any() and not got[2].any()
         assert torch.isnan(got[1, :, 3]).all()
+    da.diffattn_device_status()
+
+
+class ForeignStream:
+    """A stream that torch did not make."""
+
+    def __init__(self):
+        self.cudart = torch.cuda.cudart()
+        handle = ctypes.c_uint64(0)
+        assert int(self.cudart.cudaStreamCreate(ctypes.addressof(handle))) == 0
+        self.handle = handle.value
+
+    def close(self):
+        assert int(self.cudart.cudaStreamDestroy(self.handle)) == 0
+
+
+def test_decode_keeps_nothing_for_foreign_streams():
+    """A handle of another library may be destroyed and its value come back: scratch is not kept by it."""
+    lens = [300, 41]
+    table, pool, q, lam, w = v1_case(np.random.default_rng(227), lens, 2, 16)
+    Q, P, T, S, L = q.to(DEV), torch.tensor(pool).to(DEV), dev32(widened(table, 16, 2, True)), dev32(lens), lam.to(DEV)
+    want = da.diffattn_decode_kv4(Q, P, T, S, L)
+    out = [torch.empty_like(want) for _ in range(12)]
+    torch.cuda.synchronize()
+
+    def use(o):
+        s = ForeignStream()
+        da.diffattn_decode_kv4(Q, P, T, S, L, out=o, stream=s.handle)
+        with torch.cuda.stream(torch.cuda.ExternalStream(s.handle)):
+            da.diffattn_decode_kv4(Q, P, T, S, L, out=o)
+        return s
+
+    open_ = [use(out[0])]
+    held = torch.cuda.memory_allocated()
+    open_ += [use(o) for o in out[1:]]
+    assert torch.cuda.memory_allocated() == held
+    torch.cuda.synchronize()
+    for s in open_:
+        s.close()
+    assert all(torch.equal(o, want) for o in out)
+    da.diffattn_device_status()
+
+
+def test_decodes_on_two_foreign_streams_do_not_share_scratch_in_time():
+    lens = [5000, 41, 900]
+    streams, calls = [ForeignStream(), ForeignStream()], []
+    for i, s in enumerate(streams):
+        table, pool, q, lam, w = v1_case(np.random.default_rng(229 + i), lens, 2, 16)
+        calls.append((q.to(DEV), torch.tensor(pool).to(DEV), dev32(widened(table, 16, 2, True)), dev32(lens), lam.to(DEV)))
+    want = [da.diffattn_decode_kv4(*c) for c in calls]
+    out = [[torch.empty_like(want[0]) for _ in range(20)] for _ in streams]
+    torch.cuda.synchronize()
+    for k in range(20):
+        for s, c, o in zip(streams, calls, out):
+            da.diffattn_decode_kv4(*c, out=o[k], stream=s.handle)
+    torch.cuda.synchronize()
+    for s, o, x in zip(streams, out, want):
+        s.close()
+        assert all(torch.equal(y, x) for y in o)
     da.diffattn_device_status()
