@@ -1552,6 +1552,8 @@ def _current(stream, t):
         raw = _stream(stream).value or 0
         index = t.get_device()
         stream = torch.cuda.ExternalStream(raw, device=index) if raw else torch.cuda.default_stream(index)
+    elif stream.device_index != t.get_device():
+        raise ValueError(f"stream is of cuda:{stream.device_index}, and operands are on {t.device}")
     return torch.cuda.stream(stream)
 
 
