@@ -13,10 +13,14 @@ __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;
 // From here on (in all blocks) the kernel after this one may be set up. After grid_wait().
 __device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// Whether this file's kernels were ever launched: until then its status word is 0 and need not be read.
+static std::atomic<bool> g_launched{false};
+
 // Launches a kernel that calls grid_wait() first: it is set up while the one before it in the stream ends.
 template <typename P>
-inline cudaError_t launch_early(void (*kernel)(P), unsigned grid, int block, int smem, cudaStream_t st, int cluster,
+static cudaError_t launch_early(void (*kernel)(P), unsigned grid, int block, int smem, cudaStream_t st, int cluster,
                                 const P& p) {
+  g_launched.store(true, std::memory_order_relaxed);
   cudaLaunchAttribute at[2] = {};
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
@@ -37,7 +41,7 @@ inline cudaError_t launch_early(void (*kernel)(P), unsigned grid, int block, int
 // raised on each device's first call (`raised`: a bit each), and again where a launch is refused, as
 // after a reset of the device.
 template <typename P>
-inline cudaError_t launch_early_large(void (*kernel)(P), unsigned grid, int block, int smem, int limit, cudaStream_t st,
+static cudaError_t launch_early_large(void (*kernel)(P), unsigned grid, int block, int smem, int limit, cudaStream_t st,
                                       int cluster, const P& p, std::atomic<uint64_t>& raised) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);

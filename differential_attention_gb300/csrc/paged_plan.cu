@@ -224,6 +224,6 @@ cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t st) {
   return launch_early_large(paged_plan_kernel, blocks, kPlanThreads, smem, (4 * kPlanMaxRequests + 3) * 4, st, blocks, p, raised);
 }
 
-cudaError_t status_paged_plan(int* v) { return read_clear_status(v); }
+cudaError_t status_paged_plan(int* v) { return g_launched.load(std::memory_order_relaxed) ? read_clear_status(v) : cudaSuccess; }
 
 }  // namespace da

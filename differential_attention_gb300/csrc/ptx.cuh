@@ -30,7 +30,7 @@ static __device__ int g_device_status = 0;
 static inline cudaError_t read_clear_status(int* v) {
   const int zero = 0;
   cudaError_t e = cudaMemcpyFromSymbol(v, g_device_status, sizeof(int));
-  if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_device_status, &zero, sizeof(int));
+  if (e == cudaSuccess && *v != 0) e = cudaMemcpyToSymbol(g_device_status, &zero, sizeof(int));
   return e;
 }
 
