@@ -64,6 +64,7 @@ constexpr int kPrefillFlags =
 
 constexpr int DEV_BAD_INDEX_BIT = 2;  // the kernels' DEV_BAD_INDEX status bit
 constexpr int DEV_BOUNDS_BIT = 4;     // DEV_BOUNDS: a debug-build bounds check failed
+constexpr int DEV_NO_FIT_BIT = 8;     // DEV_NO_FIT: a page plan's step was out of range
 
 extern "C" {
 
@@ -96,8 +97,15 @@ DIFFATTN_API int diffattn_device_status(void* stream) {
     return fail(DIFFATTN_ERR_INDEX,
                 "a debug-build bounds check failed: a tile coordinate or row index was outside "
                 "its tensor (status %d)", v);
+  const char* no_fit =
+      "a page plan's step does not fit: too few free pages, more tokens than total_max, or a length, "
+      "their sum or the ring's state out of range";
   if (v & DEV_BAD_INDEX_BIT)
-    return fail(DIFFATTN_ERR_INDEX, "a block-table entry was outside [0, num_pages) (status %d)", v);
+    return fail(DIFFATTN_ERR_INDEX,
+                "a block-table entry was outside [0, num_pages), or another index on the device (a slot, "
+                "an offset) outside its range%s%s (status %d)", v & DEV_NO_FIT_BIT ? "; and " : "",
+                v & DEV_NO_FIT_BIT ? no_fit : "", v);
+  if (v & DEV_NO_FIT_BIT) return fail(DIFFATTN_ERR_INDEX, "%s (status %d)", no_fit, v);
   if (v != 0) return fail(DIFFATTN_ERR_TIMEOUT, "a bounded wait inside a kernel ran out (status %d)", v);
   return ok();
 }

@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanPara
   if (gridDim.x > 1) cluster_sync_all();
   if (bad) {
     // the step does not fit: nothing is taken or returned, and no row has a slot
-    if (lead && tid == 0) flag_device_error(DEV_BAD_INDEX);
+    if (lead && tid == 0) flag_device_error(DEV_NO_FIT);
     for (int i = gid; i < p.B; i += all)
       if (p.seqlens_out != p.seqlens) p.seqlens_out[i] = p.seqlens[i];
     for (int i = tid; lead && i <= p.B; i += kPlanThreads) p.cu_q[i] = p.cu_k[i] = 0;

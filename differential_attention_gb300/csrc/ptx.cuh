@@ -8,8 +8,9 @@
 
 namespace da {
 
-// Error codes a kernel can leave in the device status word. DEV_BOUNDS only in debug builds.
-enum : int { DEV_OK = 0, DEV_TIMEOUT = 1, DEV_BAD_INDEX = 2, DEV_BOUNDS = 4 };
+// Error codes a kernel can leave in the device status word. DEV_BOUNDS only in debug builds; DEV_NO_FIT
+// by the page plan alone.
+enum : int { DEV_OK = 0, DEV_TIMEOUT = 1, DEV_BAD_INDEX = 2, DEV_BOUNDS = 4, DEV_NO_FIT = 8 };
 
 // Debug builds (-DDIFFATTN_DEBUG; libdiffattn_debug.so, `builder.py --debug`) check every tile
 // coordinate of a TMA copy and every gathered or stored row index against the extent of its

@@ -114,3 +114,20 @@ def test_decodes_on_two_foreign_streams_do_not_share_scratch_in_time():
         s.close()
         assert all(torch.equal(y, x) for y in o)
     da.diffattn_device_status()
+
+
+def test_plan_reports_what_it_is():
+    """A step that does not fit is not reported as a bad page, and a bad page not as such a step."""
+    def plan(s, n, table, ring, state, total_max):
+        da.diffattn_paged_plan(dev32(s), dev32(n), dev32(table), dev32(ring), dev32(state), 16, total_max)
+        with pytest.raises(da.DiffAttnError) as e:
+            da.diffattn_device_status()
+        assert e.value.status == -9
+        return str(e.value)
+
+    fit = "does not fit"
+    assert fit in plan([16], [1], [[0, -1]], [1, 2], [0, 0], 1)      # no free page
+    assert fit in plan([0], [3], [[-1, -1]], [1, 2], [0, 2], 2)      # more tokens than total_max
+    assert fit in plan([33], [0], [[0, -1]], [1, 2], [0, 1], 2)      # a length past the table
+    bad = plan([16], [1], [[0, -1]], [7, 2], [0, 2], 1)              # page 7 of 2
+    assert fit not in bad and "page" in bad
