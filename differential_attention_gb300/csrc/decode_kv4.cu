@@ -20,8 +20,8 @@
 // cycles for the writes alone. P^T's fragment is S^T's transposed, by movmatrix.
 //
 // Numerics. Q enters as fp16 after a power of two of its own for each head (its largest channel at
-// 2^14 .. 2^15: bf16's 8 bits fit, channels 2^-38 of the largest are lost, which fp32 sums lose as
-// well). P is rounded to fp16 at 2^10 times its value against the reference m, so that its absolute
+// 2^14 .. 2^15; a channel at 2^-17 still has bf16's 8 bits, below that it is rounded to multiples of
+// 2^-24: off by 2^-39 of the largest at most, whatever the keys hold there). P is rounded to fp16 at 2^10 times its value against the reference m, so that its absolute
 // error is 2^-35 of the largest probability; m follows the running maximum only where a score
 // passes it by 2^4, which leaves every P below 2^14. Sums and statistics are fp32.
 //

@@ -8,7 +8,7 @@ import torch
 
 import differential_attention_gb300 as da
 from oracle import kv4_ref as kv4
-from tests.test_kv4_gpu import DEV, FLOOR, SLACK, dev32, v1_case, widened, within
+from tests.test_kv4_gpu import DEV, FLOOR, SLACK, both, dev32, v1_case, widened, within
 
 pytestmark = pytest.mark.gpu
 
@@ -131,3 +131,32 @@ def test_plan_reports_what_it_is():
     assert fit in plan([33], [0], [[0, -1]], [1, 2], [0, 1], 2)      # a length past the table
     bad = plan([16], [1], [[0, -1]], [7, 2], [0, 2], 1)              # page 7 of 2
     assert fit not in bad and "page" in bad
+
+
+@pytest.mark.parametrize("wide", [False, True])
+def test_decode_of_queries_whose_loud_channel_meets_zero_keys(wide):
+    """The scores come from the other channels alone: exact down to 2^-31 of the loud one (here 2^40 at
+    its side, by exponents), and zeros from 2^-40 on."""
+    lens = [333]
+    for name, call, want, q, pool, table in both(np.random.default_rng(239), lens, 32, wide):
+        kp, pool = (2 if name == "v1" else 1), pool.copy()
+        for i in range(16):  # channel 16 of every K plane: code 0 in the low nibble of its block's first byte
+            for p in range(kp):
+                pool[..., p * kv4.PLANE + kv4.k_code_at(i, 0) + 8] &= 0xF0
+        k = kv4.sequence_rows(pool, kp, table, 0, 333)[0]
+        assert not k[..., 16::128].any() and k[..., 17::128].any()
+
+        def loud(x, exponent):
+            """Channels of random sign and 8 significant bits, all of one exponent, beside the loud one."""
+            y = torch.sign(x.float()) * (1.0 + torch.frac(x.float().abs() * 1000.0 / 128.0).mul(128).floor() / 128.0)
+            y = y * 2.0 ** exponent
+            y[..., 16::128] = 2.0 ** 40
+            return y.to(torch.bfloat16)
+
+        near = loud(q, 40 - 31)
+        within(call(near, pool, table, lens, k_exp=-9), *want(near, pool, table, lens, k_exp=-9))
+        far, none = loud(q, 40 - 41), torch.zeros_like(q)
+        none[..., 16::128] = 2.0 ** 40
+        assert torch.equal(call(far, pool, table, lens), call(none, pool, table, lens))
+        within(call(far, pool, table, lens), *want(none, pool, table, lens))
+    da.diffattn_device_status()
