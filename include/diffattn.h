@@ -858,7 +858,9 @@ DIFFATTN_API int diffattn_gda_decode_paged(const void* q, const void* k_pool, co
  *   seqlens_out : device int32 [B], the lengths after the step; may be `seqlens` itself
  *   block_table : device int32 [B, max_pages], read and written in place: key j of request b lies in
  *                page block_table[b][j / page_size]. Only the entries of pages that a request grows
- *                into are written; those past a request's pages mean nothing
+ *                into are written; those past a request's pages mean nothing. A page belongs to one
+ *                request or to the ring: one that two requests hold (a common prompt) comes back
+ *                with each of them that ends, and would be given out twice
  *   free_ring, ring_state : device int32 [num_pages] and [2] = {head, count}: the free pages are
  *                free_ring[(head + i) % num_pages], i < count. Pages are taken from the front, in the
  *                order of the requests; returned ones go behind the last (in the order of the
@@ -873,11 +875,12 @@ DIFFATTN_API int diffattn_gda_decode_paged(const void* q, const void* k_pool, co
  *   positions  : device int32 [total_max] or NULL: each new token's position in its request; -1
  *                behind the last
  * A step that does not fit changes nothing: where a length, a new length or the ring's state is out
- * of range, the new tokens are more than total_max, or the free and returned pages fewer than
- * needed, then the tables and the ring stay, seqlens_out and ring_state_out repeat their inputs, the
- * offsets are 0 and the slots -1, and diffattn_device_status() reports DIFFATTN_ERR_INDEX. A page
- * id outside [0, num_pages) in the ring or a table is passed on as it is; its tokens get slot -1,
- * and it is reported the same way.
+ * of range, the new tokens are more than total_max, the keys of the requests that have new tokens
+ * (cu_seqlens_k) more than 2^31 - 1 together, or the free and returned pages fewer than needed or
+ * more than num_pages, then the tables and the ring stay, seqlens_out and ring_state_out repeat their
+ * inputs, the offsets are 0 and the slots -1, and diffattn_device_status() reports
+ * DIFFATTN_ERR_INDEX. A page id outside [0, num_pages) in the ring or a table is passed on as it is;
+ * its tokens get slot -1, and it is reported the same way.
  * Supported: B <= 8192, total_max <= 2^30, num_pages * page_size < 2^31, max_pages * page_size <=
  * 2^30. One launch.
  * seqlens, new_tokens and the tables must not overlap other outputs than those named.

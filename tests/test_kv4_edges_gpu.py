@@ -160,3 +160,19 @@ def test_decode_of_queries_whose_loud_channel_meets_zero_keys(wide):
         assert torch.equal(call(far, pool, table, lens), call(none, pool, table, lens))
         within(call(far, pool, table, lens), *want(none, pool, table, lens))
     da.diffattn_device_status()
+
+
+def test_plan_of_more_keys_than_32_bits_count_does_not_fit():
+    """Two requests of 2^30 keys: their sum has no place in cu_seqlens_k; with one key less it has."""
+    page, cap = 1 << 28, 1 << 30
+    for last, fits in ((cap - 2, True), (cap - 1, False)):
+        s = [cap - 1, last]
+        p = da.diffattn_paged_plan(dev32(s), dev32([1, 1]), dev32([[0, 1, 2, 3]] * 2), dev32([4, 5, 6, 0, 1, 2, 3]), dev32([0, 3]), page, 4)
+        if fits:
+            da.diffattn_device_status()
+            assert p["seqlens"].tolist() == [cap, cap - 1] and p["cu_seqlens_k"].tolist() == [0, cap, 2 * cap - 1]
+            assert p["slot_map"].tolist() == [cap - 1, cap - 2, -1, -1]
+        else:
+            with pytest.raises(da.DiffAttnError, match="does not fit"):
+                da.diffattn_device_status()
+            assert p["seqlens"].tolist() == s and not p["cu_seqlens_k"].any() and (p["slot_map"] == -1).all()
