@@ -923,7 +923,8 @@ DIFFATTN_API int diffattn_kv4_record_bytes(int kw, int vw);
  *       positive multiples of 8 (views of one fused projection, for example)
  *   slot_map : device int32 [total]; -1 skips a row; any other value outside [0, num_pages *
  *       page_size) skips it and is reported by diffattn_device_status() as DIFFATTN_ERR_INDEX.
- *       Slots that are not -1 must differ: of two rows with one slot, either's blocks may stay
+ *       Slots that are not -1 must differ: one that two rows name is left with codes and scales of
+ *       both, mixed (the other slots are not touched by that)
  *   pool : written at those slots alone. Rows of one call may share a record with rows that
  *       another kernel reads or writes at the same time, at other slots
  *   total : may be 0

@@ -8,7 +8,7 @@ import torch
 
 import differential_attention_gb300 as da
 from oracle import kv4_ref as kv4
-from tests.test_kv4_gpu import DEV, FLOOR, SLACK, both, dev32, v1_case, widened, within
+from tests.test_kv4_gpu import DEV, FLOOR, SLACK, both, dev32, expected_pool, random_rows, v1_case, widened, within
 
 pytestmark = pytest.mark.gpu
 
@@ -176,3 +176,19 @@ def test_plan_of_more_keys_than_32_bits_count_does_not_fit():
             with pytest.raises(da.DiffAttnError, match="does not fit"):
                 da.diffattn_device_status()
             assert p["seqlens"].tolist() == s and not p["cu_seqlens_k"].any() and (p["slot_map"] == -1).all()
+
+
+def test_append_of_two_rows_to_one_slot_touches_no_other():
+    rng = np.random.default_rng(241)
+    k, v = random_rows(rng, (40, 3, 256)), random_rows(rng, (40, 3, 256))
+    slots = np.concatenate([np.arange(10, 40), [20] * 10])
+    pool = rng.integers(0, 256, (4, 3, 1, 4608)).astype(np.uint8)
+    want = expected_pool(pool, 2, k[:30], v[:30], slots[:30], 16)
+    got = torch.tensor(pool).to(DEV)
+    da.diffattn_kv4_append(k.to(DEV), v.to(DEV), dev32(slots), got)
+    got = got.cpu().numpy()
+    for x in (got, want):  # (that slot itself: a row of zeros in both)
+        for h in range(3):
+            kv4.write_row(x[1, h, 0], 2, np.zeros(256), np.zeros(256), 4)
+    assert np.array_equal(got, want)
+    da.diffattn_device_status()
