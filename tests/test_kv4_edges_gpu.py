@@ -8,7 +8,8 @@ import torch
 
 import differential_attention_gb300 as da
 from oracle import kv4_ref as kv4
-from tests.test_kv4_gpu import DEV, FLOOR, SLACK, both, dev32, expected_pool, random_rows, v1_case, widened, within
+from tests import kv4_pieces as pieces
+from tests.test_kv4_gpu import (DEV, FLOOR, SLACK, both, dev32, expected_pool, random_rows, v1_case, widened, within)
 
 pytestmark = pytest.mark.gpu
 
@@ -191,4 +192,28 @@ def test_append_of_two_rows_to_one_slot_touches_no_other():
         for h in range(3):
             kv4.write_row(x[1, h, 0], 2, np.zeros(256), np.zeros(256), 4)
     assert np.array_equal(got, want)
+    da.diffattn_device_status()
+
+
+@pytest.mark.parametrize("batch", pieces.FEW + pieces.MANY + pieces.CLUSTER, ids=lambda b: f"{b.form}-{len(b.lens)}x{b.heads}-{max(b.lens)}")
+def test_decode_takes_every_piece_once(batch):
+    """Values by which each piece of each row shows (test_kv4_edges_cpu.py shows that it does), over rows cut
+    for all blocks, batches cut inside most rows, and rows over a cluster. The scratch holds NaN."""
+    B, cols = len(batch.lens), batch.columns // 2
+    Q = torch.tensor(pieces.queries(batch), dtype=torch.bfloat16, device=DEV)
+    args = Q, torch.tensor(pieces.pool(batch)).to(DEV), dev32(batch.table()), dev32(batch.lens)
+    size = (da.diffattn_decode_kv4_workspace_size(B, batch.heads) if batch.form == "v1"
+            else da.diffattn_v2_decode_kv4_workspace_size(B, batch.heads * batch.group, batch.heads))
+    ws = torch.full((size,), 255, dtype=torch.uint8, device=DEV)
+    if batch.form == "v1":
+        got = da.diffattn_decode_kv4(*args, torch.full((batch.heads,), pieces.LAMBDA, device=DEV), norm=False, scale=False, workspace=ws)
+    else:
+        logit = float(np.log(pieces.SIGMA / (1 - pieces.SIGMA)))
+        got = da.diffattn_v2_decode_kv4(*args, torch.full((B, batch.heads * cols), logit, device=DEV), workspace=ws)
+    want, bound = np.zeros((B, batch.heads * cols, batch.channels)), np.zeros((B, batch.heads * cols, batch.channels))
+    for b in range(B):
+        for h in range(batch.heads if batch.lens[b] else 0):
+            at = slice(cols * h, cols * (h + 1))
+            want[b, at], bound[b, at] = batch.outputs(b, h)
+    within(got, want, SLACK * bound)
     da.diffattn_device_status()
