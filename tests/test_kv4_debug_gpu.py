@@ -23,3 +23,13 @@ def test_kv4_suite_under_the_debug_build():
                           "no:cacheprovider"], cwd=ROOT, env=env, capture_output=True, text=True, timeout=1200)
     assert run.returncode == 0, run.stdout[-4000:] + run.stderr[-2000:]
     assert " passed" in run.stdout
+
+
+def test_kv4_edges_under_the_debug_build():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    env = dict(os.environ, DIFFATTN_DEBUG_BUILD="1")
+    run = subprocess.run([sys.executable, "-m", "pytest", "tests/test_kv4_edges_gpu.py", "-m", "gpu", "-x", "-q", "-p",
+                          "no:cacheprovider"], cwd=ROOT, env=env, capture_output=True, text=True, timeout=1200)
+    assert run.returncode == 0, run.stdout[-4000:] + run.stderr[-2000:]
+    assert " passed" in run.stdout

@@ -9,7 +9,8 @@ import torch
 import differential_attention_gb300 as da
 from oracle import kv4_ref as kv4
 from tests import kv4_pieces as pieces
-from tests.test_kv4_gpu import (DEV, FLOOR, SLACK, both, dev32, expected_pool, random_rows, v1_case, widened, within)
+from tests.test_kv4_gpu import (DEV, FLOOR, SLACK, both, dev32, expected_pool, random_rows, random_table, to64, v1_case, widened,
+                                within)
 
 pytestmark = pytest.mark.gpu
 
@@ -217,3 +218,44 @@ def test_decode_takes_every_piece_once(batch):
             want[b, at], bound[b, at] = batch.outputs(b, h)
     within(got, want, SLACK * bound)
     da.diffattn_device_status()
+
+
+def test_v1_rows_of_many_sequences_in_and_out():
+    """Four planes a record: appended by views of one projection, read back whole, over many sequences."""
+    rng = np.random.default_rng(251)
+    for H, lens, ps in ((13, [(i * 53) % 500 for i in range(30)], 32), (3, [3000, 1, 4095, 0, 77] * 2, 80)):
+        table, pages = random_table(rng, lens, ps)
+        total, cu = sum(lens), np.concatenate([[0], np.cumsum(lens)])
+        proj = torch.randn((total, 3, H, 256), device=DEV).to(torch.bfloat16)
+        pos, seq = np.concatenate([np.arange(n) for n in lens]), np.repeat(np.arange(len(lens)), lens)
+        pool = torch.zeros((pages, H, ps // 16, 4608), dtype=torch.uint8, device=DEV)
+        da.diffattn_kv4_append(proj[:, 1], proj[:, 2], dev32(table[seq, pos // ps] * ps + pos % ps), pool)
+        got = da.diffattn_kv4_gather(pool, dev32(table), dev32(cu), total, 256, 256)
+        for i, g in enumerate(got):
+            assert np.array_equal(to64(g), kv4.values(*kv4.quantize_blocks(to64(proj[:, 1 + i]))))
+    da.diffattn_device_status()
+
+
+def test_append_refuses_rows_that_heads_share():
+    """A stride of 0 between heads (one row for all of them) or tokens, and a last dimension with steps."""
+    pool = torch.full((2, 4, 1, 2304), 9, dtype=torch.uint8, device=DEV)
+    rows, slots = torch.zeros((3, 4, 128), dtype=torch.bfloat16, device=DEV), dev32([0, 1, 2])
+    for bad in (rows[:, :1].expand(3, 4, 128), rows[:1].expand(3, 4, 128)):
+        for k, v in ((bad, rows), (rows, bad)):
+            with pytest.raises(da.DiffAttnError) as e:
+                da.diffattn_kv4_append(k, v, slots, pool)
+            assert e.value.status == -4
+    with pytest.raises(ValueError, match="contiguous"):
+        da.diffattn_kv4_append(torch.zeros((3, 4, 256), dtype=torch.bfloat16, device=DEV)[..., ::2], rows, slots, pool)
+    torch.cuda.synchronize()
+    assert bool((pool == 9).all())
+
+
+def test_decode_takes_the_scalars_that_the_other_calls_take():
+    """lambda_init and eps as numpy scalars or tensors of one value."""
+    lens = [70]
+    table, pool, q, lam, w = v1_case(np.random.default_rng(233), lens, 2, 16)
+    args = q.to(DEV), torch.tensor(pool).to(DEV), dev32(table), dev32(lens), lam.to(DEV)
+    want = da.diffattn_decode_kv4(*args, 0.5, eps=2.0 ** -10)
+    for kind in (np.float32, np.float64, torch.tensor):
+        assert torch.equal(da.diffattn_decode_kv4(*args, kind(0.5), eps=kind(2.0 ** -10)), want)
