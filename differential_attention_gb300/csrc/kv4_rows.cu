@@ -50,9 +50,9 @@ __device__ __forceinline__ Block round_block(const uint4& w0, const uint4& w1, f
 // A warp rounds 8 rows of one head, plane after plane: a lane 32 channels of a row of K (two blocks, one
 // 16-byte piece of the record), then the same 16 channels of two rows of V, which are one piece too
 // where the rows' slots are the two of a pair. The next plane is loaded while one is rounded. What
-// bounds it: the bytes (2 read, 9/16 written a channel): 16K rows of 12 V1 heads, 258 MB, take 43.9 us,
-// 5.9 TB/s of a copy's 6.78, with 55 % of the ALU pipe and 63 % of the issue slots in use. (The
-// first form, with a division for each value, took about 100.)
+// bounds it: the bytes (2 read, 9/16 written a channel): 64K rows of 12 V1 heads, 1.03 GB, take 153.5 us,
+// 6.72 TB/s of a copy's 6.78, with 55 % of the ALU pipe and 63 % of the issue slots in use; 16K rows 43.9,
+// 5.9 TB/s. (With a division for each value 16K rows took about 100.)
 template <int KP>
 __global__ void __launch_bounds__(kAppendThreads) kv4_append_kernel(const Kv4AppendArgs a) {
   grid_wait();
@@ -140,7 +140,7 @@ __device__ __forceinline__ uint32_t half2_to_bf16x2(uint32_t h, float f) {
 // and writes its rows, two at a time: a lane 8 channels, so that each store of the warp is whole rows of
 // 128 channels (16 bytes a lane, side by side). What bounds it: the bytes (9/16 read, 2 written a channel,
 // so four fifths of them writes): 6 x 8160 tokens of 8 V2 heads, 257 MB, take 41.4 us, 6.2 TB/s of a
-// copy's 6.78, 4 x 4080 of 12 V1 heads 42.5. (Two or four heads a warp, which share one look-up of the
+// copy's 6.78, 4 x 4080 of 12 V1 heads 42.5, 4 x 16384 of them 157.0, 6.6 TB/s. (Two or four heads a warp, which share one look-up of the
 // sequence and the page: 42.3 and 42.3 us, 43.8 and 43.7. Streaming stores: no difference.)
 //
 // Sequence b's records have the warps from cu[b] / 16 + 2 b on: n rows touch at most n / 16 + 2 records,

@@ -913,6 +913,8 @@ DIFFATTN_API int diffattn_paged_plan(const int* seqlens, const int* new_tokens, 
  *      1024 + 16 g + 4 (i/4) + i % 4
  * (the order in which a warp's lanes take them for the attention's matrix products). Slot s is token
  * s % page_size of page s / page_size; page_size is a multiple of 16.
+ * A record is one head of both K and V. The grouped form (diffattn_gda_*), whose K has noise heads
+ * besides the signal heads that V has, has no such cache.
  * ------------------------------------------------------------------------------------------ */
 /* Bytes of one record; 0 for a pair of widths that is not supported. */
 DIFFATTN_API int diffattn_kv4_record_bytes(int kw, int vw);
