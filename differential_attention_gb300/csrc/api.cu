@@ -64,7 +64,7 @@ constexpr int kPrefillFlags =
 
 constexpr int DEV_BAD_INDEX_BIT = 2;  // the kernels' DEV_BAD_INDEX status bit
 constexpr int DEV_BOUNDS_BIT = 4;     // DEV_BOUNDS: a debug-build bounds check failed
-constexpr int DEV_NO_FIT_BIT = 8;     // DEV_NO_FIT: a page plan's step was out of range
+constexpr int DEV_NO_FIT_BIT = 8;     // the page plan's DEV_NO_FIT: a step that does not fit
 
 extern "C" {
 

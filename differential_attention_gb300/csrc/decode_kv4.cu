@@ -925,6 +925,6 @@ cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a, cudaStream_t st) {
   return a.group == 0 ? launch<2>(a, st) : launch<1>(a, st);
 }
 
-cudaError_t status_decode_kv4(int* v) { return g_launched.load(std::memory_order_relaxed) ? read_clear_status(v) : cudaSuccess; }
+cudaError_t status_decode_kv4(int* v) { return launched_status(v); }
 
 }  // namespace da

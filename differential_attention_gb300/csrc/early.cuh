@@ -4,6 +4,8 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include "ptx.cuh"
+
 namespace da {
 
 // Until the kernels before this one are done and their writes seen (by plain loads: what they wrote was not
@@ -15,6 +17,15 @@ __device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.la
 
 // Whether this file's kernels were ever launched: until then its status word is 0 and need not be read.
 static std::atomic<bool> g_launched{false};
+
+// This file's status word; cleared where it is set.
+static inline cudaError_t launched_status(int* v) {
+  if (!g_launched.load(std::memory_order_relaxed)) return cudaSuccess;
+  cudaError_t e = cudaMemcpyFromSymbol(v, g_device_status, sizeof(int));
+  const int zero = 0;
+  if (e == cudaSuccess && *v != 0) e = cudaMemcpyToSymbol(g_device_status, &zero, sizeof(int));
+  return e;
+}
 
 // Launches a kernel that calls grid_wait() first: it is set up while the one before it in the stream ends.
 template <typename P>

@@ -247,6 +247,6 @@ cudaError_t launch_kv4_gather(const Kv4GatherArgs& a, cudaStream_t st) {
   return launch_early(a.kp == 1 ? kv4_gather_kernel<1> : kv4_gather_kernel<2>, blocks, kGatherThreads, 0, st, 1, a);
 }
 
-cudaError_t status_kv4_rows(int* v) { return g_launched.load(std::memory_order_relaxed) ? read_clear_status(v) : cudaSuccess; }
+cudaError_t status_kv4_rows(int* v) { return launched_status(v); }
 
 }  // namespace da

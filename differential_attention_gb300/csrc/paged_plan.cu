@@ -20,6 +20,7 @@
 namespace da {
 namespace {
 
+constexpr int DEV_NO_FIT = 8;  // beside ptx.cuh's codes: a step that does not fit
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanCluster = 8;
 
@@ -224,6 +225,6 @@ cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t st) {
   return launch_early_large(paged_plan_kernel, blocks, kPlanThreads, smem, (4 * kPlanMaxRequests + 3) * 4, st, blocks, p, raised);
 }
 
-cudaError_t status_paged_plan(int* v) { return g_launched.load(std::memory_order_relaxed) ? read_clear_status(v) : cudaSuccess; }
+cudaError_t status_paged_plan(int* v) { return launched_status(v); }
 
 }  // namespace da

@@ -8,9 +8,8 @@
 
 namespace da {
 
-// Error codes a kernel can leave in the device status word. DEV_BOUNDS only in debug builds; DEV_NO_FIT
-// by the page plan alone.
-enum : int { DEV_OK = 0, DEV_TIMEOUT = 1, DEV_BAD_INDEX = 2, DEV_BOUNDS = 4, DEV_NO_FIT = 8 };
+// Error codes a kernel can leave in the device status word. DEV_BOUNDS only in debug builds.
+enum : int { DEV_OK = 0, DEV_TIMEOUT = 1, DEV_BAD_INDEX = 2, DEV_BOUNDS = 4 };
 
 // Debug builds (-DDIFFATTN_DEBUG; libdiffattn_debug.so, `builder.py --debug`) check every tile
 // coordinate of a TMA copy and every gathered or stored row index against the extent of its
@@ -31,7 +30,7 @@ static __device__ int g_device_status = 0;
 static inline cudaError_t read_clear_status(int* v) {
   const int zero = 0;
   cudaError_t e = cudaMemcpyFromSymbol(v, g_device_status, sizeof(int));
-  if (e == cudaSuccess && *v != 0) e = cudaMemcpyToSymbol(g_device_status, &zero, sizeof(int));
+  if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_device_status, &zero, sizeof(int));
   return e;
 }
 
