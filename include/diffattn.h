@@ -958,8 +958,8 @@ DIFFATTN_API int diffattn_kv4_gather(const void* pool, const int* block_table,
  * enters the products exactly (in fp16), a probability rounded to fp16. A head's query (V1: each of its
  * two halves) enters in fp16 after a power of two of its own: with all its bits in channels whose
  * exponent is up to 31 below that of the largest; a smaller channel is off by 2^-39 of the largest at
- * most, and one below 2^-40 of it counts as 0. (That shows only where the keys are all but zero in
- * the large channels.)
+ * most, and one below 2^-40 of it counts as 0 (the largest taken as 2^-100 where it is smaller). That
+ * shows only where the keys are all but zero in the large channels.
  *   q    : device bf16 [B, H, 2d] (V1) or [B, Hq, d] (V2)
  *   pool : V1 kw = vw = 2d; V2 H = Hkv, kw = vw = d. k_exp, v_exp as written
  *   block_table : device int32 [B, max_pages]; seqlens : device int32 [B], keys 0 .. seqlens[b] - 1

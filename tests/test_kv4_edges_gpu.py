@@ -1,6 +1,7 @@
 """The 4-bit cache's calls at the far ends of what their header allows: exponents, weights that are not
 finite, streams of other libraries, joins of every piece. Bounds as in test_kv4_gpu.py."""
 import ctypes
+import gc
 
 import numpy as np
 import pytest
@@ -89,9 +90,10 @@ def test_decode_keeps_nothing_for_foreign_streams():
         return s
 
     open_ = [use(out[0])]
+    gc.collect()
     held = torch.cuda.memory_allocated()
     open_ += [use(o) for o in out[1:]]
-    assert torch.cuda.memory_allocated() == held
+    assert torch.cuda.memory_allocated() <= held
     torch.cuda.synchronize()
     for s in open_:
         s.close()
