@@ -36,6 +36,8 @@ DIFFATTN_SCALE = 4
 DIFFATTN_CUDA_CORES = 8
 DIFFATTN_SINGLE_PASS = 16
 DIFFATTN_EXACT = 32
+DIFFATTN_ROPE_INTERLEAVED = 1
+DIFFATTN_ROPE_INVERSE = 2
 
 STATUS_NAMES = {0: "OK", -1: "ERR_ARG", -2: "ERR_SHAPE", -3: "ERR_DTYPE", -4: "ERR_ALIGN",
                 -5: "ERR_CUDA", -6: "ERR_TIMEOUT", -7: "ERR_UNSUPPORTED", -8: "ERR_WORKSPACE",
@@ -198,6 +200,14 @@ _SIGNATURES = {
                                               + [ctypes.POINTER(ctypes.c_size_t)]),
     "diffattn_v2_decode_kv4": (ctypes.c_int, [ctypes.c_void_p] * 6 + [ctypes.c_int] * 10
                                + [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "diffattn_rope_table": (ctypes.c_int, [ctypes.c_void_p] * 2 + [ctypes.c_int] * 2 + [ctypes.c_void_p]),
+    "diffattn_rope": (ctypes.c_int, [ctypes.c_void_p] * 4 + [ctypes.POINTER(ctypes.c_longlong)]
+                      + [ctypes.c_void_p] * 3 + [ctypes.c_int] * 10 + [ctypes.c_void_p]),
+    "diffattn_rope_append": (ctypes.c_int, [ctypes.c_void_p] * 6 + [ctypes.POINTER(ctypes.c_longlong)]
+                             + [ctypes.c_void_p] * 4 + [ctypes.c_int] * 12 + [ctypes.c_void_p]),
+    "diffattn_rope_kv4_append": (ctypes.c_int, [ctypes.c_void_p] * 5
+                                 + [ctypes.POINTER(ctypes.c_longlong)] + [ctypes.c_void_p] * 4
+                                 + [ctypes.c_int] * 13 + [ctypes.c_void_p]),
     "diffattn_gda_decode": (ctypes.c_int, [ctypes.c_void_p] * 6 + [ctypes.c_float, ctypes.c_void_p,
                                                                     ctypes.c_float]
                             + [ctypes.c_int] * 8 + [ctypes.c_void_p, ctypes.c_size_t,
@@ -1864,3 +1874,178 @@ def diffattn_v2_decode_kv4(q, pool, block_table, seqlens, lam_logit, k_exp: int 
     if rc:
         _check(rc)
     return out
+
+
+# ---- rotary positions ----------------------------------------------------------------------------
+
+_Strides8 = ctypes.c_longlong * 8
+
+
+def _rope_tables(table, positions, axes, total, index):
+    """Checks what the calls on rotary positions share; (table, positions, axes) addresses, pairs, number
+    of axes, positions of the table."""
+    try:
+        (top, pairs, two), n_axes = table.shape, 1 if positions.dim() == 1 else positions.shape[0]
+        shape = (total,) if positions.dim() == 1 else (n_axes, total)
+    except (AttributeError, ValueError, IndexError):
+        raise ValueError("need tensors table [top, pairs, 2] and positions [total] or [axes, total]") from None
+    t = _operand("table", table, _F32, index, (top, pairs, 2))
+    p = _operand("positions", positions, _I32, index, shape)
+    if axes is None and n_axes > 1:
+        raise ValueError("axes must name the axis of each pair where positions has several")
+    return t, p, None if axes is None else _operand("axes", axes, _I32, index, (pairs,)), pairs, n_axes, top
+
+
+def _row_operand(name, t, dtype, index, shape=None):
+    """Address and strides (token, head) of rows [total, heads, width]; a dimension of one token or head is
+    never stepped over, so that its stride may be anything."""
+    if not (isinstance(t, torch.Tensor) and t.get_device() == index and index >= 0 and t.dtype is dtype and t.dim() == 3
+            and (shape is None or t.shape == shape)):
+        if isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 3 and t.get_device() == index and t.dtype is dtype:
+            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+        raise ValueError(f"{name} must be a {dtype} tensor [total, heads, width] on cuda:{index}")
+    n, h, w = t.shape
+    ts, hs, ws = t.stride()
+    if ws != 1 and w > 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    return t.data_ptr(), ts if n > 1 else h * w or 8, hs if h > 1 else w or 8
+
+
+def _like_rows(t):
+    return torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+
+def diffattn_rope_table(inv_freq, top: int, out=None, stream=None):
+    """Cosines and sines fp32 [top, pairs, 2] of positions 0 .. top - 1 times the frequencies inv_freq
+    (fp64 [pairs], radians a position), angles in 64 bits."""
+    if stream is not None:
+        with _current(stream, inv_freq):
+            return diffattn_rope_table(inv_freq, top, out)
+    _dev("inv_freq", inv_freq, torch.float64)
+    if inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be [pairs]")
+    top, pairs, index = int(top), inv_freq.shape[0], inv_freq.get_device()
+    if top < 1 or pairs < 1:
+        raise ValueError("need top >= 1 and at least one frequency")
+    with torch.cuda.device(index):
+        if out is None:
+            out = torch.empty((top, pairs, 2), dtype=_F32, device=inv_freq.device)
+        at = _operand("out", out, _F32, index, (top, pairs, 2))
+        _check(lib().diffattn_rope_table(inv_freq.data_ptr(), at, top, pairs, _raw_stream(index)))
+    return out
+
+
+def diffattn_rope(q, k, table, positions, d: int = 128, axes=None, interleaved: bool = False,
+                  inverse: bool = False, out=None, stream=None):
+    """Queries q [total, hq, width] and keys k [total, hk, width] (or None) turned by rotary positions, each
+    part of d channels of a row by itself: table fp32 [top, pairs, 2] (diffattn_rope_table), positions
+    int32 [total], or [n, total] with axes int32 [pairs], the axis of each pair (time, height, width);
+    a token at -1 is left out. bf16 or fp32, any strides of whole 16 bytes. inverse: turned back, which
+    takes gradients of the outputs to those of the inputs. out = (q_out, k_out), which may be the inputs;
+    without it, rows of tokens left out are not initialised. Returns (q_out, k_out)."""
+    if stream is not None:
+        with _current(stream, q):
+            return diffattn_rope(q, k, table, positions, d, axes, interleaved, inverse, out)
+    if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 3:
+        raise ValueError("q must be a CUDA tensor [total, heads, width]")
+    index, (total, hq, width), dtype = q.get_device(), q.shape, q.dtype
+    code = _code(dtype)
+    if index != _get_device():
+        with torch.cuda.device(index):
+            return diffattn_rope(q, k, table, positions, d, axes, interleaved, inverse, out)
+    tab, pos, ax, pairs, n_axes, top = _rope_tables(table, positions, axes, total, index)
+    q_at, qt, qh = _row_operand("q", q, dtype, index)
+    k_at, kt, kh, hk = None, 16, 16, 0
+    if k is not None:
+        hk = k.shape[1] if isinstance(k, torch.Tensor) and k.dim() == 3 else 0
+        k_at, kt, kh = _row_operand("k", k, dtype, index, (total, hk, width))
+    q_out, k_out = (_like_rows(q), None if k is None else _like_rows(k)) if out is None else out
+    if (k is None) != (k_out is None):
+        raise ValueError("out must hold a tensor for each of q and k")
+    qo_at, qot, qoh = _row_operand("out[0]", q_out, dtype, index, (total, hq, width))
+    ko_at, kot, koh = (None, 16, 16) if k is None else _row_operand("out[1]", k_out, dtype, index, (total, hk, width))
+    rc = lib().diffattn_rope(q_at, k_at, qo_at, ko_at, _Strides8(qt, qh, kt, kh, qot, qoh, kot, koh), tab, pos, ax, total, hq, hk,
+                             width, int(d), pairs, n_axes, top,
+                             (DIFFATTN_ROPE_INTERLEAVED if interleaved else 0) | (DIFFATTN_ROPE_INVERSE if inverse else 0),
+                             code, _raw_stream(index))
+    if rc:
+        _check(rc)
+    return q_out, k_out
+
+
+def _rope_rows(q, k, v, q_out, index):
+    """Checks the rows of an append; (q, k, v, q_out) addresses, strides, hq, and q_out."""
+    if not (isinstance(v, torch.Tensor) and v.dim() == 3 and v.shape[:2] == k.shape[:2]):
+        raise ValueError("v must be [total, H, vw], of k's tokens and heads")
+    (total, H, kw), hq = k.shape, 0
+    k_at, kt, kh = _row_operand("k", k, _BF16, index)
+    v_at, vt, vh = _row_operand("v", v, _BF16, index)
+    q_at, qt, qh, o_at, ot, oh = None, 8, 8, None, 8, 8
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out without q")
+    else:
+        hq = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else 0
+        q_at, qt, qh = _row_operand("q", q, _BF16, index, (total, hq, kw))
+        if q_out is None:
+            q_out = _like_rows(q)
+        o_at, ot, oh = _row_operand("q_out", q_out, _BF16, index, (total, hq, kw))
+    return q_at, k_at, v_at, o_at, _Strides8(qt, qh, kt, kh, vt, vh, ot, oh), hq, q_out
+
+
+def diffattn_rope_append(q, k, v, table, positions, slot_map, k_pool, v_pool, d: int = 128, axes=None,
+                         interleaved: bool = False, q_out=None, stream=None):
+    """New rows into a paged bf16 cache: k [total, H, kw], turned as by diffattn_rope, and v [total, H, vw]
+    at slots slot_map (int32 [total]; -1: not at all) of k_pool [num_pages, page_size, H, kw] and v_pool
+    [.., vw]; q [total, hq, kw] (or None) turned into q_out (which may be q), which is returned."""
+    if stream is not None:
+        with _current(stream, k):
+            return diffattn_rope_append(q, k, v, table, positions, slot_map, k_pool, v_pool, d, axes, interleaved, q_out)
+    if not isinstance(k, torch.Tensor) or not k.is_cuda or k.dim() != 3:
+        raise ValueError("k must be a CUDA tensor [total, H, kw]")
+    index, (total, H, kw) = k.get_device(), k.shape
+    if index != _get_device():
+        with torch.cuda.device(index):
+            return diffattn_rope_append(q, k, v, table, positions, slot_map, k_pool, v_pool, d, axes, interleaved, q_out)
+    tab, pos, ax, pairs, n_axes, top = _rope_tables(table, positions, axes, total, index)
+    q_at, k_at, v_at, o_at, strides, hq, q_out = _rope_rows(q, k, v, q_out, index)
+    slots = _operand("slot_map", slot_map, _I32, index, (total,))
+    if not isinstance(k_pool, torch.Tensor) or k_pool.dim() != 4:
+        raise ValueError("k_pool must be [num_pages, page_size, H, kw]")
+    num_pages, page_size, vw = k_pool.shape[0], k_pool.shape[1], v.shape[2]
+    kp = _operand("k_pool", k_pool, _BF16, index, (num_pages, page_size, H, kw))
+    vp = _operand("v_pool", v_pool, _BF16, index, (num_pages, page_size, H, vw))
+    rc = lib().diffattn_rope_append(q_at, k_at, v_at, o_at, kp, vp, strides, tab, pos, ax, slots, total, hq, H, kw, vw, int(d),
+                                    pairs, n_axes, top, num_pages, page_size,
+                                    DIFFATTN_ROPE_INTERLEAVED if interleaved else 0, _raw_stream(index))
+    if rc:
+        _check(rc)
+    return q_out
+
+
+def diffattn_rope_kv4_append(q, k, v, table, positions, slot_map, pool, axes=None, interleaved: bool = False,
+                             k_exp: int = 0, v_exp: int = 0, q_out=None, stream=None):
+    """diffattn_rope_append into a 4-bit pool [num_pages, H, page_size / 16, record]: its bytes are those
+    that diffattn_kv4_append writes of diffattn_rope's keys."""
+    if stream is not None:
+        with _current(stream, k):
+            return diffattn_rope_kv4_append(q, k, v, table, positions, slot_map, pool, axes, interleaved, k_exp, v_exp, q_out)
+    if not isinstance(k, torch.Tensor) or not k.is_cuda or k.dim() != 3:
+        raise ValueError("k must be a CUDA tensor [total, H, kw]")
+    index, (total, H, kw) = k.get_device(), k.shape
+    if index != _get_device():
+        with torch.cuda.device(index):
+            return diffattn_rope_kv4_append(q, k, v, table, positions, slot_map, pool, axes, interleaved, k_exp, v_exp, q_out)
+    tab, pos, ax, pairs, n_axes, top = _rope_tables(table, positions, axes, total, index)
+    q_at, k_at, v_at, o_at, strides, hq, q_out = _rope_rows(q, k, v, q_out, index)
+    slots = _operand("slot_map", slot_map, _I32, index, (total,))
+    if not isinstance(pool, torch.Tensor) or pool.dim() != 4:
+        raise ValueError("pool must be [num_pages, H, page_size / 16, record]")
+    num_pages, recs, vw = pool.shape[0], pool.shape[2], v.shape[2]
+    at = _operand("pool", pool, _U8, index, (num_pages, H, recs, (kw + vw) * 9))
+    rc = lib().diffattn_rope_kv4_append(q_at, k_at, v_at, o_at, at, strides, tab, pos, ax, slots, total, hq, H, kw, vw, pairs, n_axes,
+                                        top, num_pages, recs * 16, int(k_exp), int(v_exp),
+                                        DIFFATTN_ROPE_INTERLEAVED if interleaved else 0, _raw_stream(index))
+    if rc:
+        _check(rc)
+    return q_out

@@ -86,11 +86,12 @@ DIFFATTN_API int diffattn_device_status(void* stream) {
   if (e == cudaSuccess) e = da::status_backward(&z);
   int dd = 0;
   if (e == cudaSuccess) e = da::status_decode(&dd);
-  int kd = 0, kr = 0, pp = 0;
+  int kd = 0, kr = 0, pp = 0, rp = 0;
   if (e == cudaSuccess) e = da::status_decode_kv4(&kd);
   if (e == cudaSuccess) e = da::status_kv4_rows(&kr);
   if (e == cudaSuccess) e = da::status_paged_plan(&pp);
-  dd |= kd | kr | pp;
+  if (e == cudaSuccess) e = da::status_rope(&rp);
+  dd |= kd | kr | pp | rp;
   if (e != cudaSuccess) return cuda_fail(e, "reading the device status word");
   v |= w | x | y | z | dd;
   if (v & DEV_BOUNDS_BIT)
@@ -103,7 +104,7 @@ DIFFATTN_API int diffattn_device_status(void* stream) {
   if (v & DEV_BAD_INDEX_BIT)
     return fail(DIFFATTN_ERR_INDEX,
                 "a block-table entry was outside [0, num_pages), or another index on the device (a slot, "
-                "an offset) outside its range%s%s (status %d)", v & DEV_NO_FIT_BIT ? "; and " : "",
+                "an offset, a position) outside its range%s%s (status %d)", v & DEV_NO_FIT_BIT ? "; and " : "",
                 v & DEV_NO_FIT_BIT ? no_fit : "", v);
   if (v & DEV_NO_FIT_BIT) return fail(DIFFATTN_ERR_INDEX, "%s (status %d)", no_fit, v);
   if (v != 0) return fail(DIFFATTN_ERR_TIMEOUT, "a bounded wait inside a kernel ran out (status %d)", v);
@@ -2369,6 +2370,180 @@ DIFFATTN_API int diffattn_v2_decode_kv4(const void* q, const void* pool, const i
   a.max_pages = max_pages;
   a.ws = workspace;
   return decode_kv4_impl(fn, a, a.group, 128, k_exp, v_exp, ws_bytes, stream);
+}
+
+}  // extern "C"
+
+namespace {
+
+// what the calls on rotary positions share; also the strides of `n` tensors (token, head each)
+int check_rope(const char* fn, const long long* strides, int n, const float* table, const int* positions, const int* axes,
+               int total, int hq, int H, int width, int d, int pairs, int n_axes, int top, int flags, int elt) {
+  if (!strides || (total > 0 && (!table || !positions || (n_axes > 1 && !axes))))
+    return fail(DIFFATTN_ERR_ARG, "%s: null pointer", fn);
+  if (flags & ~(DIFFATTN_ROPE_INTERLEAVED | DIFFATTN_ROPE_INVERSE))
+    return fail(DIFFATTN_ERR_ARG, "%s: unknown flag bits 0x%x", fn, flags);
+  if (total < 0 || hq < 0 || H < 0 || hq > 65535 || H > 65535 || static_cast<long long>(total) * (hq > H ? hq : H) > (1LL << 30))
+    return fail(DIFFATTN_ERR_SHAPE, "%s: need 0 <= heads <= 65535, total >= 0 and total * heads <= 2^30", fn);
+  if ((d != 64 && d != 128) || width < d || width > 4096 || width % d != 0)
+    return fail(DIFFATTN_ERR_SHAPE, "%s: need d of 64 or 128, and a width that is a multiple of d up to 4096 (got d=%d, width=%d)", fn, d, width);
+  if (pairs < 8 || pairs % 8 != 0 || 2 * pairs > d)
+    return fail(DIFFATTN_ERR_SHAPE, "%s: need pairs a multiple of 8 and at most d / 2 (got %d of d=%d)", fn, pairs, d);
+  if (n_axes < 1 || n_axes > 4 || top < 1)
+    return fail(DIFFATTN_ERR_SHAPE, "%s: need 1 to 4 axes and a table of at least one position", fn);
+  for (int i = 0; i < 2 * n; ++i)
+    if (strides[i] < 1 || strides[i] * elt % 16 != 0 || strides[i] > (1LL << 36))
+      return fail(DIFFATTN_ERR_ALIGN, "%s: stride %d (%lld) must be a positive multiple of 16 bytes", fn, i, strides[i]);
+  if (!aligned(table, 16) || !aligned(positions, 4) || !aligned(axes, 4))
+    return fail(DIFFATTN_ERR_ALIGN, "%s: the table must be 16-byte aligned, positions and axes 4-byte", fn);
+  return DIFFATTN_OK;
+}
+da::RopeRows rope_rows(const void* p, const long long* strides, int i) {
+  return {const_cast<void*>(p), strides[2 * i], strides[2 * i + 1]};
+}
+
+}  // namespace
+
+extern "C" {
+
+DIFFATTN_API int diffattn_rope_table(const double* inv_freq, float* table, int top, int pairs, void* stream) {
+  const char* fn = "diffattn_rope_table";
+  if (!inv_freq || !table) return fail(DIFFATTN_ERR_ARG, "%s: null pointer", fn);
+  if (top < 1 || pairs < 1 || pairs > 4096) return fail(DIFFATTN_ERR_SHAPE, "%s: need top >= 1 and 1 <= pairs <= 4096", fn);
+  if (!aligned(inv_freq, 8) || !aligned(table, 16))
+    return fail(DIFFATTN_ERR_ALIGN, "%s: inv_freq must be 8-byte aligned, the table 16-byte", fn);
+  if (int rc = check_device()) return rc;
+  cudaError_t e = da::launch_rope_table({inv_freq, reinterpret_cast<float2*>(table), top, pairs}, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, fn);
+  return ok();
+}
+
+DIFFATTN_API int diffattn_rope(const void* q, const void* k, void* q_out, void* k_out, const long long* strides,
+                               const float* table, const int* positions, const int* axes, int total, int hq, int hk,
+                               int width, int d, int pairs, int n_axes, int top, int flags, int dtype, void* stream) {
+  const char* fn = "diffattn_rope";
+  if (dtype != DIFFATTN_BF16 && dtype != DIFFATTN_FP32)
+    return fail(DIFFATTN_ERR_DTYPE, "%s: dtype must be DIFFATTN_BF16 or DIFFATTN_FP32", fn);
+  if (total > 0 && ((hq > 0 && (!q || !q_out)) || (hk > 0 && (!k || !k_out))))
+    return fail(DIFFATTN_ERR_ARG, "%s: null pointer", fn);
+  int rc = check_rope(fn, strides, 4, table, positions, axes, total, hq, hk, width, d, pairs, n_axes, top, flags,
+                      dtype == DIFFATTN_FP32 ? 4 : 2);
+  if (rc) return rc;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(q_out, 16) || !aligned(k_out, 16))
+    return fail(DIFFATTN_ERR_ALIGN, "%s: tensors must be 16-byte aligned", fn);
+  if ((rc = check_device())) return rc;
+  if (hq + hk == 0) return ok();
+  da::RopeArgs a{};
+  a.q = rope_rows(q, strides, 0);
+  a.k = rope_rows(k, strides, 1);
+  a.q_out = rope_rows(q_out, strides, 2);
+  a.k_out = rope_rows(k_out, strides, 3);
+  a.table = reinterpret_cast<const float2*>(table);
+  a.positions = positions;
+  a.axes = axes;
+  a.total = total;
+  a.hq = hq;
+  a.H = hk;
+  a.kw = width;
+  a.d = d;
+  a.pairs = pairs;
+  a.n_axes = n_axes;
+  a.top = top;
+  a.inverse = (flags & DIFFATTN_ROPE_INVERSE) != 0;
+  cudaError_t e = da::launch_rope(a, 0, dtype == DIFFATTN_FP32, (flags & DIFFATTN_ROPE_INTERLEAVED) != 0,
+                                  static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, fn);
+  return ok();
+}
+
+DIFFATTN_API int diffattn_rope_append(const void* q, const void* k, const void* v, void* q_out, void* k_pool, void* v_pool,
+                                      const long long* strides, const float* table, const int* positions, const int* axes,
+                                      const int* slot_map, int total, int hq, int H, int kw, int vw, int d, int pairs,
+                                      int n_axes, int top, int num_pages, int page_size, int flags, void* stream) {
+  const char* fn = "diffattn_rope_append";
+  if (!k_pool || !v_pool || (total > 0 && (!k || !v || !slot_map || (hq > 0 && (!q || !q_out)))))
+    return fail(DIFFATTN_ERR_ARG, "%s: null pointer", fn);
+  int rc = check_rope(fn, strides, 4, table, positions, axes, total, hq, H, kw, d, pairs, n_axes, top, flags, 2);
+  if (rc) return rc;
+  if (flags & DIFFATTN_ROPE_INVERSE) return fail(DIFFATTN_ERR_ARG, "%s: DIFFATTN_ROPE_INVERSE is diffattn_rope's", fn);
+  if (H < 1 || vw < d || vw > 4096 || vw % d != 0)
+    return fail(DIFFATTN_ERR_SHAPE, "%s: need H >= 1 and vw a multiple of d up to 4096 (got %d)", fn, vw);
+  if (num_pages < 1 || page_size < 1 || static_cast<long long>(num_pages) * page_size > 0x7fffffffLL)
+    return fail(DIFFATTN_ERR_SHAPE, "%s: need num_pages, page_size >= 1 and num_pages * page_size < 2^31", fn);
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) || !aligned(k_pool, 16) ||
+      !aligned(v_pool, 16) || !aligned(slot_map, 4))
+    return fail(DIFFATTN_ERR_ALIGN, "%s: tensors must be 16-byte aligned", fn);
+  if ((rc = check_device())) return rc;
+  da::RopeArgs a{};
+  a.q = rope_rows(q, strides, 0);
+  a.k = rope_rows(k, strides, 1);
+  a.v = rope_rows(v, strides, 2);
+  a.q_out = rope_rows(q_out, strides, 3);
+  a.table = reinterpret_cast<const float2*>(table);
+  a.positions = positions;
+  a.axes = axes;
+  a.slot_map = slot_map;
+  a.k_dst = k_pool;
+  a.v_dst = v_pool;
+  a.total = total;
+  a.hq = hq;
+  a.H = H;
+  a.kw = kw;
+  a.vw = vw;
+  a.d = d;
+  a.pairs = pairs;
+  a.n_axes = n_axes;
+  a.top = top;
+  a.num_pages = num_pages;
+  a.page_size = page_size;
+  cudaError_t e = da::launch_rope(a, 1, false, (flags & DIFFATTN_ROPE_INTERLEAVED) != 0, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, fn);
+  return ok();
+}
+
+DIFFATTN_API int diffattn_rope_kv4_append(const void* q, const void* k, const void* v, void* q_out, void* pool,
+                                          const long long* strides, const float* table, const int* positions,
+                                          const int* axes, const int* slot_map, int total, int hq, int H, int kw, int vw,
+                                          int pairs, int n_axes, int top, int num_pages, int page_size, int k_exp,
+                                          int v_exp, int flags, void* stream) {
+  const char* fn = "diffattn_rope_kv4_append";
+  if (!pool || (total > 0 && (!k || !v || !slot_map || (hq > 0 && (!q || !q_out)))))
+    return fail(DIFFATTN_ERR_ARG, "%s: null pointer", fn);
+  int rc = check_kv4(fn, H, kw, vw, num_pages, page_size, k_exp, v_exp);
+  if (!rc) rc = check_rope(fn, strides, 4, table, positions, axes, total, hq, H, kw, 128, pairs, n_axes, top, flags, 2);
+  if (rc) return rc;
+  if (flags & DIFFATTN_ROPE_INVERSE) return fail(DIFFATTN_ERR_ARG, "%s: DIFFATTN_ROPE_INVERSE is diffattn_rope's", fn);
+  if (pairs % 16 != 0 && !(flags & DIFFATTN_ROPE_INTERLEAVED))
+    return fail(DIFFATTN_ERR_SHAPE, "%s: need pairs a multiple of 16 where pairs are not neighbours (got %d)", fn, pairs);
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) || !aligned(pool, 16) || !aligned(slot_map, 4))
+    return fail(DIFFATTN_ERR_ALIGN, "%s: tensors must be 16-byte aligned", fn);
+  if ((rc = check_device())) return rc;
+  da::RopeArgs a{};
+  a.q = rope_rows(q, strides, 0);
+  a.k = rope_rows(k, strides, 1);
+  a.v = rope_rows(v, strides, 2);
+  a.q_out = rope_rows(q_out, strides, 3);
+  a.table = reinterpret_cast<const float2*>(table);
+  a.positions = positions;
+  a.axes = axes;
+  a.slot_map = slot_map;
+  a.k_dst = pool;
+  a.total = total;
+  a.hq = hq;
+  a.H = H;
+  a.kw = kw;
+  a.vw = vw;
+  a.d = 128;
+  a.pairs = pairs;
+  a.n_axes = n_axes;
+  a.top = top;
+  a.num_pages = num_pages;
+  a.page_size = page_size;
+  a.k_inv = std::ldexp(1.0f, -k_exp);
+  a.v_inv = std::ldexp(1.0f, -v_exp);
+  cudaError_t e = da::launch_rope(a, 2, false, (flags & DIFFATTN_ROPE_INTERLEAVED) != 0, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, fn);
+  return ok();
 }
 
 }  // extern "C"

@@ -342,6 +342,35 @@ size_t kv4_decode_workspace_bytes(int cols, int width);
 cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a, cudaStream_t s);
 cudaError_t status_decode_kv4(int* v);
 
+// Rotary positions (rope.cu).
+struct RopeRows {  // [total, heads, width] by element strides
+  void* data;
+  long long token, head;
+};
+struct RopeArgs {
+  RopeRows q, k, v, q_out, k_out;
+  const float2* table;   // [top, pairs]
+  const int* positions;  // [n_axes, total]
+  const int* axes;       // [pairs], or null where n_axes is 1
+  const int* slot_map;   // [total], with pages
+  void* k_dst;           // bf16 K pool [num_pages, page_size, H, kw], or the 4-bit pool
+  void* v_dst;           // bf16 V pool
+  int total, hq, H, kw, vw, d, pairs, n_axes, top;
+  int num_pages, page_size;
+  float k_inv, v_inv;    // 4 bits: 2^-k_exp, 2^-v_exp
+  bool inverse;
+  int split;             // warps a token, set by the launcher
+};
+// pages: 0 rows to rows, 1 bf16 pages, 2 4-bit pages
+cudaError_t launch_rope(RopeArgs a, int pages, bool fp32, bool interleaved, cudaStream_t s);
+struct RopeTableArgs {
+  const double* freq;  // [pairs]
+  float2* table;       // [top, pairs]
+  int top, pairs;
+};
+cudaError_t launch_rope_table(const RopeTableArgs& a, cudaStream_t s);
+cudaError_t status_rope(int* v);
+
 // A step's page plan (paged_plan.cu).
 constexpr int kPlanMaxRequests = 8192;
 struct PlanArgs {

@@ -12,41 +12,6 @@ namespace {
 // read-out alone is 0.3 slower with 64.)
 constexpr int kAppendThreads = 64, kGatherThreads = 256;
 
-__device__ __forceinline__ float2 bf16x2_to_float2(uint32_t w) {
-  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-}
-
-struct Block {  // 16 channels as they are stored
-  uint32_t lo, hi, scale;
-};
-
-// s = e4m3(amax / 6), c = e2m1(x / s) of 16 bf16 values.
-// x has 8 significant bits, s 4 and a border b of e2m1 (0.25, 0.75, .. 5) 3, so x / s is either b or
-// some 2^-8 b away from it. x times the rounded 1 / s, rounded once more to fp16's 11 bits, is then b
-// where the quotient is, and on its side of b where it is not: the decision of the exact quotient
-// without a division.
-__device__ __forceinline__ Block round_block(const uint4& w0, const uint4& w1, float exp_inv) {
-  const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-  uint32_t top2 = 0;  // the largest magnitudes' bits, ordered as the values are
-#pragma unroll
-  for (int j = 0; j < 8; ++j) top2 = __vmaxu2(top2, w[j] & 0x7fff7fffu);
-  const uint32_t top = max(top2 & 0xffffu, top2 >> 16);
-  Block b{0, 0, 0x7fu};
-  if (top >= 0x7f80u) return b;  // an Inf or NaN: the block reads as NaN
-  b.scale = float_to_e4m3(__fdiv_rn(__uint_as_float(top << 16) * exp_inv, 6.f));
-  if (b.scale == 0) return b;
-  const float r = __frcp_rn(e4m3_to_float(b.scale)) * exp_inv;
-  uint32_t y[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float2 x = bf16x2_to_float2(w[j]);
-    y[j] = pack_half2(x.x * r, x.y * r);
-  }
-  b.lo = half2x4_to_e2m1x8(y[0], y[1], y[2], y[3]);
-  b.hi = half2x4_to_e2m1x8(y[4], y[5], y[6], y[7]);
-  return b;
-}
-
 // A warp rounds 8 rows of one head, plane after plane: a lane 32 channels of a row of K (two blocks, one
 // 16-byte piece of the record), then the same 16 channels of two rows of V, which are one piece too
 // where the rows' slots are the two of a pair. The next plane is loaded while one is rounded. What
@@ -104,7 +69,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv4_append_kernel(const Kv4App
     if (plane + 1 < 2 * KP) load(plane + 1, w[(plane + 1) & 1]);
     const uint4(&c)[4] = w[plane & 1];
     const float inv = plane < KP ? a.k_inv : a.v_inv;
-    const Block x = round_block(c[0], c[1], inv), y = round_block(c[2], c[3], inv);
+    const Kv4Block x = kv4_round_block(c[0], c[1], inv), y = kv4_round_block(c[2], c[3], inv);
     if (plane < KP) {
       if (ks >= 0) {
         uint8_t* p = kdst + plane * kKv4Plane;

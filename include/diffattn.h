@@ -991,6 +991,80 @@ DIFFATTN_API int diffattn_v2_decode_kv4(const void* q, const void* pool, const i
                                         int max_pages, int k_exp, int v_exp, int flags,
                                         void* workspace, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------------------------
+ * Rotary positions (the pages do not say how positions enter; this is the usual rotation of queries
+ * and keys before the operators above). A row of a head is made of parts of d channels, each turned
+ * by itself: the two halves of a V1 query or key (width 2d), the whole of a V2 or grouped one (width
+ * d). The first 2 * pairs channels of a part are pairs, channels i and i + pairs, or 2i and 2i + 1
+ * (DIFFATTN_ROPE_INTERLEAVED); the others stay as they are. With (c, s) = table[p][i], p the token's
+ * position on the axis of pair i,
+ *   y1 = x1 c - x2 s,  y2 = x2 c + x1 s.
+ * DIFFATTN_ROPE_INVERSE turns back (s negated): the gradient with respect to x of a gradient with
+ * respect to y.
+ *   q, k : device rows [total, heads, width], the last dimension contiguous, the others by strides:
+ *       host int64 [8], {token, head} of four tensors in the order of the arguments, in elements,
+ *       positive multiples of 16 bytes (views of one fused projection, for example). Where a tensor
+ *       has no heads, its pointers may be NULL (its strides still have to hold multiples)
+ *   table : device fp32 [top, pairs, 2], cosines and sines (diffattn_rope_table, or a caller's own)
+ *   positions : device int32 [n_axes, total]. A token with a position of -1 (diffattn_paged_plan's
+ *       behind the last) is left out: nothing of it is read or written. So is one with any other
+ *       position outside [0, top), which diffattn_device_status() reports as DIFFATTN_ERR_INDEX
+ *   axes : device int32 [pairs], the axis (0 .. n_axes - 1) of each pair: time, height, width, in runs
+ *       or in turn. NULL with one axis. Another value is taken as 0, and reported the same way
+ *   total : may be 0
+ * A bf16 result is the exact value of the formula over the table's fp32 numbers, rounded once (to within
+ * 2^-149 more where it is below 2^-100), so that the calls agree in every bit; an fp32 one is within
+ * 2^-22 of its own magnitude and 2^-46 of the products'.
+ * Supported: d of 64 or 128, width a multiple of d up to 4096, pairs a multiple of 8 up to d / 2,
+ * 1 <= n_axes <= 4, total * heads <= 2^30. One launch.
+ * Errors: ERR_ARG, ERR_SHAPE, ERR_DTYPE, ERR_ALIGN, ERR_UNSUPPORTED, ERR_CUDA.
+ * ------------------------------------------------------------------------------------------ */
+#define DIFFATTN_ROPE_INTERLEAVED 1 /* pairs of neighbouring channels */
+#define DIFFATTN_ROPE_INVERSE 2     /* turn back (diffattn_rope only) */
+
+/* table[p][i] = (cos, sin)(p * inv_freq[i]) for p < top: angles in fp64, so that far positions lose
+ * nothing, each value rounded to fp32 once (to within fp64's own error in cos and sin).
+ *   inv_freq : device double [pairs], in radians a position;  table : device fp32 [top, pairs, 2]
+ * Supported: 1 <= pairs <= 4096. Errors: ERR_ARG, ERR_SHAPE, ERR_ALIGN, ERR_UNSUPPORTED, ERR_CUDA. */
+DIFFATTN_API int diffattn_rope_table(const double* inv_freq, float* table, int top, int pairs,
+                                     void* stream);
+
+/* Rows turned into rows: q [total, hq, width] to q_out and k [total, hk, width] to k_out, bf16 or
+ * fp32. strides: q, k, q_out, k_out. q_out may be q itself (with the same strides), k_out k; otherwise
+ * outputs overlap nothing. */
+DIFFATTN_API int diffattn_rope(const void* q, const void* k, void* q_out, void* k_out,
+                               const long long* strides, const float* table, const int* positions,
+                               const int* axes, int total, int hq, int hk, int width, int d,
+                               int pairs, int n_axes, int top, int flags, int dtype, void* stream);
+
+/* New rows into a paged bf16 cache, keys turned on the way, and the queries beside them: row i of k
+ * (turned) and of v goes to slot slot_map[i] = page * page_size + offset of the pools that the paged
+ * calls read, and q to q_out.
+ *   q, q_out : device bf16 [total, hq, kw]; hq may be 0 (V1 hq = H, kw = 2d; V2 hq = Hq, kw = d)
+ *   k : device bf16 [total, H, kw];  v : device bf16 [total, H, vw], vw a multiple of d
+ *   k_pool : device bf16 [num_pages, page_size, H, kw];  v_pool : [num_pages, page_size, H, vw]
+ *   strides : q, k, v, q_out. q_out may be q itself
+ *   slot_map : device int32 [total]; -1 skips the row of k and v (not of q); any other value outside
+ *       [0, num_pages * page_size) skips it and is reported as DIFFATTN_ERR_INDEX. Slots that are not
+ *       -1 must differ: one that two rows name is left with channels of both */
+DIFFATTN_API int diffattn_rope_append(const void* q, const void* k, const void* v, void* q_out,
+                                      void* k_pool, void* v_pool, const long long* strides,
+                                      const float* table, const int* positions, const int* axes,
+                                      const int* slot_map, int total, int hq, int H, int kw, int vw,
+                                      int d, int pairs, int n_axes, int top, int num_pages,
+                                      int page_size, int flags, void* stream);
+
+/* The same into a 4-bit pool (diffattn_kv4_append's, byte for byte, of diffattn_rope's keys):
+ * d = 128, kw = vw = 256 (V1) or 128 (V2), page_size a multiple of 16, and pairs a multiple of 16
+ * unless they are neighbours. */
+DIFFATTN_API int diffattn_rope_kv4_append(const void* q, const void* k, const void* v, void* q_out,
+                                          void* pool, const long long* strides, const float* table,
+                                          const int* positions, const int* axes,
+                                          const int* slot_map, int total, int hq, int H, int kw,
+                                          int vw, int pairs, int n_axes, int top, int num_pages,
+                                          int page_size, int k_exp, int v_exp, int flags,
+                                          void* stream);
+
 #ifdef __cplusplus
 }
 #endif
