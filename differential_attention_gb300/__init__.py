@@ -36,8 +36,8 @@ DIFFATTN_SCALE = 4
 DIFFATTN_CUDA_CORES = 8
 DIFFATTN_SINGLE_PASS = 16
 DIFFATTN_EXACT = 32
-DIFFATTN_ROPE_INTERLEAVED = 1
-DIFFATTN_ROPE_INVERSE = 2
+DIFFATTN_ROPE_INTERLEAVED = 64
+DIFFATTN_ROPE_INVERSE = 128
 
 STATUS_NAMES = {0: "OK", -1: "ERR_ARG", -2: "ERR_SHAPE", -3: "ERR_DTYPE", -4: "ERR_ALIGN",
                 -5: "ERR_CUDA", -6: "ERR_TIMEOUT", -7: "ERR_UNSUPPORTED", -8: "ERR_WORKSPACE",
@@ -200,6 +200,12 @@ _SIGNATURES = {
                                               + [ctypes.POINTER(ctypes.c_size_t)]),
     "diffattn_v2_decode_kv4": (ctypes.c_int, [ctypes.c_void_p] * 6 + [ctypes.c_int] * 10
                                + [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "diffattn_fwd_kv4_workspace_size": (ctypes.c_int, [ctypes.c_int] * 3 + [ctypes.POINTER(ctypes.c_size_t)]),
+    "diffattn_fwd_kv4": (ctypes.c_int, [ctypes.c_void_p] * 7 + [ctypes.c_float, ctypes.c_void_p, ctypes.c_float]
+                         + [ctypes.c_int] * 12 + [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "diffattn_v2_fwd_kv4_workspace_size": (ctypes.c_int, [ctypes.c_int] * 4 + [ctypes.POINTER(ctypes.c_size_t)]),
+    "diffattn_v2_fwd_kv4": (ctypes.c_int, [ctypes.c_void_p] * 7 + [ctypes.c_int] * 12
+                            + [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
     "diffattn_rope_table": (ctypes.c_int, [ctypes.c_void_p] * 2 + [ctypes.c_int] * 2 + [ctypes.c_void_p]),
     "diffattn_rope": (ctypes.c_int, [ctypes.c_void_p] * 4 + [ctypes.POINTER(ctypes.c_longlong)]
                       + [ctypes.c_void_p] * 3 + [ctypes.c_int] * 10 + [ctypes.c_void_p]),
@@ -1597,13 +1603,14 @@ _lent_buffers, _lent_lock = {}, threading.Lock()
 
 @contextlib.contextmanager
 def _lent(index):
-    """Scratch for one decode on a current stream that torch did not make. Such a stream may be destroyed,
+    """Scratch for one decode (or chunk) on a current stream that torch did not make. Such a stream may be destroyed,
     and its handle come back, while its work still runs, so that nothing is kept by the handle: each
-    device has one buffer, large enough for any decode, which goes from call to call by an event.
+    device has one buffer, large enough for any of them, which goes from call to call by an event.
     (Decodes of several such streams so run one after the other, unless they are given workspaces.)"""
     with _lent_lock:
         if index not in _lent_buffers:
-            n = max(diffattn_decode_kv4_workspace_size(1, 1), diffattn_v2_decode_kv4_workspace_size(1, 8, 1))
+            n = max(diffattn_decode_kv4_workspace_size(1, 1), diffattn_v2_decode_kv4_workspace_size(1, 8, 1),
+                    diffattn_fwd_kv4_workspace_size(1 << 20), diffattn_v2_fwd_kv4_workspace_size(1 << 20, 8, 1))
             _lent_buffers[index] = torch.empty(n, dtype=_U8, device=torch.device("cuda", index)), torch.cuda.Event()
         buffer, done = _lent_buffers[index]
         stream = torch.cuda.current_stream(index)
@@ -1871,6 +1878,131 @@ def diffattn_v2_decode_kv4(q, pool, block_table, seqlens, lam_logit, k_exp: int 
     rc = lib().diffattn_v2_decode_kv4(q.data_ptr(), pool.data_ptr(), block_table.data_ptr(), seqlens.data_ptr(),
                                       lam_logit.data_ptr(), out_at, B, Hq, Hkv, d, num_pages, recs * 16, max_pages,
                                       int(k_exp), int(v_exp), 0, ws, ws_bytes, raw)
+    if rc:
+        _check(rc)
+    return out
+
+
+@functools.lru_cache(maxsize=4096)
+def diffattn_fwd_kv4_workspace_size(max_seqlen_q: int, d: int = 128, dv: int = 256) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().diffattn_fwd_kv4_workspace_size(max_seqlen_q, d, dv, ctypes.byref(n)))
+    return n.value
+
+
+def diffattn_fwd_kv4(q, pool, block_table, cu_seqlens_q, seqlens, lam, lambda_init: float = 0.0, norm_weight=None,
+                     eps: float = 1e-5, causal: bool = True, norm: bool = True, scale: bool = True, max_seqlen_q=None,
+                     k_exp: int = 0, v_exp: int = 0, workspace=None, out=None, stream=None):
+    """V1 attention of chunks over a 4-bit pool [num_pages, H, page_size / 16, 4608]: packed queries q
+    [total_q, H, 256], sequence b's rows cu_seqlens_q[b] .. (int32 [B + 1]) being the last of its seqlens[b]
+    (int32 [B]) cached positions. max_seqlen_q: about the longest chunk, a hint (None: total_q). Without
+    `out`, rows behind the last sequence are not initialised."""
+    if stream is not None:
+        with _current(stream, q):
+            return diffattn_fwd_kv4(q, pool, block_table, cu_seqlens_q, seqlens, lam, lambda_init, norm_weight, eps, causal,
+                                    norm, scale, max_seqlen_q, k_exp, v_exp, workspace, out)
+    try:
+        dev = q.get_device()
+        (total, H, two_d), (num_pages, heads, recs, rec), (B, max_pages) = q.shape, pool.shape, block_table.shape
+        fit = (dev == pool.get_device() == block_table.get_device() == seqlens.get_device() == lam.get_device()
+               == cu_seqlens_q.get_device() and heads == H and rec == two_d * 18 and seqlens.shape == (B,)
+               and cu_seqlens_q.shape == (B + 1,) and lam.shape == (H,) and q.dtype is _BF16 and pool.dtype is _U8
+               and block_table.dtype is seqlens.dtype is cu_seqlens_q.dtype is _I32 and lam.dtype is _F32
+               and q.is_contiguous() and pool.is_contiguous() and block_table.is_contiguous() and seqlens.is_contiguous()
+               and cu_seqlens_q.is_contiguous() and lam.is_contiguous() and dev >= 0)
+    except (AttributeError, ValueError):
+        raise ValueError("need tensors q [total_q, H, 2d], pool [num_pages, H, page_size / 16, record], "
+                         "block_table [B, max_pages], cu_seqlens_q [B + 1], seqlens [B] and lam [H]") from None
+    if not fit:
+        _refuse(dev, ("q", q, _BF16, (total, H, two_d)), ("pool", pool, _U8, (num_pages, H, recs, two_d * 18)),
+                ("block_table", block_table, _I32, (B, max_pages)), ("cu_seqlens_q", cu_seqlens_q, _I32, (B + 1,)),
+                ("seqlens", seqlens, _I32, (B,)), ("lam", lam, _F32, (H,)))
+    if dev != _get_device():
+        with torch.cuda.device(dev):
+            return diffattn_fwd_kv4(q, pool, block_table, cu_seqlens_q, seqlens, lam, lambda_init, norm_weight, eps, causal,
+                                    norm, scale, max_seqlen_q, k_exp, v_exp, workspace, out)
+    raw, longest = _raw_stream(dev), total if max_seqlen_q is None else int(max_seqlen_q)
+    weight = None if norm_weight is None else _operand("norm_weight", norm_weight, _F32, dev, (two_d,))
+    if workspace is None:
+        kept = _workspace(dev, raw, diffattn_fwd_kv4_workspace_size(longest, two_d // 2, two_d))
+        if kept is None:
+            with _lent(dev) as workspace:
+                return diffattn_fwd_kv4(q, pool, block_table, cu_seqlens_q, seqlens, lam, lambda_init, norm_weight, eps, causal,
+                                        norm, scale, max_seqlen_q, k_exp, v_exp, workspace, out)
+        _, ws, ws_bytes = kept
+    else:
+        _, ws, ws_bytes = _given(workspace, dev)
+    if out is None:
+        out = torch.empty_like(q)
+        out_at = out.data_ptr()
+    else:
+        out_at = _operand("out", out, _BF16, dev, (total, H, two_d))
+    rc = lib().diffattn_fwd_kv4(q.data_ptr(), pool.data_ptr(), block_table.data_ptr(), cu_seqlens_q.data_ptr(), seqlens.data_ptr(),
+                                out_at, lam.data_ptr(), lambda_init, weight, eps, longest, total, B, H, two_d // 2, two_d,
+                                num_pages, recs * 16, max_pages, int(k_exp), int(v_exp), _train_flags(causal, norm, scale), ws,
+                                ws_bytes, raw)
+    if rc:
+        _check(rc)
+    return out
+
+
+@functools.lru_cache(maxsize=4096)
+def diffattn_v2_fwd_kv4_workspace_size(max_seqlen_q: int, Hq: int, Hkv: int, d: int = 128) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().diffattn_v2_fwd_kv4_workspace_size(max_seqlen_q, Hq, Hkv, d, ctypes.byref(n)))
+    return n.value
+
+
+def diffattn_v2_fwd_kv4(q, pool, block_table, cu_seqlens_q, seqlens, lam_logit, causal: bool = True, max_seqlen_q=None,
+                        k_exp: int = 0, v_exp: int = 0, workspace=None, out=None, stream=None):
+    """DIFF V2 attention of chunks over a 4-bit pool [num_pages, Hkv, page_size / 16, 2304]: packed queries q
+    [total_q, Hq, 128] and lam_logit [total_q, Hq/2] fp32, sequence b's rows cu_seqlens_q[b] .. (int32
+    [B + 1]) being the last of its seqlens[b] (int32 [B]) cached positions. max_seqlen_q: about the longest
+    chunk, a hint (None: total_q). Returns [total_q, Hq/2, 128]; without `out`, rows behind the last sequence
+    are not initialised."""
+    if stream is not None:
+        with _current(stream, q):
+            return diffattn_v2_fwd_kv4(q, pool, block_table, cu_seqlens_q, seqlens, lam_logit, causal, max_seqlen_q, k_exp,
+                                       v_exp, workspace, out)
+    try:
+        dev = q.get_device()
+        (total, Hq, d), (num_pages, Hkv, recs, rec), (B, max_pages) = q.shape, pool.shape, block_table.shape
+        fit = (dev == pool.get_device() == block_table.get_device() == seqlens.get_device() == lam_logit.get_device()
+               == cu_seqlens_q.get_device() and rec == d * 18 and seqlens.shape == (B,) and cu_seqlens_q.shape == (B + 1,)
+               and lam_logit.shape == (total, Hq // 2) and q.dtype is _BF16 and pool.dtype is _U8
+               and block_table.dtype is seqlens.dtype is cu_seqlens_q.dtype is _I32 and lam_logit.dtype is _F32
+               and q.is_contiguous() and pool.is_contiguous() and block_table.is_contiguous() and seqlens.is_contiguous()
+               and cu_seqlens_q.is_contiguous() and lam_logit.is_contiguous() and dev >= 0)
+    except (AttributeError, ValueError):
+        raise ValueError("need tensors q [total_q, Hq, d], pool [num_pages, Hkv, page_size / 16, record], "
+                         "block_table [B, max_pages], cu_seqlens_q [B + 1], seqlens [B] and lam_logit [total_q, Hq / 2]") from None
+    if not fit:
+        _refuse(dev, ("q", q, _BF16, (total, Hq, d)), ("pool", pool, _U8, (num_pages, Hkv, recs, d * 18)),
+                ("block_table", block_table, _I32, (B, max_pages)), ("cu_seqlens_q", cu_seqlens_q, _I32, (B + 1,)),
+                ("seqlens", seqlens, _I32, (B,)), ("lam_logit", lam_logit, _F32, (total, Hq // 2)))
+    if dev != _get_device():
+        with torch.cuda.device(dev):
+            return diffattn_v2_fwd_kv4(q, pool, block_table, cu_seqlens_q, seqlens, lam_logit, causal, max_seqlen_q, k_exp,
+                                       v_exp, workspace, out)
+    raw, longest = _raw_stream(dev), total if max_seqlen_q is None else int(max_seqlen_q)
+    if workspace is None:
+        kept = _workspace(dev, raw, diffattn_v2_fwd_kv4_workspace_size(longest, Hq, Hkv, d))
+        if kept is None:
+            with _lent(dev) as workspace:
+                return diffattn_v2_fwd_kv4(q, pool, block_table, cu_seqlens_q, seqlens, lam_logit, causal, max_seqlen_q, k_exp,
+                                           v_exp, workspace, out)
+        _, ws, ws_bytes = kept
+    else:
+        _, ws, ws_bytes = _given(workspace, dev)
+    if out is None:
+        out = torch.empty((total, Hq // 2, d), dtype=_BF16, device=q.device)
+        out_at = out.data_ptr()
+    else:
+        out_at = _operand("out", out, _BF16, dev, (total, Hq // 2, d))
+    rc = lib().diffattn_v2_fwd_kv4(q.data_ptr(), pool.data_ptr(), block_table.data_ptr(), cu_seqlens_q.data_ptr(),
+                                   seqlens.data_ptr(), lam_logit.data_ptr(), out_at, longest, total, B, Hq, Hkv, d, num_pages,
+                                   recs * 16, max_pages, int(k_exp), int(v_exp), DIFFATTN_CAUSAL if causal else 0, ws, ws_bytes,
+                                   raw)
     if rc:
         _check(rc)
     return out

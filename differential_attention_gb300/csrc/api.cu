@@ -86,12 +86,13 @@ DIFFATTN_API int diffattn_device_status(void* stream) {
   if (e == cudaSuccess) e = da::status_backward(&z);
   int dd = 0;
   if (e == cudaSuccess) e = da::status_decode(&dd);
-  int kd = 0, kr = 0, pp = 0, rp = 0;
+  int kd = 0, kr = 0, pp = 0, rp = 0, ck = 0;
   if (e == cudaSuccess) e = da::status_decode_kv4(&kd);
   if (e == cudaSuccess) e = da::status_kv4_rows(&kr);
   if (e == cudaSuccess) e = da::status_paged_plan(&pp);
   if (e == cudaSuccess) e = da::status_rope(&rp);
-  dd |= kd | kr | pp | rp;
+  if (e == cudaSuccess) e = da::status_chunk_kv4(&ck);
+  dd |= kd | kr | pp | rp | ck;
   if (e != cudaSuccess) return cuda_fail(e, "reading the device status word");
   v |= w | x | y | z | dd;
   if (v & DEV_BOUNDS_BIT)
@@ -2198,6 +2199,22 @@ int check_kv4_tables(const char* fn, int B, int page_size, int max_pages) {
   return DIFFATTN_OK;
 }
 
+// qk_scale, v_mul and eps of an attention over a 4-bit pool
+template <typename Args>
+void kv4_scales(Args& a, int k_exp, int v_exp) {
+  a.qk_scale = static_cast<float>(std::ldexp(1.4426950408889634 / std::sqrt(128.0), k_exp));
+  // y 2^v_exp / sqrt(mean(y^2) 2^(2 v_exp) + eps) is the same with 2^c in place of 2^v_exp and eps
+  // 2^(2 (c - v_exp)) in place of eps. Where a norm follows, c stays where the squares of what a pool can
+  // give (values up to 2688, lambda up to 2^15) are finite in fp32 and small ones are not lost.
+  int v_pow = v_exp;
+  if (a.flags & DIFFATTN_NORM) {
+    v_pow = std::max(-32, std::min(32, v_exp));
+    if (v_pow != v_exp)
+      a.eps = static_cast<float>(std::min<double>(std::max<double>(std::ldexp(static_cast<double>(a.eps), 2 * (v_pow - v_exp)), FLT_MIN), FLT_MAX));
+  }
+  a.v_mul = std::ldexp(1.0f, v_pow);
+}
+
 int decode_kv4_impl(const char* fn, da::Kv4DecodeArgs& a, int cols, int width, int k_exp, int v_exp,
                     size_t ws_bytes, void* stream) {
   int rc = check_kv4(fn, a.H, width, width, a.num_pages, a.page_size, k_exp, v_exp);
@@ -2214,17 +2231,7 @@ int decode_kv4_impl(const char* fn, da::Kv4DecodeArgs& a, int cols, int width, i
     return fail(DIFFATTN_ERR_WORKSPACE, "%s: need a 256-byte aligned workspace of %zu bytes", fn, need);
   rc = check_device();
   if (rc) return rc;
-  a.qk_scale = static_cast<float>(std::ldexp(1.4426950408889634 / std::sqrt(128.0), k_exp));
-  // y 2^v_exp / sqrt(mean(y^2) 2^(2 v_exp) + eps) is the same with 2^c in place of 2^v_exp and eps
-  // 2^(2 (c - v_exp)) in place of eps. Where a norm follows, c stays where the squares of what a pool can
-  // give (values up to 2688, lambda up to 2^15) are finite in fp32 and small ones are not lost.
-  int v_pow = v_exp;
-  if (a.flags & DIFFATTN_NORM) {
-    v_pow = std::max(-32, std::min(32, v_exp));
-    if (v_pow != v_exp)
-      a.eps = static_cast<float>(std::min<double>(std::max<double>(std::ldexp(static_cast<double>(a.eps), 2 * (v_pow - v_exp)), FLT_MIN), FLT_MAX));
-  }
-  a.v_mul = std::ldexp(1.0f, v_pow);
+  kv4_scales(a, k_exp, v_exp);
   cudaError_t e = da::launch_kv4_decode(a, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, fn);
   return ok();
@@ -2544,6 +2551,123 @@ DIFFATTN_API int diffattn_rope_kv4_append(const void* q, const void* k, const vo
   cudaError_t e = da::launch_rope(a, 2, false, (flags & DIFFATTN_ROPE_INTERLEAVED) != 0, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, fn);
   return ok();
+}
+
+}  // extern "C"
+
+namespace {
+
+int chunk_kv4_impl(const char* fn, da::Kv4ChunkArgs& a, int width, int max_seqlen_q, int k_exp, int v_exp, void* workspace,
+                   size_t ws_bytes, void* stream) {
+  int rc = check_kv4(fn, a.H, width, width, a.num_pages, a.page_size, k_exp, v_exp);
+  if (!rc) rc = check_kv4_tables(fn, a.B, a.page_size, a.max_pages);
+  if (rc) return rc;
+  const long long heads = static_cast<long long>(a.H) * (a.group == 0 ? 1 : a.group);
+  if (a.total < 0 || a.total * heads > (1LL << 30) || max_seqlen_q < 0)
+    return fail(DIFFATTN_ERR_SHAPE, "%s: need total_q, max_seqlen_q >= 0 and total_q * heads <= 2^30", fn);
+  // (places in the walk over all units are counted in 64 bits, times the ranges)
+  if ((a.total + static_cast<long long>(a.B)) * a.H > (1LL << 46) / (static_cast<long long>(a.max_pages) * a.page_size))
+    return fail(DIFFATTN_ERR_SHAPE, "%s: need (total_q + B) * heads of the cache * max_pages * page_size <= 2^46", fn);
+  if (!aligned(a.q, 16) || !aligned(a.pool, 16) || !aligned(a.out, 16) || !aligned(a.block_table, 4) || !aligned(a.seqlens, 4) ||
+      !aligned(a.cu_seqlens, 4) || !aligned(a.lambda, 4) || !aligned(a.lam_logit, 4) || !aligned(a.norm_w, 16))
+    return fail(DIFFATTN_ERR_ALIGN, "%s: tensors must be 16-byte aligned", fn);
+  const size_t need = da::kv4_chunk_workspace_bytes(a.group, max_seqlen_q);
+  if (!workspace || ws_bytes < need || !aligned(workspace, 256))
+    return fail(DIFFATTN_ERR_WORKSPACE, "%s: need a 256-byte aligned workspace of %zu bytes", fn, need);
+  a.pieces = static_cast<float*>(workspace);
+  if ((rc = check_device())) return rc;
+  kv4_scales(a, k_exp, v_exp);
+  cudaError_t e = da::launch_kv4_chunk(a, da::kv4_chunk_cols(a.group, max_seqlen_q), static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, fn);
+  return ok();
+}
+
+}  // namespace
+
+extern "C" {
+
+DIFFATTN_API int diffattn_fwd_kv4_workspace_size(int max_seqlen_q, int d, int dv, size_t* bytes) {
+  const char* fn = "diffattn_fwd_kv4_workspace_size";
+  if (!bytes) return fail(DIFFATTN_ERR_ARG, "%s: null pointer", fn);
+  if (max_seqlen_q < 0 || d != 128 || dv != 256)
+    return fail(DIFFATTN_ERR_SHAPE, "%s: need max_seqlen_q >= 0, d = 128, dv = 256", fn);
+  *bytes = da::kv4_chunk_workspace_bytes(0, max_seqlen_q);
+  return ok();
+}
+
+DIFFATTN_API int diffattn_fwd_kv4(const void* q, const void* pool, const int* block_table, const int* cu_seqlens_q,
+                                  const int* seqlens, void* out, const float* lambda, float lambda_init,
+                                  const float* norm_weight, float eps, int max_seqlen_q, int total_q, int B, int H, int d,
+                                  int dv, int num_pages, int page_size, int max_pages, int k_exp, int v_exp, int flags,
+                                  void* workspace, size_t ws_bytes, void* stream) {
+  const char* fn = "diffattn_fwd_kv4";
+  if (!pool || !block_table || !cu_seqlens_q || !seqlens || !lambda || (total_q > 0 && (!q || !out)))
+    return fail(DIFFATTN_ERR_ARG, "%s: null pointer", fn);
+  if (flags & ~(DIFFATTN_CAUSAL | DIFFATTN_NORM | DIFFATTN_SCALE))
+    return fail(DIFFATTN_ERR_ARG, "%s: unknown flag bits 0x%x", fn, flags);
+  if ((flags & DIFFATTN_NORM) && !(eps > 0.f))
+    return fail(DIFFATTN_ERR_ARG, "%s: eps must be > 0 with DIFFATTN_NORM", fn);
+  if (d != 128 || dv != 256)
+    return fail(DIFFATTN_ERR_SHAPE, "%s: need d = 128 and dv = 256 (got d=%d dv=%d)", fn, d, dv);
+  da::Kv4ChunkArgs a{};
+  a.q = q;
+  a.pool = static_cast<const uint8_t*>(pool);
+  a.block_table = block_table;
+  a.cu_seqlens = cu_seqlens_q;
+  a.seqlens = seqlens;
+  a.out = out;
+  a.lambda = lambda;
+  a.norm_w = norm_weight;
+  a.eps = eps;
+  a.lambda_init = lambda_init;
+  a.flags = flags;
+  a.causal = (flags & DIFFATTN_CAUSAL) != 0;
+  a.total = total_q;
+  a.B = B;
+  a.H = H;
+  a.group = 0;
+  a.num_pages = num_pages;
+  a.page_size = page_size;
+  a.max_pages = max_pages;
+  return chunk_kv4_impl(fn, a, 256, max_seqlen_q, k_exp, v_exp, workspace, ws_bytes, stream);
+}
+
+DIFFATTN_API int diffattn_v2_fwd_kv4_workspace_size(int max_seqlen_q, int Hq, int Hkv, int d, size_t* bytes) {
+  const char* fn = "diffattn_v2_fwd_kv4_workspace_size";
+  if (!bytes) return fail(DIFFATTN_ERR_ARG, "%s: null pointer", fn);
+  if (max_seqlen_q < 0 || Hkv < 1 || d != 128 || !(Hq == 2LL * Hkv || Hq == 4LL * Hkv || Hq == 8LL * Hkv))
+    return fail(DIFFATTN_ERR_SHAPE, "%s: need max_seqlen_q >= 0, d = 128 and Hq / Hkv in {2, 4, 8}", fn);
+  *bytes = da::kv4_chunk_workspace_bytes(Hq / Hkv, max_seqlen_q);
+  return ok();
+}
+
+DIFFATTN_API int diffattn_v2_fwd_kv4(const void* q, const void* pool, const int* block_table, const int* cu_seqlens_q,
+                                     const int* seqlens, const float* lam_logit, void* out, int max_seqlen_q, int total_q,
+                                     int B, int Hq, int Hkv, int d, int num_pages, int page_size, int max_pages, int k_exp,
+                                     int v_exp, int flags, void* workspace, size_t ws_bytes, void* stream) {
+  const char* fn = "diffattn_v2_fwd_kv4";
+  if (!pool || !block_table || !cu_seqlens_q || !seqlens || (total_q > 0 && (!q || !out || !lam_logit)))
+    return fail(DIFFATTN_ERR_ARG, "%s: null pointer", fn);
+  if (flags & ~DIFFATTN_CAUSAL) return fail(DIFFATTN_ERR_ARG, "%s: unknown flag bits 0x%x", fn, flags);
+  if (Hkv < 1 || d != 128 || !(Hq == 2LL * Hkv || Hq == 4LL * Hkv || Hq == 8LL * Hkv))
+    return fail(DIFFATTN_ERR_SHAPE, "%s: need d = 128 and Hq / Hkv in {2, 4, 8} (got Hq=%d Hkv=%d d=%d)", fn, Hq, Hkv, d);
+  da::Kv4ChunkArgs a{};
+  a.q = q;
+  a.pool = static_cast<const uint8_t*>(pool);
+  a.block_table = block_table;
+  a.cu_seqlens = cu_seqlens_q;
+  a.seqlens = seqlens;
+  a.out = out;
+  a.lam_logit = lam_logit;
+  a.causal = (flags & DIFFATTN_CAUSAL) != 0;
+  a.total = total_q;
+  a.B = B;
+  a.H = Hkv;
+  a.group = Hq / Hkv;
+  a.num_pages = num_pages;
+  a.page_size = page_size;
+  a.max_pages = max_pages;
+  return chunk_kv4_impl(fn, a, 128, max_seqlen_q, k_exp, v_exp, workspace, ws_bytes, stream);
 }
 
 }  // extern "C"

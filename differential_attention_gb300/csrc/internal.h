@@ -342,6 +342,31 @@ size_t kv4_decode_workspace_bytes(int cols, int width);
 cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a, cudaStream_t s);
 cudaError_t status_decode_kv4(int* v);
 
+// Attention of chunks over the 4-bit cache (chunk_kv4.cu).
+struct Kv4ChunkArgs {
+  const void* q;           // V1 [total, H, 256], V2 [total, H group, 128]
+  const uint8_t* pool;
+  const int* block_table;
+  const int* cu_seqlens;   // [B + 1], of the queries
+  const int* seqlens;      // [B], cached keys
+  void* out;
+  const float* lambda;     // V1 [H]
+  const float* lam_logit;  // V2 [total, H group / 2]
+  const float* norm_w;
+  float eps, lambda_init;
+  int flags;
+  bool causal;
+  int total, B, H, group;  // KV heads; V2: query heads per KV head, V1: 0
+  int num_pages, page_size, max_pages;
+  float qk_scale, v_mul;   // as in Kv4DecodeArgs
+  float* pieces;           // the workspace
+  int tokens, grid;        // tokens of a unit, ranges: set by the launcher
+};
+int kv4_chunk_cols(int group, int max_seqlen_q);
+size_t kv4_chunk_workspace_bytes(int group, int max_seqlen_q);
+cudaError_t launch_kv4_chunk(const Kv4ChunkArgs& a, int cols, cudaStream_t s);
+cudaError_t status_chunk_kv4(int* v);
+
 // Rotary positions (rope.cu).
 struct RopeRows {  // [total, heads, width] by element strides
   void* data;

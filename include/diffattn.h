@@ -991,6 +991,50 @@ DIFFATTN_API int diffattn_v2_decode_kv4(const void* q, const void* pool, const i
                                         int max_pages, int k_exp, int v_exp, int flags,
                                         void* workspace, size_t ws_bytes, void* stream);
 
+/* Chunks over a 4-bit cache: each sequence's new tokens, already appended, over all its cached keys
+ * (prompts in chunks, drafted tokens checked at once): diffattn_fwd_paged (V1) and
+ * diffattn_v2_fwd_paged (V2) with the keys and values in a pool as above, and any page size that is a
+ * multiple of 16. Sequence b's Lq = cu_seqlens_q[b + 1] - cu_seqlens_q[b] queries are the last of its
+ * seqlens[b] positions: with DIFFATTN_CAUSAL query i sees keys 0 .. seqlens[b] - Lq + i, without it all.
+ * Numerics as in the decodes over the same pool: cached values enter exactly, the query in fp16 after a
+ * power of two of its own for each head (V1: half), a probability rounded to fp16, sums and statistics
+ * in fp32.
+ *   q, out : device bf16 [total_q, H, 2d] and [total_q, H, dv] (V1), [total_q, Hq, d] and
+ *          [total_q, Hq / 2, d] (V2), packed by cu_seqlens_q. Rows of `out` behind the last sequence (and
+ *          of a sequence outside [0, total_q], which diffattn_device_status() reports as
+ *          DIFFATTN_ERR_INDEX) are not written
+ *   cu_seqlens_q : device int32 [B + 1];  seqlens : device int32 [B], clamped into [0, max_pages *
+ *          page_size]. Queries that see no key (seqlens[b] of 0, or with DIFFATTN_CAUSAL the first
+ *          Lq - seqlens[b]) give zeros. Slots past a sequence's keys never reach the result, and a key
+ *          that is masked for a query never reaches that query's, whatever they hold
+ *   lam_logit : device fp32 [total_q, Hq / 2]; lambda, lambda_init, norm_weight, eps, block_table : as for
+ *          the decodes
+ *   max_seqlen_q : the longest Lq, or any number near it: a hint by which the kernel is chosen (up to 8
+ *          tokens at Hq / Hkv = 8, 32 with V1, take one for few tokens), right or wrong the results
+ *          are right
+ *   workspace, ws_bytes : at least the *_workspace_size bytes of the same max_seqlen_q, 256-byte aligned;
+ *          as for the decodes
+ * A used table entry outside [0, num_pages) reads page 0 and is reported as DIFFATTN_ERR_INDEX. Equal
+ * inputs give equal bits.
+ * Supported: as the decodes; total_q * query heads <= 2^30, (total_q + B) * heads of the cache *
+ * max_pages * page_size <= 2^46.
+ * Errors: ERR_ARG, ERR_SHAPE, ERR_ALIGN, ERR_WORKSPACE, ERR_UNSUPPORTED, ERR_CUDA. */
+DIFFATTN_API int diffattn_fwd_kv4_workspace_size(int max_seqlen_q, int d, int dv, size_t* bytes);
+DIFFATTN_API int diffattn_fwd_kv4(const void* q, const void* pool, const int* block_table,
+                                  const int* cu_seqlens_q, const int* seqlens, void* out,
+                                  const float* lambda, float lambda_init, const float* norm_weight,
+                                  float eps, int max_seqlen_q, int total_q, int B, int H, int d, int dv,
+                                  int num_pages, int page_size, int max_pages, int k_exp, int v_exp,
+                                  int flags, void* workspace, size_t ws_bytes, void* stream);
+DIFFATTN_API int diffattn_v2_fwd_kv4_workspace_size(int max_seqlen_q, int Hq, int Hkv, int d,
+                                                    size_t* bytes);
+DIFFATTN_API int diffattn_v2_fwd_kv4(const void* q, const void* pool, const int* block_table,
+                                     const int* cu_seqlens_q, const int* seqlens,
+                                     const float* lam_logit, void* out, int max_seqlen_q, int total_q,
+                                     int B, int Hq, int Hkv, int d, int num_pages, int page_size,
+                                     int max_pages, int k_exp, int v_exp, int flags, void* workspace,
+                                     size_t ws_bytes, void* stream);
+
 /* ------------------------------------------------------------------------------------------
  * Rotary positions (the pages do not say how positions enter; this is the usual rotation of queries
  * and keys before the operators above). A row of a head is made of parts of d channels, each turned
@@ -1019,8 +1063,8 @@ DIFFATTN_API int diffattn_v2_decode_kv4(const void* q, const void* pool, const i
  * 1 <= n_axes <= 4, total * heads <= 2^30. One launch.
  * Errors: ERR_ARG, ERR_SHAPE, ERR_DTYPE, ERR_ALIGN, ERR_UNSUPPORTED, ERR_CUDA.
  * ------------------------------------------------------------------------------------------ */
-#define DIFFATTN_ROPE_INTERLEAVED 1 /* pairs of neighbouring channels */
-#define DIFFATTN_ROPE_INVERSE 2     /* turn back (diffattn_rope only) */
+#define DIFFATTN_ROPE_INTERLEAVED 64 /* pairs of neighbouring channels */
+#define DIFFATTN_ROPE_INVERSE 128    /* turn back (diffattn_rope only) */
 
 /* table[p][i] = (cos, sin)(p * inv_freq[i]) for p < top: angles in fp64, so that far positions lose
  * nothing, each value rounded to fp32 once (to within fp64's own error in cos and sin).

@@ -9,7 +9,7 @@ import differential_attention_gb300 as da
 from oracle import rope_ref as rope
 
 RNG = np.random.default_rng(7)
-INTERLEAVED, INVERSE = 1, 2
+INTERLEAVED, INVERSE = 64, 128
 
 
 @pytest.mark.parametrize("interleaved", [False, True])
@@ -119,7 +119,7 @@ def test_rope_refuses(change, want):
 
 @pytest.mark.parametrize("kv4", [False, True])
 @pytest.mark.parametrize("change,want", COMMON + [
-    (dict(v=None), ARG), (dict(kp=None), ARG), (dict(slots=None), ARG), (dict(flags=2), ARG), (dict(H=0), SHAPE), (dict(vw=192), SHAPE),
+    (dict(v=None), ARG), (dict(kp=None), ARG), (dict(slots=None), ARG), (dict(flags=128), ARG), (dict(H=0), SHAPE), (dict(vw=192), SHAPE),
     (dict(vw=0), SHAPE), (dict(pages=0), SHAPE), (dict(page=0), SHAPE), (dict(pages=1 << 27, page=16), SHAPE), (dict(kp=1032), ALIGN),
     (dict(slots=6), ALIGN), (dict(v=264), ALIGN)])
 def test_appends_refuse(kv4, change, want):
