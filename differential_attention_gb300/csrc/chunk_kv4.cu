@@ -12,7 +12,7 @@
 // o1/l1 - lambda o2/l2, the norm and the scale, V2: o_2p/l_2p - sigmoid(lam) o_2p+1/l_2p+1.
 //
 // Warps. 8 for the softmax: warpgroup w has half of the columns (w R/2 ..), thread `key` one key of the
-// tile, so its P go to shared memory as whole pieces of 16 bytes, over the K plane that S came from. 4
+// tile, so its P go to shared memory as whole pieces of 16 bytes, over the K plane that S came from. 8
 // unpack: they read records into registers, four planes ahead, and write K and V as fp16 (exact: an e2m1
 // times an e4m3 has 6 significant bits) in the products' 128-byte swizzle. One issues the products: S of
 // the next tile before P V of this one.
@@ -38,19 +38,17 @@ namespace da {
 namespace {
 
 constexpr int kSms = 152;
-constexpr int kSoftmaxWarps = 8, kUnpackWarps = 4, kMmaWarp = kSoftmaxWarps + kUnpackWarps;
-constexpr int kThreads = (kMmaWarp + 4) * 32;
-// Registers a thread: the launch's 128, dealt out anew to the warpgroups (2 x 160 + 120 + 72 of 4 x 128).
-constexpr int kSoftmaxRegs = 160, kUnpackRegs = 120, kMmaRegs = 72;
-static_assert(2 * kSoftmaxRegs + kUnpackRegs + kMmaRegs <= 4 * 128, "more registers than the launch has");
+// warps: softmax 0 .. 7, K 8 .. 11, V 12 .. 15, products 16, addresses 17
+constexpr int kKWarp = 8, kVWarp = 12, kMmaWarp = 16, kAddressWarp = 17;
+constexpr int kSoftmaxWarps = 8, kThreads = 20 * 32;
 constexpr int kTile = 128;                       // keys
 constexpr int kSlot = kTile * 128 * 2;           // one plane of a tile in fp16
-constexpr int kSlots = 6;
 constexpr int kHalf = kSlot / 2;                 // 64 of its channels (or columns of P)
 constexpr int kUnitCost = 3;                     // what a unit costs besides its tiles, in tiles
 constexpr int kMinCost = 2;                      // the smallest range
-constexpr float kPScale = 10.f, kMoveRef = 14.f;
+constexpr float kPScale = 6.f, kMoveRef = 15.f;  // log2 of P's scale, and of the P at which the reference moves
 constexpr int kNanSets = 4;
+constexpr int kRing = 4;                         // tiles whose records' addresses are known
 
 template <int KP, int R>
 struct Cfg {
@@ -58,17 +56,33 @@ struct Cfg {
   static constexpr int kQRows = KP == 1 ? R : R / 2;  // rows of one product's Q
   static constexpr int kQBytes = R * 256;
   static constexpr int kWidth = KP * 128;
-  static constexpr int kO = 2 * R;                    // tensor memory: S twice, then O's planes
+  static constexpr int kVSlots = KP == 1 ? 3 : 4;     // V: stages of a plane (V2), of two planes (V1)
+  static constexpr int kP = kVSlots * kSlot;          // shared memory: V, P twice, Q
+  static constexpr int kQ = kP + 2 * R * 256;
+  static constexpr int kSmall = kQ + kQBytes;
+  static constexpr int kO = 2 * R;                    // tensor memory: S twice, O's planes, K twice
+  static constexpr int kK = kO + KP * R;
   static constexpr int kPiece = 2 * R + R * kWidth;   // floats: m, l, o
-  static_assert(2 * R + KP * R <= 512, "tensor memory");
+  // Registers a thread: the launch's 96, dealt out anew to the warpgroups (2 of softmax, K, V, the rest).
+  static constexpr int kSoftmaxRegs = R == 64 ? 128 : 152, kUnpackRegs = R == 64 ? 96 : 72, kRestRegs = 32;
+  static_assert(2 * kSoftmaxRegs + 2 * kUnpackRegs + kRestRegs <= 5 * 96, "more registers than the launch has");
+  static_assert(kK + 2 * KP * 64 <= 512, "tensor memory");
 };
 
-struct Small {  // behind the slots and Q
-  float4 cm[64];       // columns 2i and 2i + 1: scales, and the references (less kPScale) negated
+struct TileAt {
+  const uint8_t* rec[8];
+  int key0, left, unit, pad;  // its first key, keys from there on (0: the stream has ended), its unit's number
+};
+struct Small {  // behind Q
+  float ref[128];      // the columns' references (less kPScale), negated
+  float fac[128];      // where the columns' queries have powers of two of their own: what S is to be multiplied with
   int lim[128];        // keys that a column sees; 0 where there is no such token
   int top[128];        // a move: the columns' largest exponents (ordered), then the factors
-  uint64_t full[kSlots], free[kSlots], s_full[2], p_full[2], pv_done[2], q_full, teardown;
+  uint64_t v_full[4], v_free[4], k_full[2], k_free[2], s_full[2], p_full[2], pv_done[2], q_full, teardown;
+  uint64_t tile_full[kRing], tile_free[kRing];
+  TileAt tile[kRing];
   int nan_key[kNanSets][16];
+  int exp_max, exp_min;  // exponents of the unit's queries
   uint32_t tmem;
   int abort, seg;      // seg: tiles of the unit whose Q is there, 0 behind the last
 };
@@ -86,11 +100,11 @@ struct Scan {
 };
 static_assert(sizeof(Scan) <= 64 * 256, "fits in the smaller Q");
 
-template <int R>
+template <int KP, int R>
 constexpr int smem_bytes() {
-  return kSlots * kSlot + R * 256 + static_cast<int>(sizeof(Small));
+  return Cfg<KP, R>::kSmall + static_cast<int>(sizeof(Small));
 }
-static_assert(smem_bytes<128>() <= 232448, "shared memory");
+static_assert(smem_bytes<1, 128>() <= 232448 && smem_bytes<2, 64>() <= 232448, "shared memory");
 
 // ---- the batch's units -------------------------------------------------------------------------
 struct Seq {
@@ -257,16 +271,27 @@ __device__ __forceinline__ void registers_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// one lane of a converged warp; the compiler knows that it is one, and keeps what it computes in uniform
+// registers, which the products' descriptors have to be in
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // ---- small parts -------------------------------------------------------------------------------
 __device__ __forceinline__ uint4 ldg128(const uint8_t* p) {
   uint4 v;
   asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
   return v;
 }
-__device__ __forceinline__ float4 lds_f4(uint32_t at) {
-  float4 v;
-  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at));
+__device__ __forceinline__ uint32_t ldg32(const uint8_t* p) {
+  uint32_t v;
+  asm volatile("ld.global.L1::no_allocate.u32 %0, [%1];" : "=r"(v) : "l"(p));
   return v;
+}
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 // whether any of `count` threads of the block's barrier `id` has p
 __device__ __forceinline__ bool barrier_any(uint32_t id, uint32_t count, bool p) {
@@ -290,49 +315,46 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int a_mn, int b_m
   return umma_idesc_bf16(M, N, a_mn, b_mn) & ~((1u << 7) | (1u << 10));
 }
 
-// where a tile's planes lie, and the phase of their slot's use; j counts the block's tiles. V2: three stages
-// of two slots. V1: two stages of three; P takes K1's slot and V2 takes K2's, so that of a stage's slots
-// 0 and 1 the one that held K1 and P goes to V1 the next time.
-template <int KP>
+// where V's plane `half` of the block's tile j lies, and the phase of its slot's use
 struct Place {
   int slot, phase;
 };
 template <int KP>
-__device__ __forceinline__ Place<KP> place_k(int j, int map) {
-  if constexpr (KP == 1) return {2 * (j % 3), (j / 3) & 1};
-  if (map == 0) return {3 * (j & 1) + ((j >> 1) & 1), (j >> 1) & 1};
-  return {3 * (j & 1) + 2, 0};
-}
-template <int KP>
-__device__ __forceinline__ Place<KP> place_v(int j, int half) {
-  if constexpr (KP == 1) return {2 * (j % 3) + 1, (j / 3) & 1};
-  if (half == 0) return {3 * (j & 1) + 1 - ((j >> 1) & 1), (j >> 1) & 1};
-  return {3 * (j & 1) + 2, 1};
+__device__ __forceinline__ Place place_v(int j, int half) {
+  if constexpr (KP == 1) return {j % 3, (j / 3) & 1};
+  return {2 * (j & 1) + half, (j >> 1) & 1};
 }
 
 template <int KP, int R>
 __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const Kv4ChunkArgs a) {
   using C = Cfg<KP, R>;
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t* const s_q = smem + kSlots * kSlot;
-  Small& sm = *reinterpret_cast<Small*>(s_q + C::kQBytes);
+  uint8_t* const s_q = smem + C::kQ;
+  Small& sm = *reinterpret_cast<Small*>(smem + C::kSmall);
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-  const uint32_t slots = smem_u32(smem), q_at = smem_u32(s_q);
+  const uint32_t slots = smem_u32(smem), p_slots = slots + C::kP, q_at = smem_u32(s_q);
   auto bar = [](uint64_t& x) { return smem_u32(&x); };
 
   if (tid == 0) {
-    for (int i = 0; i < kSlots; ++i) {
-      mbar_init(bar(sm.full[i]), kUnpackWarps);
-      mbar_init(bar(sm.free[i]), 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(bar(sm.v_full[i]), 4);
+      mbar_init(bar(sm.v_free[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(sm.k_full[i]), 4);
+      mbar_init(bar(sm.k_free[i]), 1);
       mbar_init(bar(sm.s_full[i]), 1);
       mbar_init(bar(sm.p_full[i]), kSoftmaxWarps);
       mbar_init(bar(sm.pv_done[i]), 1);
     }
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(bar(sm.tile_full[i]), 1);
+      mbar_init(bar(sm.tile_free[i]), 8);
+    }
     mbar_init(bar(sm.q_full), kSoftmaxWarps);
     mbar_init(bar(sm.teardown), 1);
     sm.abort = 0;
+    sm.exp_max = INT_MIN, sm.exp_min = INT_MAX;
     fence_barrier_init();
     fence_proxy_async_smem();
   }
@@ -369,27 +391,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const Kv4ChunkAr
   volatile int* abrt = &sm.abort;
 
   if (warp >= kMmaWarp) {
-    // ================================ products ================================
-    registers_down<kMmaRegs>();
-    if (warp == kMmaWarp && lane == 0) {
+    registers_down<C::kRestRegs>();
+    if (warp == kMmaWarp && elect_one()) {
+      // ================================ products ================================
       constexpr uint32_t idesc_s = idesc_f16(kTile, C::kQRows, 0, 0), idesc_o = idesc_f16(128, R, 1, 1);
-      const uint64_t dk = umma_smem_desc(slots, 16, 1024), dq = umma_smem_desc(q_at, 16, 1024);
-      const uint64_t dmn = umma_smem_desc(slots, kHalf, 1024);  // V and P: 64 channels or columns a half
+      const uint64_t dq = umma_smem_desc(q_at, 16, 1024);
+      const uint64_t dv = umma_smem_desc(slots, kHalf, 1024), dp = umma_smem_desc(p_slots, kHalf, 1024);
       int j = 0;
       bool ok = true;
       auto scores = [&](int t) {
-#pragma unroll
-        for (int map = 0; map < KP; ++map) {
-          const Place<KP> k = place_k<KP>(t, map);
-          if (!(ok = ok && mbar_wait(bar(sm.full[k.slot]), k.phase, abrt))) return;
-          tc_fence_after();
-#pragma unroll
+        if (!(ok = mbar_wait(bar(sm.k_full[t & 1]), (t >> 1) & 1, abrt))) return;
+        tc_fence_after();
+#pragma unroll 1
+        for (int map = 0; map < KP; ++map)
+#pragma unroll 2
           for (int kk = 0; kk < 8; ++kk)
-            mma_bf16_ss(tmem + (t & 1) * R + map * C::kQRows, desc_add(dk, k.slot * kSlot + (kk >> 2) * kHalf + (kk & 3) * 32),
+            mma_bf16_ts(tmem + (t & 1) * R + map * C::kQRows, tmem + C::kK + ((t & 1) * KP + map) * 64 + kk * 8,
                         desc_add(dq, map * C::kQRows * 256 + (kk >> 2) * C::kQRows * 128 + (kk & 3) * 32), idesc_s, kk > 0);
-          if (map == 1) tc_commit(bar(sm.free[k.slot]));  // V1: K2's slot goes to V2
-        }
         tc_commit(bar(sm.s_full[t & 1]));
+        tc_commit(bar(sm.k_free[t & 1]));
       };
       for (int unit = 0; ok; ++unit) {
         if (!(ok = mbar_wait(bar(sm.q_full), unit & 1, abrt))) break;
@@ -400,185 +420,266 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const Kv4ChunkAr
         for (int i = 0; ok && i < seg; ++i, ++j) {
           if (i + 1 < seg) scores(j + 1);
           if (!ok) break;
-          const Place<KP> p = place_k<KP>(j, 0);
           if (!(ok = mbar_wait(bar(sm.p_full[j & 1]), (j >> 1) & 1, abrt))) break;
-#pragma unroll
+#pragma unroll 1
           for (int half = 0; half < KP; ++half) {
-            const Place<KP> v = place_v<KP>(j, half);
-            if (!(ok = ok && mbar_wait(bar(sm.full[v.slot]), v.phase, abrt))) break;
+            const Place v = place_v<KP>(j, half);
+            if (!(ok = ok && mbar_wait(bar(sm.v_full[v.slot]), v.phase, abrt))) break;
             tc_fence_after();
-#pragma unroll
+#pragma unroll 2
             for (int kk = 0; kk < 8; ++kk)
-              mma_bf16_ss(tmem + C::kO + half * R, desc_add(dmn, v.slot * kSlot + kk * 2048),
-                          desc_add(dmn, p.slot * kSlot + kk * 2048), idesc_o, i > 0 || kk > 0);
-            tc_commit(bar(sm.free[v.slot]));
+              mma_bf16_ss(tmem + C::kO + half * R, desc_add(dv, v.slot * kSlot + kk * 2048),
+                          desc_add(dp, (j & 1) * R * 256 + kk * 2048), idesc_o, i > 0 || kk > 0);
+            tc_commit(bar(sm.v_free[v.slot]));
           }
           if (!ok) break;
-          tc_commit(bar(sm.free[p.slot]));
           tc_commit(bar(sm.pv_done[j & 1]));
         }
       }
       // every product that was issued ends before tensor memory is given back
       tc_commit(bar(sm.teardown));
       mbar_wait(bar(sm.teardown), 0, nullptr);
-    }
-  } else if (warp >= kSoftmaxWarps) {
-    // ================================ unpack ================================
-    registers_down<kUnpackRegs>();
-    // Warp u takes records u and u + 4 of each plane of a tile; a step is a plane.
-    constexpr int kSteps = 4, kPerTile = 2 * KP;
-    const int u = warp - kSoftmaxWarps;
-    struct Step {
-      uint4 lo[2], hi[2];
-      uint32_t sc[2];
-      int key0, left, unit;  // of the tile: its first key, keys from there on (0 or less: the stream has ended)
-    };
-    Step st[kSteps];
-    const int recs = a.page_size >> 4;
-    const size_t rec_bytes = static_cast<size_t>(2 * KP) * kKv4Plane;
-    int unit = 0, page[2];
-    const uint8_t* src[2];
-    // the pages of this warp's records of the tile at w
-    auto look_up = [&]() {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int key = w.tile * kTile + (u + 4 * i) * 16;
-        page[i] = w.todo > 0 && key < w.Lk && dbg_index_ok(key / a.page_size, a.max_pages)
-                      ? *(a.block_table + static_cast<size_t>(w.b) * a.max_pages + key / a.page_size) : 0;
-      }
-    };
-    auto issue = [&](Step& s, int plane) {
-      if (plane == 0) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int rec = w.tile * 8 + u + 4 * i;
-          if (page[i] < 0 || page[i] >= a.num_pages) {
-            if (lane == 0) flag_device_error(DEV_BAD_INDEX);
-            page[i] = 0;
+    } else if (warp == kAddressWarp) {
+      // ================================ addresses ================================
+      // Lane 8 i + r looks up record r of tile i of a batch: up to four tiles of a unit. The next batch's pages
+      // are looked up before this one is passed on, tile by tile, as the ring has room.
+      const int recs = a.page_size >> 4, i4 = lane >> 3, r8 = lane & 7;
+      struct Batch {
+        int n, h, page, off, key0, left, unit;  // tiles; this lane's page and record of the page; the first tile's
+        bool used;
+      };
+      auto look_up = [&](int unit) {
+        Batch x;
+        x.n = static_cast<int>(min(min(4LL, static_cast<long long>(w.tiles - w.tile)), max(w.todo, 0LL)));
+        const int rec = min((w.tile + i4) * 8 + r8, max(0, (w.Lk - 1) >> 4)), pi = (__umulhi(rec, a.rec_magic) + rec) >> a.rec_shift;
+        x.used = i4 < x.n && ((w.tile + i4) * 8 + r8) * 16 < w.Lk && dbg_index_ok(pi, a.max_pages);
+        x.page = x.used ? *(a.block_table + static_cast<size_t>(w.b) * a.max_pages + pi) : 0;
+        x.off = rec - pi * recs;
+        x.h = w.h, x.key0 = w.tile * kTile, x.left = w.Lk - x.key0, x.unit = unit;
+        return x;
+      };
+      int t = 0, unit = 0;
+      bool ok = true;
+      Batch next = look_up(0);
+      while (ok) {
+        Batch x = next;
+        if (x.n > 0) {
+          if (w.tile + x.n == w.tiles) ++unit;
+          advance(a, w, x.n);
+          next = look_up(unit);
+        }
+        if (x.used && (x.page < 0 || x.page >= a.num_pages)) {
+          flag_device_error(DEV_BAD_INDEX);
+          x.page = 0;
+        }
+        const uint8_t* src = a.pool + ((static_cast<size_t>(x.page) * a.H + x.h) * recs + x.off) * (2 * KP * kKv4Plane);
+        for (int i = 0; ok && i < max(x.n, 1); ++i, ++t) {
+          ok = __all_sync(0xffffffffu, mbar_wait(bar(sm.tile_free[t % kRing]), ((t / kRing) & 1) ^ 1, abrt));
+          TileAt& at = sm.tile[t % kRing];
+          if (i4 == i) {
+            at.rec[r8] = src;
+            if (x.used) prefetch_l2(src, 2 * KP * kKv4Plane);
           }
-          src[i] = a.pool + ((static_cast<size_t>(page[i]) * a.H + w.h) * recs + rec % recs) * rec_bytes + lane * 16;
+          if (lane == 0) at.key0 = x.key0 + i * kTile, at.left = x.n > 0 ? x.left - i * kTile : 0, at.unit = x.unit;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(sm.tile_full[t % kRing]));
         }
+        if (x.n == 0) break;
       }
-      s.key0 = w.tile * kTile;
-      s.left = w.todo > 0 ? w.Lk - s.key0 : 0;
-      s.unit = unit;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (s.left > (u + 4 * i) * 16) {
-          const uint8_t* p = src[i] + plane * kKv4Plane;
-          s.lo[i] = ldg128(p);
-          s.hi[i] = ldg128(p + 512);
-          s.sc[i] = *reinterpret_cast<const uint32_t*>(p - lane * 12 + kKv4PlaneCodes);
-        } else {
-          s.lo[i] = s.hi[i] = make_uint4(0, 0, 0, 0);
-          s.sc[i] = 0;
-        }
-      }
-      if (plane == kPerTile - 1 && w.todo > 0) {
-        if (w.tile + 1 == w.tiles) ++unit;
-        advance(a, w, 1);
-        look_up();
-      }
+    }
+  } else if (warp >= kKWarp) {
+    // ================================ unpack ================================
+    // Both kinds of warps load a tile's bytes into registers one or two tiles before they unpack them (also
+    // where the sequence has no such record, from page 0: no branch comes between loads in flight).
+    registers_down<C::kUnpackRegs>();
+    const int q4 = warp & 3;
+    int next = 0, end = INT_MAX;  // the next tile to load; behind the stream's last its end stays, and is read again
+    bool ok = true;
+    struct Tile {
+      int key0, left, unit;
+    };
+    auto tile_at = [&](Tile& t) -> const TileAt& {
+      const int i = min(next, end);
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(sm.tile_full[i % kRing]), (i / kRing) & 1, abrt));
+      const TileAt& at = sm.tile[i % kRing];
+      t.key0 = at.key0, t.left = ok ? at.left : 0, t.unit = at.unit;
+      if (t.left <= 0) end = i;
+      ++next;
+      return at;
+    };
+    auto tile_read = [&](const Tile& t) {  // (its addresses are in registers)
+      __syncwarp();
+      if (lane == 0 && t.left > 0) mbar_arrive(bar(sm.tile_free[(next - 1) % kRing]));
     };
     auto dup = [](uint32_t two, int high) { return __byte_perm(two, 0, high ? 0x3232 : 0x1010); };
-    auto put = [](uint32_t at, uint32_t word, uint32_t scale) {
-      uint32_t v[4];
-      e2m1x8_to_half2(word, v);
-      st_shared_v4(at, half2_mul(v[0], scale), half2_mul(v[1], scale), half2_mul(v[2], scale), half2_mul(v[3], scale));
-    };
-    auto unpack_k = [&](const Step& s, uint32_t slot) {
-      const int ka = lane >> 3, r = (lane >> 2) & 1, t = lane & 3;
-      const bool far = t & 2;  // its channels lie in the upper half: the pieces in another order, for the banks
+    if (warp < kVWarp) {
+      // K: lane `key` takes a key of the tile, tensor memory's lane of that number: its 64 bytes of codes are
+      // on end, its scales two bytes of each word of 16.
+      constexpr int kAhead = 1;
+      struct Data {
+        uint4 w[4], sc;
+      };
+      Data d[kAhead][KP];
+      Tile tl[kAhead], tile;
+      const int key = lane & 15, h = (key >> 1) & 1, row = 32 * q4 + lane;
+      const int code = kv4_k_code(key, 0), scale = kKv4PlaneCodes + (key >> 2) * 32 + (key & 1) * 16;
+      const uint32_t to = tmem + (static_cast<uint32_t>(q4 * 32) << 16) + C::kK;
+      const uint8_t* src = nullptr;
+      auto load = [&](Data& x, int plane) {
+        const uint8_t* p = src + plane * kKv4Plane;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        uint32_t s0, s1;
-        e4m3x4_to_half2(s.sc[i], s0, s1);
+        for (int i = 0; i < 4; ++i) x.w[i] = ldg128(p + code + 16 * i);
+        x.sc = ldg128(p + scale);
+      };
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint4 w4 = h ? s.hi[i] : s.lo[i];
-          const int in_rec = 4 * ka + 2 * h + r, row = (u + 4 * i) * 16 + in_rec;
-          const bool live = row < s.left;
-          const uint32_t sc = live ? (h ? s1 : s0) : 0u;
-          const uint32_t a0 = dup(sc, far), a1 = dup(sc, !far);
-          const uint32_t x0 = far ? w4.z : w4.x, x1 = far ? w4.w : w4.y, x2 = far ? w4.x : w4.z, x3 = far ? w4.y : w4.w;
-          const uint32_t base = slot + (t >> 1) * kHalf + row * 128;
-          const int c = ((t & 1) * 4 + (t & 2)) ^ (row & 7);
-          put(base + (c << 4), x0, a0);
-          put(base + ((c ^ 1) << 4), x1, a0);
-          put(base + ((c ^ 2) << 4), x2, a1);
-          put(base + ((c ^ 3) << 4), x3, a1);
-        }
+      for (int i = 0; i < kAhead; ++i) {
+        src = tile_at(tl[i]).rec[2 * q4 + (lane >> 4)];
+        tile_read(tl[i]);
+#pragma unroll
+        for (int p = 0; p < KP; ++p) load(d[i][p], p);
       }
-    };
-    auto unpack_v = [&](const Step& s, uint32_t slot, int half) {
-      const int g = lane >> 2, t = lane & 3;
-      const bool far = t & 2;
+      for (int j = 0; ok; j += kAhead) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int row0 = (u + 4 * i) * 16 + 4 * t;  // this lane's four tokens
-        uint32_t sc = s.sc[i];
-        const int live = s.left - row0;
-        if (live < 4) sc = live <= 0 ? 0u : sc & (0xffffffffu >> (32 - 8 * live));
-        const uint32_t odd = (((sc & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u);  // scales that are NaN
-        if (odd) {
-          atomicMin(&sm.nan_key[s.unit & (kNanSets - 1)][half * 8 + g], s.key0 + row0 + ((__ffs(odd) - 1) >> 3));
-          sc &= ~((odd >> 7) * 0xffu);
-        }
-        uint32_t s01, s23;
-        e4m3x4_to_half2(sc, s01, s23);
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          const uint4 w4 = p ? s.hi[i] : s.lo[i];
-          const uint32_t s2 = p ? s23 : s01;
-#pragma unroll
-          for (int jj = 0; jj < 2; ++jj) {
-            const int row = row0 + 2 * p + jj;
-            const uint32_t x0 = jj ? w4.z : w4.x, x1 = jj ? w4.w : w4.y, f = dup(s2, jj);
-            const uint32_t base = slot + (g >> 2) * kHalf + row * 128;
-            const int c = (((g & 3) * 2) ^ (row & 7)) ^ (far ? 1 : 0);
-            put(base + (c << 4), far ? x1 : x0, f);
-            put(base + ((c ^ 1) << 4), far ? x0 : x1, f);
+        for (int i = 0; i < kAhead; ++i) {
+          tile = tl[i];
+          if (tile.left <= 0) {
+            ok = false;
+            break;
           }
+          const int t = j + i;
+          ok = __all_sync(0xffffffffu, mbar_wait(bar(sm.k_free[t & 1]), ((t >> 1) & 1) ^ 1, abrt));
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int p = 0; p < KP; ++p) {
+            const uint32_t sc4[4] = {d[i][p].sc.x, d[i][p].sc.y, d[i][p].sc.z, d[i][p].sc.w};
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              uint32_t v[32];
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const uint4 w4 = d[i][p].w[2 * half + x];
+                const uint32_t word[4] = {w4.x, w4.y, w4.z, w4.w};
+                const uint32_t two = row < tile.left ? e4m3x2_to_half2(sc4[2 * half + x] >> (16 * h)) : 0u;
+                const uint32_t f0 = dup(two, 0), f1 = dup(two, 1);
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                  uint32_t o[4];
+                  e2m1x8_to_half2(word[y], o);
+#pragma unroll
+                  for (int z = 0; z < 4; ++z) v[x * 16 + y * 4 + z] = half2_mul(o[z], y < 2 ? f0 : f1);
+                }
+              }
+              tmem_st32(to + ((t & 1) * KP + p) * 64 + half * 32, v);
+            }
+            if (p == 0) {
+              src = tile_at(tl[i]).rec[2 * q4 + (lane >> 4)];
+              tile_read(tl[i]);
+            }
+            load(d[i][p], p);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(sm.k_full[t & 1]));
         }
       }
-    };
-    int j = 0;
-    bool ok = true;
-    look_up();
+    } else {
+      // V: warp v takes records v and v + 4, to shared memory. A piece of 8 channels lies at its number XOR the
+      // row's; lanes of a quarter-warp whose places would meet in the banks (t4 of 0 and 2, 1 and 3) take
+      // their pieces in another order.
+      constexpr int kAhead = 1;
+      struct Data {
+        uint4 lo[2], hi[2];
+        uint32_t sc[2];
+      };
+      Data d[kAhead][KP];
+      Tile tl[kAhead], tile;
+      const int t4 = lane & 3, g8 = lane >> 2;  // tokens 4 t4 .., channels 16 g8 ..
+      const bool far = t4 & 2;
+      const uint32_t at0 = slots + (g8 >> 2) * kHalf + (q4 * 16 + 4 * t4) * 128;
+      const int c0 = ((g8 & 3) * 2) ^ (4 * (t4 & 1)) ^ (far ? 1 : 0);
+      const uint8_t* src[2] = {nullptr, nullptr};
+      auto load = [&](Data& x, int half) {
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) issue(st[s], s % kPerTile);
-    while (ok) {
+        for (int i = 0; i < 2; ++i) {
+          const uint8_t* p = src[i] + (KP + half) * kKv4Plane;
+          x.lo[i] = ldg128(p + lane * 16);
+          x.hi[i] = ldg128(p + lane * 16 + 512);
+          x.sc[i] = ldg32(p + lane * 4 + kKv4PlaneCodes);
+        }
+      };
+      auto fetch = [&](Tile& t) {
+        const TileAt& at = tile_at(t);
+        src[0] = at.rec[q4], src[1] = at.rec[q4 + 4];
+        tile_read(t);
+      };
+      auto put = [](uint32_t at, uint32_t word, uint32_t f) {
+        uint32_t v[4];
+        e2m1x8_to_half2(word, v);
+        st_shared_v4(at, half2_mul(v[0], f), half2_mul(v[1], f), half2_mul(v[2], f), half2_mul(v[3], f));
+      };
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        constexpr int kTilesHere = kSteps / kPerTile;
-        const int plane = s % kPerTile, t = j + s / kPerTile;
-        static_assert(kTilesHere * kPerTile == kSteps, "whole tiles");
-        if (st[s].left <= 0) {
-          ok = false;
-          break;
-        }
-        const Place<KP> d = plane < KP ? place_k<KP>(t, plane) : place_v<KP>(t, plane - KP);
-        if (!__all_sync(0xffffffffu, mbar_wait(bar(sm.free[d.slot]), d.phase ^ 1, abrt))) {
-          ok = false;
-          break;
-        }
-        if (plane < KP) unpack_k(st[s], slots + d.slot * kSlot);
-        else unpack_v(st[s], slots + d.slot * kSlot, plane - KP);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(sm.full[d.slot]));
-        issue(st[s], plane);
+      for (int i = 0; i < kAhead; ++i) {
+        fetch(tl[i]);
+#pragma unroll
+        for (int p = 0; p < KP; ++p) load(d[i][p], p);
       }
-      j += kSteps / kPerTile;
+      for (int j = 0; ok; j += kAhead) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          tile = tl[i];
+          if (tile.left <= 0) {
+            ok = false;
+            break;
+          }
+#pragma unroll
+          for (int half = 0; half < KP; ++half) {
+            const Place to = place_v<KP>(j + i, half);
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(sm.v_free[to.slot]), to.phase ^ 1, abrt));
+            if (!ok) break;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const Data& y = d[i][half];
+              uint32_t sc = y.sc[x];
+              const int token = (q4 + 4 * x) * 16 + 4 * t4, live = tile.left - token;
+              if (live < 4) sc = live <= 0 ? 0u : sc & (0xffffffffu >> (32 - 8 * live));
+              const uint32_t odd = ((sc & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;  // scales that are NaN
+              if (odd) {
+                atomicMin(&sm.nan_key[tile.unit & (kNanSets - 1)][half * 8 + g8], tile.key0 + token + ((__ffs(odd) - 1) >> 3));
+                sc &= ~((odd >> 7) * 0xffu);
+              }
+              uint32_t s01, s23;
+              e4m3x4_to_half2(sc, s01, s23);
+              const uint32_t base = at0 + to.slot * kSlot + x * 64 * 128;
+              const uint32_t a0 = base + (c0 << 4), a1 = base + ((c0 ^ 1) << 4), a2 = base + ((c0 ^ 2) << 4), a3 = base + ((c0 ^ 3) << 4);
+              const uint32_t f0 = dup(s01, 0), f1 = dup(s01, 1), f2 = dup(s23, 0), f3 = dup(s23, 1);
+              put(a0, far ? y.lo[x].y : y.lo[x].x, f0);
+              put(a1, far ? y.lo[x].x : y.lo[x].y, f0);
+              put(a1 + 128, far ? y.lo[x].w : y.lo[x].z, f1);
+              put(a0 + 128, far ? y.lo[x].z : y.lo[x].w, f1);
+              put(a2 + 256, far ? y.hi[x].y : y.hi[x].x, f2);
+              put(a3 + 256, far ? y.hi[x].x : y.hi[x].y, f2);
+              put(a3 + 384, far ? y.hi[x].w : y.hi[x].z, f3);
+              put(a2 + 384, far ? y.hi[x].z : y.hi[x].w, f3);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(sm.v_full[to.slot]));
+            if (half == 0) fetch(tl[i]);
+            load(d[i][half], half);
+          }
+          if (!ok) break;
+        }
+      }
     }
   } else {
     // ================================ softmax ================================
-    registers_up<kSoftmaxRegs>();
+    registers_up<C::kSoftmaxRegs>();
     const int wg = warp >> 2, quarter = warp & 3, key = quarter * 32 + lane, wtid = tid & 127;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-    constexpr int NC = C::kHalfCols;
+    constexpr int NC = C::kHalfCols, NH = NC / 32;  // columns, 32 at a time
     const int col0 = wg * NC;
-    const uint32_t cm_at = smem_u32(sm.cm) + wg * NC * 8;
     bool ok = true;
     int j = 0, unit = 0;
     // tokens that see no key get zeros
@@ -594,6 +695,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const Kv4ChunkAr
       const bool starts = w.tile == 0, whole = starts && seg == w.tiles;
       const int tok0 = w.rt * a.tokens, toks = min(a.tokens, w.Lq - tok0);  // tokens of the unit
       const int edge = a.causal ? w.Lk - w.Lq + tok0 + 1 : w.Lk;            // keys that its first token sees
+      float scale;  // what S is to be multiplied with
+      bool mixed;   // and with the column's factor
       // Q, with 256 / R threads for a column
       {
         constexpr int TPR = 256 / R, kPieces = 16 / TPR;  // 16-byte pieces for a thread
@@ -615,10 +718,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const Kv4ChunkAr
         }
 #pragma unroll
         for (int d = 1; d < TPR; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-        const int e = max(static_cast<int>(top >> 7) - 127, -100);
+        // One power of two for all columns where their largest channels lie within 2^12 of each other (zeros
+        // lie anywhere), else one for each column.
+        const int own = max(static_cast<int>(top >> 7) - 127, -100);
+        const int hi = __reduce_max_sync(0xffffffffu, top ? own : INT_MIN), lo = __reduce_min_sync(0xffffffffu, top ? own : INT_MAX);
+        if (lane == 0) atomicMax(&sm.exp_max, hi), atomicMin(&sm.exp_min, lo);
+        named_barrier_sync(1, kSoftmaxWarps * 32);
+        const int all = max(sm.exp_max, -100);
+        mixed = sm.exp_max != INT_MIN && sm.exp_max - sm.exp_min > 12;
+        const int e = mixed ? own : all;
         const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);  // 2^(14 - e)
         // (never 0 or Inf, which a score of 0 or a masked one's Inf would turn into NaN)
-        const float down = fminf(fmaxf(ldexpf(a.qk_scale, e - 14), FLT_MIN), FLT_MAX);
+        auto down = [&](int x) { return fminf(fmaxf(ldexpf(a.qk_scale, x - 14), FLT_MIN), FLT_MAX); };
+        scale = mixed ? 1.f : down(all);
         auto two = [&](uint32_t v) { return pack_half2(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xffff0000u) * up); };
         const int qrow = KP == 2 ? t : col;
         const uint32_t base = q_at + (KP == 2 ? sub * C::kQRows * 256 : 0) + qrow * 128;
@@ -629,124 +741,124 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const Kv4ChunkAr
                        two(x[i].w));
         }
         if (part == 0) {
-          float* cm = reinterpret_cast<float*>(&sm.cm[col >> 1]) + (col & 1);
-          cm[0] = live ? down : 0.f;
-          cm[2] = live ? FLT_MAX : 0.f;
+          sm.ref[col] = live ? FLT_MAX : 0.f;
+          sm.fac[col] = down(own);
           sm.lim[col] = !live ? 0 : a.causal ? max(0, w.Lk - w.Lq + tok0 + t + 1) : w.Lk;
         }
         if (tid == 0) sm.seg = seg;
         fence_proxy_async_smem();
         named_barrier_sync(1, kSoftmaxWarps * 32);
+        if (tid == 0) sm.exp_max = INT_MIN, sm.exp_min = INT_MAX;
         if (lane == 0) mbar_arrive(bar(sm.q_full));
       }
       uint64_t l2[NC / 2];
 #pragma unroll
       for (int i = 0; i < NC / 2; ++i) l2[i] = 0;
+      const uint64_t scale2 = f2pack(scale, scale);
 
       for (int i = 0; i < seg; ++i, ++j) {
         const int key0 = (w.tile + i) * kTile;
-        ok = ok && mbar_wait(bar(sm.s_full[j & 1]), (j >> 1) & 1, abrt);
-        __syncwarp();
-        tc_fence_after();
-        float e[NC];
-        const uint32_t s_at = tmem + lanes + (j & 1) * R + col0;
-        auto load = [&]() {
-          uint32_t raw[NC / 32][32];
+        const uint32_t p_at = p_slots + (j & 1) * R * 256 + (R == 128 ? wg * kHalf : 0) + key * 128;
 #pragma unroll
-          for (int c = 0; c < NC / 32; ++c) tmem_ld32(s_at + 32 * c, raw[c]);
-          tmem_wait_ld();
+        for (int h = 0; h < NH; ++h) {
+          const int c0 = col0 + 32 * h;
+          float4 ref[8];
 #pragma unroll
-          for (int c = 0; c < NC; ++c) e[c] = __uint_as_float(raw[c >> 5][c & 31]);
-        };
-        auto mask = [&]() {
-          if (key0 + kTile <= edge) return;
-#pragma unroll
-          for (int c = 0; c < NC; ++c)
-            if (key0 + key >= sm.lim[col0 + c]) e[c] = -INFINITY;
-        };
-        auto exponents = [&]() {  // s c - m; the largest
-          float top0 = -INFINITY, top1 = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < NC; c += 2) {
-            const float4 cm = lds_f4(cm_at + c * 8);
-            const uint64_t x = f2fma(f2pack(e[c], e[c + 1]), f2pack(cm.x, cm.y), f2pack(cm.z, cm.w));
-            f2unpack(x, e[c], e[c + 1]);
+          for (int x = 0; x < 8; ++x) ref[x] = *reinterpret_cast<const float4*>(&sm.ref[c0 + 4 * x]);
+          if (h == 0) {
+            ok = ok && mbar_wait(bar(sm.s_full[j & 1]), (j >> 1) & 1, abrt);
+            __syncwarp();
+            tc_fence_after();
           }
-          mask();
+          float e[32];
+          auto load = [&]() {
+            uint32_t raw[32];
+            tmem_ld32(tmem + lanes + (j & 1) * R + c0, raw);
+            tmem_wait_ld();
 #pragma unroll
-          for (int c = 0; c < NC; c += 4) {
-            top0 = fmax3(top0, e[c], e[c + 1]);
-            top1 = fmax3(top1, e[c + 2], e[c + 3]);
-          }
-          return fmaxf(top0, top1);
-        };
-        load();
-        if (barrier_any(2 + wg, 128, exponents() > kMoveRef)) {
-          // New references. The columns' largest y = s c over the tile's keys:
-          load();
+            for (int c = 0; c < 32; ++c) e[c] = __uint_as_float(raw[c]);
+            if (mixed) {
 #pragma unroll
-          for (int c = 0; c < NC; c += 2) {
-            const float4 cm = lds_f4(cm_at + c * 8);
-            e[c] *= cm.x, e[c + 1] *= cm.y;
-          }
-          mask();
+              for (int c = 0; c < 32; ++c) e[c] *= sm.fac[c0 + c];
+            }
+          };
+          auto mask = [&]() {
 #pragma unroll
-          for (int c0 = 0; c0 < NC; c0 += 32) {
+            for (int c = 0; c < 32; ++c)
+              if (key0 + key >= sm.lim[c0 + c]) e[c] = -INFINITY;
+          };
+          for (bool moved = false;; moved = true) {  // exponents s c - m; once more where a column needs a new reference
+            load();
+            float top0 = -INFINITY, top1 = -INFINITY;
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+              f2unpack(f2fma(f2pack(e[4 * x], e[4 * x + 1]), scale2, f2pack(ref[x].x, ref[x].y)), e[4 * x], e[4 * x + 1]);
+              f2unpack(f2fma(f2pack(e[4 * x + 2], e[4 * x + 3]), scale2, f2pack(ref[x].z, ref[x].w)), e[4 * x + 2], e[4 * x + 3]);
+            }
+            if (key0 + kTile > edge) mask();
+#pragma unroll
+            for (int c = 0; c < 32; c += 4) {
+              top0 = fmax3(top0, e[c], e[c + 1]);
+              top1 = fmax3(top1, e[c + 2], e[c + 3]);
+            }
+            if (__builtin_expect(!barrier_any(2 + wg, 128, fmaxf(top0, top1) > kMoveRef) || moved, 1)) break;
+            // New references. The columns' largest y = s c over the tile's keys:
+            load();
+#pragma unroll
+            for (int c = 0; c < 32; ++c) e[c] *= scale;
+            if (key0 + kTile > edge) mask();
             int mine = INT_MIN;
 #pragma unroll
             for (int c = 0; c < 32; ++c) {
-              const int v = __reduce_max_sync(0xffffffffu, ordered(e[c0 + c]));
+              const int v = __reduce_max_sync(0xffffffffu, ordered(e[c]));
               if (lane == c) mine = v;
             }
-            atomicMax(&sm.top[col0 + c0 + lane], mine);
-          }
-          named_barrier_sync(2 + wg, 128);
-          if (wtid < NC) {
-            float* m = reinterpret_cast<float*>(&sm.cm[(col0 + wtid) >> 1]) + (wtid & 1) + 2;
-            const float old = -*m, next = fmaxf(old, unordered(sm.top[col0 + wtid]) - kPScale);
-            *m = -next;
-            sm.top[col0 + wtid] = __float_as_int(ex2_approx(old - next));
-          }
-          named_barrier_sync(2 + wg, 128);
-#pragma unroll
-          for (int c = 0; c < NC / 2; ++c) {
-            const uint64_t f = f2pack(__int_as_float(sm.top[col0 + 2 * c]), __int_as_float(sm.top[col0 + 2 * c + 1]));
-            l2[c] = f2fma(l2[c], f, 0ull);
-          }
-          if (i > 0) {  // O holds the tiles before this one
-            ok = ok && mbar_wait(bar(sm.pv_done[(j - 1) & 1]), ((j - 1) >> 1) & 1, abrt);
-            __syncwarp();
-            tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < KP * NC; c += 32) {
-              const int col = c % NC, at = tmem + lanes + C::kO + (c / NC) * R + col0 + col;
-              uint32_t o[32];
-              tmem_ld32(at, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int x = 0; x < 32; ++x)
-                o[x] = __float_as_uint(__uint_as_float(o[x]) * __int_as_float(sm.top[col0 + col + x]));
-              tmem_st32(at, o);
+            atomicMax(&sm.top[c0 + lane], mine);
+            named_barrier_sync(2 + wg, 128);
+            if (wtid < 32) {
+              const float old = -sm.ref[c0 + wtid], to = fmaxf(old, __fsub_ru(unordered(sm.top[c0 + wtid]), kPScale));
+              sm.ref[c0 + wtid] = -to;
+              sm.top[c0 + wtid] = __float_as_int(ex2_approx(old - to));
             }
-            tmem_wait_st();
-          }
-          named_barrier_sync(2 + wg, 128);
-          if (wtid < NC) sm.top[col0 + wtid] = INT_MIN;
-          load();
-          exponents();
-        }
-        const uint32_t p_at = slots + place_k<KP>(j, 0).slot * kSlot + (R == 128 ? wg * kHalf : 0) + key * 128;
+            named_barrier_sync(2 + wg, 128);
 #pragma unroll
-        for (int c = 0; c < NC; c += 8) {
-          uint32_t pk[4];
+            for (int x = 0; x < 8; ++x) ref[x] = *reinterpret_cast<const float4*>(&sm.ref[c0 + 4 * x]);
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const float p0 = ex2_approx(e[c + 2 * x]), p1 = ex2_approx(e[c + 2 * x + 1]);
-            l2[c / 2 + x] = f2add(l2[c / 2 + x], f2pack(p0, p1));
-            pk[x] = pack_half2(p0, p1);
+            for (int c = 0; c < 16; ++c) {
+              const uint64_t f = f2pack(__int_as_float(sm.top[c0 + 2 * c]), __int_as_float(sm.top[c0 + 2 * c + 1]));
+              l2[16 * h + c] = f2fma(l2[16 * h + c], f, 0ull);
+            }
+            if (i > 0) {  // O holds the tiles before this one
+              ok = ok && mbar_wait(bar(sm.pv_done[(j - 1) & 1]), ((j - 1) >> 1) & 1, abrt);
+              __syncwarp();
+              tc_fence_after();
+#pragma unroll 1
+              for (int p = 0; p < KP; ++p) {
+                const uint32_t at = tmem + lanes + C::kO + p * R + c0;
+                uint32_t o[32];
+                tmem_ld32(at, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * __int_as_float(sm.top[c0 + x]));
+                tmem_st32(at, o);
+              }
+              tmem_wait_st();
+            }
+            named_barrier_sync(2 + wg, 128);
+            if (wtid < 32) sm.top[c0 + wtid] = INT_MIN;
           }
-          const int piece = c / 8 + (R == 64 ? wg * 4 : 0);
-          st_shared_v4(p_at + ((piece ^ (key & 7)) << 4), pk[0], pk[1], pk[2], pk[3]);
+#pragma unroll
+          for (int c = 0; c < 32; c += 8) {
+            uint32_t pk[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const float p0 = ex2_approx(e[c + 2 * x]), p1 = ex2_approx(e[c + 2 * x + 1]);
+              l2[16 * h + c / 2 + x] = f2add(l2[16 * h + c / 2 + x], f2pack(p0, p1));
+              pk[x] = pack_half2(p0, p1);
+            }
+            const int piece = 4 * (R == 64 ? wg : h) + c / 8;
+            st_shared_v4(p_at + ((piece ^ (key & 7)) << 4), pk[0], pk[1], pk[2], pk[3]);
+          }
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -803,7 +915,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const Kv4ChunkAr
           }
           s_fac[tid] = f;
         } else {
-          rec[tid] = -*(reinterpret_cast<const float*>(&sm.cm[tid >> 1]) + (tid & 1) + 2);
+          rec[tid] = -sm.ref[tid];
           rec[R + tid] = l;
         }
       }
@@ -850,68 +962,59 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const Kv4ChunkAr
           }
         }
       } else {
-        constexpr int T = C::kQRows, TN = T / 2;  // the warpgroup's tokens
-        const int t0 = wg * TN;
-        float y[2][TN], ss[TN];
+        constexpr int T = C::kQRows, TN = 16;  // the warpgroup's tokens, 16 at a time
+        float wgt[2] = {1.f, 1.f};
+        if ((a.flags & 2) && a.norm_w) wgt[0] = *(a.norm_w + key), wgt[1] = *(a.norm_w + 128 + key);
+        const float f = (a.flags & 4) ? 1.f - a.lambda_init : 1.f;
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + (static_cast<size_t>(w.q0 + tok0) * a.H + w.h) * 256 + key;
+#pragma unroll 1
+        for (int t0 = wg * (T / 2); t0 < (wg + 1) * (T / 2); t0 += TN) {
+          float y[2][TN];
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          uint32_t o1[TN], o2[TN];
-          if constexpr (TN == 32) {
-            tmem_ld32(o_at + p * R + t0, o1);
-            tmem_ld32(o_at + p * R + T + t0, o2);
-          } else {
+          for (int p = 0; p < 2; ++p) {
+            uint32_t o1[TN], o2[TN];
             tmem_ld16(o_at + p * R + t0, o1);
             tmem_ld16(o_at + p * R + T + t0, o2);
+            tmem_wait_ld();
+#pragma unroll
+            for (int t = 0; t < TN; ++t) {
+              const float v = __uint_as_float(o1[t]) * s_fac[t0 + t] - __uint_as_float(o2[t]) * s_fac[T + t0 + t];
+              y[p][t] = bad[p] < sm.lim[t0 + t] ? kNan : v;
+            }
           }
-          tmem_wait_ld();
+          if (a.flags & 2) {
+            float ss[TN];
 #pragma unroll
-          for (int t = 0; t < TN; ++t) {
-            const int lim = sm.lim[t0 + t];
-            float v = __uint_as_float(o1[t]) * s_fac[t0 + t] - __uint_as_float(o2[t]) * s_fac[T + t0 + t];
-            if (bad[p] < lim) v = kNan;
-            y[p][t] = v;
-          }
-        }
-        float f = 1.f;
-        if (a.flags & 2) {
+            for (int t = 0; t < TN; ++t) ss[t] = fmaf(y[0][t], y[0][t], y[1][t] * y[1][t]);
+            int at = 0;
 #pragma unroll
-          for (int t = 0; t < TN; ++t) ss[t] = fmaf(y[0][t], y[0][t], y[1][t] * y[1][t]);
-          int at = 0;
-#pragma unroll
-          for (int d = 16, n = TN / 2; d >= 1; d >>= 1, n >>= 1) {
-            const bool up = lane & d;
-            if (n >= 1) {
+            for (int d = 16, n = TN / 2; d >= 2; d >>= 1, n >>= 1) {
+              const bool up = lane & d;
               at += up ? n : 0;
 #pragma unroll
               for (int c = 0; c < n; ++c) {
                 const float give = up ? ss[c] : ss[c + n], keep = up ? ss[c + n] : ss[c];
                 ss[c] = keep + __shfl_xor_sync(0xffffffffu, give, d);
               }
-            } else {
-              ss[0] += __shfl_xor_sync(0xffffffffu, ss[0], d);
             }
+            s_norm[warp * TN + at] = ss[0] + __shfl_xor_sync(0xffffffffu, ss[0], 1);
+            named_barrier_sync(2 + wg, 128);
+            if (wtid < TN) {
+              const float* q = s_norm + wg * 4 * TN + wtid;
+              const float sum = (q[0] + q[TN]) + (q[2 * TN] + q[3 * TN]);
+              s_part[t0 + wtid] = f / sqrtf(sum / 256.f + a.eps);
+            }
+            named_barrier_sync(2 + wg, 128);
           }
-          s_norm[warp * 32 + at] = ss[0];
-          named_barrier_sync(2 + wg, 128);
-          if (wtid < TN) {
-            const float* q = s_norm + wg * 4 * 32 + wtid;
-            const float sum = (q[0] + q[32]) + (q[64] + q[96]);
-            s_part[t0 + wtid] = 1.f / sqrtf(sum / 256.f + a.eps);
+#pragma unroll
+          for (int t = 0; t < TN; ++t) {
+            if (t0 + t >= toks || !dbg_index_ok(w.q0 + tok0 + t0 + t, a.total)) continue;
+            const float n = (a.flags & 2) ? s_part[t0 + t] : f;
+            const bool none = sm.lim[t0 + t] <= 0;  // (zeros, whatever the weight and the scale hold)
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+              out[static_cast<size_t>(t0 + t) * a.H * 256 + p * 128] = __float2bfloat16_rn(none ? 0.f : y[p][t] * n * wgt[p]);
           }
-          named_barrier_sync(2 + wg, 128);
-        }
-        if (a.flags & 4) f = 1.f - a.lambda_init;
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + (static_cast<size_t>(w.q0 + tok0) * a.H + w.h) * 256 + key;
-        float wgt[2] = {1.f, 1.f};
-        if ((a.flags & 2) && a.norm_w) wgt[0] = *(a.norm_w + key), wgt[1] = *(a.norm_w + 128 + key);
-#pragma unroll
-        for (int t = 0; t < TN; ++t) {
-          if (t0 + t >= toks || !dbg_index_ok(w.q0 + tok0 + t0 + t, a.total)) continue;
-          const float n = (a.flags & 2) ? s_part[t0 + t] * f : f;
-          const bool none = sm.lim[t0 + t] <= 0;  // (zeros, whatever the weight and the scale hold)
-#pragma unroll
-          for (int p = 0; p < 2; ++p)
-            out[static_cast<size_t>(t0 + t) * a.H * 256 + p * 128] = __float2bfloat16_rn(none ? 0.f : y[p][t] * n * wgt[p]);
         }
       }
       tc_fence_before();
@@ -1018,12 +1121,13 @@ template <int KP, int R>
 cudaError_t launch(Kv4ChunkArgs a, cudaStream_t st) {
   static std::atomic<uint64_t> raised{};
   a.tokens = KP == 2 ? R / 2 : R / a.group;
+  page_magic(a.page_size >> 4, &a.rec_magic, &a.rec_shift);
   // no more blocks than the tables' capacity can give ranges: a sequence's tiles of tokens overlap the total's
   const long long tiles = (static_cast<long long>(a.max_pages) * a.page_size + kTile - 1) / kTile;
   const long long units = (static_cast<long long>(a.total) / a.tokens + a.B) * a.H;
   const long long most = units >= kSms ? kSms : (tiles + kUnitCost) * units / kMinCost;
   a.grid = static_cast<int>(most < 1 ? 1 : most > kSms ? kSms : most);
-  cudaError_t e = launch_early_large(kv4_chunk_kernel<KP, R>, a.grid, kThreads, smem_bytes<R>(), smem_bytes<R>(), st, 1, a, raised);
+  cudaError_t e = launch_early_large(kv4_chunk_kernel<KP, R>, a.grid, kThreads, smem_bytes<KP, R>(), smem_bytes<KP, R>(), st, 1, a, raised);
   if (e != cudaSuccess || a.grid == 1) return e;
   g_launched.store(true, std::memory_order_relaxed);
   cudaLaunchAttribute at[1] = {};
@@ -1040,9 +1144,10 @@ cudaError_t launch(Kv4ChunkArgs a, cudaStream_t st) {
 
 }  // namespace
 
-// Columns of a unit: 64 where the longest chunk fits in them, which halves a tile's products and softmax.
+// Columns of a unit. V2: 64 where the longest chunk fits in them, which halves a tile's products and softmax.
+// V1: 64, as tensor memory holds both planes of O.
 int kv4_chunk_cols(int group, int max_seqlen_q) {
-  return static_cast<long long>(max_seqlen_q) * (group == 0 ? 2 : group) <= 64 ? 64 : 128;
+  return group == 0 || static_cast<long long>(max_seqlen_q) * group <= 64 ? 64 : 128;
 }
 size_t kv4_chunk_workspace_bytes(int group, int max_seqlen_q) {
   const size_t cols = kv4_chunk_cols(group, max_seqlen_q), width = group == 0 ? 256 : 128;
@@ -1051,7 +1156,7 @@ size_t kv4_chunk_workspace_bytes(int group, int max_seqlen_q) {
 
 cudaError_t launch_kv4_chunk(const Kv4ChunkArgs& a, int cols, cudaStream_t st) {
   if (a.total == 0) return cudaSuccess;
-  if (a.group == 0) return cols == 64 ? launch<2, 64>(a, st) : launch<2, 128>(a, st);
+  if (a.group == 0) return launch<2, 64>(a, st);
   return cols == 64 ? launch<1, 64>(a, st) : launch<1, 128>(a, st);
 }
 

@@ -361,6 +361,7 @@ struct Kv4ChunkArgs {
   float qk_scale, v_mul;   // as in Kv4DecodeArgs
   float* pieces;           // the workspace
   int tokens, grid;        // tokens of a unit, ranges: set by the launcher
+  uint32_t rec_magic, rec_shift;  // j / (page_size / 16), as in V2DecodeArgs' page_magic; the launcher's
 };
 int kv4_chunk_cols(int group, int max_seqlen_q);
 size_t kv4_chunk_workspace_bytes(int group, int max_seqlen_q);
