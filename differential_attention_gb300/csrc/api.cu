@@ -2571,13 +2571,13 @@ int chunk_kv4_impl(const char* fn, da::Kv4ChunkArgs& a, int width, int max_seqle
   if (!aligned(a.q, 16) || !aligned(a.pool, 16) || !aligned(a.out, 16) || !aligned(a.block_table, 4) || !aligned(a.seqlens, 4) ||
       !aligned(a.cu_seqlens, 4) || !aligned(a.lambda, 4) || !aligned(a.lam_logit, 4) || !aligned(a.norm_w, 16))
     return fail(DIFFATTN_ERR_ALIGN, "%s: tensors must be 16-byte aligned", fn);
-  const size_t need = da::kv4_chunk_workspace_bytes(a.group, max_seqlen_q);
+  const size_t need = da::kv4_chunk_workspace_bytes(a.group);
   if (!workspace || ws_bytes < need || !aligned(workspace, 256))
     return fail(DIFFATTN_ERR_WORKSPACE, "%s: need a 256-byte aligned workspace of %zu bytes", fn, need);
   a.pieces = static_cast<float*>(workspace);
   if ((rc = check_device())) return rc;
   kv4_scales(a, k_exp, v_exp);
-  cudaError_t e = da::launch_kv4_chunk(a, da::kv4_chunk_cols(a.group, max_seqlen_q), static_cast<cudaStream_t>(stream));
+  cudaError_t e = da::launch_kv4_chunk(a, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, fn);
   return ok();
 }
@@ -2591,7 +2591,7 @@ DIFFATTN_API int diffattn_fwd_kv4_workspace_size(int max_seqlen_q, int d, int dv
   if (!bytes) return fail(DIFFATTN_ERR_ARG, "%s: null pointer", fn);
   if (max_seqlen_q < 0 || d != 128 || dv != 256)
     return fail(DIFFATTN_ERR_SHAPE, "%s: need max_seqlen_q >= 0, d = 128, dv = 256", fn);
-  *bytes = da::kv4_chunk_workspace_bytes(0, max_seqlen_q);
+  *bytes = da::kv4_chunk_workspace_bytes(0);
   return ok();
 }
 
@@ -2637,7 +2637,7 @@ DIFFATTN_API int diffattn_v2_fwd_kv4_workspace_size(int max_seqlen_q, int Hq, in
   if (!bytes) return fail(DIFFATTN_ERR_ARG, "%s: null pointer", fn);
   if (max_seqlen_q < 0 || Hkv < 1 || d != 128 || !(Hq == 2LL * Hkv || Hq == 4LL * Hkv || Hq == 8LL * Hkv))
     return fail(DIFFATTN_ERR_SHAPE, "%s: need max_seqlen_q >= 0, d = 128 and Hq / Hkv in {2, 4, 8}", fn);
-  *bytes = da::kv4_chunk_workspace_bytes(Hq / Hkv, max_seqlen_q);
+  *bytes = da::kv4_chunk_workspace_bytes(Hq / Hkv);
   return ok();
 }
 

@@ -1,27 +1,24 @@
 // chunk_kv4.cu -- attention of chunks over the 4-bit cache: each sequence's new tokens, the last of its
 // positions, over all its cached keys (V1: both maps of a head; V2: the query heads of a KV head's group).
 //
-// A unit is a KV head, a sequence and a tile of its new tokens: R columns (64 or 128), a column being one
-// softmax (V2: column G t + g is query head g of token t; V1: column m T + t is map m of token t). Over the
-// keys, 128 at a time, everything is held transposed, keys or channels on the 128 lanes of tensor memory:
-//   S^T [128 keys x R] = K Q^T              (V1: map m's columns by the K plane of map m)
-//   P = 2^(s c - m),  l += P                (column by column: m a reference, c the scale)
-//   O^T [128 channels x R] += V^T P         (V1: two planes of channels)
-// so that a product costs what its columns cost: few new tokens leave the machine to the loads, and V1's
-// maps multiply no zeros, which rows of both maps over one K of 256 channels would. At the end V1:
-// o1/l1 - lambda o2/l2, the norm and the scale, V2: o_2p/l_2p - sigmoid(lam) o_2p+1/l_2p+1.
+// A unit is a KV head, a sequence and a tile of its new tokens: 128 rows, a row being one softmax (V2: row
+// G t + g is query head g of token t; V1: row 2 t + m is map m of token t, its query in the m-th half of 256
+// channels whose other half is 0). Over the keys, 128 at a time:
+//   S [128 x 128] = Q K^T,   P = 2^(s c - m),   l += P,   O [128 x 128 or 256] += P V
+// with S, P and O in tensor memory, a row a lane. At the end V1: o1/l1 - lambda o2/l2, the norm and the
+// scale, V2: o_2p/l_2p - sigmoid(lam) o_2p+1/l_2p+1: the two rows of a pair are neighbouring lanes.
 //
-// Warps. 8 for the softmax: warpgroup w has half of the columns (w R/2 ..), thread `key` one key of the
-// tile, so its P go to shared memory as whole pieces of 16 bytes, over the K plane that S came from. 8
-// unpack: they read records into registers, four planes ahead, and write K and V as fp16 (exact: an e2m1
-// times an e4m3 has 6 significant bits) in the products' 128-byte swizzle. One issues the products: S of
-// the next tile before P V of this one.
+// Warps. Softmax: a thread a row. V2 has two warpgroups, which take tiles in turn and have an O, m and l of
+// their own each, joined at the unit's end; V1, whose products take twice as long a tile, has one. K and V:
+// four warps each read records into registers, a tile ahead, and write fp16 (exact: an e2m1 times an e4m3 has
+// 6 significant bits) in the products' 128-byte swizzle, into a ring of planes. One warp looks the records'
+// addresses up and has L2 fetch them; one issues the products: S of the next tile before P V of this one.
 //
 // Numerics, as in the decode over the same cache: the query enters as fp16 after a power of two of its own
-// for each column, P is rounded to fp16 at 2^10 times its value against m, which moves only where a score
-// passes it by 2^4 (the whole warpgroup then finds the columns' new references and rescales O and l).
-// Sums and statistics are fp32. Keys that a column may not see have P = 0, and a V block that is NaN is held
-// as zeros and its first key noted: the columns that see that key get NaN at the end, the others nothing.
+// for each row, P is rounded to fp16 at 2^6 times its value against m, which moves only where a score passes
+// it by 2^9 (the row's l and O are then rescaled). Sums and statistics are fp32. Keys that a row may not see
+// have P = 0, and a V block that is NaN is held as zeros and its first key noted: the rows that see that key
+// get NaN at the end, the others nothing.
 //
 // Work. All units one behind the other are cut into equal ranges of tiles, one for each SM; pieces of units
 // that are cut go to the workspace, at most two a range, and a second kernel joins them in the order of the
@@ -38,35 +35,33 @@ namespace da {
 namespace {
 
 constexpr int kSms = 152;
-// warps: softmax 0 .. 7, K 8 .. 11, V 12 .. 15, products 16, addresses 17
-constexpr int kKWarp = 8, kVWarp = 12, kMmaWarp = 16, kAddressWarp = 17;
-constexpr int kSoftmaxWarps = 8, kThreads = 20 * 32;
+constexpr int kRows = 128;
 constexpr int kTile = 128;                       // keys
 constexpr int kSlot = kTile * 128 * 2;           // one plane of a tile in fp16
-constexpr int kHalf = kSlot / 2;                 // 64 of its channels (or columns of P)
+constexpr int kHalf = kSlot / 2;                 // 64 of its channels
 constexpr int kUnitCost = 3;                     // what a unit costs besides its tiles, in tiles
 constexpr int kMinCost = 2;                      // the smallest range
 constexpr float kPScale = 6.f, kMoveRef = 15.f;  // log2 of P's scale, and of the P at which the reference moves
-constexpr int kNanSets = 4;
+constexpr int kNanSets = 8;
 constexpr int kRing = 4;                         // tiles whose records' addresses are known
 
-template <int KP, int R>
+template <int KP>
 struct Cfg {
-  static constexpr int kHalfCols = R / 2;
-  static constexpr int kQRows = KP == 1 ? R : R / 2;  // rows of one product's Q
-  static constexpr int kQBytes = R * 256;
+  static constexpr int kStreams = KP == 1 ? 2 : 1;  // softmax warpgroups
+  static constexpr int kKWarp = 4 * kStreams, kVWarp = kKWarp + 4, kMmaWarp = kVWarp + 4, kAddressWarp = kMmaWarp + 1;
+  static constexpr int kThreads = (kMmaWarp + 4) * 32;
   static constexpr int kWidth = KP * 128;
-  static constexpr int kVSlots = KP == 1 ? 3 : 4;     // V: stages of a plane (V2), of two planes (V1)
-  static constexpr int kP = kVSlots * kSlot;          // shared memory: V, P twice, Q
-  static constexpr int kQ = kP + 2 * R * 256;
-  static constexpr int kSmall = kQ + kQBytes;
-  static constexpr int kO = 2 * R;                    // tensor memory: S twice, O's planes, K twice
-  static constexpr int kK = kO + KP * R;
-  static constexpr int kPiece = 2 * R + R * kWidth;   // floats: m, l, o
-  // Registers a thread: the launch's 96, dealt out anew to the warpgroups (2 of softmax, K, V, the rest).
-  static constexpr int kSoftmaxRegs = R == 64 ? 128 : 152, kUnpackRegs = R == 64 ? 96 : 72, kRestRegs = 32;
-  static_assert(2 * kSoftmaxRegs + 2 * kUnpackRegs + kRestRegs <= 5 * 96, "more registers than the launch has");
-  static_assert(kK + 2 * KP * 64 <= 512, "tensor memory");
+  static constexpr int kSlots = KP == 1 ? 6 : 5;    // the ring of planes: of each tile K's, then V's
+  static constexpr int kQ = kSlots * kSlot;         // Q: 64 channels of 128 rows at a time
+  static constexpr int kSmall = kQ + kRows * kWidth * 2;
+  static constexpr int kO = 2 * kTile;              // tensor memory: S (P in its place) twice, O of each stream
+  static constexpr int kPiece = 2 * kRows + kRows * kWidth;  // floats: m, l, o
+  // Registers a thread: the launch's (96 or 128) dealt out anew to the warpgroups
+  static constexpr int kLaunchRegs = KP == 1 ? 96 : 128;
+  static constexpr int kSoftmaxRegs = KP == 1 ? 128 : 168, kUnpackRegs = KP == 1 ? 88 : 120, kRestRegs = KP == 1 ? 48 : 64;
+  static_assert(kSoftmaxRegs >= kLaunchRegs && kUnpackRegs <= kLaunchRegs && kRestRegs <= kLaunchRegs, "raised and lowered");
+  static_assert(kStreams * kSoftmaxRegs + 2 * kUnpackRegs + kRestRegs <= (kThreads / 128) * kLaunchRegs, "more registers than the launch has");
+  static_assert(kO + kStreams * kWidth <= 512, "tensor memory");
 };
 
 struct TileAt {
@@ -74,15 +69,10 @@ struct TileAt {
   int key0, left, unit, pad;  // its first key, keys from there on (0: the stream has ended), its unit's number
 };
 struct Small {  // behind Q
-  float ref[128];      // the columns' references (less kPScale), negated
-  float fac[128];      // where the columns' queries have powers of two of their own: what S is to be multiplied with
-  int lim[128];        // keys that a column sees; 0 where there is no such token
-  int top[128];        // a move: the columns' largest exponents (ordered), then the factors
-  uint64_t v_full[4], v_free[4], k_full[2], k_free[2], s_full[2], p_full[2], pv_done[2], q_full, teardown;
+  uint64_t full[6], free[6], s_full[2], p_full[2], pv_done[2], q_full, teardown;
   uint64_t tile_full[kRing], tile_free[kRing];
   TileAt tile[kRing];
   int nan_key[kNanSets][16];
-  int exp_max, exp_min;  // exponents of the unit's queries
   uint32_t tmem;
   int abort, seg;      // seg: tiles of the unit whose Q is there, 0 behind the last
 };
@@ -92,19 +82,16 @@ struct Walk {  // place in the walk over units: sequences, heads, tiles of token
   int tile, tiles;
   long long todo;  // tiles of the range, and the costs of the units that begin in it, from here on
 };
-// at startup, in Q's place
-struct Scan {
-  long long pre[kThreads + 1], sum[kThreads / 32];
+constexpr int kMaxThreads = 640;
+struct Scan {  // at startup, in Q's place
+  long long pre[kMaxThreads + 1], sum[kMaxThreads / 32];
   Walk walk;
-  int ranges;
 };
-static_assert(sizeof(Scan) <= 64 * 256, "fits in the smaller Q");
-
-template <int KP, int R>
+template <int KP>
 constexpr int smem_bytes() {
-  return Cfg<KP, R>::kSmall + static_cast<int>(sizeof(Small));
+  return Cfg<KP>::kSmall + static_cast<int>(sizeof(Small));
 }
-static_assert(smem_bytes<1, 128>() <= 232448 && smem_bytes<2, 64>() <= 232448, "shared memory");
+static_assert(smem_bytes<1>() <= 232448 && smem_bytes<2>() <= 232448, "shared memory");
 
 // ---- the batch's units -------------------------------------------------------------------------
 struct Seq {
@@ -293,74 +280,53 @@ __device__ __forceinline__ uint32_t ldg32(const uint8_t* p) {
 __device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
-// whether any of `count` threads of the block's barrier `id` has p
-__device__ __forceinline__ bool barrier_any(uint32_t id, uint32_t count, bool p) {
-  uint32_t any;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\tbar.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(any)
-      : "r"(id), "r"(count), "r"(static_cast<uint32_t>(p))
-      : "memory");
-  return any != 0;
-}
-// an order-preserving map of floats to ints; a NaN counts as the least
-__device__ __forceinline__ int ordered(float x) {
-  const int i = __float_as_int(x);
-  return x != x ? INT_MIN : i >= 0 ? i : i ^ 0x7fffffff;
-}
-__device__ __forceinline__ float unordered(int i) {
-  return i == INT_MIN ? -INFINITY : __int_as_float(i >= 0 ? i : i ^ 0x7fffffff);
-}
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int a_mn, int b_mn) {
   return umma_idesc_bf16(M, N, a_mn, b_mn) & ~((1u << 7) | (1u << 10));
 }
 
-// where V's plane `half` of the block's tile j lies, and the phase of its slot's use
+// where plane p of the block's tile j lies, and the phase of its slot's use
 struct Place {
   int slot, phase;
 };
 template <int KP>
-__device__ __forceinline__ Place place_v(int j, int half) {
-  if constexpr (KP == 1) return {j % 3, (j / 3) & 1};
-  return {2 * (j & 1) + half, (j >> 1) & 1};
+__device__ __forceinline__ Place place(int j, int p) {
+  const uint32_t n = static_cast<uint32_t>(j) * (2 * KP) + p, use = n / Cfg<KP>::kSlots;
+  return {static_cast<int>(n - use * Cfg<KP>::kSlots), static_cast<int>(use & 1)};
 }
 
-template <int KP, int R>
-__global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const Kv4ChunkArgs a) {
-  using C = Cfg<KP, R>;
+template <int KP>
+__global__ void __launch_bounds__(Cfg<KP>::kThreads, 1) kv4_chunk_kernel(const Kv4ChunkArgs a) {
+  using C = Cfg<KP>;
+  constexpr int kThreads = C::kThreads, kStreams = C::kStreams;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* const s_q = smem + C::kQ;
   Small& sm = *reinterpret_cast<Small*>(smem + C::kSmall);
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-  const uint32_t slots = smem_u32(smem), p_slots = slots + C::kP, q_at = smem_u32(s_q);
+  const uint32_t slots = smem_u32(smem), q_at = smem_u32(s_q);
   auto bar = [](uint64_t& x) { return smem_u32(&x); };
 
   if (tid == 0) {
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(bar(sm.v_full[i]), 4);
-      mbar_init(bar(sm.v_free[i]), 1);
+    for (int i = 0; i < 6; ++i) {
+      mbar_init(bar(sm.full[i]), 4);
+      mbar_init(bar(sm.free[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(sm.k_full[i]), 4);
-      mbar_init(bar(sm.k_free[i]), 1);
       mbar_init(bar(sm.s_full[i]), 1);
-      mbar_init(bar(sm.p_full[i]), kSoftmaxWarps);
+      mbar_init(bar(sm.p_full[i]), 4);
       mbar_init(bar(sm.pv_done[i]), 1);
     }
     for (int i = 0; i < kRing; ++i) {
       mbar_init(bar(sm.tile_full[i]), 1);
       mbar_init(bar(sm.tile_free[i]), 8);
     }
-    mbar_init(bar(sm.q_full), kSoftmaxWarps);
+    mbar_init(bar(sm.q_full), 4 * kStreams);
     mbar_init(bar(sm.teardown), 1);
     sm.abort = 0;
-    sm.exp_max = INT_MIN, sm.exp_min = INT_MAX;
     fence_barrier_init();
     fence_proxy_async_smem();
   }
   for (int i = tid; i < kNanSets * 16; i += kThreads) sm.nan_key[i >> 4][i & 15] = INT_MAX;
-  for (int i = tid; i < 128; i += kThreads) sm.top[i] = INT_MIN;
-  if (warp == kMmaWarp) {
+  if (warp == C::kMmaWarp) {
     tmem_alloc(smem_u32(&sm.tmem), 512);
     tmem_relinquish();
   }
@@ -390,47 +356,54 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const Kv4ChunkAr
   const uint32_t tmem = sm.tmem;
   volatile int* abrt = &sm.abort;
 
-  if (warp >= kMmaWarp) {
+  if (warp >= C::kMmaWarp) {
     registers_down<C::kRestRegs>();
-    if (warp == kMmaWarp && elect_one()) {
+    if (warp == C::kMmaWarp && elect_one()) {
       // ================================ products ================================
-      constexpr uint32_t idesc_s = idesc_f16(kTile, C::kQRows, 0, 0), idesc_o = idesc_f16(128, R, 1, 1);
-      const uint64_t dq = umma_smem_desc(q_at, 16, 1024);
-      const uint64_t dv = umma_smem_desc(slots, kHalf, 1024), dp = umma_smem_desc(p_slots, kHalf, 1024);
+      constexpr uint32_t idesc_s = idesc_f16(kRows, kTile, 0, 0), idesc_v = idesc_f16(kRows, 128, 0, 1);
+      const uint64_t dq = umma_smem_desc(q_at, 16, 1024), dk = umma_smem_desc(slots, 16, 1024);
+      const uint64_t dv = umma_smem_desc(slots, kHalf, 1024);
       int j = 0;
       bool ok = true;
-      auto scores = [&](int t) {
-        if (!(ok = mbar_wait(bar(sm.k_full[t & 1]), (t >> 1) & 1, abrt))) return;
-        tc_fence_after();
+      auto scores = [&](int t, bool wait) {
+        // (P of tile t - 2 lay where S goes)
+        if (wait && !(ok = mbar_wait(bar(sm.pv_done[t & 1]), ((t - 2) >> 1) & 1, abrt))) return;
 #pragma unroll 1
-        for (int map = 0; map < KP; ++map)
-#pragma unroll 2
-          for (int kk = 0; kk < 8; ++kk)
-            mma_bf16_ts(tmem + (t & 1) * R + map * C::kQRows, tmem + C::kK + ((t & 1) * KP + map) * 64 + kk * 8,
-                        desc_add(dq, map * C::kQRows * 256 + (kk >> 2) * C::kQRows * 128 + (kk & 3) * 32), idesc_s, kk > 0);
+        for (int p = 0; p < KP; ++p) {
+          const Place k = place<KP>(t, p);
+          if (!(ok = mbar_wait(bar(sm.full[k.slot]), k.phase, abrt))) return;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
+            mma_bf16_ss(tmem + (t & 1) * kTile, desc_add(dq, p * 2 * kHalf + off), desc_add(dk, k.slot * kSlot + off), idesc_s,
+                        p > 0 || kk > 0);
+          }
+          tc_commit(bar(sm.free[k.slot]));
+        }
         tc_commit(bar(sm.s_full[t & 1]));
-        tc_commit(bar(sm.k_free[t & 1]));
       };
       for (int unit = 0; ok; ++unit) {
         if (!(ok = mbar_wait(bar(sm.q_full), unit & 1, abrt))) break;
         tc_fence_after();
         const int seg = *static_cast<volatile int*>(&sm.seg);
         if (seg == 0) break;
-        scores(j);
+        scores(j, false);
         for (int i = 0; ok && i < seg; ++i, ++j) {
-          if (i + 1 < seg) scores(j + 1);
+          if (i + 1 < seg) scores(j + 1, i > 0);
           if (!ok) break;
           if (!(ok = mbar_wait(bar(sm.p_full[j & 1]), (j >> 1) & 1, abrt))) break;
+          const uint32_t o = tmem + C::kO + (kStreams == 2 ? (j & 1) * 128 : 0);
 #pragma unroll 1
-          for (int half = 0; half < KP; ++half) {
-            const Place v = place_v<KP>(j, half);
-            if (!(ok = ok && mbar_wait(bar(sm.v_full[v.slot]), v.phase, abrt))) break;
+          for (int p = 0; p < KP; ++p) {
+            const Place v = place<KP>(j, KP + p);
+            if (!(ok = mbar_wait(bar(sm.full[v.slot]), v.phase, abrt))) break;
             tc_fence_after();
-#pragma unroll 2
+#pragma unroll
             for (int kk = 0; kk < 8; ++kk)
-              mma_bf16_ss(tmem + C::kO + half * R, desc_add(dv, v.slot * kSlot + kk * 2048),
-                          desc_add(dp, (j & 1) * R * 256 + kk * 2048), idesc_o, i > 0 || kk > 0);
-            tc_commit(bar(sm.v_free[v.slot]));
+              mma_bf16_ts(o + p * 128, tmem + (j & 1) * kTile + kk * 8, desc_add(dv, v.slot * kSlot + kk * 2048), idesc_v,
+                          i >= kStreams || kk > 0);
+            tc_commit(bar(sm.free[v.slot]));
           }
           if (!ok) break;
           tc_commit(bar(sm.pv_done[j & 1]));
@@ -439,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const Kv4ChunkAr
       // every product that was issued ends before tensor memory is given back
       tc_commit(bar(sm.teardown));
       mbar_wait(bar(sm.teardown), 0, nullptr);
-    } else if (warp == kAddressWarp) {
+    } else if (warp == C::kAddressWarp) {
       // ================================ addresses ================================
       // Lane 8 i + r looks up record r of tile i of a batch: up to four tiles of a unit. The next batch's pages
       // are looked up before this one is passed on, tile by tile, as the ring has room.
@@ -487,539 +460,391 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const Kv4ChunkAr
         if (x.n == 0) break;
       }
     }
-  } else if (warp >= kKWarp) {
+  } else if (warp >= C::kKWarp) {
     // ================================ unpack ================================
-    // Both kinds of warps load a tile's bytes into registers one or two tiles before they unpack them (also
-    // where the sequence has no such record, from page 0: no branch comes between loads in flight).
+    // A tile's bytes are loaded into registers before the tile before it is waited for (also where the
+    // sequence has no such record, from page 0: no branch comes between loads in flight). Warp q4 of K's or
+    // V's four takes records q4 and q4 + 4 of each plane. A piece of 8 channels lies at its number XOR the
+    // row's; lanes of a quarter-warp whose places would meet in the banks (t4 of 0 and 2, 1 and 3) take their
+    // pieces in another order.
     registers_down<C::kUnpackRegs>();
-    const int q4 = warp & 3;
-    int next = 0, end = INT_MAX;  // the next tile to load; behind the stream's last its end stays, and is read again
-    bool ok = true;
+    const int q4 = warp & 3, t4 = lane & 3, hi8 = lane >> 2;
+    const bool far = t4 & 2, is_k = warp < C::kVWarp;
     struct Tile {
       int key0, left, unit;
     };
-    auto tile_at = [&](Tile& t) -> const TileAt& {
-      const int i = min(next, end);
-      ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(sm.tile_full[i % kRing]), (i / kRing) & 1, abrt));
-      const TileAt& at = sm.tile[i % kRing];
-      t.key0 = at.key0, t.left = ok ? at.left : 0, t.unit = at.unit;
-      if (t.left <= 0) end = i;
-      ++next;
-      return at;
+    struct Data {
+      uint4 lo[2], hi[2];
+      uint32_t sc[2];
     };
-    auto tile_read = [&](const Tile& t) {  // (its addresses are in registers)
+    Data d[KP];
+    Tile next{}, tile;
+    const uint8_t* src[2] = {nullptr, nullptr};
+    int loaded = 0;
+    bool ok = true;
+    auto fetch = [&]() {  // the next tile's addresses; behind the stream's end they stay
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(sm.tile_full[loaded % kRing]), (loaded / kRing) & 1, abrt));
+      const TileAt& at = sm.tile[loaded % kRing];
+      src[0] = at.rec[q4] + (is_k ? 0 : KP * kKv4Plane), src[1] = at.rec[q4 + 4] + (is_k ? 0 : KP * kKv4Plane);
+      next.key0 = at.key0, next.left = ok ? at.left : 0, next.unit = at.unit;
       __syncwarp();
-      if (lane == 0 && t.left > 0) mbar_arrive(bar(sm.tile_free[(next - 1) % kRing]));
+      if (next.left > 0) {
+        if (lane == 0) mbar_arrive(bar(sm.tile_free[loaded % kRing]));
+        ++loaded;
+      }
+    };
+    auto load = [&](Data& x, int p) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint8_t* from = src[i] + p * kKv4Plane;
+        x.lo[i] = ldg128(from + lane * 16);
+        x.hi[i] = ldg128(from + lane * 16 + 512);
+        x.sc[i] = ldg32(from + lane * 4 + kKv4PlaneCodes);
+      }
     };
     auto dup = [](uint32_t two, int high) { return __byte_perm(two, 0, high ? 0x3232 : 0x1010); };
-    if (warp < kVWarp) {
-      // K: lane `key` takes a key of the tile, tensor memory's lane of that number: its 64 bytes of codes are
-      // on end, its scales two bytes of each word of 16.
-      constexpr int kAhead = 1;
-      struct Data {
-        uint4 w[4], sc;
-      };
-      Data d[kAhead][KP];
-      Tile tl[kAhead], tile;
-      const int key = lane & 15, h = (key >> 1) & 1, row = 32 * q4 + lane;
-      const int code = kv4_k_code(key, 0), scale = kKv4PlaneCodes + (key >> 2) * 32 + (key & 1) * 16;
-      const uint32_t to = tmem + (static_cast<uint32_t>(q4 * 32) << 16) + C::kK;
-      const uint8_t* src = nullptr;
-      auto load = [&](Data& x, int plane) {
-        const uint8_t* p = src + plane * kKv4Plane;
+    auto put = [](uint32_t at, uint32_t word, uint32_t f) {
+      uint32_t v[4];
+      e2m1x8_to_half2(word, v);
+      st_shared_v4(at, half2_mul(v[0], f), half2_mul(v[1], f), half2_mul(v[2], f), half2_mul(v[3], f));
+    };
+    // K: key 4 (hi8 / 2) + hi8 % 2 and that + 2, channels 32 t4 ..; V: tokens 4 t4 .., channels 16 hi8 ..
+    const int row = q4 * 16 + (is_k ? 4 * (hi8 >> 1) + (hi8 & 1) : 4 * t4);
+    const int c0 = is_k ? ((t4 & 1) * 4 + (t4 & 2)) ^ (row & 7) : ((hi8 & 3) * 2) ^ (row & 7) ^ (far ? 1 : 0);
+    const uint32_t at0 = slots + (is_k ? t4 >> 1 : hi8 >> 2) * kHalf + row * 128;
+    auto loop = [&](auto&& unpack) {
+      fetch();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x.w[i] = ldg128(p + code + 16 * i);
-        x.sc = ldg128(p + scale);
-      };
+      for (int p = 0; p < KP; ++p) load(d[p], p);
+      for (int j = 0; ok; ++j) {
+        tile = next;
+        if (tile.left <= 0) break;
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        src = tile_at(tl[i]).rec[2 * q4 + (lane >> 4)];
-        tile_read(tl[i]);
-#pragma unroll
-        for (int p = 0; p < KP; ++p) load(d[i][p], p);
-      }
-      for (int j = 0; ok; j += kAhead) {
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-          tile = tl[i];
-          if (tile.left <= 0) {
-            ok = false;
-            break;
-          }
-          const int t = j + i;
-          ok = __all_sync(0xffffffffu, mbar_wait(bar(sm.k_free[t & 1]), ((t >> 1) & 1) ^ 1, abrt));
+        for (int p = 0; p < KP; ++p) {
+          const Place to = place<KP>(j, (is_k ? 0 : KP) + p);
+          ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(sm.free[to.slot]), to.phase ^ 1, abrt));
           if (!ok) break;
-          tc_fence_after();
 #pragma unroll
-          for (int p = 0; p < KP; ++p) {
-            const uint32_t sc4[4] = {d[i][p].sc.x, d[i][p].sc.y, d[i][p].sc.z, d[i][p].sc.w};
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              uint32_t v[32];
-#pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                const uint4 w4 = d[i][p].w[2 * half + x];
-                const uint32_t word[4] = {w4.x, w4.y, w4.z, w4.w};
-                const uint32_t two = row < tile.left ? e4m3x2_to_half2(sc4[2 * half + x] >> (16 * h)) : 0u;
-                const uint32_t f0 = dup(two, 0), f1 = dup(two, 1);
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                  uint32_t o[4];
-                  e2m1x8_to_half2(word[y], o);
-#pragma unroll
-                  for (int z = 0; z < 4; ++z) v[x * 16 + y * 4 + z] = half2_mul(o[z], y < 2 ? f0 : f1);
-                }
-              }
-              tmem_st32(to + ((t & 1) * KP + p) * 64 + half * 32, v);
-            }
-            if (p == 0) {
-              src = tile_at(tl[i]).rec[2 * q4 + (lane >> 4)];
-              tile_read(tl[i]);
-            }
-            load(d[i][p], p);
+          for (int x = 0; x < 2; ++x) {
+            const uint32_t base = at0 + to.slot * kSlot + x * 64 * 128;
+            unpack(d[p].lo[x], d[p].hi[x], d[p].sc[x], p, tile.left - x * 64, x * 64, base + (c0 << 4), base + ((c0 ^ 1) << 4),
+                   base + ((c0 ^ 2) << 4), base + ((c0 ^ 3) << 4));
           }
-          tmem_wait_st();
-          tc_fence_before();
+          fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar(sm.k_full[t & 1]));
+          if (lane == 0) mbar_arrive(bar(sm.full[to.slot]));
+          if (p == 0) fetch();
+          load(d[p], p);
         }
       }
+    };
+    if (is_k) {
+      loop([&](const uint4& lo, const uint4& hi, uint32_t sc, int, int left, int, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+        uint32_t s0, s1;
+        e4m3x4_to_half2(sc, s0, s1);
+        if (left <= row) s0 = 0;
+        if (left <= row + 2) s1 = 0;
+        const uint32_t f0 = dup(s0, far), f1 = dup(s0, !far), g0 = dup(s1, far), g1 = dup(s1, !far);
+        put(a0, far ? lo.z : lo.x, f0);
+        put(a1, far ? lo.w : lo.y, f0);
+        put(a2, far ? lo.x : lo.z, f1);
+        put(a3, far ? lo.y : lo.w, f1);
+        put(a2 + 256, far ? hi.z : hi.x, g0);  // two rows on
+        put(a3 + 256, far ? hi.w : hi.y, g0);
+        put(a0 + 256, far ? hi.x : hi.z, g1);
+        put(a1 + 256, far ? hi.y : hi.w, g1);
+      });
     } else {
-      // V: warp v takes records v and v + 4, to shared memory. A piece of 8 channels lies at its number XOR the
-      // row's; lanes of a quarter-warp whose places would meet in the banks (t4 of 0 and 2, 1 and 3) take
-      // their pieces in another order.
-      constexpr int kAhead = 1;
-      struct Data {
-        uint4 lo[2], hi[2];
-        uint32_t sc[2];
-      };
-      Data d[kAhead][KP];
-      Tile tl[kAhead], tile;
-      const int t4 = lane & 3, g8 = lane >> 2;  // tokens 4 t4 .., channels 16 g8 ..
-      const bool far = t4 & 2;
-      const uint32_t at0 = slots + (g8 >> 2) * kHalf + (q4 * 16 + 4 * t4) * 128;
-      const int c0 = ((g8 & 3) * 2) ^ (4 * (t4 & 1)) ^ (far ? 1 : 0);
-      const uint8_t* src[2] = {nullptr, nullptr};
-      auto load = [&](Data& x, int half) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint8_t* p = src[i] + (KP + half) * kKv4Plane;
-          x.lo[i] = ldg128(p + lane * 16);
-          x.hi[i] = ldg128(p + lane * 16 + 512);
-          x.sc[i] = ldg32(p + lane * 4 + kKv4PlaneCodes);
+      loop([&](const uint4& lo, const uint4& hi, uint32_t sc, int p, int left, int key, uint32_t a0, uint32_t a1, uint32_t a2,
+               uint32_t a3) {
+        const int live = left - row;
+        if (live < 4) sc = live <= 0 ? 0u : sc & (0xffffffffu >> (32 - 8 * live));
+        const uint32_t odd = ((sc & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;  // scales that are NaN
+        if (odd) {
+          atomicMin(&sm.nan_key[tile.unit & (kNanSets - 1)][p * 8 + hi8], tile.key0 + key + row + ((__ffs(odd) - 1) >> 3));
+          sc &= ~((odd >> 7) * 0xffu);
         }
-      };
-      auto fetch = [&](Tile& t) {
-        const TileAt& at = tile_at(t);
-        src[0] = at.rec[q4], src[1] = at.rec[q4 + 4];
-        tile_read(t);
-      };
-      auto put = [](uint32_t at, uint32_t word, uint32_t f) {
-        uint32_t v[4];
-        e2m1x8_to_half2(word, v);
-        st_shared_v4(at, half2_mul(v[0], f), half2_mul(v[1], f), half2_mul(v[2], f), half2_mul(v[3], f));
-      };
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        fetch(tl[i]);
-#pragma unroll
-        for (int p = 0; p < KP; ++p) load(d[i][p], p);
-      }
-      for (int j = 0; ok; j += kAhead) {
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-          tile = tl[i];
-          if (tile.left <= 0) {
-            ok = false;
-            break;
-          }
-#pragma unroll
-          for (int half = 0; half < KP; ++half) {
-            const Place to = place_v<KP>(j + i, half);
-            ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(sm.v_free[to.slot]), to.phase ^ 1, abrt));
-            if (!ok) break;
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const Data& y = d[i][half];
-              uint32_t sc = y.sc[x];
-              const int token = (q4 + 4 * x) * 16 + 4 * t4, live = tile.left - token;
-              if (live < 4) sc = live <= 0 ? 0u : sc & (0xffffffffu >> (32 - 8 * live));
-              const uint32_t odd = ((sc & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;  // scales that are NaN
-              if (odd) {
-                atomicMin(&sm.nan_key[tile.unit & (kNanSets - 1)][half * 8 + g8], tile.key0 + token + ((__ffs(odd) - 1) >> 3));
-                sc &= ~((odd >> 7) * 0xffu);
-              }
-              uint32_t s01, s23;
-              e4m3x4_to_half2(sc, s01, s23);
-              const uint32_t base = at0 + to.slot * kSlot + x * 64 * 128;
-              const uint32_t a0 = base + (c0 << 4), a1 = base + ((c0 ^ 1) << 4), a2 = base + ((c0 ^ 2) << 4), a3 = base + ((c0 ^ 3) << 4);
-              const uint32_t f0 = dup(s01, 0), f1 = dup(s01, 1), f2 = dup(s23, 0), f3 = dup(s23, 1);
-              put(a0, far ? y.lo[x].y : y.lo[x].x, f0);
-              put(a1, far ? y.lo[x].x : y.lo[x].y, f0);
-              put(a1 + 128, far ? y.lo[x].w : y.lo[x].z, f1);
-              put(a0 + 128, far ? y.lo[x].z : y.lo[x].w, f1);
-              put(a2 + 256, far ? y.hi[x].y : y.hi[x].x, f2);
-              put(a3 + 256, far ? y.hi[x].x : y.hi[x].y, f2);
-              put(a3 + 384, far ? y.hi[x].w : y.hi[x].z, f3);
-              put(a2 + 384, far ? y.hi[x].z : y.hi[x].w, f3);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(sm.v_full[to.slot]));
-            if (half == 0) fetch(tl[i]);
-            load(d[i][half], half);
-          }
-          if (!ok) break;
-        }
-      }
+        uint32_t s01, s23;
+        e4m3x4_to_half2(sc, s01, s23);
+        const uint32_t f0 = dup(s01, 0), f1 = dup(s01, 1), f2 = dup(s23, 0), f3 = dup(s23, 1);
+        put(a0, far ? lo.y : lo.x, f0);
+        put(a1, far ? lo.x : lo.y, f0);
+        put(a1 + 128, far ? lo.w : lo.z, f1);
+        put(a0 + 128, far ? lo.z : lo.w, f1);
+        put(a2 + 256, far ? hi.y : hi.x, f2);
+        put(a3 + 256, far ? hi.x : hi.y, f2);
+        put(a3 + 384, far ? hi.w : hi.z, f3);
+        put(a2 + 384, far ? hi.z : hi.w, f3);
+      });
     }
   } else {
     // ================================ softmax ================================
     registers_up<C::kSoftmaxRegs>();
-    const int wg = warp >> 2, quarter = warp & 3, key = quarter * 32 + lane, wtid = tid & 127;
+    constexpr int kAll = kStreams * 128;
+    const int wg = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-    constexpr int NC = C::kHalfCols, NH = NC / 32;  // columns, 32 at a time
-    const int col0 = wg * NC;
     bool ok = true;
     int j = 0, unit = 0;
     // tokens that see no key get zeros
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
       const Seq s = sequence<false>(a, b);
       const int z = hidden(a, s);
-      const size_t row = static_cast<size_t>(a.H) * (KP == 2 ? 256 : a.group * 64);
-      uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + s.q0 * row);
-      for (size_t i = tid; i < z * row / 8; i += kSoftmaxWarps * 32) out[i] = make_uint4(0, 0, 0, 0);
+      const size_t width = static_cast<size_t>(a.H) * (KP == 2 ? 256 : a.group * 64);
+      uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + s.q0 * width);
+      for (size_t i = tid; i < z * width / 8; i += kAll) out[i] = make_uint4(0, 0, 0, 0);
     }
     while (w.todo > 0) {
       const int seg = static_cast<int>(min(static_cast<long long>(w.tiles - w.tile), w.todo));
       const bool starts = w.tile == 0, whole = starts && seg == w.tiles;
       const int tok0 = w.rt * a.tokens, toks = min(a.tokens, w.Lq - tok0);  // tokens of the unit
-      const int edge = a.causal ? w.Lk - w.Lq + tok0 + 1 : w.Lk;            // keys that its first token sees
-      float scale;  // what S is to be multiplied with
-      bool mixed;   // and with the column's factor
-      // Q, with 256 / R threads for a column
+      const int per = KP == 2 ? 2 : a.group, rows = toks * per;            // rows of a token, rows in use
+      // Q: kStreams threads for a row, each 128 / kStreams of its channels
+      float scale;  // what the row's S is to be multiplied with
       {
-        constexpr int TPR = 256 / R, kPieces = 16 / TPR;  // 16-byte pieces for a thread
-        const int col = tid / TPR, part = tid % TPR;
-        const int t = KP == 2 ? col % C::kQRows : col / a.group, sub = KP == 2 ? col / C::kQRows : col % a.group;
-        const bool live = t < toks;
-        const size_t row = KP == 2 ? (static_cast<size_t>(w.q0 + tok0 + t) * a.H + w.h) * 2 + sub
-                                   : static_cast<size_t>(w.q0 + tok0 + t) * a.H * a.group + w.h * a.group + sub;
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + row * 128) + part * kPieces;
-        uint4 x[kPieces];
+        constexpr int kPieces = 16 / kStreams;  // of 16 bytes, for a thread
+        const int t = row / per, sub = row - t * per;
+        const bool live = row < rows;
+        const size_t from = (static_cast<size_t>(w.q0 + tok0 + t) * a.H + w.h) * per + sub;
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + from * 128);
         uint32_t top = 0;  // the largest magnitude's bits (ordered as the values are)
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) x[i] = live ? *(src + i) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-          const uint32_t m2 = __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
-                                       __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu));
+        for (int i = 0; i < 16; ++i) {
+          const uint4 x = live ? *(src + i) : make_uint4(0, 0, 0, 0);
+          const uint32_t m2 = __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu), __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
           top = max(top, max(m2 & 0xffffu, m2 >> 16));
         }
-#pragma unroll
-        for (int d = 1; d < TPR; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-        // One power of two for all columns where their largest channels lie within 2^12 of each other (zeros
-        // lie anywhere), else one for each column.
-        const int own = max(static_cast<int>(top >> 7) - 127, -100);
-        const int hi = __reduce_max_sync(0xffffffffu, top ? own : INT_MIN), lo = __reduce_min_sync(0xffffffffu, top ? own : INT_MAX);
-        if (lane == 0) atomicMax(&sm.exp_max, hi), atomicMin(&sm.exp_min, lo);
-        named_barrier_sync(1, kSoftmaxWarps * 32);
-        const int all = max(sm.exp_max, -100);
-        mixed = sm.exp_max != INT_MIN && sm.exp_max - sm.exp_min > 12;
-        const int e = mixed ? own : all;
+        const int e = max(static_cast<int>(top >> 7) - 127, -100);
         const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);  // 2^(14 - e)
         // (never 0 or Inf, which a score of 0 or a masked one's Inf would turn into NaN)
-        auto down = [&](int x) { return fminf(fmaxf(ldexpf(a.qk_scale, x - 14), FLT_MIN), FLT_MAX); };
-        scale = mixed ? 1.f : down(all);
+        scale = fminf(fmaxf(ldexpf(a.qk_scale, e - 14), FLT_MIN), FLT_MAX);
         auto two = [&](uint32_t v) { return pack_half2(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xffff0000u) * up); };
-        const int qrow = KP == 2 ? t : col;
-        const uint32_t base = q_at + (KP == 2 ? sub * C::kQRows * 256 : 0) + qrow * 128;
+        const uint32_t base = q_at + row * 128;
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
-          const int p = part * kPieces + i;  // of 16: 8 in each half of the channels
-          st_shared_v4(base + (p >> 3) * C::kQRows * 128 + (((p & 7) ^ (qrow & 7)) << 4), two(x[i].x), two(x[i].y), two(x[i].z),
-                       two(x[i].w));
-        }
-        if (part == 0) {
-          sm.ref[col] = live ? FLT_MAX : 0.f;
-          sm.fac[col] = down(own);
-          sm.lim[col] = !live ? 0 : a.causal ? max(0, w.Lk - w.Lq + tok0 + t + 1) : w.Lk;
+          const int p = wg * kPieces + i;  // of 16: 8 in each 64 channels
+          const uint4 x = live ? *(src + p) : make_uint4(0, 0, 0, 0);
+          const uint32_t at = base + (p >> 3) * kHalf + (((p & 7) ^ (row & 7)) << 4);
+          const uint32_t mine = KP == 2 ? sub * 2 * kHalf : 0;
+          st_shared_v4(at + mine, two(x.x), two(x.y), two(x.z), two(x.w));
+          if (KP == 2) st_shared_v4(at + (2 * kHalf - mine), 0u, 0u, 0u, 0u);  // the other map's channels
         }
         if (tid == 0) sm.seg = seg;
         fence_proxy_async_smem();
-        named_barrier_sync(1, kSoftmaxWarps * 32);
-        if (tid == 0) sm.exp_max = INT_MIN, sm.exp_min = INT_MAX;
+        named_barrier_sync(1, kAll);
         if (lane == 0) mbar_arrive(bar(sm.q_full));
       }
-      uint64_t l2[NC / 2];
-#pragma unroll
-      for (int i = 0; i < NC / 2; ++i) l2[i] = 0;
-      const uint64_t scale2 = f2pack(scale, scale);
+      // keys that the row sees (none where there is no such token)
+      const int lim = row >= rows ? 0 : a.causal ? max(0, w.Lk - w.Lq + tok0 + row / per + 1) : w.Lk;
+      const bool busy = quarter * 32 < rows;  // the warp has rows in use
+      const int edge = __reduce_min_sync(0xffffffffu, row < rows ? lim : INT_MAX);
+      float m = -FLT_MAX, l = 0.f;
 
       for (int i = 0; i < seg; ++i, ++j) {
+        if (kStreams == 2 && (j & 1) != wg) continue;
         const int key0 = (w.tile + i) * kTile;
-        const uint32_t p_at = p_slots + (j & 1) * R * 256 + (R == 128 ? wg * kHalf : 0) + key * 128;
-#pragma unroll
-        for (int h = 0; h < NH; ++h) {
-          const int c0 = col0 + 32 * h;
-          float4 ref[8];
-#pragma unroll
-          for (int x = 0; x < 8; ++x) ref[x] = *reinterpret_cast<const float4*>(&sm.ref[c0 + 4 * x]);
-          if (h == 0) {
-            ok = ok && mbar_wait(bar(sm.s_full[j & 1]), (j >> 1) & 1, abrt);
-            __syncwarp();
-            tc_fence_after();
-          }
-          float e[32];
-          auto load = [&]() {
+        ok = ok && mbar_wait(bar(sm.s_full[j & 1]), (j >> 1) & 1, abrt);
+        __syncwarp();
+        tc_fence_after();
+        if (busy) {
+          const uint32_t s_at = tmem + lanes + (j & 1) * kTile;
+          const bool cut = key0 + kTile > edge;
+          auto load = [&](float (&e)[32], int c) {
             uint32_t raw[32];
-            tmem_ld32(tmem + lanes + (j & 1) * R + c0, raw);
+            tmem_ld32(s_at + c, raw);
             tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < 32; ++c) e[c] = __uint_as_float(raw[c]);
-            if (mixed) {
+            for (int x = 0; x < 32; ++x) e[x] = __uint_as_float(raw[x]);
+            if (cut) {
 #pragma unroll
-              for (int c = 0; c < 32; ++c) e[c] *= sm.fac[c0 + c];
+              for (int x = 0; x < 32; ++x)
+                if (key0 + c + x >= lim) e[x] = -INFINITY;
             }
+            __syncwarp();
           };
-          auto mask = [&]() {
-#pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (key0 + key >= sm.lim[c0 + c]) e[c] = -INFINITY;
-          };
-          for (bool moved = false;; moved = true) {  // exponents s c - m; once more where a column needs a new reference
-            load();
-            float top0 = -INFINITY, top1 = -INFINITY;
-#pragma unroll
-            for (int x = 0; x < 8; ++x) {
-              f2unpack(f2fma(f2pack(e[4 * x], e[4 * x + 1]), scale2, f2pack(ref[x].x, ref[x].y)), e[4 * x], e[4 * x + 1]);
-              f2unpack(f2fma(f2pack(e[4 * x + 2], e[4 * x + 3]), scale2, f2pack(ref[x].z, ref[x].w)), e[4 * x + 2], e[4 * x + 3]);
-            }
-            if (key0 + kTile > edge) mask();
-#pragma unroll
-            for (int c = 0; c < 32; c += 4) {
-              top0 = fmax3(top0, e[c], e[c + 1]);
-              top1 = fmax3(top1, e[c + 2], e[c + 3]);
-            }
-            if (__builtin_expect(!barrier_any(2 + wg, 128, fmaxf(top0, top1) > kMoveRef) || moved, 1)) break;
-            // New references. The columns' largest y = s c over the tile's keys:
-            load();
-#pragma unroll
-            for (int c = 0; c < 32; ++c) e[c] *= scale;
-            if (key0 + kTile > edge) mask();
-            int mine = INT_MIN;
-#pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              const int v = __reduce_max_sync(0xffffffffu, ordered(e[c]));
-              if (lane == c) mine = v;
-            }
-            atomicMax(&sm.top[c0 + lane], mine);
-            named_barrier_sync(2 + wg, 128);
-            if (wtid < 32) {
-              const float old = -sm.ref[c0 + wtid], to = fmaxf(old, __fsub_ru(unordered(sm.top[c0 + wtid]), kPScale));
-              sm.ref[c0 + wtid] = -to;
-              sm.top[c0 + wtid] = __float_as_int(ex2_approx(old - to));
-            }
-            named_barrier_sync(2 + wg, 128);
-#pragma unroll
-            for (int x = 0; x < 8; ++x) ref[x] = *reinterpret_cast<const float4*>(&sm.ref[c0 + 4 * x]);
-#pragma unroll
-            for (int c = 0; c < 16; ++c) {
-              const uint64_t f = f2pack(__int_as_float(sm.top[c0 + 2 * c]), __int_as_float(sm.top[c0 + 2 * c + 1]));
-              l2[16 * h + c] = f2fma(l2[16 * h + c], f, 0ull);
-            }
-            if (i > 0) {  // O holds the tiles before this one
-              ok = ok && mbar_wait(bar(sm.pv_done[(j - 1) & 1]), ((j - 1) >> 1) & 1, abrt);
-              __syncwarp();
-              tc_fence_after();
+          float top = -INFINITY;
 #pragma unroll 1
-              for (int p = 0; p < KP; ++p) {
-                const uint32_t at = tmem + lanes + C::kO + p * R + c0;
+          for (int c = 0; c < kTile; c += 32) {
+            float e[32], t1 = -INFINITY;
+            load(e, c);
+#pragma unroll
+            for (int x = 0; x < 32; x += 4) {
+              top = fmax3(top, e[x], e[x + 1]);
+              t1 = fmax3(t1, e[x + 2], e[x + 3]);
+            }
+            top = fmaxf(top, t1);
+          }
+          top *= scale;
+          const bool move = top - m > kMoveRef;
+          if (__any_sync(0xffffffffu, move)) {
+            const float to = move ? fmaxf(m, __fsub_ru(top, kPScale)) : m, f = ex2_approx(m - to);
+            m = to;
+            l *= f;
+            if (i >= kStreams) {  // O holds earlier tiles (V2: S of this one came behind their product)
+              if (kStreams == 1) {
+                ok = ok && mbar_wait(bar(sm.pv_done[(j - 1) & 1]), ((j - 1) >> 1) & 1, abrt);
+                __syncwarp();
+                tc_fence_after();
+              }
+#pragma unroll 1
+              for (int c = 0; c < C::kWidth; c += 32) {
+                const uint32_t at = tmem + lanes + C::kO + wg * 128 + c;
                 uint32_t o[32];
                 tmem_ld32(at, o);
                 tmem_wait_ld();
 #pragma unroll
-                for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * __int_as_float(sm.top[c0 + x]));
+                for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
                 tmem_st32(at, o);
               }
-              tmem_wait_st();
             }
-            named_barrier_sync(2 + wg, 128);
-            if (wtid < 32) sm.top[c0 + wtid] = INT_MIN;
           }
+          const uint64_t scale2 = f2pack(scale, scale), ref2 = f2pack(-m, -m);
+          uint64_t sum = f2pack(0.f, 0.f);
+#pragma unroll 1
+          for (int c = 0; c < kTile; c += 32) {
+            float e[32];
+            load(e, c);
+            uint32_t pk[16];
 #pragma unroll
-          for (int c = 0; c < 32; c += 8) {
-            uint32_t pk[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const float p0 = ex2_approx(e[c + 2 * x]), p1 = ex2_approx(e[c + 2 * x + 1]);
-              l2[16 * h + c / 2 + x] = f2add(l2[16 * h + c / 2 + x], f2pack(p0, p1));
+            for (int x = 0; x < 16; ++x) {
+              float e0, e1;
+              f2unpack(f2fma(f2pack(e[2 * x], e[2 * x + 1]), scale2, ref2), e0, e1);
+              const float p0 = ex2_approx(e0), p1 = ex2_approx(e1);
+              sum = f2add(sum, f2pack(p0, p1));
               pk[x] = pack_half2(p0, p1);
             }
-            const int piece = 4 * (R == 64 ? wg : h) + c / 8;
-            st_shared_v4(p_at + ((piece ^ (key & 7)) << 4), pk[0], pk[1], pk[2], pk[3]);
+            tmem_st16(s_at + c / 2, pk);
           }
+          float l0, l1;
+          f2unpack(sum, l0, l1);
+          l += l0 + l1;
+          tmem_wait_st();
         }
-        fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(sm.p_full[j & 1]));
       }
 
       // ---- the unit's end ----
+      if (kStreams == 2 && seg > 1) ok = ok && mbar_wait(bar(sm.pv_done[(j - 2) & 1]), ((j - 2) >> 1) & 1, abrt);
       ok = ok && mbar_wait(bar(sm.pv_done[(j - 1) & 1]), ((j - 1) >> 1) & 1, abrt);
       __syncwarp();
       tc_fence_after();
-      // Q's place is free: all scores are done
-      float* s_part = reinterpret_cast<float*>(s_q);         // [8 warps][64]
-      float* s_fac = s_part + 8 * 64;                        // [R]
-      float* s_norm = s_fac + 128;                           // [8 warps][32], then [64]
-      {
-        float l[NC];
-#pragma unroll
-        for (int c = 0; c < NC / 2; ++c) f2unpack(l2[c], l[2 * c], l[2 * c + 1]);
-        int at = 0;
-#pragma unroll
-        for (int d = 16, n = NC / 2; d >= 1; d >>= 1, n >>= 1) {  // halves of the columns to halves of the lanes
-          const bool up = lane & d;
-          at += up ? n : 0;
-#pragma unroll
-          for (int c = 0; c < n; ++c) {
-            const float give = up ? l[c] : l[c + n], keep = up ? l[c + n] : l[c];
-            l[c] = keep + __shfl_xor_sync(0xffffffffu, give, d);
-          }
-        }
-#pragma unroll
-        for (int c = 0; c < NC / 32; ++c) s_part[warp * 64 + at + c] = l[c];
+      float w0 = 1.f, w1 = 0.f;  // what the streams' O are to be multiplied with
+      if constexpr (kStreams == 2) {
+        float2* ml = reinterpret_cast<float2*>(s_q);  // (Q's place is free: all scores are done)
+        ml[wg * kRows + row] = make_float2(m, l);
+        named_barrier_sync(1, kAll);
+        const float2 a0 = ml[row], a1 = ml[kRows + row];
+        const float m0 = a0.x, m1 = a1.x;
+        m = fmaxf(m0, m1);
+        w0 = ex2_approx(m0 - m), w1 = ex2_approx(m1 - m);
+        l = fmaf(a0.y, w0, a1.y * w1);
       }
-      named_barrier_sync(1, kSoftmaxWarps * 32);
-      float* rec = a.pieces + static_cast<size_t>(2 * blockIdx.x + (starts ? 1 : 0)) * C::kPiece;
-      if (tid < R) {
-        const int g = tid / NC, c = tid % NC;
-        const float* p = s_part + g * 4 * 64 + c;
-        const float l = (p[0] + p[64]) + (p[128] + p[192]);
-        if (whole) {
-          const int t = KP == 2 ? tid % C::kQRows : tid / a.group;
-          float f = 0.f;
-          if (t < toks && sm.lim[tid] > 0) {
-            f = 1.f / l;
-            if constexpr (KP == 2) {
-              f *= tid < C::kQRows ? a.v_mul : *(a.lambda + w.h) * a.v_mul;
-            } else {
-              const int sub = tid - t * a.group;
-              f *= a.v_mul;
-              if (sub & 1)
-                f *= 1.f / (1.f + __expf(-*(a.lam_logit + static_cast<size_t>(w.q0 + tok0 + t) * (a.H * a.group / 2) +
-                                            (w.h * a.group + sub) / 2)));
-            }
-          }
-          s_fac[tid] = f;
-        } else {
-          rec[tid] = -sm.ref[tid];
-          rec[R + tid] = l;
-        }
-      }
-      named_barrier_sync(1, kSoftmaxWarps * 32);
-      int* nan = sm.nan_key[unit & (kNanSets - 1)];
-      // channel `key` of each plane, and the first key whose value there is NaN
-      int bad[KP];
-#pragma unroll
-      for (int p = 0; p < KP; ++p) bad[p] = nan[p * 8 + (key >> 4)];
-      const float kNan = __int_as_float(0x7fffffff);
+      // (an O that no tile of this unit went to is left out)
+      const bool use0 = kStreams == 1 || seg > 1 || ((j - 1) & 1) == 0, use1 = kStreams == 2 && (seg > 1 || ((j - 1) & 1) == 1);
+      const int* nan = sm.nan_key[unit & (kNanSets - 1)];
       const uint32_t o_at = tmem + lanes + C::kO;
-      if (!whole) {
-        const int cols = KP == 2 ? R : toks * a.group;
-#pragma unroll 1
-        for (int c = 0; c < KP * NC; c += 32) {
-          const int p = c / NC, col = col0 + c % NC;
-          uint32_t o[32];
-          tmem_ld32(o_at + p * R + col, o);
+      const float kNan = __int_as_float(0x7fffffff);
+      auto load_o = [&](float (&y)[32], int c, float f) {  // channels c .. c + 31
+        uint32_t o[32];
+        if (use0) {
+          tmem_ld32(o_at + c, o);
           tmem_wait_ld();
-          const int first_bad = KP == 2 && p == 1 ? bad[KP - 1] : bad[0];
+#pragma unroll
+          for (int x = 0; x < 32; ++x) y[x] = __uint_as_float(o[x]) * (w0 * f);
+        } else {
+#pragma unroll
+          for (int x = 0; x < 32; ++x) y[x] = 0.f;
+        }
+        if (use1) {
+          tmem_ld32(o_at + 128 + c, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int x = 0; x < 32; ++x) y[x] = fmaf(__uint_as_float(o[x]), w1 * f, y[x]);
+        }
+        const bool bad0 = nan[c >> 4] < lim, bad1 = nan[(c >> 4) + 1] < lim;
+        if (__any_sync(0xffffffffu, bad0 || bad1)) {
 #pragma unroll
           for (int x = 0; x < 32; ++x)
-            if (col + x < cols && (KP == 1 || (col + x) % C::kQRows < toks))
-              rec[2 * R + static_cast<size_t>(col + x) * C::kWidth + p * 128 + key] =
-                  first_bad < sm.lim[col + x] ? kNan : __uint_as_float(o[x]);
+            if (x < 16 ? bad0 : bad1) y[x] = kNan;
         }
-      } else if constexpr (KP == 1) {
-        const int pairs = a.H * a.group / 2;
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + static_cast<size_t>(w.q0 + tok0) * pairs * 128 + key;
+      };
+      if (!busy) {
+      } else if (!whole) {
+        // a piece: m, l, and o by fours of channels, so that a warp's stores lie side by side
+        float* rec = a.pieces + static_cast<size_t>(2 * blockIdx.x + (starts ? 1 : 0)) * C::kPiece;
+        if (wg == 0) rec[row] = m, rec[kRows + row] = l;
 #pragma unroll 1
-        for (int c = 0; c < NC; c += 32) {
-          uint32_t o[32];
-          tmem_ld32(o_at + col0 + c, o);
-          tmem_wait_ld();
-          if ((col0 + c) / a.group >= toks) continue;
+        for (int c = wg * 32; c < C::kWidth; c += 32 * kStreams) {
+          float y[32];
+          load_o(y, c, 1.f);
 #pragma unroll
-          for (int x = 0; x < 32; x += 2) {
-            const int col = col0 + c + x, t = col / a.group, sub = col - t * a.group;
-            float y = __uint_as_float(o[x]) * s_fac[col] - __uint_as_float(o[x + 1]) * s_fac[col + 1];
-            if (bad[0] < sm.lim[col]) y = kNan;
-            if (sm.lim[col] <= 0) y = 0.f;
-            if (t < toks && dbg_index_ok(w.q0 + tok0 + t, a.total))
-              out[(static_cast<size_t>(t) * pairs + (w.h * a.group + sub) / 2) * 128] = __float2bfloat16_rn(y);
-          }
+          for (int x = 0; x < 32; x += 4)
+            *reinterpret_cast<float4*>(rec + 2 * kRows + ((c + x) / 4 * kRows + row) * 4) = make_float4(y[x], y[x + 1], y[x + 2], y[x + 3]);
         }
       } else {
-        constexpr int T = C::kQRows, TN = 16;  // the warpgroup's tokens, 16 at a time
-        float wgt[2] = {1.f, 1.f};
-        if ((a.flags & 2) && a.norm_w) wgt[0] = *(a.norm_w + key), wgt[1] = *(a.norm_w + 128 + key);
-        const float f = (a.flags & 4) ? 1.f - a.lambda_init : 1.f;
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + (static_cast<size_t>(w.q0 + tok0) * a.H + w.h) * 256 + key;
-#pragma unroll 1
-        for (int t0 = wg * (T / 2); t0 < (wg + 1) * (T / 2); t0 += TN) {
-          float y[2][TN];
-#pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            uint32_t o1[TN], o2[TN];
-            tmem_ld16(o_at + p * R + t0, o1);
-            tmem_ld16(o_at + p * R + T + t0, o2);
-            tmem_wait_ld();
-#pragma unroll
-            for (int t = 0; t < TN; ++t) {
-              const float v = __uint_as_float(o1[t]) * s_fac[t0 + t] - __uint_as_float(o2[t]) * s_fac[T + t0 + t];
-              y[p][t] = bad[p] < sm.lim[t0 + t] ? kNan : v;
-            }
+        // this row's share of its pair's output: f times o (the odd row with its lambda, negative)
+        const int t = row / per, sub = row - t * per;
+        const size_t token = static_cast<size_t>(w.q0) + tok0 + t;
+        float f = 0.f;
+        if (lim > 0) {
+          f = a.v_mul / l;
+          if (row & 1) {
+            if constexpr (KP == 2) f *= -*(a.lambda + w.h);
+            else f *= -1.f / (1.f + __expf(-*(a.lam_logit + token * (a.H * per / 2) + (w.h * per + sub) / 2)));
           }
+        }
+        float g = 1.f;  // V1: the norm's factor and the scale
+        // 32 channels of the pair's output, 16 for each of its two lanes
+        auto pair = [&](float (&z)[16], int c) {
+          float y[32];
+          load_o(y, c, f);
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            const float give = row & 1 ? y[x] : y[x + 16], keep = row & 1 ? y[x + 16] : y[x];
+            z[x] = keep + __shfl_xor_sync(0xffffffffu, give, 1);
+          }
+        };
+        if (KP == 2) {
           if (a.flags & 2) {
-            float ss[TN];
+            float ss = 0.f;
+#pragma unroll 1
+            for (int c = 0; c < C::kWidth; c += 32) {
+              float z[16];
+              pair(z, c);
 #pragma unroll
-            for (int t = 0; t < TN; ++t) ss[t] = fmaf(y[0][t], y[0][t], y[1][t] * y[1][t]);
-            int at = 0;
-#pragma unroll
-            for (int d = 16, n = TN / 2; d >= 2; d >>= 1, n >>= 1) {
-              const bool up = lane & d;
-              at += up ? n : 0;
-#pragma unroll
-              for (int c = 0; c < n; ++c) {
-                const float give = up ? ss[c] : ss[c + n], keep = up ? ss[c + n] : ss[c];
-                ss[c] = keep + __shfl_xor_sync(0xffffffffu, give, d);
-              }
+              for (int x = 0; x < 16; ++x) ss = fmaf(z[x], z[x], ss);
             }
-            s_norm[warp * TN + at] = ss[0] + __shfl_xor_sync(0xffffffffu, ss[0], 1);
-            named_barrier_sync(2 + wg, 128);
-            if (wtid < TN) {
-              const float* q = s_norm + wg * 4 * TN + wtid;
-              const float sum = (q[0] + q[TN]) + (q[2 * TN] + q[3 * TN]);
-              s_part[t0 + wtid] = f / sqrtf(sum / 256.f + a.eps);
-            }
-            named_barrier_sync(2 + wg, 128);
+            ss += __shfl_xor_sync(0xffffffffu, ss, 1);
+            g = 1.f / sqrtf(ss / 256.f + a.eps);
           }
+          if (a.flags & 4) g *= 1.f - a.lambda_init;
+        }
+        const size_t at = KP == 2 ? (token * a.H + w.h) * 256 : (token * (a.H * per / 2) + (w.h * per + sub) / 2) * 128;
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + at + (row & 1) * 16;
+        const bool weights = KP == 2 && (a.flags & 2) && a.norm_w;
+        const bool store = row < rows && dbg_index_ok(static_cast<long long>(token), a.total);
+#pragma unroll 1
+        for (int c = wg * 32; c < C::kWidth; c += 32 * kStreams) {
+          float z[16];
+          pair(z, c);
+          uint32_t o[8];
 #pragma unroll
-          for (int t = 0; t < TN; ++t) {
-            if (t0 + t >= toks || !dbg_index_ok(w.q0 + tok0 + t0 + t, a.total)) continue;
-            const float n = (a.flags & 2) ? s_part[t0 + t] : f;
-            const bool none = sm.lim[t0 + t] <= 0;  // (zeros, whatever the weight and the scale hold)
-#pragma unroll
-            for (int p = 0; p < 2; ++p)
-              out[static_cast<size_t>(t0 + t) * a.H * 256 + p * 128] = __float2bfloat16_rn(none ? 0.f : y[p][t] * n * wgt[p]);
+          for (int x = 0; x < 16; x += 2) {
+            float y0 = z[x] * g, y1 = z[x + 1] * g;
+            if (weights) y0 *= *(a.norm_w + c + (row & 1) * 16 + x), y1 *= *(a.norm_w + c + (row & 1) * 16 + x + 1);
+            o[x / 2] = lim > 0 ? pack_bf16x2(y0, y1) : 0u;  // (zeros, whatever the weight and the scale hold)
+          }
+          if (store) {
+            *reinterpret_cast<uint4*>(out + c) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(out + c + 8) = make_uint4(o[4], o[5], o[6], o[7]);
           }
         }
       }
+      __syncwarp();
       tc_fence_before();
-      named_barrier_sync(1, kSoftmaxWarps * 32);
-      if (tid < 16) nan[tid] = INT_MAX;
+      named_barrier_sync(1, kAll);
+      if (tid < 16) sm.nan_key[unit & (kNanSets - 1)][tid] = INT_MAX;
       ++unit;
       advance(a, w, seg);
     }
@@ -1032,7 +857,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const Kv4ChunkAr
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == C::kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -1041,9 +866,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const Kv4ChunkAr
 // Joins, of each unit whose tiles lie in more than one range, its pieces: that of the range that begins it and
 // of the ranges that begin inside it, in this order. Block (i, y): the unit that range i + 1 begins inside,
 // if no earlier range does, and every gridDim.y-th of its tokens (V1) or pairs (V2) from y on; a thread a channel.
-template <int KP, int R>
+template <int KP>
 __global__ void __launch_bounds__(KP * 128) kv4_chunk_join_kernel(const Kv4ChunkArgs a) {
-  using C = Cfg<KP, R>;
+  using C = Cfg<KP>;
   constexpr int NT = KP * 128;
   __shared__ long long s_pre[NT + 1], s_sum[NT / 32], s_first;
   __shared__ Walk s_walk;
@@ -1075,14 +900,14 @@ __global__ void __launch_bounds__(KP * 128) kv4_chunk_join_kernel(const Kv4Chunk
   float wgt = 1.f;
   if (KP == 2 && (a.flags & 2) && a.norm_w) wgt = *(a.norm_w + tid);
   for (int o = blockIdx.y; o < outs; o += gridDim.y) {
-    const int c[2] = {KP == 2 ? o : 2 * o, KP == 2 ? C::kQRows + o : 2 * o + 1};
+    const int c[2] = {2 * o, 2 * o + 1};  // its rows
     float m[2] = {-FLT_MAX, -FLT_MAX}, l[2] = {0.f, 0.f}, v[2] = {0.f, 0.f};
 #pragma unroll 4
     for (int k = 0; k < pieces; ++k) {
       const float* r = a.pieces + static_cast<size_t>(2 * (i0 + k) + (k == 0 ? 1 : 0)) * C::kPiece;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float mk = r[c[e]], lk = r[R + c[e]], vk = r[2 * R + static_cast<size_t>(c[e]) * C::kWidth + tid];
+        const float mk = r[c[e]], lk = r[kRows + c[e]], vk = r[2 * kRows + (tid / 4 * kRows + c[e]) * 4 + tid % 4];
         const float top = fmaxf(m[e], mk), f = ex2_approx(m[e] - top), fk = ex2_approx(mk - top);
         m[e] = top;
         l[e] = l[e] * f + lk * fk;
@@ -1117,47 +942,40 @@ __global__ void __launch_bounds__(KP * 128) kv4_chunk_join_kernel(const Kv4Chunk
   }
 }
 
-template <int KP, int R>
+template <int KP>
 cudaError_t launch(Kv4ChunkArgs a, cudaStream_t st) {
   static std::atomic<uint64_t> raised{};
-  a.tokens = KP == 2 ? R / 2 : R / a.group;
+  a.tokens = kRows / (KP == 2 ? 2 : a.group);
   page_magic(a.page_size >> 4, &a.rec_magic, &a.rec_shift);
   // no more blocks than the tables' capacity can give ranges: a sequence's tiles of tokens overlap the total's
   const long long tiles = (static_cast<long long>(a.max_pages) * a.page_size + kTile - 1) / kTile;
   const long long units = (static_cast<long long>(a.total) / a.tokens + a.B) * a.H;
   const long long most = units >= kSms ? kSms : (tiles + kUnitCost) * units / kMinCost;
   a.grid = static_cast<int>(most < 1 ? 1 : most > kSms ? kSms : most);
-  cudaError_t e = launch_early_large(kv4_chunk_kernel<KP, R>, a.grid, kThreads, smem_bytes<KP, R>(), smem_bytes<KP, R>(), st, 1, a, raised);
+  cudaError_t e = launch_early_large(kv4_chunk_kernel<KP>, a.grid, Cfg<KP>::kThreads, smem_bytes<KP>(), smem_bytes<KP>(), st, 1, a, raised);
   if (e != cudaSuccess || a.grid == 1) return e;
   g_launched.store(true, std::memory_order_relaxed);
   cudaLaunchAttribute at[1] = {};
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(a.grid - 1, R / 16);
+  cfg.gridDim = dim3(a.grid - 1, kRows / 16);
   cfg.blockDim = dim3(KP * 128);
   cfg.stream = st;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv4_chunk_join_kernel<KP, R>, a);
+  return cudaLaunchKernelEx(&cfg, kv4_chunk_join_kernel<KP>, a);
 }
 
 }  // namespace
 
-// Columns of a unit. V2: 64 where the longest chunk fits in them, which halves a tile's products and softmax.
-// V1: 64, as tensor memory holds both planes of O.
-int kv4_chunk_cols(int group, int max_seqlen_q) {
-  return group == 0 || static_cast<long long>(max_seqlen_q) * group <= 64 ? 64 : 128;
-}
-size_t kv4_chunk_workspace_bytes(int group, int max_seqlen_q) {
-  const size_t cols = kv4_chunk_cols(group, max_seqlen_q), width = group == 0 ? 256 : 128;
-  return 2 * static_cast<size_t>(kSms) * (2 * cols + cols * width) * sizeof(float);
+size_t kv4_chunk_workspace_bytes(int group) {
+  return 2 * static_cast<size_t>(kSms) * (group == 0 ? Cfg<2>::kPiece : Cfg<1>::kPiece) * sizeof(float);
 }
 
-cudaError_t launch_kv4_chunk(const Kv4ChunkArgs& a, int cols, cudaStream_t st) {
+cudaError_t launch_kv4_chunk(const Kv4ChunkArgs& a, cudaStream_t st) {
   if (a.total == 0) return cudaSuccess;
-  if (a.group == 0) return launch<2, 64>(a, st);
-  return cols == 64 ? launch<1, 64>(a, st) : launch<1, 128>(a, st);
+  return a.group == 0 ? launch<2>(a, st) : launch<1>(a, st);
 }
 
 cudaError_t status_chunk_kv4(int* v) { return launched_status(v); }

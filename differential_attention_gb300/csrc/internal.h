@@ -363,9 +363,8 @@ struct Kv4ChunkArgs {
   int tokens, grid;        // tokens of a unit, ranges: set by the launcher
   uint32_t rec_magic, rec_shift;  // j / (page_size / 16), as in V2DecodeArgs' page_magic; the launcher's
 };
-int kv4_chunk_cols(int group, int max_seqlen_q);
-size_t kv4_chunk_workspace_bytes(int group, int max_seqlen_q);
-cudaError_t launch_kv4_chunk(const Kv4ChunkArgs& a, int cols, cudaStream_t s);
+size_t kv4_chunk_workspace_bytes(int group);
+cudaError_t launch_kv4_chunk(const Kv4ChunkArgs& a, cudaStream_t s);
 cudaError_t status_chunk_kv4(int* v);
 
 // Rotary positions (rope.cu).
