@@ -39,7 +39,7 @@ constexpr int kRows = 128;
 constexpr int kTile = 128;                       // keys
 constexpr int kSlot = kTile * 128 * 2;           // one plane of a tile in fp16
 constexpr int kHalf = kSlot / 2;                 // 64 of its channels
-constexpr int kUnitCost = 3;                     // what a unit costs besides its tiles, in tiles
+constexpr int kUnitCost = 5;                     // what a unit costs besides its tiles, in tiles
 constexpr int kMinCost = 2;                      // the smallest range
 constexpr float kPScale = 6.f, kMoveRef = 15.f;  // log2 of P's scale, and of the P at which the reference moves
 constexpr int kNanSets = 8;
@@ -69,6 +69,7 @@ struct TileAt {
   int key0, left, unit, pad;  // its first key, keys from there on (0: the stream has ended), its unit's number
 };
 struct Small {  // behind Q
+  float scale[kRows];  // what the rows' S is to be multiplied with
   uint64_t full[6], free[6], s_full[2], p_full[2], pv_done[2], q_full, teardown;
   uint64_t tile_full[kRing], tile_free[kRing];
   TileAt tile[kRing];
@@ -598,34 +599,36 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, 1) kv4_chunk_kernel(const K
       const bool starts = w.tile == 0, whole = starts && seg == w.tiles;
       const int tok0 = w.rt * a.tokens, toks = min(a.tokens, w.Lq - tok0);  // tokens of the unit
       const int per = KP == 2 ? 2 : a.group, rows = toks * per;            // rows of a token, rows in use
-      // Q: kStreams threads for a row, each 128 / kStreams of its channels
-      float scale;  // what the row's S is to be multiplied with
+      // Q: a half-warp a row, two rows at a time
       {
-        constexpr int kPieces = 16 / kStreams;  // of 16 bytes, for a thread
-        const int t = row / per, sub = row - t * per;
-        const bool live = row < rows;
-        const size_t from = (static_cast<size_t>(w.q0 + tok0 + t) * a.H + w.h) * per + sub;
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + from * 128);
-        uint32_t top = 0;  // the largest magnitude's bits (ordered as the values are)
+        constexpr int kWarps = 4 * kStreams, kRounds = kRows / 2 / kWarps;
+        const int part = lane & 15;  // of 16 bytes: 8 in each 64 channels
+        uint4 x[kRounds];
+        auto row_of = [&](int i) { return (i * kWarps + warp) * 2 + (lane >> 4); };
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const uint4 x = live ? *(src + i) : make_uint4(0, 0, 0, 0);
-          const uint32_t m2 = __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu), __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
-          top = max(top, max(m2 & 0xffffu, m2 >> 16));
+        for (int i = 0; i < kRounds; ++i) {
+          const int r = row_of(i), t = r / per, sub = r - t * per;
+          const size_t from = (static_cast<size_t>(w.q0 + tok0 + t) * a.H + w.h) * per + sub;
+          x[i] = r < rows ? *(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + from * 128) + part)
+                          : make_uint4(0, 0, 0, 0);
         }
-        const int e = max(static_cast<int>(top >> 7) - 127, -100);
-        const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);  // 2^(14 - e)
-        // (never 0 or Inf, which a score of 0 or a masked one's Inf would turn into NaN)
-        scale = fminf(fmaxf(ldexpf(a.qk_scale, e - 14), FLT_MIN), FLT_MAX);
-        auto two = [&](uint32_t v) { return pack_half2(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xffff0000u) * up); };
-        const uint32_t base = q_at + row * 128;
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-          const int p = wg * kPieces + i;  // of 16: 8 in each 64 channels
-          const uint4 x = live ? *(src + p) : make_uint4(0, 0, 0, 0);
-          const uint32_t at = base + (p >> 3) * kHalf + (((p & 7) ^ (row & 7)) << 4);
-          const uint32_t mine = KP == 2 ? sub * 2 * kHalf : 0;
-          st_shared_v4(at + mine, two(x.x), two(x.y), two(x.z), two(x.w));
+        for (int i = 0; i < kRounds; ++i) {
+          const int r = row_of(i);
+          const uint32_t m2 = __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
+                                       __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu));
+          uint32_t top = max(m2 & 0xffffu, m2 >> 16);  // the largest magnitude's bits (ordered as the values are)
+#pragma unroll
+          for (int d = 1; d < 16; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+          const int e = max(static_cast<int>(top >> 7) - 127, -100);
+          const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);  // 2^(14 - e)
+          // what the row's S is to be multiplied with (never 0 or Inf, which a score of 0 or a masked one's Inf
+          // would turn into NaN)
+          if (part == 0) sm.scale[r] = fminf(fmaxf(ldexpf(a.qk_scale, e - 14), FLT_MIN), FLT_MAX);
+          auto two = [&](uint32_t v) { return pack_half2(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xffff0000u) * up); };
+          const uint32_t at = q_at + r * 128 + (part >> 3) * kHalf + (((part & 7) ^ (r & 7)) << 4);
+          const uint32_t mine = KP == 2 ? (r & 1) * 2 * kHalf : 0;
+          st_shared_v4(at + mine, two(x[i].x), two(x[i].y), two(x[i].z), two(x[i].w));
           if (KP == 2) st_shared_v4(at + (2 * kHalf - mine), 0u, 0u, 0u, 0u);  // the other map's channels
         }
         if (tid == 0) sm.seg = seg;
@@ -633,6 +636,7 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, 1) kv4_chunk_kernel(const K
         named_barrier_sync(1, kAll);
         if (lane == 0) mbar_arrive(bar(sm.q_full));
       }
+      const float scale = sm.scale[row];
       // keys that the row sees (none where there is no such token)
       const int lim = row >= rows ? 0 : a.causal ? max(0, w.Lk - w.Lq + tok0 + row / per + 1) : w.Lk;
       const bool busy = quarter * 32 < rows;  // the warp has rows in use
