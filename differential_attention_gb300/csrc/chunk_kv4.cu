@@ -48,7 +48,9 @@ constexpr int kRing = 4;                         // tiles whose records' address
 template <int KP>
 struct Cfg {
   static constexpr int kStreams = KP == 1 ? 2 : 1;  // softmax warpgroups
-  static constexpr int kKWarp = 4 * kStreams, kVWarp = kKWarp + 4, kMmaWarp = kVWarp + 4, kAddressWarp = kMmaWarp + 1;
+  static constexpr int kRecs = KP == 1 ? 2 : 1, kUnpackWarps = 8 / kRecs;  // K's, and V's: records of a plane for each
+  static constexpr int kKWarp = 4 * kStreams, kVWarp = kKWarp + kUnpackWarps, kMmaWarp = kVWarp + kUnpackWarps;
+  static constexpr int kAddressWarp = kMmaWarp + 1;
   static constexpr int kThreads = (kMmaWarp + 4) * 32;
   static constexpr int kWidth = KP * 128;
   static constexpr int kSlots = KP == 1 ? 6 : 5;    // the ring of planes: of each tile K's, then V's
@@ -56,11 +58,12 @@ struct Cfg {
   static constexpr int kSmall = kQ + kRows * kWidth * 2;
   static constexpr int kO = 2 * kTile;              // tensor memory: S (P in its place) twice, O of each stream
   static constexpr int kPiece = 2 * kRows + kRows * kWidth;  // floats: m, l, o
-  // Registers a thread: the launch's (96 or 128) dealt out anew to the warpgroups
-  static constexpr int kLaunchRegs = KP == 1 ? 96 : 128;
-  static constexpr int kSoftmaxRegs = KP == 1 ? 128 : 168, kUnpackRegs = KP == 1 ? 88 : 120, kRestRegs = KP == 1 ? 48 : 64;
+  // Registers a thread: the launch's (96 or 80) dealt out anew to the warpgroups
+  static constexpr int kLaunchRegs = KP == 1 ? 96 : 80;
+  static constexpr int kSoftmaxRegs = KP == 1 ? 128 : 152, kUnpackRegs = KP == 1 ? 88 : 64, kRestRegs = KP == 1 ? 48 : 64;
   static_assert(kSoftmaxRegs >= kLaunchRegs && kUnpackRegs <= kLaunchRegs && kRestRegs <= kLaunchRegs, "raised and lowered");
-  static_assert(kStreams * kSoftmaxRegs + 2 * kUnpackRegs + kRestRegs <= (kThreads / 128) * kLaunchRegs, "more registers than the launch has");
+  static_assert(kStreams * kSoftmaxRegs + kUnpackWarps / 2 * kUnpackRegs + kRestRegs <= (kThreads / 128) * kLaunchRegs, "more registers than the launch has");
+  static_assert(kThreads <= 768, "Scan");
   static_assert(kO + kStreams * kWidth <= 512, "tensor memory");
 };
 
@@ -83,7 +86,7 @@ struct Walk {  // place in the walk over units: sequences, heads, tiles of token
   int tile, tiles;
   long long todo;  // tiles of the range, and the costs of the units that begin in it, from here on
 };
-constexpr int kMaxThreads = 640;
+constexpr int kMaxThreads = 768;
 struct Scan {  // at startup, in Q's place
   long long pre[kMaxThreads + 1], sum[kMaxThreads / 32];
   Walk walk;
@@ -285,13 +288,14 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int a_mn, int b_m
   return umma_idesc_bf16(M, N, a_mn, b_mn) & ~((1u << 7) | (1u << 10));
 }
 
-// where plane p of the block's tile j lies, and the phase of its slot's use
+// Where plane p of the block's tile j lies in the ring (0 .. KP - 1: K's, then V's), and the phase of its slot's
+// use. The ring's order is K(0), K(1), V(0), K(2), V(1), ..: V is needed a softmax later than K.
 struct Place {
   int slot, phase;
 };
 template <int KP>
 __device__ __forceinline__ Place place(int j, int p) {
-  const uint32_t n = static_cast<uint32_t>(j) * (2 * KP) + p, use = n / Cfg<KP>::kSlots;
+  const uint32_t n = p >= KP ? 2 * KP * j + KP + p : j == 0 ? p : 2 * KP * j - KP + p, use = n / Cfg<KP>::kSlots;
   return {static_cast<int>(n - use * Cfg<KP>::kSlots), static_cast<int>(use & 1)};
 }
 
@@ -308,7 +312,7 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, 1) kv4_chunk_kernel(const K
 
   if (tid == 0) {
     for (int i = 0; i < 6; ++i) {
-      mbar_init(bar(sm.full[i]), 4);
+      mbar_init(bar(sm.full[i]), C::kUnpackWarps);
       mbar_init(bar(sm.free[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -318,7 +322,7 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, 1) kv4_chunk_kernel(const K
     }
     for (int i = 0; i < kRing; ++i) {
       mbar_init(bar(sm.tile_full[i]), 1);
-      mbar_init(bar(sm.tile_free[i]), 8);
+      mbar_init(bar(sm.tile_free[i]), 2 * C::kUnpackWarps);
     }
     mbar_init(bar(sm.q_full), 4 * kStreams);
     mbar_init(bar(sm.teardown), 1);
@@ -464,29 +468,32 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, 1) kv4_chunk_kernel(const K
   } else if (warp >= C::kKWarp) {
     // ================================ unpack ================================
     // A tile's bytes are loaded into registers before the tile before it is waited for (also where the
-    // sequence has no such record, from page 0: no branch comes between loads in flight). Warp q4 of K's or
-    // V's four takes records q4 and q4 + 4 of each plane. A piece of 8 channels lies at its number XOR the
+    // sequence has no such record, from page 0: no branch comes between loads in flight). Warp q of K's or
+    // V's takes record q (V2: and q + 4) of each plane. A piece of 8 channels lies at its number XOR the
     // row's; lanes of a quarter-warp whose places would meet in the banks (t4 of 0 and 2, 1 and 3) take their
     // pieces in another order.
     registers_down<C::kUnpackRegs>();
-    const int q4 = warp & 3, t4 = lane & 3, hi8 = lane >> 2;
-    const bool far = t4 & 2, is_k = warp < C::kVWarp;
+    constexpr int kRecs = C::kRecs;
+    const bool is_k = warp < C::kVWarp;
+    const int q = warp - (is_k ? C::kKWarp : C::kVWarp), t4 = lane & 3, hi8 = lane >> 2;
+    const bool far = t4 & 2;
     struct Tile {
       int key0, left, unit;
     };
     struct Data {
-      uint4 lo[2], hi[2];
-      uint32_t sc[2];
+      uint4 lo[kRecs], hi[kRecs];
+      uint32_t sc[kRecs];
     };
     Data d[KP];
     Tile next{}, tile;
-    const uint8_t* src[2] = {nullptr, nullptr};
+    const uint8_t* src[kRecs] = {};
     int loaded = 0;
     bool ok = true;
     auto fetch = [&]() {  // the next tile's addresses; behind the stream's end they stay
       ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(sm.tile_full[loaded % kRing]), (loaded / kRing) & 1, abrt));
       const TileAt& at = sm.tile[loaded % kRing];
-      src[0] = at.rec[q4] + (is_k ? 0 : KP * kKv4Plane), src[1] = at.rec[q4 + 4] + (is_k ? 0 : KP * kKv4Plane);
+#pragma unroll
+      for (int x = 0; x < kRecs; ++x) src[x] = at.rec[q + 4 * x] + (is_k ? 0 : KP * kKv4Plane);
       next.key0 = at.key0, next.left = ok ? at.left : 0, next.unit = at.unit;
       __syncwarp();
       if (next.left > 0) {
@@ -496,7 +503,7 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, 1) kv4_chunk_kernel(const K
     };
     auto load = [&](Data& x, int p) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < kRecs; ++i) {
         const uint8_t* from = src[i] + p * kKv4Plane;
         x.lo[i] = ldg128(from + lane * 16);
         x.hi[i] = ldg128(from + lane * 16 + 512);
@@ -510,7 +517,7 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, 1) kv4_chunk_kernel(const K
       st_shared_v4(at, half2_mul(v[0], f), half2_mul(v[1], f), half2_mul(v[2], f), half2_mul(v[3], f));
     };
     // K: key 4 (hi8 / 2) + hi8 % 2 and that + 2, channels 32 t4 ..; V: tokens 4 t4 .., channels 16 hi8 ..
-    const int row = q4 * 16 + (is_k ? 4 * (hi8 >> 1) + (hi8 & 1) : 4 * t4);
+    const int row = q * 16 + (is_k ? 4 * (hi8 >> 1) + (hi8 & 1) : 4 * t4);
     const int c0 = is_k ? ((t4 & 1) * 4 + (t4 & 2)) ^ (row & 7) : ((hi8 & 3) * 2) ^ (row & 7) ^ (far ? 1 : 0);
     const uint32_t at0 = slots + (is_k ? t4 >> 1 : hi8 >> 2) * kHalf + row * 128;
     auto loop = [&](auto&& unpack) {
@@ -526,7 +533,7 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, 1) kv4_chunk_kernel(const K
           ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(sm.free[to.slot]), to.phase ^ 1, abrt));
           if (!ok) break;
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
+          for (int x = 0; x < kRecs; ++x) {
             const uint32_t base = at0 + to.slot * kSlot + x * 64 * 128;
             unpack(d[p].lo[x], d[p].hi[x], d[p].sc[x], p, tile.left - x * 64, x * 64, base + (c0 << 4), base + ((c0 ^ 1) << 4),
                    base + ((c0 ^ 2) << 4), base + ((c0 ^ 3) << 4));
