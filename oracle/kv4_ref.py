@@ -197,3 +197,76 @@ def v2_decode(q, pool, block_table, seqlens, lam_logit, k_exp=0, v_exp=0, slack=
             off = [_off(x, v[:, h], slack, floor) for x in a]
             bound[b, p] = off[0] + sig[b, p] * off[1]
     return out, bound
+
+
+def _chunk_weights(q, k, n, length, causal):
+    """softmax weights [n, length] of the last n of `length` positions; rows that see no key are zeros."""
+    s = (q @ k.T) / np.sqrt(q.shape[1])
+    if causal:
+        s = np.where(np.arange(length)[None] <= length - n + np.arange(n)[:, None], s, -np.inf)
+    top = s.max(axis=1, keepdims=True, initial=-np.inf)
+    p = np.exp(s - np.where(np.isfinite(top), top, 0.0))
+    total = p.sum(axis=1, keepdims=True)
+    return np.divide(p, total, out=np.zeros_like(p), where=total > 0)
+
+
+def _off_rows(a, v, slack, floor):
+    """_off of every row of a, over the keys that the row sees."""
+    seen = (a > 0).astype(np.float64)
+    return slack * (a @ np.abs(v)) + floor * a.max(axis=1, initial=0.0)[:, None] * (seen @ np.abs(v))
+
+
+def fwd(q, pool, block_table, cu, seqlens, lam, lam_init, norm_weight=None, eps=1e-5, causal=True, norm=True, apply_scale=True,
+        k_exp=0, v_exp=0, slack=0.0, floor=0.0):
+    """V1 chunks over a pool: q [total, H, 256], sequence b's rows cu[b] .. cu[b + 1] - 1 being the last of its
+    seqlens[b] positions. Returns (out, bound) [total, H, 256] as `decode` does; rows in no sequence are NaN."""
+    q = ref._f64(q)
+    total, H, _ = q.shape
+    out, bound = np.full((total, H, 256), np.nan), np.zeros((total, H, 256))
+    for b, length in enumerate(int(n) for n in seqlens):
+        rows = slice(int(cu[b]), int(cu[b + 1]))
+        n = rows.stop - rows.start
+        if n == 0:
+            continue
+        if length == 0:
+            out[rows] = 0.0
+            continue
+        k, v = sequence_rows(pool, 2, block_table, b, length, 0, k_exp, v_exp)
+        for h in range(H):
+            a = [_chunk_weights(q[rows, h, 128 * m:128 * m + 128], k[:, h, 128 * m:128 * m + 128], n, length, causal) for m in (0, 1)]
+            o = a[0] @ v[:, h] - lam[h] * (a[1] @ v[:, h])
+            e = _off_rows(a[0], v[:, h], slack, floor) + abs(lam[h]) * _off_rows(a[1], v[:, h], slack, floor)
+            y = ref.head_epilogue(o, norm_weight, eps, lam_init, norm, apply_scale)
+            g = np.ones(256) if norm_weight is None or not norm else np.abs(ref._f64(norm_weight))
+            g = g * (abs(1 - lam_init) if apply_scale else 1.0)
+            if norm:
+                rms = np.sqrt(np.mean(o * o, axis=1, keepdims=True) + eps)
+                e = (e + np.abs(o) * np.linalg.norm(e, axis=1, keepdims=True) / (np.sqrt(256) * rms)) / rms * 1.05
+            out[rows, h], bound[rows, h] = y, g * e
+    return out, bound
+
+
+def v2_fwd(q, pool, block_table, cu, seqlens, lam_logit, causal=True, k_exp=0, v_exp=0, slack=0.0, floor=0.0):
+    """V2 chunks over a pool: q [total, Hq, 128]. Returns (out, bound) [total, Hq/2, 128] as above."""
+    q = ref._f64(q)
+    total, Hq, _ = q.shape
+    G = Hq // pool.shape[1]
+    sig = ref.sigmoid(lam_logit)
+    out, bound = np.full((total, Hq // 2, 128), np.nan), np.zeros((total, Hq // 2, 128))
+    for b, length in enumerate(int(n) for n in seqlens):
+        rows = slice(int(cu[b]), int(cu[b + 1]))
+        n = rows.stop - rows.start
+        if n == 0:
+            continue
+        if length == 0:
+            out[rows] = 0.0
+            continue
+        k, v = sequence_rows(pool, 1, block_table, b, length, 0, k_exp, v_exp)
+        for p in range(Hq // 2):
+            h = 2 * p // G
+            a = [_chunk_weights(q[rows, 2 * p + r], k[:, h], n, length, causal) for r in (0, 1)]
+            g = sig[rows, p][:, None]
+            out[rows, p] = a[0] @ v[:, h] - g * (a[1] @ v[:, h])
+            off = [_off_rows(x, v[:, h], slack, floor) for x in a]
+            bound[rows, p] = off[0] + g * off[1]
+    return out, bound
