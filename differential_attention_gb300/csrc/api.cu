@@ -86,13 +86,14 @@ DIFFATTN_API int diffattn_device_status(void* stream) {
   if (e == cudaSuccess) e = da::status_backward(&z);
   int dd = 0;
   if (e == cudaSuccess) e = da::status_decode(&dd);
-  int kd = 0, kr = 0, pp = 0, rp = 0, ck = 0;
+  int kd = 0, kr = 0, pp = 0, rp = 0, ck = 0, cf = 0;
   if (e == cudaSuccess) e = da::status_decode_kv4(&kd);
   if (e == cudaSuccess) e = da::status_kv4_rows(&kr);
   if (e == cudaSuccess) e = da::status_paged_plan(&pp);
   if (e == cudaSuccess) e = da::status_rope(&rp);
   if (e == cudaSuccess) e = da::status_chunk_kv4(&ck);
-  dd |= kd | kr | pp | rp | ck;
+  if (e == cudaSuccess) e = da::status_chunk_kv4_few(&cf);
+  dd |= kd | kr | pp | rp | ck | cf;
   if (e != cudaSuccess) return cuda_fail(e, "reading the device status word");
   v |= w | x | y | z | dd;
   if (v & DEV_BOUNDS_BIT)
@@ -2575,6 +2576,7 @@ int chunk_kv4_impl(const char* fn, da::Kv4ChunkArgs& a, int width, int max_seqle
   if (!workspace || ws_bytes < need || !aligned(workspace, 256))
     return fail(DIFFATTN_ERR_WORKSPACE, "%s: need a 256-byte aligned workspace of %zu bytes", fn, need);
   a.pieces = static_cast<float*>(workspace);
+  a.longest = max_seqlen_q;
   if ((rc = check_device())) return rc;
   kv4_scales(a, k_exp, v_exp);
   cudaError_t e = da::launch_kv4_chunk(a, static_cast<cudaStream_t>(stream));

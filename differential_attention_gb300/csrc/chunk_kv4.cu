@@ -28,19 +28,17 @@
 
 #include "early.cuh"
 #include "internal.h"
-#include "kv4.cuh"
+#include "kv4_chunk.cuh"
 #include "ptx.cuh"
 
 namespace da {
 namespace {
 
-constexpr int kSms = 152;
 constexpr int kRows = 128;
-constexpr int kTile = 128;                       // keys
+constexpr int kTile = 128;                       // keys (2^7)
 constexpr int kSlot = kTile * 128 * 2;           // one plane of a tile in fp16
 constexpr int kHalf = kSlot / 2;                 // 64 of its channels
 constexpr int kUnitCost = 5;                     // what a unit costs besides its tiles, in tiles
-constexpr int kMinCost = 2;                      // the smallest range
 constexpr float kPScale = 6.f, kMoveRef = 15.f;  // log2 of P's scale, and of the P at which the reference moves
 constexpr int kNanSets = 8;
 constexpr int kRing = 4;                         // tiles whose records' addresses are known
@@ -81,11 +79,6 @@ struct Small {  // behind Q
   int abort, seg;      // seg: tiles of the unit whose Q is there, 0 behind the last
 };
 
-struct Walk {  // place in the walk over units: sequences, heads, tiles of tokens
-  int b, h, rt, q0, Lq, Lk, nrt;
-  int tile, tiles;
-  long long todo;  // tiles of the range, and the costs of the units that begin in it, from here on
-};
 constexpr int kMaxThreads = 768;
 struct Scan {  // at startup, in Q's place
   long long pre[kMaxThreads + 1], sum[kMaxThreads / 32];
@@ -96,162 +89,6 @@ constexpr int smem_bytes() {
   return Cfg<KP>::kSmall + static_cast<int>(sizeof(Small));
 }
 static_assert(smem_bytes<1>() <= 232448 && smem_bytes<2>() <= 232448, "shared memory");
-
-// ---- the batch's units -------------------------------------------------------------------------
-struct Seq {
-  int q0, Lq, Lk;
-};
-// kEarly: before grid_wait(), in a kernel that knows of the write by the release of the one before it
-template <bool kEarly>
-__device__ __forceinline__ int ld(const int* p) {
-  return kEarly ? __ldcg(p) : *p;
-}
-template <bool kEarly>
-__device__ __forceinline__ Seq sequence(const Kv4ChunkArgs& a, int b, bool report = false) {
-  Seq s{ld<kEarly>(a.cu_seqlens + b), 0, 0};
-  const int end = ld<kEarly>(a.cu_seqlens + b + 1);
-  if (s.q0 < 0 || end < s.q0 || end > a.total) {
-    if (report) flag_device_error(DEV_BAD_INDEX);
-    return s;
-  }
-  const int cap = a.max_pages * a.page_size, n = ld<kEarly>(a.seqlens + b);
-  s.Lq = end - s.q0;
-  s.Lk = n < 0 ? 0 : n > cap ? cap : n;
-  return s;
-}
-// leading tokens that see no key
-__device__ __forceinline__ int hidden(const Kv4ChunkArgs& a, const Seq& s) {
-  return s.Lk == 0 ? s.Lq : a.causal ? max(0, s.Lq - s.Lk) : 0;
-}
-__device__ __forceinline__ int tiles_of(const Kv4ChunkArgs& a, int Lq, int Lk, int rt) {
-  const int end = a.causal ? Lk - Lq + min(Lq, (rt + 1) * a.tokens) : Lk;
-  return (end + kTile - 1) / kTile;
-}
-// of one head
-template <bool kEarly>
-__device__ __forceinline__ long long cost_of(const Kv4ChunkArgs& a, int b, bool report) {
-  const Seq s = sequence<kEarly>(a, b, report);
-  const int z = hidden(a, s), n = (s.Lq + a.tokens - 1) / a.tokens;
-  if (z >= s.Lq) return 0;
-  long long sum = 0;
-  for (int rt = z / a.tokens; rt < n; ++rt) sum += tiles_of(a, s.Lq, s.Lk, rt) + kUnitCost;
-  return sum;
-}
-// the first unit of sequence w.b, head w.h; false: it has none
-template <bool kEarly>
-__device__ __forceinline__ bool enter(const Kv4ChunkArgs& a, Walk& w) {
-  const Seq s = sequence<kEarly>(a, w.b);
-  const int z = hidden(a, s);
-  w.q0 = s.q0, w.Lq = s.Lq, w.Lk = s.Lk;
-  w.nrt = (s.Lq + a.tokens - 1) / a.tokens;
-  w.rt = z / a.tokens;
-  w.tile = 0;
-  if (z >= s.Lq) return false;
-  w.tiles = tiles_of(a, s.Lq, s.Lk, w.rt);
-  return true;
-}
-__device__ __forceinline__ void next_unit(const Kv4ChunkArgs& a, Walk& w) {
-  w.todo -= kUnitCost;
-  if (w.todo <= 0) return;
-  if (++w.rt < w.nrt) {
-    w.tile = 0;
-    w.tiles = tiles_of(a, w.Lq, w.Lk, w.rt);
-    return;
-  }
-  if (++w.h < a.H) {
-    enter<false>(a, w);
-    return;
-  }
-  w.h = 0;
-  do {
-    if (++w.b >= a.B) {
-      w.todo = 0;
-      return;
-    }
-  } while (!enter<false>(a, w));
-}
-// `n` tiles of the unit are done
-__device__ __forceinline__ void advance(const Kv4ChunkArgs& a, Walk& w, int n) {
-  w.tile += n;
-  w.todo -= n;
-  if (w.tile == w.tiles) next_unit(a, w);
-}
-
-__device__ __forceinline__ int range_count(long long total, int grid) {
-  const long long want = total / kMinCost;
-  return static_cast<int>(want < 1 ? 1 : want > grid ? grid : want);
-}
-__device__ __forceinline__ long long range_start(long long total, int n, int i) {
-  return total / n * i + total % n * i / n;
-}
-// the range that holds x < total: the largest i with total i / n < x + 1
-__device__ __forceinline__ int range_of(long long total, int n, long long x) { return static_cast<int>(((x + 1) * n - 1) / total); }
-
-// The costs before each thread's share of the sequences; a whole block of NT threads. Returns their sum.
-template <int NT, bool kEarly>
-__device__ __forceinline__ long long fill(const Kv4ChunkArgs& a, long long* pre, long long* sum, bool report) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, per = (a.B + NT - 1) / NT;
-  const int lo = min(a.B, tid * per), hi = min(a.B, lo + per);
-  long long incl = 0;
-  for (int b = lo; b < hi; ++b) incl += cost_of<kEarly>(a, b, report);
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const long long o = __shfl_up_sync(0xffffffffu, incl, d);
-    if (lane >= d) incl += o;
-  }
-  if (lane == 31) sum[warp] = incl;
-  __syncthreads();
-  for (int w = 0; w < warp; ++w) incl += sum[w];
-  pre[tid + 1] = incl;
-  if (tid == 0) pre[0] = 0;
-  __syncthreads();
-  return pre[NT] * a.H;
-}
-// The unit that holds place t0 of all costs (a whole warp). w.tile: the first tile at or behind t0; `first`:
-// where the unit's tiles begin.
-template <int NT, bool kEarly>
-__device__ __forceinline__ void locate(const Kv4ChunkArgs& a, const long long* pre, long long t0, Walk& w, long long& first) {
-  const int lane = threadIdx.x & 31, per = (a.B + NT - 1) / NT;
-  w = Walk{};
-  int share = 0;
-  for (int i = 0; i < NT; i += 32)
-    if (const unsigned hit = __ballot_sync(0xffffffffu, pre[i + lane] * a.H <= t0 && t0 < pre[i + lane + 1] * a.H)) {
-      share = i + __ffs(hit) - 1;
-      break;
-    }
-  long long at = pre[share], cost = 0;
-  const int end = min(a.B, (share + 1) * per);
-  for (int b = share * per; b < end; ++b) {
-    cost = per == 1 ? pre[share + 1] - pre[share] : cost_of<kEarly>(a, b, false);
-    w.b = b;
-    if (t0 < (at + cost) * a.H) break;
-    at += cost;
-  }
-  long long left = t0 - at * a.H;  // in the sequence
-  w.h = static_cast<int>(left / cost);
-  left -= w.h * cost;
-  enter<kEarly>(a, w);
-  for (int rt = w.rt;; rt += 32) {  // 32 tiles of tokens at a time
-    const int mine = rt + lane < w.nrt ? tiles_of(a, w.Lq, w.Lk, rt + lane) + kUnitCost : 0;
-    long long incl = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const long long o = __shfl_up_sync(0xffffffffu, incl, d);
-      if (lane >= d) incl += o;
-    }
-    const unsigned hit = __ballot_sync(0xffffffffu, left < incl);
-    if (hit || rt + 32 >= w.nrt) {
-      const int l = hit ? __ffs(hit) - 1 : 0;
-      w.rt = rt + l;
-      w.tiles = __shfl_sync(0xffffffffu, mine, l) - kUnitCost;
-      left -= __shfl_sync(0xffffffffu, incl - mine, l);
-      break;
-    }
-    left -= __shfl_sync(0xffffffffu, incl, 31);
-  }
-  first = t0 - left + kUnitCost;
-  w.tile = static_cast<int>(max(0LL, left - kUnitCost));
-}
 
 template <int N>
 __device__ __forceinline__ void registers_up() {
@@ -879,7 +716,6 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, 1) kv4_chunk_kernel(const K
 // if no earlier range does, and every gridDim.y-th of its tokens (V1) or pairs (V2) from y on; a thread a channel.
 template <int KP>
 __global__ void __launch_bounds__(KP * 128) kv4_chunk_join_kernel(const Kv4ChunkArgs a) {
-  using C = Cfg<KP>;
   constexpr int NT = KP * 128;
   __shared__ long long s_pre[NT + 1], s_sum[NT / 32], s_first;
   __shared__ Walk s_walk;
@@ -908,6 +744,7 @@ __global__ void __launch_bounds__(KP * 128) kv4_chunk_join_kernel(const Kv4Chunk
   const int i0 = range_of(total, n, first), pieces = range_of(total, n, first + w.tiles - 1) - i0 + 1;
   const int tok0 = w.rt * a.tokens, toks = min(a.tokens, w.Lq - tok0);
   const int outs = KP == 2 ? toks : toks * a.group / 2;  // of the unit
+  const size_t piece = static_cast<size_t>(a.rows) * (2 + NT);
   float wgt = 1.f;
   if (KP == 2 && (a.flags & 2) && a.norm_w) wgt = *(a.norm_w + tid);
   for (int o = blockIdx.y; o < outs; o += gridDim.y) {
@@ -915,10 +752,10 @@ __global__ void __launch_bounds__(KP * 128) kv4_chunk_join_kernel(const Kv4Chunk
     float m[2] = {-FLT_MAX, -FLT_MAX}, l[2] = {0.f, 0.f}, v[2] = {0.f, 0.f};
 #pragma unroll 4
     for (int k = 0; k < pieces; ++k) {
-      const float* r = a.pieces + static_cast<size_t>(2 * (i0 + k) + (k == 0 ? 1 : 0)) * C::kPiece;
+      const float* r = a.pieces + static_cast<size_t>(2 * (i0 + k) + (k == 0 ? 1 : 0)) * piece;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float mk = r[c[e]], lk = r[kRows + c[e]], vk = r[2 * kRows + (tid / 4 * kRows + c[e]) * 4 + tid % 4];
+        const float mk = r[c[e]], lk = r[a.rows + c[e]], vk = r[2 * a.rows + (tid / 4 * a.rows + c[e]) * 4 + tid % 4];
         const float top = fmaxf(m[e], mk), f = ex2_approx(m[e] - top), fk = ex2_approx(mk - top);
         m[e] = top;
         l[e] = l[e] * f + lk * fk;
@@ -954,23 +791,13 @@ __global__ void __launch_bounds__(KP * 128) kv4_chunk_join_kernel(const Kv4Chunk
 }
 
 template <int KP>
-cudaError_t launch(Kv4ChunkArgs a, cudaStream_t st) {
-  static std::atomic<uint64_t> raised{};
-  a.tokens = kRows / (KP == 2 ? 2 : a.group);
-  page_magic(a.page_size >> 4, &a.rec_magic, &a.rec_shift);
-  // no more blocks than the tables' capacity can give ranges: a sequence's tiles of tokens overlap the total's
-  const long long tiles = (static_cast<long long>(a.max_pages) * a.page_size + kTile - 1) / kTile;
-  const long long units = (static_cast<long long>(a.total) / a.tokens + a.B) * a.H;
-  const long long most = units >= kSms ? kSms : (tiles + kUnitCost) * units / kMinCost;
-  a.grid = static_cast<int>(most < 1 ? 1 : most > kSms ? kSms : most);
-  cudaError_t e = launch_early_large(kv4_chunk_kernel<KP>, a.grid, Cfg<KP>::kThreads, smem_bytes<KP>(), smem_bytes<KP>(), st, 1, a, raised);
-  if (e != cudaSuccess || a.grid == 1) return e;
+cudaError_t launch_join(const Kv4ChunkArgs& a, cudaStream_t st) {
   g_launched.store(true, std::memory_order_relaxed);
   cudaLaunchAttribute at[1] = {};
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(a.grid - 1, kRows / 16);
+  cfg.gridDim = dim3(a.grid - 1, a.rows < kRows ? a.rows / 4 : 8);
   cfg.blockDim = dim3(KP * 128);
   cfg.stream = st;
   cfg.attrs = at;
@@ -978,15 +805,38 @@ cudaError_t launch(Kv4ChunkArgs a, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, kv4_chunk_join_kernel<KP>, a);
 }
 
+template <int KP>
+cudaError_t launch(Kv4ChunkArgs a, cudaStream_t st) {
+  static std::atomic<uint64_t> raised{};
+  a.rows = kRows;
+  a.tokens = kRows / (KP == 2 ? 2 : a.group);
+  a.tile_log2 = 7;
+  a.unit_cost = kUnitCost;
+  page_magic(a.page_size >> 4, &a.rec_magic, &a.rec_shift);
+  // no more blocks than the tables' capacity can give ranges: a sequence's tiles of tokens overlap the total's
+  const long long tiles = (static_cast<long long>(a.max_pages) * a.page_size + kTile - 1) / kTile;
+  const long long units = (static_cast<long long>(a.total) / a.tokens + a.B) * a.H;
+  const long long most = units >= kChunkSms ? kChunkSms : (tiles + kUnitCost) * units / kMinCost;
+  a.grid = static_cast<int>(most < 1 ? 1 : most > kChunkSms ? kChunkSms : most);
+  cudaError_t e = launch_early_large(kv4_chunk_kernel<KP>, a.grid, Cfg<KP>::kThreads, smem_bytes<KP>(), smem_bytes<KP>(), st, 1, a, raised);
+  if (e != cudaSuccess || a.grid == 1) return e;
+  return launch_kv4_chunk_join(a, st);
+}
+
 }  // namespace
 
 size_t kv4_chunk_workspace_bytes(int group) {
-  return 2 * static_cast<size_t>(kSms) * (group == 0 ? Cfg<2>::kPiece : Cfg<1>::kPiece) * sizeof(float);
+  return 2 * static_cast<size_t>(kChunkSms) * (group == 0 ? Cfg<2>::kPiece : Cfg<1>::kPiece) * sizeof(float);
 }
 
 cudaError_t launch_kv4_chunk(const Kv4ChunkArgs& a, cudaStream_t st) {
   if (a.total == 0) return cudaSuccess;
+  if (kv4_chunk_few(a)) return launch_kv4_chunk_few(a, st);
   return a.group == 0 ? launch<2>(a, st) : launch<1>(a, st);
+}
+
+cudaError_t launch_kv4_chunk_join(const Kv4ChunkArgs& a, cudaStream_t st) {
+  return a.group == 0 ? launch_join<2>(a, st) : launch_join<1>(a, st);
 }
 
 cudaError_t status_chunk_kv4(int* v) { return launched_status(v); }

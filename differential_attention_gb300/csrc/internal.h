@@ -360,12 +360,15 @@ struct Kv4ChunkArgs {
   int num_pages, page_size, max_pages;
   float qk_scale, v_mul;   // as in Kv4DecodeArgs
   float* pieces;           // the workspace
-  int tokens, grid;        // tokens of a unit, ranges: set by the launcher
+  int longest;             // about the longest chunk: a hint
+  // Set by the launcher: tokens and rows of a unit, ranges, log2 of a tile's keys, what a unit costs in tiles.
+  int tokens, rows, grid, tile_log2, unit_cost;
   uint32_t rec_magic, rec_shift;  // j / (page_size / 16), as in V2DecodeArgs' page_magic; the launcher's
 };
 size_t kv4_chunk_workspace_bytes(int group);
 cudaError_t launch_kv4_chunk(const Kv4ChunkArgs& a, cudaStream_t s);
 cudaError_t status_chunk_kv4(int* v);
+cudaError_t status_chunk_kv4_few(int* v);
 
 // Rotary positions (rope.cu).
 struct RopeRows {  // [total, heads, width] by element strides

@@ -1000,7 +1000,7 @@ DIFFATTN_API int diffattn_v2_decode_kv4(const void* q, const void* pool, const i
  * power of two of its own for each head (V1: half), a probability rounded to fp16, sums and statistics
  * in fp32.
  *   q, out : device bf16 [total_q, H, 2d] and [total_q, H, dv] (V1), [total_q, Hq, d] and
- *          [total_q, Hq / 2, d] (V2), packed by cu_seqlens_q. Rows of `out` behind the last sequence (and
+ *          [total_q, Hq / 2, d] (V2), packed by cu_seqlens_q (ascending). Rows of `out` behind the last sequence (and
  *          of a sequence outside [0, total_q], which diffattn_device_status() reports as
  *          DIFFATTN_ERR_INDEX) are not written
  *   cu_seqlens_q : device int32 [B + 1];  seqlens : device int32 [B], clamped into [0, max_pages *
@@ -1009,11 +1009,10 @@ DIFFATTN_API int diffattn_v2_decode_kv4(const void* q, const void* pool, const i
  *          that is masked for a query never reaches that query's, whatever they hold
  *   lam_logit : device fp32 [total_q, Hq / 2]; lambda, lambda_init, norm_weight, eps, block_table : as for
  *          the decodes
- *   max_seqlen_q : the longest Lq, or any number near it: a hint by which the kernel is chosen (up to 8
- *          tokens at Hq / Hkv = 8, 32 with V1, take one for few tokens), right or wrong the results
- *          are right
- *   workspace, ws_bytes : at least the *_workspace_size bytes of the same max_seqlen_q, 256-byte aligned;
- *          as for the decodes
+ *   max_seqlen_q : the longest Lq, or any number near it: a hint (V1 has a kernel for up to 8 tokens).
+ *          The results are right whatever it says
+ *   workspace, ws_bytes : at least the *_workspace_size bytes (for V2, of the same Hq / Hkv), 256-byte
+ *          aligned; as for the decodes
  * A used table entry outside [0, num_pages) reads page 0 and is reported as DIFFATTN_ERR_INDEX. Equal
  * inputs give equal bits.
  * Supported: as the decodes; total_q * query heads <= 2^30, (total_q + B) * heads of the cache *
