@@ -386,6 +386,7 @@ struct RopeArgs {
   int total, hq, H, kw, vw, d, pairs, n_axes, top;
   int num_pages, page_size;
   float k_inv, v_inv;    // 4 bits: 2^-k_exp, 2^-v_exp
+  uint32_t kw_magic, kw_shift, vw_magic, vw_shift;  // j / (kw / d), j / (vw / d) by page_magic; the launcher's
   bool inverse;
   int split;             // warps a token, set by the launcher
 };

@@ -23,8 +23,13 @@
 namespace da {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kAhead = 4;  // parts a lane has under way
+// Parts that a lane has under way, and blocks an SM. More parts take registers from warps, whose chains of position,
+// table and rows are what is waited for. (16384 tokens of 24 heads of 256 channels, backward / 16400 of 64 + 8 heads
+// into bf16 pages / 16384 of 12 + 12 of 256 into 4-bit pages, us: 4 parts and 5 blocks 102, 140, 190; 3 and 6 91,
+// 136, 177; 2 and 7 77, 124, 153; 2 and 8, which spills, 79, 127, 155; 1 and 8 85, 135, 151. The same bytes at a
+// copy's rate: 60, 99, 105. Streaming hints change nothing.)
+constexpr int kThreads = 128, kBlocks = 7;
+constexpr int kAhead = 2;
 
 // fp64 to bf16 in one rounding: cut to fp32 with the last bit set where anything was cut off ("round to
 // odd"), which the second rounding then takes the right way.
@@ -37,15 +42,16 @@ __device__ __noinline__ uint32_t turn_exact(float x1, float x2, float c, float s
   const double a = x1, b = x2, dc = c, ds = s;
   return bf16_of(a * dc - b * ds) | bf16_of(b * dc + a * ds) << 16;
 }
-// (y1, y2) of one pair, packed
-__device__ __forceinline__ uint32_t turn_bf16(float x1, float x2, float c, float s) {
+// (y1, y2) of one pair, packed; `unsure` gets bits where it may not be the exact value's rounding
+__device__ __forceinline__ uint32_t turn_fast(float x1, float x2, float c, float s, uint32_t& unsure) {
   constexpr float kTwo = 1.f / (1 << 23);
   const float p1 = x2 * s, p2 = x2 * c;
   const float y1 = fmaf(x1, c, -p1), y2 = fmaf(x1, s, p2);
   const float t1 = fabsf(p1) + fabsf(y1), t2 = fabsf(p2) + fabsf(y2);
   const uint32_t lo = pack_bf16x2(fmaf(t1, -kTwo, y1), fmaf(t2, -kTwo, y2));
   const uint32_t hi = pack_bf16x2(fmaf(t1, kTwo, y1), fmaf(t2, kTwo, y2));
-  return lo == hi ? lo : turn_exact(x1, x2, c, s);
+  unsure |= lo ^ hi;
+  return lo;
 }
 // x1 c - x2 s to within 1.5 steps, whatever cancels (the first product's rounding error is put back)
 __device__ __forceinline__ float turn_f32(float x1, float x2, float c, float s) {
@@ -60,26 +66,35 @@ struct Item {
   uint4 run[2][kWords];
 };
 
+// (One test for all eight pairs: a branch for each is more instructions than the turning.)
 template <bool kInter>
 __device__ __forceinline__ void turn(Item<__nv_bfloat16>& x, const float2 (&cs)[8]) {
   uint32_t* a = reinterpret_cast<uint32_t*>(&x.run[0][0]);
   uint32_t* b = reinterpret_cast<uint32_t*>(&x.run[1][0]);
-  auto low = [](uint32_t w) { return __uint_as_float(w << 16); };
-  auto high = [](uint32_t w) { return __uint_as_float(w & 0xffff0000u); };
-  if constexpr (kInter) {  // a word is a pair
+  // pair i of the item
+  auto first = [&](int i) {
+    if constexpr (kInter) return __uint_as_float((i < 4 ? a : b)[i & 3] << 16);  // a word is a pair
+    else return __uint_as_float(i & 1 ? a[i >> 1] & 0xffff0000u : a[i >> 1] << 16);
+  };
+  auto second = [&](int i) {
+    if constexpr (kInter) return __uint_as_float((i < 4 ? a : b)[i & 3] & 0xffff0000u);
+    else return __uint_as_float(i & 1 ? b[i >> 1] & 0xffff0000u : b[i >> 1] << 16);
+  };
+  uint32_t y[8], unsure = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      a[i] = turn_bf16(low(a[i]), high(a[i]), cs[i].x, cs[i].y);
-      b[i] = turn_bf16(low(b[i]), high(b[i]), cs[4 + i].x, cs[4 + i].y);
-    }
-  } else {
+  for (int i = 0; i < 8; ++i) y[i] = turn_fast(first(i), second(i), cs[i].x, cs[i].y, unsure);
+  if (unsure) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t u = turn_bf16(low(a[i]), low(b[i]), cs[2 * i].x, cs[2 * i].y);
-      const uint32_t v = turn_bf16(high(a[i]), high(b[i]), cs[2 * i + 1].x, cs[2 * i + 1].y);
-      a[i] = __byte_perm(u, v, 0x5410);
-      b[i] = __byte_perm(u, v, 0x7632);
+    for (int i = 0; i < 8; ++i) {
+      uint32_t mine = 0;
+      turn_fast(first(i), second(i), cs[i].x, cs[i].y, mine);
+      if (mine) y[i] = turn_exact(first(i), second(i), cs[i].x, cs[i].y);
     }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    a[i] = kInter ? y[i] : __byte_perm(y[2 * i], y[2 * i + 1], 0x5410);
+    b[i] = kInter ? y[4 + i] : __byte_perm(y[2 * i], y[2 * i + 1], 0x7632);
   }
 }
 template <bool kInter>
@@ -95,26 +110,26 @@ __device__ __forceinline__ void turn(Item<float>& x, const float2 (&cs)[8]) {
   }
 }
 
-// Where a tensor's rows lie: part `r` of a token's row (head r / parts) from its first channel
+// Where a tensor's rows lie: part `r` of a token's row (head h = r / parts) from its first channel
 template <typename T>
-__device__ __forceinline__ T* part_of(const RopeRows& t, long long token, int r, int parts, int d) {
-  const int h = r / parts;
+__device__ __forceinline__ T* part_of(const RopeRows& t, long long token, int r, int h, int parts, int d) {
   return static_cast<T*>(t.data) + token * t.token + h * t.head + (r - h * parts) * d;
 }
+__device__ __forceinline__ int quotient(int j, uint32_t magic, uint32_t shift) { return (__umulhi(j, magic) + j) >> shift; }
 
 // kPages 0: rows to rows; 1: keys and values to bf16 pages; 2: to 4-bit pages (the values by warps of
 // their own, 8 rows of a head each).
 template <typename T, bool kInter, int kPages>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, kBlocks) rope_kernel(const RopeArgs a) {
   grid_wait();
   grid_release();
   const int lane = threadIdx.x & 31;
   long long w = static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
   const long long rope_warps = static_cast<long long>(a.total) * a.split;
 
-  auto slot_of = [&](long long row) {
-    if (row >= a.total) return -1;
-    const int s = *(a.slot_map + row);
+  // (`s` is loaded with the position, not behind it)
+  auto raw_slot = [&](long long row) { return row < a.total ? *(a.slot_map + row) : -1; };
+  auto slot_of = [&](int s) {
     if (s >= 0 && s < a.num_pages * a.page_size) return s;
     if (s != -1) flag_device_error(DEV_BAD_INDEX);
     return -1;
@@ -139,7 +154,8 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
       w -= rope_warps;
       const int h = static_cast<int>(w % a.H), g = lane & 7;
       const long long row = w / a.H * 8 + 2 * (lane >> 3);
-      const int s0 = placed(row) ? slot_of(row) : -1, s1 = placed(row + 1) ? slot_of(row + 1) : -1;
+      const int raw0 = raw_slot(row), raw1 = raw_slot(row + 1);
+      const int s0 = placed(row) ? slot_of(raw0) : -1, s1 = placed(row + 1) ? slot_of(raw1) : -1;
       const int vp = a.vw >> 7;
       const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.v.data) + row * a.v.token + h * a.v.head + g * 16;
       auto place = [&](int slot) {
@@ -179,6 +195,8 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
   if (w >= rope_warps) return;
   const long long token = w / a.split;
   const int share = static_cast<int>(w - token * a.split);
+  int raw = -1;
+  if constexpr (kPages != 0) raw = raw_slot(token);
   if (!placed(token)) return;
 
   // lane: item `it` (16 channels) of slot `sl` of the parts that the warp has in hand
@@ -215,16 +233,16 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
     }
   }
 
-  // all parts of the token's rows of one tensor, kAhead of them at a time
-  auto rows = [&](const RopeRows& t, int heads, int parts, bool rotate, auto&& store) {
-    const int n = heads * parts, step = slots * a.split;
+  // n parts, kAhead of them at a time, from where `source` says
+  auto rows = [&](int n, bool rotate, auto&& source, auto&& store) {
+    const int step = slots * a.split;
     for (int r0 = share * slots + sl; r0 - sl < n; r0 += step * kAhead) {
       Item<T> x[kAhead];
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
         const int r = r0 + u * step;
         if (r < n) {
-          const T* src = part_of<T>(t, token, r, parts, a.d);
+          const T* src = source(r);
 #pragma unroll
           for (int i = 0; i < Item<T>::kWords; ++i) {
             x[u].run[0][i] = *(reinterpret_cast<const uint4*>(src + run0) + i);
@@ -247,28 +265,43 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
       *(reinterpret_cast<uint4*>(dst + run1) + i) = x.run[1][i];
     }
   };
-  const int parts = a.kw / a.d;
-  rows(a.q, a.hq, parts, true, [&](const Item<T>& x, int r, bool live) {
-    if (live) put(part_of<T>(a.q_out, token, r, parts, a.d), x);
-  });
+  const int parts = a.kw / a.d, nq = a.hq * parts, nk = a.H * parts;
+  auto head = [&](int r) { return quotient(r, a.kw_magic, a.kw_shift); };
+  auto q_or_k = [&](const RopeRows& q, const RopeRows& k, int r) {
+    const bool is_k = r >= nq;
+    const int i = is_k ? r - nq : r;
+    return part_of<T>(is_k ? k : q, token, i, head(i), parts, a.d);
+  };
   if constexpr (kPages == 0) {
-    rows(a.k, a.H, parts, true, [&](const Item<T>& x, int r, bool live) {
-      if (live) put(part_of<T>(a.k_out, token, r, parts, a.d), x);
-    });
+    rows(nq + nk, true, [&](int r) { return q_or_k(a.q, a.k, r); },
+         [&](const Item<T>& x, int r, bool live) {
+           if (live) put(q_or_k(a.q_out, a.k_out, r), x);
+         });
   } else {
-    const int slot = slot_of(token);
-    if (slot < 0) return;
+    const int slot = slot_of(raw);
     if constexpr (kPages == 1) {
-      rows(a.k, a.H, parts, true, [&](const Item<T>& x, int r, bool live) {
-        if (live) put(static_cast<T*>(a.k_dst) + static_cast<size_t>(slot) * a.H * a.kw + static_cast<size_t>(r) * a.d, x);
-      });
-      rows(a.v, a.H, a.vw / a.d, false, [&](const Item<T>& x, int r, bool live) {
-        if (live) put(static_cast<T*>(a.v_dst) + static_cast<size_t>(slot) * a.H * a.vw + static_cast<size_t>(r) * a.d, x);
-      });
+      const RopeRows k_out{static_cast<T*>(a.k_dst) + static_cast<size_t>(max(slot, 0)) * a.H * a.kw, 0, a.kw};
+      rows(slot < 0 ? nq : nq + nk, true, [&](int r) { return q_or_k(a.q, a.k, r); },
+           [&](const Item<T>& x, int r, bool live) {
+             if (live) put(q_or_k(a.q_out, k_out, r), x);
+           });
+      if (slot < 0) return;
+      const int vparts = a.vw / a.d;
+      rows(a.H * vparts, false,
+           [&](int r) { return part_of<T>(a.v, token, r, quotient(r, a.vw_magic, a.vw_shift), vparts, a.d); },
+           [&](const Item<T>& x, int r, bool live) {
+             if (live) put(static_cast<T*>(a.v_dst) + static_cast<size_t>(slot) * a.H * a.vw + static_cast<size_t>(r) * a.d, x);
+           });
     } else {
+      rows(nq, true, [&](int r) { return part_of<T>(a.q, token, r, head(r), parts, a.d); },
+           [&](const Item<T>& x, int r, bool live) {
+             if (live) put(part_of<T>(a.q_out, token, r, head(r), parts, a.d), x);
+           });
+      if (slot < 0) return;
       const int page = slot / a.page_size, off = slot - page * a.page_size, key = off & 15;
       const size_t rec = static_cast<size_t>((a.kw + a.vw) / 128 * kKv4Plane);
-      rows(a.k, a.H, parts, true, [&](const Item<T>& x, int r, bool live) {
+      rows(nk, true, [&](int r) { return part_of<T>(a.k, token, r, head(r), parts, a.d); },
+           [&](const Item<T>& x, int r, bool live) {
         // a lane wants 16 channels on end: where its runs are of two blocks, it trades one with its neighbour
         uint4 lo = x.run[0][0], hi = x.run[1][0];
         int blk = it;
@@ -288,7 +321,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
         }
         const Kv4Block b = kv4_round_block(lo, hi, a.k_inv);
         if (!live) return;
-        const int h = r / parts;
+        const int h = head(r);
         uint8_t* p = static_cast<uint8_t*>(a.k_dst) + ((static_cast<size_t>(page) * a.H + h) * (a.page_size >> 4) + (off >> 4)) * rec +
                      (r - h * parts) * kKv4Plane;
         *reinterpret_cast<uint2*>(p + kv4_k_code(key, blk >> 1) + 8 * (blk & 1)) = make_uint2(b.lo, b.hi);
@@ -322,7 +355,10 @@ cudaError_t launch_rope(RopeArgs a, int pages, bool fp32, bool interleaved, cuda
   if (a.total == 0) return cudaSuccess;
   // warps of a token: as many as give each of the 152 SMs 16, but not more than its rows have work for
   const int slots = 512 / a.d;
-  const int most = ((a.hq > a.H ? a.hq : a.H) * (a.kw / a.d) + slots - 1) / slots;
+  const int heads = pages == 2 ? (a.hq > a.H ? a.hq : a.H) : a.hq + a.H;
+  const int most = (heads * (a.kw / a.d) + slots - 1) / slots;
+  page_magic(a.kw / a.d, &a.kw_magic, &a.kw_shift);
+  page_magic(pages ? a.vw / a.d : 1, &a.vw_magic, &a.vw_shift);
   const long long want = (152 * 16 + a.total - 1) / a.total;
   a.split = static_cast<int>(want < 1 ? 1 : want > most ? most : want);
   if (a.split < 1) a.split = 1;
