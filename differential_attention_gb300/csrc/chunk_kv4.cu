@@ -12,7 +12,8 @@
 // their own each, joined at the unit's end; V1, whose products take twice as long a tile, has one. K and V:
 // four warps each read records into registers, a tile ahead, and write fp16 (exact: an e2m1 times an e4m3 has
 // 6 significant bits) in the products' 128-byte swizzle, into a ring of planes. One warp looks the records'
-// addresses up and has L2 fetch them; one issues the products: S of the next tile before P V of this one.
+// addresses up and has L2 fetch them; one issues the products: S of the next tile before P V of this one. At a unit's
+// end the next unit's queries go in first, so that its first scores are there when the output is written.
 //
 // Numerics, as in the decode over the same cache: the query enters as fp16 after a power of two of its own
 // for each row, P is rounded to fp16 at 2^6 times its value against m, which moves only where a score passes
@@ -23,6 +24,15 @@
 // Work. All units one behind the other are cut into equal ranges of tiles, one for each SM; pieces of units
 // that are cut go to the workspace, at most two a range, and a second kernel joins them in the order of the
 // ranges, so that equal inputs give equal bits.
+//
+// What bounds it: the products, and shared memory beside them. A V2 tile is 8 products S (103 cycles each, both
+// operands from shared memory) and 8 of P V (70, P in tensor memory): 1380 cycles; what the unpacking writes (64 KB,
+// 512 cycles) and the products read (768) comes on top, as it uses the same port, and a tile takes 2150. V1: 3150, of
+// which 2750 are its 32 products, a half of S's by zeros. Measured: 20 ragged prompts of up to 2048 new tokens over up
+// to 16384, G = 8 (V2) 1241 us, 915 TFLOP/s; 4 x 1024 over 4096, V1, 337 us, 800; 24 x 8 tokens over 32768, V2, where
+// half of the 128 rows are empty, 394 us. Measured on the way: everything transposed, keys and channels on the 128
+// lanes and 64 queries as columns, 360 for the last and 2950 for the first; one O for both streams, its m handed
+// on, slower for all; 8 unpacking warps for V1, and V in front of the next tile's K, 444 where 4 x 1024 took 353.
 #include <cfloat>
 #include <cmath>
 
@@ -38,13 +48,17 @@ constexpr int kRows = 128;
 constexpr int kTile = 128;                       // keys (2^7)
 constexpr int kSlot = kTile * 128 * 2;           // one plane of a tile in fp16
 constexpr int kHalf = kSlot / 2;                 // 64 of its channels
-constexpr int kUnitCost = 5;                     // what a unit costs besides its tiles, in tiles
 constexpr float kPScale = 6.f, kMoveRef = 15.f;  // log2 of P's scale, and of the P at which the reference moves
 constexpr int kNanSets = 8;
 constexpr int kRing = 4;                         // tiles whose records' addresses are known
 
 template <int KP>
 struct Cfg {
+  // What a unit costs besides its tiles, in tiles: its query, the wait for its first scores, the join and the output,
+  // 9 to 12 thousand cycles with V2 (a tile 2150) and 13 with V1 (3150). (With 5 and 8, us: V2, 20 ragged prompts of up
+  // to 2048 new and 16384 cached tokens 1406 and 1241, 100 of up to 300 and 1000 200 and 218, 64 of up to 64 and 30000
+  // with G = 4 206 and 198; V1, 40 of up to 512 and 4096 161 and 181, 64 of up to 64 and 8000 134 and 151.)
+  static constexpr int kUnitCost = KP == 1 ? 8 : 5;
   static constexpr int kStreams = KP == 1 ? 2 : 1;  // softmax warpgroups
   static constexpr int kRecs = KP == 1 ? 2 : 1, kUnpackWarps = 8 / kRecs;  // K's, and V's: records of a plane for each
   static constexpr int kKWarp = 4 * kStreams, kVWarp = kKWarp + kUnpackWarps, kMmaWarp = kVWarp + kUnpackWarps;
@@ -70,7 +84,8 @@ struct TileAt {
   int key0, left, unit, pad;  // its first key, keys from there on (0: the stream has ended), its unit's number
 };
 struct Small {  // behind Q
-  float scale[kRows];  // what the rows' S is to be multiplied with
+  int top[kRows];      // the exponent of the rows' largest query channel
+  float2 join[kRows];  // V2, at a unit's end: the second stream's m and l, then both streams' weights
   uint64_t full[6], free[6], s_full[2], p_full[2], pv_done[2], q_full, teardown;
   uint64_t tile_full[kRing], tile_free[kRing];
   TileAt tile[kRing];
@@ -207,9 +222,9 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, 1) kv4_chunk_kernel(const K
       const uint64_t dv = umma_smem_desc(slots, kHalf, 1024);
       int j = 0;
       bool ok = true;
-      auto scores = [&](int t, bool wait) {
+      auto scores = [&](int t) {
         // (P of tile t - 2 lay where S goes)
-        if (wait && !(ok = mbar_wait(bar(sm.pv_done[t & 1]), ((t - 2) >> 1) & 1, abrt))) return;
+        if (t >= 2 && !(ok = mbar_wait(bar(sm.pv_done[t & 1]), ((t - 2) >> 1) & 1, abrt))) return;
 #pragma unroll 1
         for (int p = 0; p < KP; ++p) {
           const Place k = place<KP>(t, p);
@@ -230,9 +245,9 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, 1) kv4_chunk_kernel(const K
         tc_fence_after();
         const int seg = *static_cast<volatile int*>(&sm.seg);
         if (seg == 0) break;
-        scores(j, false);
+        scores(j);
         for (int i = 0; ok && i < seg; ++i, ++j) {
-          if (i + 1 < seg) scores(j + 1, i > 0);
+          if (i + 1 < seg) scores(j + 1);
           if (!ok) break;
           if (!(ok = mbar_wait(bar(sm.p_full[j & 1]), (j >> 1) & 1, abrt))) break;
           const uint32_t o = tmem + C::kO + (kStreams == 2 ? (j & 1) * 128 : 0);
@@ -438,49 +453,68 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, 1) kv4_chunk_kernel(const K
       uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + s.q0 * width);
       for (size_t i = tid; i < z * width / 8; i += kAll) out[i] = make_uint4(0, 0, 0, 0);
     }
-    while (w.todo > 0) {
-      const int seg = static_cast<int>(min(static_cast<long long>(w.tiles - w.tile), w.todo));
-      const bool starts = w.tile == 0, whole = starts && seg == w.tiles;
-      const int tok0 = w.rt * a.tokens, toks = min(a.tokens, w.Lq - tok0);  // tokens of the unit
-      const int per = KP == 2 ? 2 : a.group, rows = toks * per;            // rows of a token, rows in use
-      // Q: a half-warp a row, two rows at a time
-      {
-        constexpr int kWarps = 4 * kStreams, kRounds = kRows / 2 / kWarps;
-        const int part = lane & 15;  // of 16 bytes: 8 in each 64 channels
-        uint4 x[kRounds];
-        auto row_of = [&](int i) { return (i * kWarps + warp) * 2 + (lane >> 4); };
+    const int per = KP == 2 ? 2 : a.group;  // rows of a token
+    auto tiles_here = [](const Walk& x) { return static_cast<int>(max(0LL, min(static_cast<long long>(x.tiles - x.tile), x.todo))); };
+    // A unit's queries: a half-warp a row, two rows at a time, kRounds times in batches of 8
+    constexpr int kQWarps = 4 * kStreams, kBatches = kRows / 2 / kQWarps / 8;
+    auto row_of = [&](int i) { return (i * kQWarps + warp) * 2 + (lane >> 4); };
+    const int part = lane & 15;  // of 16 bytes: 8 in each 64 channels
+    auto fetch = [&](uint4 (&x)[8], const Walk& u, int batch) {
+      const int tok0 = u.rt * a.tokens, rows = min(a.tokens, u.Lq - tok0) * per;
 #pragma unroll
-        for (int i = 0; i < kRounds; ++i) {
-          const int r = row_of(i), t = r / per, sub = r - t * per;
-          const size_t from = (static_cast<size_t>(w.q0 + tok0 + t) * a.H + w.h) * per + sub;
-          x[i] = r < rows ? *(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + from * 128) + part)
-                          : make_uint4(0, 0, 0, 0);
-        }
-#pragma unroll
-        for (int i = 0; i < kRounds; ++i) {
-          const int r = row_of(i);
-          const uint32_t m2 = __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
-                                       __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu));
-          uint32_t top = max(m2 & 0xffffu, m2 >> 16);  // the largest magnitude's bits (ordered as the values are)
-#pragma unroll
-          for (int d = 1; d < 16; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-          const int e = max(static_cast<int>(top >> 7) - 127, -100);
-          const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);  // 2^(14 - e)
-          // what the row's S is to be multiplied with (never 0 or Inf, which a score of 0 or a masked one's Inf
-          // would turn into NaN)
-          if (part == 0) sm.scale[r] = fminf(fmaxf(ldexpf(a.qk_scale, e - 14), FLT_MIN), FLT_MAX);
-          auto two = [&](uint32_t v) { return pack_half2(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xffff0000u) * up); };
-          const uint32_t at = q_at + r * 128 + (part >> 3) * kHalf + (((part & 7) ^ (r & 7)) << 4);
-          const uint32_t mine = KP == 2 ? (r & 1) * 2 * kHalf : 0;
-          st_shared_v4(at + mine, two(x[i].x), two(x[i].y), two(x[i].z), two(x[i].w));
-          if (KP == 2) st_shared_v4(at + (2 * kHalf - mine), 0u, 0u, 0u, 0u);  // the other map's channels
-        }
-        if (tid == 0) sm.seg = seg;
-        fence_proxy_async_smem();
-        named_barrier_sync(1, kAll);
-        if (lane == 0) mbar_arrive(bar(sm.q_full));
+      for (int i = 0; i < 8; ++i) {
+        const int r = row_of(batch * 8 + i), t = r / per, sub = r - t * per;
+        const size_t from = (static_cast<size_t>(u.q0 + tok0 + t) * a.H + u.h) * per + sub;
+        x[i] = u.todo > 0 && r < rows ? *(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + from * 128) + part)
+                                      : make_uint4(0, 0, 0, 0);
       }
-      const float scale = sm.scale[row];
+    };
+    auto write = [&](const uint4 (&x)[8], int batch) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = row_of(batch * 8 + i);
+        const uint32_t m2 = __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
+                                     __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu));
+        uint32_t top = max(m2 & 0xffffu, m2 >> 16);  // the largest magnitude's bits (ordered as the values are)
+#pragma unroll
+        for (int d = 1; d < 16; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+        const int e = max(static_cast<int>(top >> 7) - 127, -100);
+        const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);  // 2^(14 - e)
+        if (part == 0) sm.top[r] = e;
+        auto two = [&](uint32_t v) { return pack_half2(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xffff0000u) * up); };
+        const uint32_t at = q_at + r * 128 + (part >> 3) * kHalf + (((part & 7) ^ (r & 7)) << 4);
+        const uint32_t mine = KP == 2 ? (r & 1) * 2 * kHalf : 0;
+        st_shared_v4(at + mine, two(x[i].x), two(x[i].y), two(x[i].z), two(x[i].w));
+        if (KP == 2) st_shared_v4(at + (2 * kHalf - mine), 0u, 0u, 0u, 0u);  // the other map's channels
+      }
+    };
+    // The unit `u` (tiles_here of 0: the range's end) to the products, whose place for Q is free; `x`: its first batch.
+    auto present = [&](uint4 (&x)[8], const Walk& u) {
+      if (u.todo > 0) {
+#pragma unroll
+        for (int b = 0; b < kBatches; ++b) {
+          if (b > 0) fetch(x, u, b);
+          write(x, b);
+        }
+      }
+      if (tid == 0) sm.seg = tiles_here(u);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(sm.q_full));
+    };
+    {
+      uint4 x[8];
+      fetch(x, w, 0);
+      present(x, w);
+      named_barrier_sync(1, kAll);
+    }
+    while (w.todo > 0) {
+      const int seg = tiles_here(w);
+      const bool starts = w.tile == 0, whole = starts && seg == w.tiles;
+      const int tok0 = w.rt * a.tokens, toks = min(a.tokens, w.Lq - tok0), rows = toks * per;  // tokens and rows of the unit
+      // what the row's S is to be multiplied with (never 0 or Inf, which a score of 0 or a masked one's Inf would
+      // turn into NaN)
+      const float scale = fminf(fmaxf(ldexpf(a.qk_scale, sm.top[row] - 14), FLT_MIN), FLT_MAX);
       // keys that the row sees (none where there is no such token)
       const int lim = row >= rows ? 0 : a.causal ? max(0, w.Lk - w.Lq + tok0 + row / per + 1) : w.Lk;
       const bool busy = quarter * 32 < rows;  // the warp has rows in use
@@ -573,21 +607,43 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, 1) kv4_chunk_kernel(const K
       }
 
       // ---- the unit's end ----
+      // The next unit's queries first: their products run meanwhile. Q's place is free once the last scores are there.
+      Walk next = w;
+      advance(a, next, seg);
+      const int t = row / per, sub = row - t * per;
+      const size_t token = static_cast<size_t>(w.q0) + tok0 + t;
+      float lam = 0.f;
+      {
+        uint4 x[8];
+        fetch(x, next, 0);
+        if (whole && (row & 1) && row < rows)
+          lam = KP == 2 ? *(a.lambda + w.h) : *(a.lam_logit + token * (a.H * per / 2) + (w.h * per + sub) / 2);
+        if (kStreams == 2) ok = ok && mbar_wait(bar(sm.s_full[(j - 1) & 1]), ((j - 1) >> 1) & 1, abrt);
+        if (kStreams == 2 && wg == 1) sm.join[row] = make_float2(m, l);
+        named_barrier_sync(1, kAll);  // (nor does a warp still want this unit's exponents)
+        present(x, next);
+      }
+      float w0 = 1.f, w1 = 0.f;  // what the streams' O are to be multiplied with
+      if constexpr (kStreams == 2) {
+        if (wg == 0) {
+          const float2 other = sm.join[row];
+          const float m0 = m, m1 = other.x;
+          m = fmaxf(m0, m1);
+          w0 = ex2_approx(m0 - m), w1 = ex2_approx(m1 - m);
+          l = fmaf(l, w0, other.y * w1);
+          const float f = whole ? 1.f / l : 1.f;
+          w0 *= f, w1 *= f;
+          sm.join[row] = make_float2(w0, w1);
+        }
+        named_barrier_sync(1, kAll);
+        if (wg == 1) w0 = sm.join[row].x, w1 = sm.join[row].y;
+      } else if (whole) {
+        w0 = 1.f / l;
+      }
       if (kStreams == 2 && seg > 1) ok = ok && mbar_wait(bar(sm.pv_done[(j - 2) & 1]), ((j - 2) >> 1) & 1, abrt);
       ok = ok && mbar_wait(bar(sm.pv_done[(j - 1) & 1]), ((j - 1) >> 1) & 1, abrt);
       __syncwarp();
       tc_fence_after();
-      float w0 = 1.f, w1 = 0.f;  // what the streams' O are to be multiplied with
-      if constexpr (kStreams == 2) {
-        float2* ml = reinterpret_cast<float2*>(s_q);  // (Q's place is free: all scores are done)
-        ml[wg * kRows + row] = make_float2(m, l);
-        named_barrier_sync(1, kAll);
-        const float2 a0 = ml[row], a1 = ml[kRows + row];
-        const float m0 = a0.x, m1 = a1.x;
-        m = fmaxf(m0, m1);
-        w0 = ex2_approx(m0 - m), w1 = ex2_approx(m1 - m);
-        l = fmaf(a0.y, w0, a1.y * w1);
-      }
       // (an O that no tile of this unit went to is left out)
       const bool use0 = kStreams == 1 || seg > 1 || ((j - 1) & 1) == 0, use1 = kStreams == 2 && (seg > 1 || ((j - 1) & 1) == 1);
       const int* nan = sm.nan_key[unit & (kNanSets - 1)];
@@ -632,15 +688,10 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, 1) kv4_chunk_kernel(const K
         }
       } else {
         // this row's share of its pair's output: f times o (the odd row with its lambda, negative)
-        const int t = row / per, sub = row - t * per;
-        const size_t token = static_cast<size_t>(w.q0) + tok0 + t;
         float f = 0.f;
         if (lim > 0) {
-          f = a.v_mul / l;
-          if (row & 1) {
-            if constexpr (KP == 2) f *= -*(a.lambda + w.h);
-            else f *= -1.f / (1.f + __expf(-*(a.lam_logit + token * (a.H * per / 2) + (w.h * per + sub) / 2)));
-          }
+          f = a.v_mul;
+          if (row & 1) f *= KP == 2 ? -lam : -1.f / (1.f + __expf(-lam));
         }
         float g = 1.f;  // V1: the norm's factor and the scale
         // 32 channels of the pair's output, 16 for each of its two lanes
@@ -654,15 +705,19 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, 1) kv4_chunk_kernel(const K
           }
         };
         if (KP == 2) {
-          if (a.flags & 2) {
-            float ss = 0.f;
+          // into O's place on the way, for the second pass
+          float ss = 0.f;
 #pragma unroll 1
-            for (int c = 0; c < C::kWidth; c += 32) {
-              float z[16];
-              pair(z, c);
+          for (int c = 0; c < C::kWidth; c += 32) {
+            float z[16];
+            pair(z, c);
+            uint32_t raw[16];
 #pragma unroll
-              for (int x = 0; x < 16; ++x) ss = fmaf(z[x], z[x], ss);
-            }
+            for (int x = 0; x < 16; ++x) ss = fmaf(z[x], z[x], ss), raw[x] = __float_as_uint(z[x]);
+            tmem_st16(o_at + c, raw);
+          }
+          tmem_wait_st();
+          if (a.flags & 2) {
             ss += __shfl_xor_sync(0xffffffffu, ss, 1);
             g = 1.f / sqrtf(ss / 256.f + a.eps);
           }
@@ -675,14 +730,27 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, 1) kv4_chunk_kernel(const K
 #pragma unroll 1
         for (int c = wg * 32; c < C::kWidth; c += 32 * kStreams) {
           float z[16];
-          pair(z, c);
+          if constexpr (KP == 2) {
+            uint32_t raw[16];
+            tmem_ld16(o_at + c, raw);
+            tmem_wait_ld();
+#pragma unroll
+            for (int x = 0; x < 16; ++x) z[x] = __uint_as_float(raw[x]) * g;
+            if (weights) {
+              const float4* wgt = reinterpret_cast<const float4*>(a.norm_w + c + (row & 1) * 16);
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const float4 v = wgt[x];
+                z[4 * x] *= v.x, z[4 * x + 1] *= v.y, z[4 * x + 2] *= v.z, z[4 * x + 3] *= v.w;
+              }
+            }
+          } else {
+            pair(z, c);
+          }
           uint32_t o[8];
 #pragma unroll
-          for (int x = 0; x < 16; x += 2) {
-            float y0 = z[x] * g, y1 = z[x + 1] * g;
-            if (weights) y0 *= *(a.norm_w + c + (row & 1) * 16 + x), y1 *= *(a.norm_w + c + (row & 1) * 16 + x + 1);
-            o[x / 2] = lim > 0 ? pack_bf16x2(y0, y1) : 0u;  // (zeros, whatever the weight and the scale hold)
-          }
+          for (int x = 0; x < 16; x += 2)  // (zeros where no key is seen, whatever the weight and the scale hold)
+            o[x / 2] = lim > 0 ? pack_bf16x2(z[x], z[x + 1]) : 0u;
           if (store) {
             *reinterpret_cast<uint4*>(out + c) = make_uint4(o[0], o[1], o[2], o[3]);
             *reinterpret_cast<uint4*>(out + c + 8) = make_uint4(o[4], o[5], o[6], o[7]);
@@ -694,11 +762,8 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, 1) kv4_chunk_kernel(const K
       named_barrier_sync(1, kAll);
       if (tid < 16) sm.nan_key[unit & (kNanSets - 1)][tid] = INT_MAX;
       ++unit;
-      advance(a, w, seg);
+      w = next;
     }
-    if (tid == 0) sm.seg = 0;
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar(sm.q_full));
   }
 
   // ---- teardown ----
@@ -810,13 +875,14 @@ cudaError_t launch(Kv4ChunkArgs a, cudaStream_t st) {
   static std::atomic<uint64_t> raised{};
   a.rows = kRows;
   a.tokens = kRows / (KP == 2 ? 2 : a.group);
+  a.tok_log2 = KP == 2 ? 6 : a.group == 2 ? 6 : a.group == 4 ? 5 : 4;
   a.tile_log2 = 7;
-  a.unit_cost = kUnitCost;
+  a.unit_cost = Cfg<KP>::kUnitCost;
   page_magic(a.page_size >> 4, &a.rec_magic, &a.rec_shift);
   // no more blocks than the tables' capacity can give ranges: a sequence's tiles of tokens overlap the total's
   const long long tiles = (static_cast<long long>(a.max_pages) * a.page_size + kTile - 1) / kTile;
   const long long units = (static_cast<long long>(a.total) / a.tokens + a.B) * a.H;
-  const long long most = units >= kChunkSms ? kChunkSms : (tiles + kUnitCost) * units / kMinCost;
+  const long long most = units >= kChunkSms ? kChunkSms : (tiles + a.unit_cost) * units / kMinCost;
   a.grid = static_cast<int>(most < 1 ? 1 : most > kChunkSms ? kChunkSms : most);
   cudaError_t e = launch_early_large(kv4_chunk_kernel<KP>, a.grid, Cfg<KP>::kThreads, smem_bytes<KP>(), smem_bytes<KP>(), st, 1, a, raised);
   if (e != cudaSuccess || a.grid == 1) return e;

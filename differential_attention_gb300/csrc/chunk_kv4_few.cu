@@ -532,6 +532,7 @@ cudaError_t launch_kv4_chunk_few(Kv4ChunkArgs a, cudaStream_t st) {
   static std::atomic<uint64_t> raised{};
   a.rows = kRows;
   a.tokens = kTokens;
+  a.tok_log2 = 3;
   a.tile_log2 = kTileLog2;
   a.unit_cost = kUnitCost;
   page_magic(a.page_size >> 4, &a.rec_magic, &a.rec_shift);

@@ -361,8 +361,9 @@ struct Kv4ChunkArgs {
   float qk_scale, v_mul;   // as in Kv4DecodeArgs
   float* pieces;           // the workspace
   int longest;             // about the longest chunk: a hint
-  // Set by the launcher: tokens and rows of a unit, ranges, log2 of a tile's keys, what a unit costs in tiles.
-  int tokens, rows, grid, tile_log2, unit_cost;
+  // Set by the launcher: tokens of a unit (and their log2) and rows, ranges, log2 of a tile's keys, what a unit costs in
+  // tiles.
+  int tokens, tok_log2, rows, grid, tile_log2, unit_cost;
   uint32_t rec_magic, rec_shift;  // j / (page_size / 16), as in V2DecodeArgs' page_magic; the launcher's
 };
 size_t kv4_chunk_workspace_bytes(int group);

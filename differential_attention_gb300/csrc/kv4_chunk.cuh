@@ -44,17 +44,18 @@ __device__ __forceinline__ int hidden(const Kv4ChunkArgs& a, const Seq& s) {
   return s.Lk == 0 ? s.Lq : a.causal ? max(0, s.Lq - s.Lk) : 0;
 }
 __device__ __forceinline__ int tiles_of(const Kv4ChunkArgs& a, int Lq, int Lk, int rt) {
-  const int end = a.causal ? Lk - Lq + min(Lq, (rt + 1) * a.tokens) : Lk;
+  const int end = a.causal ? Lk - Lq + min(Lq, (rt + 1) << a.tok_log2) : Lk;
   return (end + (1 << a.tile_log2) - 1) >> a.tile_log2;
 }
 // of one head
 template <bool kEarly>
 __device__ __forceinline__ long long cost_of(const Kv4ChunkArgs& a, int b, bool report) {
   const Seq s = sequence<kEarly>(a, b, report);
-  const int z = hidden(a, s), n = (s.Lq + a.tokens - 1) / a.tokens;
+  const int z = hidden(a, s), n = (s.Lq + a.tokens - 1) >> a.tok_log2;
   if (z >= s.Lq) return 0;
   long long sum = 0;
-  for (int rt = z / a.tokens; rt < n; ++rt) sum += tiles_of(a, s.Lq, s.Lk, rt) + a.unit_cost;
+#pragma unroll 1
+  for (int rt = z >> a.tok_log2; rt < n; ++rt) sum += tiles_of(a, s.Lq, s.Lk, rt) + a.unit_cost;
   return sum;
 }
 // the first unit of sequence w.b, head w.h; false: it has none
@@ -63,8 +64,8 @@ __device__ __forceinline__ bool enter(const Kv4ChunkArgs& a, Walk& w) {
   const Seq s = sequence<kEarly>(a, w.b);
   const int z = hidden(a, s);
   w.q0 = s.q0, w.Lq = s.Lq, w.Lk = s.Lk;
-  w.nrt = (s.Lq + a.tokens - 1) / a.tokens;
-  w.rt = z / a.tokens;
+  w.nrt = (s.Lq + a.tokens - 1) >> a.tok_log2;
+  w.rt = z >> a.tok_log2;
   w.tile = 0;
   if (z >= s.Lq) return false;
   w.tiles = tiles_of(a, s.Lq, s.Lk, w.rt);
@@ -97,15 +98,24 @@ __device__ __forceinline__ void advance(const Kv4ChunkArgs& a, Walk& w, int n) {
   if (w.tile == w.tiles) next_unit(a, w);
 }
 
+// x / y for 0 <= x, 0 < y: one copy of the code, and nearly always both have 32 bits. (All of this is run once a
+// launch or unit, cold: what counts is that it is short.)
+static __device__ __noinline__ long long quotient64(long long x, long long y) {
+  if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+  return x / y;
+}
 __device__ __forceinline__ int range_count(long long total, int grid) {
   const long long want = total / kMinCost;
   return static_cast<int>(want < 1 ? 1 : want > grid ? grid : want);
 }
 __device__ __forceinline__ long long range_start(long long total, int n, int i) {
-  return total / n * i + total % n * i / n;
+  const long long each = quotient64(total, n);
+  return each * i + quotient64((total - each * n) * i, n);
 }
 // the range that holds x < total: the largest i with total i / n < x + 1
-__device__ __forceinline__ int range_of(long long total, int n, long long x) { return static_cast<int>(((x + 1) * n - 1) / total); }
+__device__ __forceinline__ int range_of(long long total, int n, long long x) {
+  return static_cast<int>(quotient64((x + 1) * n - 1, total));
+}
 
 // The costs before each thread's share of the sequences; a whole block of NT threads. Returns their sum.
 template <int NT, bool kEarly>
@@ -113,6 +123,7 @@ __device__ __forceinline__ long long fill(const Kv4ChunkArgs& a, long long* pre,
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, per = (a.B + NT - 1) / NT;
   const int lo = min(a.B, tid * per), hi = min(a.B, lo + per);
   long long incl = 0;
+#pragma unroll 1
   for (int b = lo; b < hi; ++b) incl += cost_of<kEarly>(a, b, report);
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -121,6 +132,7 @@ __device__ __forceinline__ long long fill(const Kv4ChunkArgs& a, long long* pre,
   }
   if (lane == 31) sum[warp] = incl;
   __syncthreads();
+#pragma unroll 1
   for (int w = 0; w < warp; ++w) incl += sum[w];
   pre[tid + 1] = incl;
   if (tid == 0) pre[0] = 0;
@@ -134,6 +146,7 @@ __device__ __forceinline__ void locate(const Kv4ChunkArgs& a, const long long* p
   const int lane = threadIdx.x & 31, per = (a.B + NT - 1) / NT;
   w = Walk{};
   int share = 0;
+#pragma unroll 1
   for (int i = 0; i < NT; i += 32)
     if (const unsigned hit = __ballot_sync(0xffffffffu, pre[i + lane] * a.H <= t0 && t0 < pre[i + lane + 1] * a.H)) {
       share = i + __ffs(hit) - 1;
@@ -141,6 +154,7 @@ __device__ __forceinline__ void locate(const Kv4ChunkArgs& a, const long long* p
     }
   long long at = pre[share], cost = 0;
   const int end = min(a.B, (share + 1) * per);
+#pragma unroll 1
   for (int b = share * per; b < end; ++b) {
     cost = per == 1 ? pre[share + 1] - pre[share] : cost_of<kEarly>(a, b, false);
     w.b = b;
@@ -148,9 +162,10 @@ __device__ __forceinline__ void locate(const Kv4ChunkArgs& a, const long long* p
     at += cost;
   }
   long long left = t0 - at * a.H;  // in the sequence
-  w.h = static_cast<int>(left / cost);
+  w.h = static_cast<int>(quotient64(left, cost));
   left -= w.h * cost;
   enter<kEarly>(a, w);
+#pragma unroll 1
   for (int rt = w.rt;; rt += 32) {  // 32 tiles of tokens at a time
     const int mine = rt + lane < w.nrt ? tiles_of(a, w.Lq, w.Lk, rt + lane) + a.unit_cost : 0;
     long long incl = mine;
