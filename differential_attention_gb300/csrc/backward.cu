@@ -303,6 +303,12 @@ __global__ void __launch_bounds__(kPreWarps * 32) bwd_pre_kernel(const Args a) {
       reinterpret_cast<float4*>(a.dkacc + static_cast<size_t>(r) * kD)[lane] =
           make_float4(0.f, 0.f, 0.f, 0.f);
   }
+  // dO behind the last sequence, which its last tile reads: a masked weight of 0 times what lay there (a NaN)
+  // would still reach dV
+  const long long all = a.cu ? static_cast<long long>(a.total) * a.H : rows;
+  for (long long r = rows + static_cast<long long>(blockIdx.x) * kPreWarps + warp; r < all;
+       r += static_cast<long long>(gridDim.x) * kPreWarps)
+    *reinterpret_cast<uint4*>(a.dO + static_cast<size_t>(r) * kDV + 8 * lane) = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
   for (int i = 0; i < 8; ++i) sdw[warp][8 * lane + i] = dwl[i];
   __syncthreads();
