@@ -29,12 +29,11 @@ __device__ __forceinline__ int ld(const int* p) {
 template <bool kEarly>
 __device__ __forceinline__ Seq sequence(const Kv4ChunkArgs& a, int b, bool report = false) {
   Seq s{ld<kEarly>(a.cu_seqlens + b), 0, 0};
-  const int end = ld<kEarly>(a.cu_seqlens + b + 1);
+  const int end = ld<kEarly>(a.cu_seqlens + b + 1), n = ld<kEarly>(a.seqlens + b), cap = a.max_pages * a.page_size;
   if (s.q0 < 0 || end < s.q0 || end > a.total) {
     if (report) flag_device_error(DEV_BAD_INDEX);
     return s;
   }
-  const int cap = a.max_pages * a.page_size, n = ld<kEarly>(a.seqlens + b);
   s.Lq = end - s.q0;
   s.Lk = n < 0 ? 0 : n > cap ? cap : n;
   return s;
