@@ -7,9 +7,9 @@
 // V's channels, are the 16 rows of a product, 8 tokens its columns. K's planes meet a column tile each (map m's
 // queries), V's planes both.
 //
-// Warps. One copies records into a ring of tiles, two prepare the queries of the next unit; two sets of four attend, a tile of 128 keys in turn, two records of
-// 16 keys a warp at a time, so that there are independent instructions to issue. Each warp has a running maximum, sum
-// and O of its own, joined through shared memory at the unit's end.
+// Warps. One copies records into a ring of tiles, two prepare the queries of the next unit; two sets of four attend,
+// a tile of 128 keys in turn, two records of 16 keys a warp at a time, so that there are independent instructions to
+// issue. Each warp has a running maximum, sum and O of its own, joined through shared memory at the unit's end.
 //
 // Numerics as in decode_kv4.cu: the query as fp16 after a power of two of its own for each row, P rounded to fp16
 // at 2^10 times its value against a reference that moves where a score passes it by 2^4, sums and statistics in fp32.
