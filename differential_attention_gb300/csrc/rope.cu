@@ -25,9 +25,9 @@ namespace {
 
 // Parts that a lane has under way, and blocks an SM. More parts take registers from warps, whose chains of position,
 // table and rows are what is waited for. (16384 tokens of 24 heads of 256 channels, backward / 16400 of 64 + 8 heads
-// into bf16 pages / 16384 of 12 + 12 of 256 into 4-bit pages, us: 4 parts and 5 blocks 102, 140, 190; 3 and 6 91,
-// 136, 177; 2 and 7 77, 124, 153; 2 and 8, which spills, 79, 127, 155; 1 and 8 85, 135, 151. The same bytes at a
-// copy's rate: 60, 99, 105. Streaming hints change nothing.)
+// into bf16 pages / 16384 of 12 + 12 of 256 into 4-bit pages and read back, us: 4 parts and 5 blocks 102, 140, 190;
+// 3 and 6 91, 136, 177; 2 and 7 77, 124, 153; 2 and 8, which spills, 79, 127, 155; 1 and 8 85, 135, 151. The same
+// bytes at a copy's rate: 60, 99, 105. Streaming hints change nothing.)
 constexpr int kThreads = 128, kBlocks = 7;
 constexpr int kAhead = 2;
 
