@@ -29,7 +29,7 @@
 // operands from shared memory) and 8 of P V (70, P in tensor memory): 1380 cycles; what the unpacking writes (64 KB,
 // 512 cycles) and the products read (768) comes on top, as it uses the same port, and a tile takes 2150. V1: 3150, of
 // which 2750 are its 32 products, a half of S's by zeros. Measured: 20 ragged prompts of up to 2048 new tokens over up
-// to 16384, G = 8 (V2) 1241 us, 915 TFLOP/s; 4 x 1024 over 4096, V1, 337 us, 800; 24 x 8 tokens over 32768, V2, where
+// to 16384, G = 8 (V2) 1222 us, 930 TFLOP/s; 4 x 1024 over 4096, V1, 337 us, 800; 24 x 8 tokens over 32768, V2, where
 // half of the 128 rows are empty, 394 us. Measured on the way: everything transposed, keys and channels on the 128
 // lanes and 64 queries as columns, 360 for the last and 2950 for the first; one O for both streams, its m handed
 // on, slower for all; 8 unpacking warps for V1, and V in front of the next tile's K, 444 where 4 x 1024 took 353.
@@ -520,6 +520,8 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, 1) kv4_chunk_kernel(const K
       const bool busy = quarter * 32 < rows;  // the warp has rows in use
       const int edge = __reduce_min_sync(0xffffffffu, row < rows ? lim : INT_MAX);
       float m = -FLT_MAX, l = 0.f;
+      Walk next = w;  // (here its loads are not waited for)
+      advance(a, next, seg);
 
       for (int i = 0; i < seg; ++i, ++j) {
         if (kStreams == 2 && (j & 1) != wg) continue;
@@ -608,8 +610,6 @@ __global__ void __launch_bounds__(Cfg<KP>::kThreads, 1) kv4_chunk_kernel(const K
 
       // ---- the unit's end ----
       // The next unit's queries first: their products run meanwhile. Q's place is free once the last scores are there.
-      Walk next = w;
-      advance(a, next, seg);
       const int t = row / per, sub = row - t * per;
       const size_t token = static_cast<size_t>(w.q0) + tok0 + t;
       float lam = 0.f;
