@@ -115,6 +115,14 @@ __device__ __forceinline__ uint64_t f2mul(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+// Row r of a tile, past its sequence's end, in `boxes` boxes `stride` bytes apart (whole 128 bytes of it,
+// so in any order: this one meets no bank twice). What hands the tile on to the product comes with
+// fence_proxy_async_smem().
+__device__ __forceinline__ void zero_row(uint32_t at, int r, int boxes, uint32_t stride) {
+  for (int c = 0; c < boxes; ++c)
+#pragma unroll
+    for (int u = 0; u < 8; ++u) st_shared_v4(at + c * stride + r * 128 + ((u ^ (r & 7)) << 4), 0u, 0u, 0u, 0u);
+}
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
@@ -185,8 +193,10 @@ __device__ __forceinline__ int qk_col(int m) {
 // Rows of sequence b: [s0, s0 + len) of the token axis (batched: b N .. b N + N - 1), and the
 // TMA coordinates (row, batch) of its first row. False for offsets outside the packed tensor
 // or longer than N: the caller reports DEV_BAD_INDEX and skips the sequence. A tile that reaches
-// past the sequence's end reads (and, for dQ, adds zeros into) the next sequence's rows, which
-// every mask treats as past the end.
+// past the sequence's end reads (and, for dQ, adds zeros into) the next sequence's rows, or rows of
+// none. Scores against them are masked. Where a product sums over such rows (V, K, Q and dO in turn),
+// a masked weight of 0 times a NaN there would still be one: those rows are zeroed in shared memory
+// before the product (zero_row), as the prefill does for V.
 struct SeqRows {
   int s0, len, trow, tb;
 };
@@ -303,12 +313,6 @@ __global__ void __launch_bounds__(kPreWarps * 32) bwd_pre_kernel(const Args a) {
       reinterpret_cast<float4*>(a.dkacc + static_cast<size_t>(r) * kD)[lane] =
           make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  // dO behind the last sequence, which its last tile reads: a masked weight of 0 times what lay there (a NaN)
-  // would still reach dV
-  const long long all = a.cu ? static_cast<long long>(a.total) * a.H : rows;
-  for (long long r = rows + static_cast<long long>(blockIdx.x) * kPreWarps + warp; r < all;
-       r += static_cast<long long>(gridDim.x) * kPreWarps)
-    *reinterpret_cast<uint4*>(a.dO + static_cast<size_t>(r) * kDV + 8 * lane) = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
   for (int i = 0; i < 8; ++i) sdw[warp][8 * lane + i] = dwl[i];
   __syncthreads();
@@ -558,6 +562,16 @@ __global__ void __launch_bounds__(dl::kThreads, 1)
         const int blk = u >> 3, uu = u & 7;
         st_shared_v4(p_row + blk * kBox + ((uu ^ (r & 7)) << 4), pk[4 * u], pk[4 * u + 1],
                      pk[4 * u + 2], pk[4 * u + 3]);
+      }
+      if (key0 + kT > sq.len) {  // the last tile: V's rows past the end (two half slots, nothing behind them)
+        for (int hf = 0; hf < 2; ++hf) {
+          const int idx = k_idx(n) + hf;
+          ok = ok && mbar_wait(bar(cs.slot_full[idx % kNSlot]), (idx / kNSlot) & 1, abrt);
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const int idx = k_idx(n) + (r >> 6);
+        if (key0 + r >= sq.len) zero_row(sRing + (idx % kNSlot) * kSlot, r & 63, 4, kVHalfBox);
       }
       fence_proxy_async_smem();
       mbar_arrive(bar(cs.p_full));
@@ -926,6 +940,12 @@ __global__ void __launch_bounds__(kq::kThreads, 1)
       for (int u = 0; u < 8; ++u)
         st_shared_v4(ds_row + ((u ^ (r & 7)) << 4), pk[4 * u], pk[4 * u + 1], pk[4 * u + 2],
                      pk[4 * u + 3]);
+      if (edge) {
+        // rows past the end, of Q before dK and (once) of K before dQ; S_t has read both, and S_{t+1} is
+        // issued behind them
+        if (qq >= sq.len) zero_row(sQ + wg * kBox, r, 1, 0);
+        if (t == 0 && key >= sq.len) zero_row(sK + wg * kBox, r, 1, 0);
+      }
       fence_proxy_async_smem();
       tc_fence_before();  // dW_t has been read: dQ_t may overwrite P(t & 1)
       mbar_arrive(bar(cs.ds_full));
@@ -991,12 +1011,18 @@ __global__ void __launch_bounds__(kq::kThreads, 1)
       if (!(ok = bar_and(2, 128, g))) break;
       tc_fence_after();
       const int i = i0 + t;
+      // rows past the sequence's end are the next one's: they get zeros, whatever this one's keys hold
+      const bool past = i * kT + r >= sq.len;
 #pragma unroll 1
       for (int pr = 0; pr < 2; ++pr) {
         uint32_t o[2][32];
         tmem_ld32(tmem + tl + pbuf(t) + 64 * pr, o[0]);
         tmem_ld32(tmem + tl + pbuf(t) + 64 * pr + 32, o[1]);
         tmem_wait_ld();
+        if (past) {
+#pragma unroll
+          for (int u = 0; u < 32; ++u) o[0][u] = o[1][u] = 0u;
+        }
         if (pr == 1) {
           tc_fence_before();
           mbar_arrive(bar(cs.dq_free));
@@ -1308,6 +1334,11 @@ __global__ void __launch_bounds__(vv::kThreads, 1)
       for (int u = 0; u < 8; ++u)
         st_shared_v4(w_row + ((u ^ (r & 7)) << 4), pk[4 * u], pk[4 * u + 1], pk[4 * u + 2],
                      pk[4 * u + 3]);
+      if ((i + 1) * kT > sq.len) {  // the last tile: dO's rows past the end
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(cs.do_full), t & 1, abrt));
+        if (!ok) break;
+        if (qq >= sq.len) zero_row(sDO + 2 * wg * kBox, r, 2, kBox);
+      }
       fence_proxy_async_smem();
       mbar_arrive(bar(cs.w_full));
     }

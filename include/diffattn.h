@@ -601,8 +601,9 @@ DIFFATTN_API int diffattn_bwd(const void* q, const void* k, const void* v, const
  *   stats : device fp32 [B, H, 2, Npad], Npad = max_seqlen rounded up to a multiple of 128;
  *            row i of sequence b at index i (entries past the sequence's length mean nothing)
  *   workspace, ws_bytes : at least diffattn_bwd_varlen_workspace_size() bytes
- * Rows that belong to no sequence are not written. dlambda and dnorm_weight sum over every
- * sequence. Other arguments, support and errors as diffattn_fwd_train and diffattn_bwd.
+ * Rows that belong to no sequence are not written, and what they hold, or another sequence's rows,
+ * does not reach a sequence's dq, dk and dv. dlambda and dnorm_weight sum over every sequence.
+ * Other arguments, support and errors as diffattn_fwd_train and diffattn_bwd.
  * ------------------------------------------------------------------------------------------ */
 DIFFATTN_API int diffattn_fwd_train_varlen(const void* q, const void* k, const void* v,
                                            void* out, void* o_pre, float* stats,
