@@ -53,10 +53,11 @@ __device__ __forceinline__ uint32_t turn_fast(float x1, float x2, float c, float
   unsure |= lo ^ hi;
   return lo;
 }
-// x1 c - x2 s to within 1.5 steps, whatever cancels (the first product's rounding error is put back)
+// x1 c - x2 s to within 1.5 steps, whatever cancels (the first product's rounding error is put back: of an
+// infinite product there is none, and Inf - Inf would make a NaN of the infinity that the formula gives)
 __device__ __forceinline__ float turn_f32(float x1, float x2, float c, float s) {
-  const float p = x2 * s;
-  return fmaf(x1, c, -p) + fmaf(-x2, s, p);
+  const float p = x2 * s, e = fmaf(-x2, s, p);
+  return fmaf(x1, c, -p) + (fabsf(p) < INFINITY ? e : 0.f);
 }
 
 // 16 channels of a part as a lane holds them: two runs of 8 (bf16: one uint4 each, fp32: two)
