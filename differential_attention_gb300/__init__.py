@@ -1602,17 +1602,17 @@ _lent_buffers, _lent_lock = {}, threading.Lock()
 
 
 @contextlib.contextmanager
-def _lent(index):
-    """Scratch for one decode (or chunk) on a current stream that torch did not make. Such a stream may be destroyed,
+def _lent(index, chunk=False):
+    """Scratch for one decode (or one chunk) on a current stream that torch did not make. Such a stream may be destroyed,
     and its handle come back, while its work still runs, so that nothing is kept by the handle: each
-    device has one buffer, large enough for any of them, which goes from call to call by an event.
-    (Decodes of several such streams so run one after the other, unless they are given workspaces.)"""
+    device has one buffer for decodes and one for chunks, large enough for any of them, which goes from call to call by
+    an event. (Decodes of several such streams so run one after the other, unless they are given workspaces.)"""
     with _lent_lock:
-        if index not in _lent_buffers:
-            n = max(diffattn_decode_kv4_workspace_size(1, 1), diffattn_v2_decode_kv4_workspace_size(1, 8, 1),
-                    diffattn_fwd_kv4_workspace_size(1 << 20), diffattn_v2_fwd_kv4_workspace_size(1 << 20, 8, 1))
-            _lent_buffers[index] = torch.empty(n, dtype=_U8, device=torch.device("cuda", index)), torch.cuda.Event()
-        buffer, done = _lent_buffers[index]
+        if (index, chunk) not in _lent_buffers:
+            n = (max(diffattn_fwd_kv4_workspace_size(1 << 20), diffattn_v2_fwd_kv4_workspace_size(1 << 20, 8, 1)) if chunk
+                 else max(diffattn_decode_kv4_workspace_size(1, 1), diffattn_v2_decode_kv4_workspace_size(1, 8, 1)))
+            _lent_buffers[index, chunk] = torch.empty(n, dtype=_U8, device=torch.device("cuda", index)), torch.cuda.Event()
+        buffer, done = _lent_buffers[index, chunk]
         stream = torch.cuda.current_stream(index)
         done.wait(stream)
         try:
@@ -1926,7 +1926,7 @@ def diffattn_fwd_kv4(q, pool, block_table, cu_seqlens_q, seqlens, lam, lambda_in
     if workspace is None:
         kept = _workspace(dev, raw, diffattn_fwd_kv4_workspace_size(longest, two_d // 2, two_d))
         if kept is None:
-            with _lent(dev) as workspace:
+            with _lent(dev, True) as workspace:
                 return diffattn_fwd_kv4(q, pool, block_table, cu_seqlens_q, seqlens, lam, lambda_init, norm_weight, eps, causal,
                                         norm, scale, max_seqlen_q, k_exp, v_exp, workspace, out)
         _, ws, ws_bytes = kept
@@ -1988,7 +1988,7 @@ def diffattn_v2_fwd_kv4(q, pool, block_table, cu_seqlens_q, seqlens, lam_logit, 
     if workspace is None:
         kept = _workspace(dev, raw, diffattn_v2_fwd_kv4_workspace_size(longest, Hq, Hkv, d))
         if kept is None:
-            with _lent(dev) as workspace:
+            with _lent(dev, True) as workspace:
                 return diffattn_v2_fwd_kv4(q, pool, block_table, cu_seqlens_q, seqlens, lam_logit, causal, max_seqlen_q, k_exp,
                                            v_exp, workspace, out)
         _, ws, ws_bytes = kept
