@@ -9,10 +9,10 @@
 // heads that the warp goes through, and 16 channels of a part, so that a load or store of the warp is whole
 // pieces of 128 bytes. Where the tokens are few, a token's parts are dealt out over several warps.
 //
-// A bf16 result is the exact value rounded once, so that the three calls agree in every bit, and the
-// 4-bit codes, which have borders too, are those of the exact keys' bf16. In fp32 a value is off by at most
-// t = 2^-24 (|x2 s| + |y|); where y - 2t and y + 2t round to the same bf16 (all but one in some 2^12),
-// that is the exact value's; else the value is formed in fp64, in which both products are exact.
+// A bf16 result is the fp64 sum of the two products (which are exact in fp64) rounded to bf16, so that the three
+// calls agree in every bit, and the 4-bit codes, which have borders too, are those of these keys' bf16. In fp32 a
+// value is off by at most t = 2^-24 (|x2 s| + |y|); where y - 2t and y + 2t round to the same bf16 (all but one in
+// some 2^12), that is the fp64 sum's; else the sum is formed.
 #include <type_traits>
 
 #include "early.cuh"
@@ -42,7 +42,7 @@ __device__ __noinline__ uint32_t turn_exact(float x1, float x2, float c, float s
   const double a = x1, b = x2, dc = c, ds = s;
   return bf16_of(a * dc - b * ds) | bf16_of(b * dc + a * ds) << 16;
 }
-// (y1, y2) of one pair, packed; `unsure` gets bits where it may not be the exact value's rounding
+// (y1, y2) of one pair, packed; `unsure` gets bits where it may not be the fp64 sum's rounding
 __device__ __forceinline__ uint32_t turn_fast(float x1, float x2, float c, float s, uint32_t& unsure) {
   constexpr float kTwo = 1.f / (1 << 23);
   const float p1 = x2 * s, p2 = x2 * c;

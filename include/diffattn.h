@@ -997,6 +997,7 @@ DIFFATTN_API int diffattn_v2_decode_kv4(const void* q, const void* pool, const i
  * diffattn_v2_fwd_paged (V2) with the keys and values in a pool as above, and any page size that is a
  * multiple of 16. Sequence b's Lq = cu_seqlens_q[b + 1] - cu_seqlens_q[b] queries are the last of its
  * seqlens[b] positions: with DIFFATTN_CAUSAL query i sees keys 0 .. seqlens[b] - Lq + i, without it all.
+ * A batch of single tokens alone is the decodes' (which take 0.4 to 0.9 times as long for it).
  * Numerics as in the decodes over the same pool: cached values enter exactly, the query in fp16 after a
  * power of two of its own for each head (V1: half), a probability rounded to fp16, sums and statistics
  * in fp32.
@@ -1010,8 +1011,10 @@ DIFFATTN_API int diffattn_v2_decode_kv4(const void* q, const void* pool, const i
  *          that is masked for a query never reaches that query's, whatever they hold
  *   lam_logit : device fp32 [total_q, Hq / 2]; lambda, lambda_init, norm_weight, eps, block_table : as for
  *          the decodes
- *   max_seqlen_q : the longest Lq, or any number near it: a hint (V1 has a kernel for up to 8 tokens).
- *          The results are right whatever it says
+ *   max_seqlen_q : the longest Lq, or any number near it: a hint. The results are right whatever it
+ *          says (not the same in every bit), and one workspace serves all. It chooses V1's kernel for
+ *          the whole batch: up to 8, the one for short chunks; above, or where a batch of such chunks
+ *          is called with its total, the one for 128 rows, which takes up to 1.7 times as long for them
  *   workspace, ws_bytes : at least the *_workspace_size bytes (for V2, of the same Hq / Hkv), 256-byte
  *          aligned; as for the decodes
  * A used table entry outside [0, num_pages) reads page 0 and is reported as DIFFATTN_ERR_INDEX. Equal
@@ -1046,19 +1049,22 @@ DIFFATTN_API int diffattn_v2_fwd_kv4(const void* q, const void* pool, const int*
  * DIFFATTN_ROPE_INVERSE turns back (s negated): the gradient with respect to x of a gradient with
  * respect to y.
  *   q, k : device rows [total, heads, width], the last dimension contiguous, the others by strides:
- *       host int64 [8], {token, head} of four tensors in the order of the arguments, in elements,
- *       positive multiples of 16 bytes (views of one fused projection, for example). Where a tensor
+ *       host int64 [8], {token, head} of four tensors in the order of the arguments, in elements, up to
+ *       2^36, positive multiples of 16 bytes (views of one fused projection, for example). Where a tensor
  *       has no heads, its pointers may be NULL (its strides still have to hold multiples)
  *   table : device fp32 [top, pairs, 2], cosines and sines (diffattn_rope_table, or a caller's own)
  *   positions : device int32 [n_axes, total]. A token with a position of -1 (diffattn_paged_plan's
  *       behind the last) is left out: nothing of it is read or written. So is one with any other
  *       position outside [0, top), which diffattn_device_status() reports as DIFFATTN_ERR_INDEX
  *   axes : device int32 [pairs], the axis (0 .. n_axes - 1) of each pair: time, height, width, in runs
- *       or in turn. NULL with one axis. Another value is taken as 0, and reported the same way
+ *       or in turn. Another value is taken as 0, and reported the same way. With one axis it is not
+ *       read, and may be NULL
  *   total : may be 0
- * A bf16 result is the exact value of the formula over the table's fp32 numbers, rounded once (to within
- * 2^-149 more where it is below 2^-100), so that the calls agree in every bit; an fp32 one is within
- * 2^-22 of its own magnitude and 2^-46 of the products'.
+ * A bf16 result is the fp64 sum of the two products (exact there) of the table's fp32 numbers, rounded to
+ * bf16 (to within 2^-149 more where it is below 2^-100), so that the calls agree in every bit. That is
+ * the exact value rounded once, but where one product is less than 2^-52 of the other and that other
+ * alone lies on a border of bf16. An fp32 result is within 2^-22 of its own magnitude and 2^-46 of the
+ * products' (and 2^-148 more, where those are subnormal).
  * Supported: d of 64 or 128, width a multiple of d up to 4096, pairs a multiple of 8 up to d / 2,
  * 1 <= n_axes <= 4, total * heads <= 2^30. One launch.
  * Errors: ERR_ARG, ERR_SHAPE, ERR_DTYPE, ERR_ALIGN, ERR_UNSUPPORTED, ERR_CUDA.
