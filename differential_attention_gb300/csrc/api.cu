@@ -2400,7 +2400,7 @@ int check_rope(const char* fn, const long long* strides, int n, const float* tab
   if (n_axes < 1 || n_axes > 4 || top < 1)
     return fail(DIFFATTN_ERR_SHAPE, "%s: need 1 to 4 axes and a table of at least one position", fn);
   for (int i = 0; i < 2 * n; ++i)
-    if (strides[i] < 1 || strides[i] * elt % 16 != 0 || strides[i] > (1LL << 36))
+    if (strides[i] < 1 || strides[i] > (1LL << 36) || strides[i] * elt % 16 != 0)
       return fail(DIFFATTN_ERR_ALIGN, "%s: stride %d (%lld) must be a positive multiple of 16 bytes, at most 2^36 elements", fn, i,
                   strides[i]);
   if (!aligned(table, 16) || !aligned(positions, 4) || !aligned(axes, 4))

@@ -29,11 +29,11 @@
 // operands from shared memory) and 8 of P V (70, P in tensor memory): 1380 cycles; what the unpacking writes (64 KB,
 // 512 cycles) and the products read (768) comes on top, as it uses the same port, and a tile takes 2150. V1: 3150, of
 // which 2750 are its 32 products, a half of S's by zeros. Measured (calls one by one, each after a write of 256 MB):
-// 20 ragged prompts of up to 2048 new tokens over up
-// to 16384, G = 8 (V2) 1222 us, 930 TFLOP/s; 4 x 1024 over 4096, V1, 337 us, 800; 24 x 8 tokens over 32768, V2, where
-// half of the 128 rows are empty, 394 us. Measured on the way: everything transposed, keys and channels on the 128
-// lanes and 64 queries as columns, 360 for the last and 2950 for the first; one O for both streams, its m handed
-// on, slower for all; 8 unpacking warps for V1, and V in front of the next tile's K, 444 where 4 x 1024 took 353.
+// 20 ragged prompts of up to 2048 new tokens over up to 16384, G = 8 (V2) 1222 us, 930 TFLOP/s; 4 x 1024 over 4096, V1,
+// 337 us, 800; 24 x 8 tokens over 32768, V2, where half of the 128 rows are empty, 394 us. Measured on the way:
+// everything transposed, keys and channels on the 128 lanes and 64 queries as columns, 360 for the last and 2950 for the
+// first; one O for both streams, its m handed on, slower for all; 8 unpacking warps for V1, and V in front of the next
+// tile's K, 444 where 4 x 1024 took 353.
 #include <cfloat>
 #include <cmath>
 

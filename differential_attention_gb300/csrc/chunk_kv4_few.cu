@@ -19,10 +19,10 @@
 // What bounds it: issue. A record takes some 590 instructions, 147 cycles of the SM's four schedulers where its bytes
 // take 196 at the memory's rate, but the accumulators (16 x 256 floats a warp) leave room for only two warps a
 // scheduler, and those issue in about half of the cycles. 16 sequences of 16384 keys, 6 new tokens, 12 heads (907 MB):
-// 184 us, 4.9 TB/s (calls one by one, each after a write of 256 MB; in a row 173, 5.2); the kernel for
-// 128 rows takes 307. Measured on the way, same case: a record at a time 206, two
-// records and tiles of 256 keys 191 (whose two stages are both in use while no copy runs), a record at a time with the
-// next tile's scores among this one's outputs 204. The same with V2 (four column tiles a warp, 32 rows) took 335 us
+// 184 us, 4.9 TB/s (calls one by one, each after a write of 256 MB; in a row 173, 5.2); the kernel for 128 rows takes
+// 307. Measured on the way, same case: a record at a time 206, two records and tiles of 256 keys 191 (whose two stages
+// are both in use while no copy runs), a record at a time with the next tile's scores among this one's outputs 204. The
+// same with V2 (four column tiles a warp, 32 rows) took 335 us
 // for 24 x 32768 keys, where 128 rows take 386, and more than those with mixed lengths (104 and 87 us) or 64 rows
 // (645); so V2 has no such kernel.
 #include <cfloat>
