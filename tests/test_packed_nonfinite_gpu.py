@@ -97,3 +97,26 @@ def test_a_sequence_of_nans_reaches_no_other(grouped, norm, causal, lens):
         assert torch.isnan(got["dq"][mine].float()).any() or torch.isnan(got["dv"][mine].float()).any()
         for b in (0, 2):
             s.same(got, want, slice(int(s.ends[b]), int(s.ends[b + 1])), (names, b))
+
+
+@pytest.mark.parametrize("grouped,norm,causal", CASES)
+def test_long_sequences_with_ragged_ends(grouped, norm, causal):
+    """Rings that went round several times before the last tile. dQ has up to 16 terms here (8 tiles by two heads): 30
+    additions of 2^-24 of at most 16 * 16 times the largest gradient, 2^-11 of it."""
+    lens = [700, 1000, 385]
+    s = Step(lens, 40, grouped, norm, causal)
+    want = s.run(s.clean)
+    x = {name: t.clone() for name, t in s.clean.items()}
+    for t in x.values():
+        t[int(s.ends[1]):int(s.ends[2])] = float("nan")
+        t[int(s.ends[3]):] = float("nan")
+    got = s.run(x)
+    for b in (0, 2):
+        rows = slice(int(s.ends[b]), int(s.ends[b + 1]))
+        for name in ("out", "dq", "dk", "dv"):
+            a, w = got[name][rows].float(), want[name][rows].float()
+            assert torch.isfinite(a).all(), (b, name)
+            if name == "dq":
+                assert torch.all((a - w).abs() <= STEP * w.abs() + 2.0 ** -11 * w.abs().max()), (b, name)
+            else:
+                assert torch.equal(a, w), (b, name)
